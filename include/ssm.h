@@ -334,6 +334,182 @@ int ssm_hippo_dplr(int kind, int64_t N, double theta,
                    ssm_c64* Lambda, ssm_c64* P, ssm_c64* V, ssm_c64* Bt, ssm_c64* Ct,
                    void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Selective state-space operators: the input-dependent counterpart of the
+ * filter and step modes above, with the short causal convolution before it.
+ * Per channel h with N real states, and B and C shared by the H/G channels of
+ * a group:
+ *   dt_t  = softplus(delta_t + delta_bias)   (or without softplus)
+ *   x_t   = exp(dt_t A[h]) x_{t-1} + dt_t u_t B_t
+ *   y_t   = (C_t . x_t + D u_t) silu(z_t)    (without z: no gate)
+ * and
+ *   pre_t = bias + sum_k w[k] u_{t-W+1+k},  y_t = pre_t or silu(pre_t).
+ *
+ * Conventions beside those at the top
+ *   - Activations (u, delta, z, B, C, y and their gradients, and convolution
+ *     states) are of one element type; parameters (A, D, delta_bias, weight,
+ *     bias), their gradients and the scan's states are float.  All sums, states
+ *     and exponentials are float32 or wider; an output is rounded once.
+ *   - Activations come as views with strides in elements, so that a slice or a
+ *     transpose needs no copy; any non-negative strides work, and two orders are
+ *     fast: steps contiguous ([Bsz,H,L] as everywhere in this library) and
+ *     channels contiguous ([Bsz,L,H] as a projection writes it).  Strides along
+ *     channels and states must be below 2^25 elements, along steps below 2^24
+ *     (else SSM_ERR_UNSUPPORTED).  Outputs must not overlap inputs or each other,
+ *     and no two elements of an output may share an address.
+ *   - Sequences.  Without `offsets` there are S = Bsz of them, one per batch
+ *     row, each of L steps or of lengths[s] <= L (device int32 [S], nullable).
+ *     With `offsets` (device int32 [S+1], ascending) Bsz is 1 and sequence s
+ *     takes the steps offsets[s] .. offsets[s+1] - 1 of the one row.  A sequence
+ *     may have no step: its state goes through unchanged.  Steps outside every
+ *     sequence are neither read nor written.  Entries outside [0, L] are clamped
+ *     into it; descending offsets leave the affected outputs unspecified.
+ *   - States.  state_in / x_in (nullable: zeros) are read before the first step
+ *     and state_out / x_out (nullable) written after the last; both may be the
+ *     same array.  Sequence s has row s, or row slots[s] of a pool of n_slots
+ *     rows (device int32 [S], nullable).  A slot outside [0, n_slots) names no
+ *     state: its sequence is skipped and its outputs are left as they were (the
+ *     padding rows of a captured decode batch).  No two sequences of a call may
+ *     name the same slot.
+ *   - The calls use no atomics: a repeated call gives the same bits.
+ * ---------------------------------------------------------------------- */
+
+/* Element types of activations. */
+#define SSM_F32 0
+#define SSM_BF16 1
+#define SSM_F16 2
+
+/* element (b, h, l) at data + b sb + h sh + l sl */
+typedef struct ssm_view {
+    const void* data;
+    int64_t sb, sh, sl;
+} ssm_view;
+
+/* element (b, g, n, l) at data + b sb + g sg + n sn + l sl */
+typedef struct ssm_group_view {
+    const void* data;
+    int64_t sb, sg, sn, sl;
+} ssm_group_view;
+
+typedef struct ssm_sequences {
+    int64_t Bsz, L, S;       /* S = Bsz without offsets */
+    const int32_t* offsets;  /* [S+1], nullable */
+    const int32_t* lengths;  /* [S], nullable; not with offsets */
+    const int32_t* slots;    /* [S], nullable; forward calls only */
+    int64_t n_slots;         /* rows of the state arrays where slots are given */
+} ssm_sequences;
+
+/* Operation ids for ssm_selective_bytes. */
+#define SSM_OP_SELECTIVE_SCAN 0           /* workspace of ssm_selective_scan */
+#define SSM_OP_SELECTIVE_SCAN_BACKWARD 1  /* workspace of ssm_selective_scan_backward, saved given */
+#define SSM_OP_SELECTIVE_SAVED 2          /* the states ssm_selective_scan keeps for the backward pass */
+#define SSM_OP_CAUSAL_CONV_BACKWARD 3     /* workspace of ssm_causal_conv_backward; N is the width */
+
+/*
+ * Bytes that a selective operator needs beside its arguments, from the sizes
+ * alone (`packed`: nonzero when the call has offsets; S as in ssm_sequences).
+ * Zero is possible (then the pointer may be null).  N and G are read by the
+ * scan's ops, N as the width by SSM_OP_CAUSAL_CONV_BACKWARD.
+ */
+int ssm_selective_bytes(int op, int64_t Bsz, int64_t H, int64_t N, int64_t G, int64_t L, int64_t S, int packed,
+                        size_t* bytes);
+
+/*
+ * Short causal convolution.  Sizes: Bsz, H, L, S >= 1, 1 <= width <= 4, Bsz H and
+ * S H below 2^31, L below 2^31.
+ *   u, y       views [Bsz,H,L]
+ *   weight     [H,width] float, weight[h][width-1] on the current step; bias [H], nullable
+ *   state_in, state_out   [S or n_slots, H, width-1] of u's type, the inputs before
+ *              the next step, oldest first (width 1: none, must be null)
+ * No workspace.
+ */
+int ssm_causal_conv(int dtype, const ssm_sequences* seq, int64_t H, int64_t width, int silu, const ssm_view* u,
+                    const float* weight, const float* bias, const void* state_in, void* state_out,
+                    const ssm_view* y, void* stream);
+
+/*
+ * Its gradients, from the gradient dy of y and (nullable) dstate_out of the
+ * final states, float [S,H,width-1].  u, weight, bias, state_in as in the forward call.
+ *   du [Bsz,H,L] view; dweight [H,width], dbias [H], dstate_in [S,H,width-1]
+ *   float, each nullable
+ * Workspace: SSM_OP_CAUSAL_CONV_BACKWARD.
+ */
+int ssm_causal_conv_backward(int dtype, const ssm_sequences* seq, int64_t H, int64_t width, int silu,
+                             const ssm_view* u, const float* weight, const float* bias, const void* state_in,
+                             const ssm_view* dy, const float* dstate_out, const ssm_view* du, float* dweight,
+                             float* dbias, float* dstate_in, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The convolution of one token per sequence: y = act(bias + w . [state, u]) and
+ * the state moves on by u.  u, y [Bsz,H] with rows u_stride, y_stride apart;
+ * state [Bsz or n_slots, H, width-1], updated.  No workspace.
+ */
+int ssm_causal_conv_step(int dtype, int64_t Bsz, int64_t H, int64_t width, int silu, const void* u, int64_t u_stride,
+                         const float* weight, const float* bias, void* state, const int32_t* slots,
+                         int64_t n_slots, void* y, int64_t y_stride, void* stream);
+
+/* The arguments of ssm_selective_scan, and of its backward pass. */
+typedef struct ssm_selective {
+    int64_t H, N, G;          /* G divides H; 1 <= N <= 64 */
+    int32_t dtype, softplus;
+    ssm_view u, delta, z;     /* [Bsz,H,L]; z.data nullable */
+    ssm_group_view B, C;      /* [Bsz,G,N,L] */
+    const float* A;           /* [H,N] */
+    const float* D;           /* [H], nullable (= 0) */
+    const float* delta_bias;  /* [H], nullable (= 0) */
+    const float* x_in;        /* [S or n_slots, H, N], nullable (= 0) */
+} ssm_selective;
+
+/*
+ * Selective scan.  y: view [Bsz,H,L], nullable where x_out or saved is given
+ * (the states alone).  x_out [S or n_slots, H, N] nullable.
+ * saved (nullable, SSM_OP_SELECTIVE_SAVED bytes): the states at every 16th step,
+ * for ssm_selective_scan_backward; not with slots.  Workspace:
+ * SSM_OP_SELECTIVE_SCAN.
+ */
+int ssm_selective_scan(const ssm_sequences* seq, const ssm_selective* p, const ssm_view* y, float* x_out, void* saved,
+                       size_t saved_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradients that ssm_selective_scan_backward writes. */
+typedef struct ssm_selective_grads {
+    ssm_view du, ddelta, dz;       /* [Bsz,H,L]; dz with z only */
+    ssm_group_view dB, dC;         /* [Bsz,G,N,L], summed over a group's channels */
+    float* dA;                     /* [H,N] */
+    float* dD;                     /* [H], nullable */
+    float* ddelta_bias;            /* [H], nullable */
+    float* dx_in;                  /* [S,H,N], nullable */
+} ssm_selective_grads;
+
+/*
+ * Gradients of ssm_selective_scan for the gradient dy of y and (nullable) dx_out
+ * of the final states, float [S,H,N].  p as in the forward call, saved as it
+ * wrote it for the same p and seq (no slots).  Gradients of steps outside every
+ * sequence are left as they were.  Workspace: SSM_OP_SELECTIVE_SCAN_BACKWARD.
+ */
+int ssm_selective_scan_backward(const ssm_sequences* seq, const ssm_selective* p, const void* saved,
+                                size_t saved_bytes, const ssm_view* dy, const float* dx_out,
+                                const ssm_selective_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The scan of one token per sequence, on states kept in x.
+ *   u, delta, z, y [Bsz,H], rows u_stride, ... elements apart; z nullable
+ *   B, C [Bsz,G,N], rows and groups B_stride, B_group, ... elements apart
+ *   A [H,N], D, delta_bias [H] as above; x [Bsz or n_slots, H, N], updated
+ * No workspace.
+ */
+typedef struct ssm_selective_token {
+    int64_t Bsz, H, N, G;
+    int32_t dtype, softplus;
+    const int32_t* slots;  /* [Bsz], nullable */
+    int64_t n_slots;
+    const void *u, *delta, *z, *B, *C;
+    void* y;
+    int64_t u_stride, delta_stride, z_stride, y_stride, B_stride, B_group, C_stride, C_group;
+    const float *A, *D, *delta_bias;
+    float* x;
+} ssm_selective_token;
+int ssm_selective_step(const ssm_selective_token* p, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,650 @@
+// Short causal convolution per channel, forward and backward:
+//   pre_t = bias + sum_k w[k] u_{t-W+1+k},  y_t = pre_t or silu(pre_t)
+// with the W - 1 inputs before a sequence's first step taken from its state
+// (zero without one), and the state after its last step handed on.
+//
+// Both directions read and write each element once and are bound by HBM; the
+// arithmetic per element is 2 W operations and one exponential.
+//   tokens  channels contiguous: a thread holds V channels (16 bytes) and walks
+//           kWalk steps with the W - 1 last inputs in registers; 64 lanes read
+//           1 KB of one step.  Any other strides take V = 1.
+//   rows    steps contiguous: a thread holds 8 steps of one channel and reads the
+//           steps around them again (an L1 hit).
+// Backward: dpre_t = dy_t silu'(pre_t) is recomputed, du_t sums W of them, so a
+// thread reads W - 1 steps past its own.  The weights' gradients are summed per
+// workgroup in a fixed order, written as one row of partial sums per workgroup
+// and added up in float64 by a second launch, so a repeated call gives the same bits.
+#include "selective.hpp"
+
+namespace ssm {
+
+namespace {
+
+constexpr int kWalk = 32;  // steps a thread walks ("tokens")
+
+template <class T, int V>
+struct __attribute__((packed, aligned(sizeof(T)))) VecN {
+    T v[V];
+};
+
+struct Geometry {
+    int Q;        // steps of an item
+    int cx;       // threads along the channels (tokens) or along the steps (rows); 256 / cx along the other
+    int blocks;   // channel blocks
+};
+
+__device__ __forceinline__ float silu_slope(float v) {
+    const float p = sigmoid_f(v);
+    return p * fmaf(v, 1.0f - p, 1.0f);
+}
+
+// V channels of one step; the last channel block may hold fewer
+template <class T, int V>
+__device__ __forceinline__ void load_v(float (&r)[V], const T* p, int64_t sh, int n) {
+    if (V > 1 && n == V) {
+        const VecN<T, V> w = *reinterpret_cast<const VecN<T, V>*>(p);
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = to_f(w.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = i < n ? to_f(p[i * sh]) : 0.0f;
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ void store_v(const float (&r)[V], T* p, int64_t sh, int n) {
+    if (V > 1 && n == V) {
+        VecN<T, V> w;
+#pragma unroll
+        for (int i = 0; i < V; ++i) w.v[i] = from_f<T>(r[i]);
+        *reinterpret_cast<VecN<T, V>*>(p) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < n) p[i * sh] = from_f<T>(r[i]);
+    }
+}
+
+// input `back` steps before the sequence's step 0 (back >= 1), from its state
+template <class T, int W>
+__device__ __forceinline__ float old_input(const T* state, int64_t row, int64_t H, int h, int back) {
+    return state ? to_f(state[(row * H + h) * (W - 1) + (W - 1 - back)]) : 0.0f;
+}
+
+// the state after the sequence: its last W - 1 inputs, from u where it has
+// them and from the state before it where it is shorter (read before anything
+// is written: state_out may be state_in)
+template <class T, int W>
+__device__ __forceinline__ void hand_on(const ConvArgs& a, const Item& it, int h) {
+    if constexpr (W > 1) {
+        if (!a.state_out) return;
+        const int len = it.end - it.beg;
+        T next[W - 1];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            const int t = len - (W - 1) + j;
+            if (t >= 0)
+                next[j] = ((const T*)a.u.data)[it.row * a.u.sb + h * a.u.sh + (it.beg + t) * a.u.sl];
+            else
+                next[j] = a.state_in ? ((const T*)a.state_in)[(it.state * a.H + h) * (W - 1) + (W - 1 + t)]
+                                     : from_f<T>(0.0f);
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) ((T*)a.state_out)[(it.state * a.H + h) * (W - 1) + j] = next[j];
+    }
+}
+
+template <class T, int W, int V>
+__global__ __launch_bounds__(256) void conv_tokens_kernel(ConvArgs a, Geometry geo) {
+    const int cb = blockIdx.x % geo.blocks;
+    Item it;
+    if (!find_item(a.q, blockIdx.x / geo.blocks, geo.Q, it) || it.state < 0) return;
+    const int cx = threadIdx.x & (geo.cx - 1), seg = threadIdx.x / geo.cx;
+    const int64_t h = ((int64_t)cb * geo.cx + cx) * V;
+    if (h >= a.H) return;
+    const int n = (int)min((int64_t)V, a.H - h);
+    const int64_t first = (int64_t)it.beg + (int64_t)it.c * geo.Q + seg * kWalk;  // this thread's steps
+    const int last = (int)min((int64_t)it.end, first + kWalk);
+
+    float w[W][V], b[V], past[W > 1 ? W - 1 : 1][V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        b[i] = a.bias && i < n ? a.bias[h + i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k][i] = i < n ? a.weight[(h + i) * W + k] : 0.0f;
+    }
+    const T* u = (const T*)a.u.data + it.row * a.u.sb + h * a.u.sh;
+    T* y = (T*)a.y.data + it.row * a.y.sb + h * a.y.sh;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {  // past[k]: the input W - 1 - k steps before `first`
+        const int64_t t = first - (W - 1) + k;
+        if (first < last && t >= it.beg) {
+            load_v<T, V>(past[k], u + t * a.u.sl, a.u.sh, n);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                past[k][i] = first < last && i < n
+                                 ? old_input<T, W>((const T*)a.state_in, it.state, a.H, (int)h + i, (int)(it.beg - t))
+                                 : 0.0f;
+        }
+    }
+    if (it.c == 0 && seg == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < n) hand_on<T, W>(a, it, (int)h + i);
+    }
+    constexpr int kAhead = 8;  // steps loaded together
+    for (int64_t t0 = first; t0 < last; t0 += kAhead) {
+        float v[kAhead][V];
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+            if (t0 + s < last) load_v<T, V>(v[s], u + (t0 + s) * a.u.sl, a.u.sh, n);
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+            if (t0 + s >= last) break;
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float acc = b[i];
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], past[k][i], acc);
+                acc = fmaf(w[W - 1][i], v[s][i], acc);
+                o[i] = a.silu ? silu_f(acc) : acc;
+#pragma unroll
+                for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
+                if (W > 1) past[W > 1 ? W - 2 : 0][i] = v[s][i];
+            }
+            store_v<T, V>(o, y + (t0 + s) * a.y.sl, a.y.sh, n);
+        }
+    }
+}
+
+// steps t - 4 .. t + 7 of a row as 12 floats; outside [beg, end): before it from
+// `state` (nullable), behind it 0
+template <class T, int W>
+__device__ __forceinline__ void row_before(float (&r)[4], const T* p, int64_t t, const Item& it, const T* state,
+                                           int64_t H, int h) {
+    if (t - 4 >= it.beg) {
+        const Vec4<T> v = *reinterpret_cast<const Vec4<T>*>(p + t - 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = to_f(v.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t at = t - 4 + i;
+            const int back = (int)(it.beg - at);
+            r[i] = at >= it.beg ? to_f(p[at]) : back < W ? old_input<T, W>(state, it.state, H, h, back) : 0.0f;
+        }
+    }
+}
+template <class T, int N>
+__device__ __forceinline__ void row_steps(float (&r)[N], const T* p, int64_t t, int64_t end) {
+    if (t + N <= end) {
+        const VecN<T, N> v = *reinterpret_cast<const VecN<T, N>*>(p + t);
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = to_f(v.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = t + i < end ? to_f(p[t + i]) : 0.0f;
+    }
+}
+template <class T>
+__device__ __forceinline__ void put_row(const float (&r)[8], T* p, int64_t t, int64_t end) {
+    if (t + 8 <= end) {
+        Vec8<T> v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.v[i] = from_f<T>(r[i]);
+        *reinterpret_cast<Vec8<T>*>(p + t) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (t + i < end) p[t + i] = from_f<T>(r[i]);
+    }
+}
+
+template <class T, int W>
+__global__ __launch_bounds__(256) void conv_rows_kernel(ConvArgs a, Geometry geo) {
+    const int cb = blockIdx.x % geo.blocks;
+    Item it;
+    if (!find_item(a.q, blockIdx.x / geo.blocks, geo.Q, it) || it.state < 0) return;
+    const int x = threadIdx.x & (geo.cx - 1);
+    const int64_t h = (int64_t)cb * (256 / geo.cx) + threadIdx.x / geo.cx;
+    if (h >= a.H) return;
+    float w[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = a.weight[h * W + k];
+    const float b = a.bias ? a.bias[h] : 0.0f;
+    const T* u = (const T*)a.u.data + it.row * a.u.sb + h * a.u.sh;
+    T* y = (T*)a.y.data + it.row * a.y.sb + h * a.y.sh;
+    const int64_t t = (int64_t)it.beg + (int64_t)it.c * geo.Q + x * 8;
+    float v[12] = {}, lo[4], hi[8];
+    if (t < it.end) {
+        row_before<T, W>(lo, u, t, it, (const T*)a.state_in, a.H, (int)h);
+        row_steps<T, 8>(hi, u, t, it.end);
+#pragma unroll
+        for (int i = 0; i < 12; ++i) v[i] = i < 4 ? lo[i] : hi[i - 4];
+    }
+    if (it.c == 0 && x == 0) hand_on<T, W>(a, it, (int)h);
+    if (t >= it.end) return;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float acc = b;
+#pragma unroll
+        for (int k = 0; k < W; ++k) acc = fmaf(w[k], v[i + 4 - (W - 1) + k], acc);
+        o[i] = a.silu ? silu_f(acc) : acc;
+    }
+    put_row<T>(o, y, t, it.end);
+}
+
+// ---- backward ----
+
+// gradient that the final state's gradient hands to input `t` (0 <= t < len), or
+// to the old input at state index j = W - 1 + t for t < 0
+template <int W>
+__device__ __forceinline__ float from_final(const ConvGradArgs& a, const Item& it, int64_t h, int64_t t) {
+    if (!a.dstate_out) return 0.0f;
+    const int64_t j = t - (it.end - it.beg) + (W - 1);
+    return j >= 0 && j < W - 1 ? a.dstate_out[(it.state * a.f.H + h) * (W - 1) + j] : 0.0f;
+}
+
+// gradient of the state before the sequence: old input i (i = 0 oldest) stands
+// W - 1 - i steps before step 0
+template <class T, int W>
+__device__ __forceinline__ void grad_old(const ConvGradArgs& a, const Item& it, int64_t h) {
+    if constexpr (W > 1) {
+        if (!a.dstate_in) return;
+        const T* u = (const T*)a.f.u.data + it.row * a.f.u.sb + h * a.f.u.sh;
+        const T* dy = (const T*)a.dy.data + it.row * a.dy.sb + h * a.dy.sh;
+        const int len = it.end - it.beg;
+        float line[2 * (W - 1)];  // the inputs from W - 1 steps before the sequence to W - 2 behind its first
+#pragma unroll
+        for (int i = 0; i < 2 * (W - 1); ++i) {
+            const int t = i - (W - 1);
+            line[i] = t < 0 ? old_input<T, W>((const T*)a.f.state_in, it.state, a.f.H, (int)h, -t)
+                            : t < len ? to_f(u[(it.beg + t) * a.f.u.sl]) : 0.0f;
+        }
+        float d[W - 1];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) d[i] = from_final<W>(a, it, h, i - (W - 1));
+#pragma unroll
+        for (int t = 0; t < W - 1; ++t) {  // the steps whose window reaches back over the start
+            if (t >= len) break;
+            float pre = a.f.bias ? a.f.bias[h] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) pre = fmaf(a.f.weight[h * W + k], line[t + k], pre);
+            const float g = to_f(dy[(it.beg + t) * a.dy.sl]);
+            const float dpre = a.f.silu ? g * silu_slope(pre) : g;
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                if (t + k < W - 1) d[t + k < W - 1 ? t + k : 0] += a.f.weight[h * W + k] * dpre;
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) a.dstate_in[(it.state * a.f.H + h) * (W - 1) + i] = d[i];
+    }
+}
+
+template <class T, int W, int V>
+__global__ __launch_bounds__(256) void conv_grad_tokens_kernel(ConvGradArgs g, Geometry geo, float* partial) {
+    __shared__ float red[256 * V];
+    const ConvArgs& a = g.f;
+    const int cb = blockIdx.x % geo.blocks;
+    const int64_t item = blockIdx.x / geo.blocks;
+    Item it;
+    const bool there = find_item(a.q, item, geo.Q, it);
+    const int cx = threadIdx.x & (geo.cx - 1), seg = threadIdx.x / geo.cx;
+    const int64_t h = ((int64_t)cb * geo.cx + cx) * V;
+    const int n = (int)max((int64_t)0, min((int64_t)V, a.H - h));
+    float dw[W][V] = {}, db[V] = {};
+    if (there && n > 0) {
+        const int64_t first = (int64_t)it.beg + (int64_t)it.c * geo.Q + seg * kWalk;
+        const int64_t last = min((int64_t)it.end, first + kWalk);
+        const T* u = (const T*)a.u.data + it.row * a.u.sb + h * a.u.sh;
+        const T* dy = (const T*)g.dy.data + it.row * g.dy.sb + h * g.dy.sh;
+        T* du = (T*)g.du.data + it.row * g.du.sb + h * g.du.sh;
+        if (it.c == 0 && seg == 0)
+            for (int i = 0; i < n; ++i) grad_old<T, W>(g, it, h + i);
+        if (first < last) {
+            float w[W][V], b[V], past[W > 1 ? W - 1 : 1][V], ahead[W][V] = {};
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                b[i] = a.bias && i < n ? a.bias[h + i] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) w[k][i] = i < n ? a.weight[(h + i) * W + k] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                const int64_t t = first - (W - 1) + k;
+                if (t >= it.beg) {
+                    load_v<T, V>(past[k], u + t * a.u.sl, a.u.sh, n);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        past[k][i] = i < n ? old_input<T, W>((const T*)a.state_in, it.state, a.H, (int)h + i,
+                                                             (int)(it.beg - t))
+                                           : 0.0f;
+                }
+            }
+            // ahead[j]: the gradient collected so far for input t - (W - 1) + j; the
+            // walk goes W - 1 steps past `last` so that the own inputs get all theirs
+            const int64_t stop = last + W - 1;
+            constexpr int kAhead = 4;
+            for (int64_t t0 = first; t0 < stop; t0 += kAhead) {
+                float v[kAhead][V], d[kAhead][V];
+#pragma unroll
+                for (int s = 0; s < kAhead; ++s) {
+                    const int64_t t = t0 + s;
+                    if (t < stop && t < it.end) {
+                        load_v<T, V>(v[s], u + t * a.u.sl, a.u.sh, n);
+                        load_v<T, V>(d[s], dy + t * g.dy.sl, g.dy.sh, n);
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < kAhead; ++s) {
+                    const int64_t t = t0 + s;
+                    if (t >= stop) break;
+                    const bool inside = t < it.end;
+                    const bool mine = t < last;
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        float dpre = 0.0f, x = 0.0f;
+                        if (inside) {
+                            x = v[s][i];
+                            dpre = d[s][i];
+                            if (a.silu) {
+                                float pre = b[i];
+#pragma unroll
+                                for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][i], past[k][i], pre);
+                                pre = fmaf(w[W - 1][i], x, pre);
+                                dpre *= silu_slope(pre);
+                            }
+                            if (mine) {
+                                db[i] += dpre;
+#pragma unroll
+                                for (int k = 0; k < W - 1; ++k) dw[k][i] = fmaf(dpre, past[k][i], dw[k][i]);
+                                dw[W - 1][i] = fmaf(dpre, x, dw[W - 1][i]);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < W; ++j) ahead[j][i] = fmaf(w[j][i], dpre, ahead[j][i]);
+                        o[i] = ahead[0][i];
+#pragma unroll
+                        for (int j = 0; j + 1 < W; ++j) ahead[j][i] = ahead[j + 1][i];
+                        ahead[W - 1][i] = 0.0f;
+#pragma unroll
+                        for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
+                        if (W > 1) past[W > 1 ? W - 2 : 0][i] = x;
+                    }
+                    const int64_t done = t - (W - 1);  // this input's gradient is whole
+                    if (done >= first) {
+                        if (g.dstate_out && done >= it.end - (W - 1)) {
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                if (i < n) o[i] += from_final<W>(g, it, h + i, done - it.beg);
+                        }
+                        store_v<T, V>(o, du + done * g.du.sl, g.du.sh, n);
+                    }
+                }
+            }
+        }
+    }
+    if (!partial) return;
+    // sum over the workgroup's stretches of steps in order, then one row per workgroup
+    float* out = partial + item * a.H * (W + 1);
+#pragma unroll
+    for (int k = 0; k <= W; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) red[i * 256 + threadIdx.x] = k < W ? dw[k < W ? k : 0][i] : db[i];
+        __syncthreads();
+        if (seg == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) {
+                    float s = 0.0f;
+                    for (int j = 0; j < 256 / geo.cx; ++j) s += red[i * 256 + j * geo.cx + cx];
+                    out[(int64_t)k * a.H + h + i] = s;
+                }
+        }
+    }
+}
+
+template <class T, int W>
+__global__ __launch_bounds__(256) void conv_grad_rows_kernel(ConvGradArgs g, Geometry geo, float* partial) {
+    __shared__ float red[(W + 1) * 256];
+    const ConvArgs& a = g.f;
+    const int cb = blockIdx.x % geo.blocks;
+    const int64_t item = blockIdx.x / geo.blocks;
+    Item it;
+    const bool there = find_item(a.q, item, geo.Q, it);
+    const int x = threadIdx.x & (geo.cx - 1);
+    const int64_t h = (int64_t)cb * (256 / geo.cx) + threadIdx.x / geo.cx;
+    float dw[W] = {}, db = 0.0f;
+    if (there && h < a.H) {
+        const T* u = (const T*)a.u.data + it.row * a.u.sb + h * a.u.sh;
+        const T* dy = (const T*)g.dy.data + it.row * g.dy.sb + h * g.dy.sh;
+        T* du = (T*)g.du.data + it.row * g.du.sb + h * g.du.sh;
+        if (it.c == 0 && x == 0) grad_old<T, W>(g, it, h);
+        float w[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k] = a.weight[h * W + k];
+        const float b = a.bias ? a.bias[h] : 0.0f;
+        const int64_t from = (int64_t)it.beg + (int64_t)it.c * geo.Q;
+        const int64_t to = min((int64_t)it.end, from + geo.Q);
+        for (int64_t t = from + x * 8; t < to; t += geo.cx * 8) {
+            float lo[4], mid[8], hi[4], dm[8], dh[4], v[16], d[12];
+            row_before<T, W>(lo, u, t, it, (const T*)a.state_in, a.H, (int)h);
+            row_steps<T, 8>(mid, u, t, it.end);
+            row_steps<T, 4>(hi, u, t + 8, it.end);
+            row_steps<T, 8>(dm, dy, t, it.end);
+            row_steps<T, 4>(dh, dy, t + 8, it.end);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = i < 4 ? lo[i] : i < 12 ? mid[i - 4] : hi[i - 12];
+#pragma unroll
+            for (int i = 0; i < 12; ++i) d[i] = i < 8 ? dm[i] : dh[i - 8];  // 0 behind the sequence
+#pragma unroll
+            for (int i = 0; i < 8 + W - 1; ++i) {
+                if (a.silu) {
+                    float pre = b;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) pre = fmaf(w[k], v[i + 4 - (W - 1) + k], pre);
+                    d[i] = t + i < it.end ? d[i] * silu_slope(pre) : 0.0f;
+                }
+                if (i < 8) {
+                    db += d[i];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) dw[k] = fmaf(d[i], v[i + 4 - (W - 1) + k], dw[k]);
+                }
+            }
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < W; ++j) s = fmaf(w[W - 1 - j], d[i + j], s);
+                o[i] = s;
+            }
+            if (g.dstate_out && t + 8 > it.end - (W - 1)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += from_final<W>(g, it, h, t + i - it.beg);
+            }
+            put_row<T>(o, du, t, it.end);
+        }
+    }
+    if (!partial) return;
+#pragma unroll
+    for (int k = 0; k <= W; ++k) red[k * 256 + threadIdx.x] = k < W ? dw[k < W ? k : 0] : db;
+    for (int half = geo.cx >> 1; half > 0; half >>= 1) {
+        __syncthreads();
+        if (x < half) {
+#pragma unroll
+            for (int k = 0; k <= W; ++k) red[k * 256 + threadIdx.x] += red[k * 256 + threadIdx.x + half];
+        }
+    }
+    if (x == 0 && h < a.H) {
+        float* out = partial + item * a.H * (W + 1);
+#pragma unroll
+        for (int k = 0; k <= W; ++k) out[(int64_t)k * a.H + h] = red[k * 256 + threadIdx.x];
+    }
+}
+
+// dweight[h, k] and dbias[h] from the rows of partial sums [rows][W + 1][H]
+constexpr int kSumCols = 32, kSumRows = 8;
+__global__ __launch_bounds__(256) void conv_grad_sum_kernel(const float* partial, int64_t rows, int64_t H, int W,
+                                                            float* dweight, float* dbias) {
+    __shared__ double red[kSumRows][kSumCols];
+    const int c = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+    const int64_t cols = H * (W + 1), col = (int64_t)blockIdx.x * kSumCols + c;
+    double s = 0.0;
+    if (col < cols)
+        for (int64_t i = r; i < rows; i += kSumRows) s += (double)partial[i * cols + col];
+    red[r][c] = s;
+    __syncthreads();
+    if (r == 0 && col < cols) {
+#pragma unroll
+        for (int i = 1; i < kSumRows; ++i) s += red[i][c];
+        const int64_t k = col / H, h = col % H;
+        if (k < W) {
+            if (dweight) dweight[h * W + k] = (float)s;
+        } else if (dbias) {
+            dbias[h] = (float)s;
+        }
+    }
+}
+
+int pow2_at_least(int64_t v, int most) {
+    int p = 1;
+    while (p < v && p < most) p <<= 1;
+    return p;
+}
+
+enum Order { kRows, kTokens, kAny };
+
+Order order_of(const View3* const* v, int n) {
+    bool rows = true, tokens = true;
+    for (int i = 0; i < n; ++i) {
+        rows = rows && v[i]->sl == 1;
+        tokens = tokens && v[i]->sh == 1;
+    }
+    return rows ? kRows : tokens ? kTokens : kAny;
+}
+
+template <class T>
+constexpr int vec() { return 16 / (int)sizeof(T); }
+
+Geometry geometry(Order o, int V, int64_t H, int64_t L, int iters) {
+    Geometry g;
+    if (o == kRows) {
+        g.cx = pow2_at_least((L + 7) / 8, 64);
+        g.Q = g.cx * 8 * iters;
+        const int chans = 256 / g.cx;
+        g.blocks = (int)((H + chans - 1) / chans);
+    } else {
+        const int64_t n = (H + V - 1) / V;
+        g.cx = pow2_at_least(n, 64);
+        g.Q = 256 / g.cx * kWalk;
+        g.blocks = (int)((n + g.cx - 1) / g.cx);
+    }
+    return g;
+}
+
+constexpr int kGradIters = 4;
+
+template <class T, int W>
+hipError_t forward_as(const ConvArgs& a, hipStream_t s) {
+    const View3* views[] = {&a.u, &a.y};
+    const Order o = order_of(views, 2);
+    const int V = o == kTokens ? vec<T>() : 1;
+    const Geometry geo = geometry(o, V, a.H, a.q.L, 1);
+    const int64_t wgs = item_count(a.q, geo.Q) * geo.blocks;
+    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)wgs), wg(256);
+    if (o == kRows)
+        conv_rows_kernel<T, W><<<grid, wg, 0, s>>>(a, geo);
+    else if (o == kTokens)
+        conv_tokens_kernel<T, W, vec<T>()><<<grid, wg, 0, s>>>(a, geo);
+    else
+        conv_tokens_kernel<T, W, 1><<<grid, wg, 0, s>>>(a, geo);
+    return hipGetLastError();
+}
+
+template <class T, int W>
+hipError_t backward_as(const ConvGradArgs& g, float* partial, hipStream_t s) {
+    const ConvArgs& a = g.f;
+    const View3* views[] = {&a.u, &g.dy, &g.du};
+    const Order o = order_of(views, 3);
+    const int V = o == kTokens ? vec<T>() : 1;
+    const Geometry geo = geometry(o, V, a.H, a.q.L, kGradIters);
+    const int64_t items = item_count(a.q, geo.Q), wgs = items * geo.blocks;
+    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)wgs), wg(256);
+    float* to = g.dweight || g.dbias ? partial : nullptr;
+    if (o == kRows)
+        conv_grad_rows_kernel<T, W><<<grid, wg, 0, s>>>(g, geo, to);
+    else if (o == kTokens)
+        conv_grad_tokens_kernel<T, W, vec<T>()><<<grid, wg, 0, s>>>(g, geo, to);
+    else
+        conv_grad_tokens_kernel<T, W, 1><<<grid, wg, 0, s>>>(g, geo, to);
+    if (to) {
+        const int64_t cols = a.H * (W + 1);
+        conv_grad_sum_kernel<<<dim3((unsigned)((cols + kSumCols - 1) / kSumCols)), wg, 0, s>>>(to, items, a.H, W,
+                                                                                             g.dweight, g.dbias);
+    }
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t forward_of(const ConvArgs& a, hipStream_t s) {
+    switch (a.width) {
+        case 1: return forward_as<T, 1>(a, s);
+        case 2: return forward_as<T, 2>(a, s);
+        case 3: return forward_as<T, 3>(a, s);
+        default: return forward_as<T, 4>(a, s);
+    }
+}
+template <class T>
+hipError_t backward_of(const ConvGradArgs& g, float* partial, hipStream_t s) {
+    switch (g.f.width) {
+        case 1: return backward_as<T, 1>(g, partial, s);
+        case 2: return backward_as<T, 2>(g, partial, s);
+        case 3: return backward_as<T, 3>(g, partial, s);
+        default: return backward_as<T, 4>(g, partial, s);
+    }
+}
+
+}  // namespace
+
+// partial sums of the weights' gradients; the largest over the storage orders
+size_t conv_grad_workspace_bytes(const Seqs& q, int64_t H, int width) {
+    int64_t items = 0;
+    for (Order o : {kRows, kTokens, kAny})
+        for (int V : {1, 4, 8}) {
+            const int64_t n = item_count(q, geometry(o, V, H, q.L, kGradIters).Q);
+            items = n > items ? n : items;
+        }
+    return (size_t)items * H * (width + 1) * sizeof(float);
+}
+
+// whether every storage order's launch stays below 2^31 workgroups
+bool conv_fits(const Seqs& q, int64_t H) {
+    for (Order o : {kRows, kTokens, kAny})
+        for (int V : {1, 4, 8}) {
+            const Geometry g = geometry(o, V, H, q.L, 1);
+            if (item_count(q, g.Q) * g.blocks >= ((int64_t)1 << 31)) return false;
+        }
+    return true;
+}
+
+hipError_t launch_causal_conv(int dtype, const ConvArgs& a, hipStream_t s) {
+    if (dtype == SSM_F32) return forward_of<float>(a, s);
+    if (dtype == SSM_BF16) return forward_of<bf16>(a, s);
+    return forward_of<f16>(a, s);
+}
+
+hipError_t launch_causal_conv_backward(int dtype, const ConvGradArgs& g, void* ws, hipStream_t s) {
+    if (dtype == SSM_F32) return backward_of<float>(g, (float*)ws, s);
+    if (dtype == SSM_BF16) return backward_of<bf16>(g, (float*)ws, s);
+    return backward_of<f16>(g, (float*)ws, s);
+}
+
+}  // namespace ssm

@@ -1,0 +1,282 @@
+// Shared pieces of the selective state-space kernels: element types, the
+// argument blocks the launchers take, the map from a work item to a stretch of
+// one sequence, quad (4-lane) exchanges and the scalar functions.
+#pragma once
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssm.h"
+
+namespace ssm {
+
+// ---- element types: activations are read to float32 and rounded once on the way out ----
+struct bf16 { uint16_t v; };
+struct f16 { _Float16 v; };
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __uint_as_float((uint32_t)x.v << 16); }
+__device__ __forceinline__ float to_f(f16 x) { return (float)x.v; }
+template <class T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ f16 from_f<f16>(float x) { return f16{(_Float16)x}; }
+template <>
+__device__ __forceinline__ bf16 from_f<bf16>(float x) {  // round to nearest, ties to even
+    return bf16{__builtin_bit_cast(uint16_t, (__bf16)x)};
+}
+
+// 8 consecutive elements as one (or, in float32, two) 16-byte accesses; the
+// address needs no more than the element's own alignment
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Vec8 {
+    T v[8];
+};
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Vec4 {
+    T v[4];
+};
+
+// ---- views: element (b, h, l) at data + b sb + h sh + l sl (in elements) ----
+struct View3 {
+    const void* data = nullptr;
+    int64_t sb = 0, sh = 0, sl = 0;
+};
+struct View4 {
+    const void* data = nullptr;
+    int64_t sb = 0, sg = 0, sn = 0, sl = 0;
+};
+
+// ---- sequences of a call ----
+// dense: sequence s is batch row s, of L or lengths[s] steps.  packed (offsets
+// given): one batch row of L steps, sequence s at [offsets[s], offsets[s+1]).
+// Values outside [0, L] are clamped, so that no content of these arrays can
+// lead an access out of the tensors.
+struct Seqs {
+    int64_t S = 0, L = 0;
+    const int32_t* offsets = nullptr;
+    const int32_t* lengths = nullptr;
+    const int32_t* slots = nullptr;
+    int64_t n_slots = 0;
+};
+
+// the stretch of steps a workgroup handles
+struct Item {
+    int s;         // sequence
+    int c;         // its chunk
+    int64_t row;   // batch row
+    int beg, end;  // the sequence's steps along the row's time axis
+    int64_t state; // its state row, or -1: no such state, nothing to do
+};
+
+__device__ __forceinline__ void seq_bounds(const Seqs& q, int s, int64_t& row, int& beg, int& end) {
+    const int L = (int)q.L;
+    if (q.offsets) {
+        row = 0;
+        beg = min(max(q.offsets[s], 0), L);
+        end = min(max(q.offsets[s + 1], beg), L);
+    } else {
+        row = s;
+        beg = 0;
+        end = q.lengths ? min(max(q.lengths[s], 0), L) : L;
+    }
+}
+
+__device__ __forceinline__ int chunks_of(int len, int Q) { return max(1, (int)(((int64_t)len + Q - 1) / Q)); }
+
+// Work items enumerate the chunks of Q steps of every sequence, at least one
+// per sequence.  Dense: item = s * ceil(L/Q) + c.  Packed: the sequences'
+// chunks one behind the other; a wave finds its item by a prefix sum over 64
+// sequences at a time.  Returns false where the item is behind the last one.
+__device__ __forceinline__ bool find_item(const Seqs& q, int64_t item, int Q, Item& it) {
+    if (!q.offsets) {
+        const int per = chunks_of((int)q.L, Q);
+        it.s = (int)(item / per);
+        it.c = (int)(item % per);
+    } else {
+        const int lane = threadIdx.x & 63;
+        int64_t left = item;
+        int s0 = 0, found = -1;
+        for (; s0 < q.S; s0 += 64) {
+            int n = 0;
+            if (s0 + lane < q.S) {
+                int64_t row;
+                int b, e;
+                seq_bounds(q, s0 + lane, row, b, e);
+                n = chunks_of(e - b, Q);
+            }
+            int64_t incl = n;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int64_t o = __shfl_up(incl, d);
+                if (lane >= d) incl += o;
+            }
+            const uint64_t hit = __ballot(left < incl);
+            if (hit) {
+                found = __builtin_ctzll(hit);
+                const int64_t before = __shfl(incl - n, found);
+                left -= before;
+                break;
+            }
+            left -= __shfl(incl, 63);
+        }
+        if (found < 0) return false;
+        it.s = s0 + found;
+        it.c = (int)left;
+    }
+    it.s = __builtin_amdgcn_readfirstlane(it.s);
+    it.c = __builtin_amdgcn_readfirstlane(it.c);
+    seq_bounds(q, it.s, it.row, it.beg, it.end);
+    it.state = it.s;
+    if (q.slots) {
+        const int64_t slot = q.slots[it.s];
+        it.state = slot >= 0 && slot < q.n_slots ? slot : -1;
+    }
+    return true;
+}
+
+// items a launch has to cover (host side): exact when dense, an upper bound when packed
+inline int64_t item_count(const Seqs& q, int64_t Q) {
+    if (!q.offsets) return q.S * ((q.L + Q - 1) / Q);
+    return q.S + q.L / Q;
+}
+
+// ---- quad exchanges (v_*_dpp quad_perm) ----
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+// the value of quad lane K in all four lanes (K a compile-time value once unrolled)
+__device__ __forceinline__ float quad_bcast(float v, int K) {
+    switch (K) {
+        case 0: return dpp<0x00>(v);
+        case 1: return dpp<0x55>(v);
+        case 2: return dpp<0xAA>(v);
+        default: return dpp<0xFF>(v);
+    }
+}
+// lane q of each quad gets the sum over the quad of p_q: 9 instructions for four sums
+__device__ __forceinline__ float quad_sums(float p0, float p1, float p2, float p3, bool odd, bool high) {
+    const float a = (odd ? p1 : p0) + dpp<0xB1>(odd ? p0 : p1);
+    const float b = (odd ? p3 : p2) + dpp<0xB1>(odd ? p2 : p3);
+    return (high ? b : a) + dpp<0x4E>(high ? a : b);
+}
+
+// ---- scalar functions ----
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLo = 1.925963033500717e-08f;  // log2(e) - kLog2e
+constexpr float kLn2 = 0.6931471805599453f;
+
+// exp(v) to about one unit in the last place: the product v log2(e) is carried
+// in two parts (its rounding alone would cost |v| units)
+__device__ __forceinline__ float exp_f(float v) {
+    const float p = v * kLog2e;
+    const float lo = fmaf(v, kLog2eLo, fmaf(v, kLog2e, -p));
+    const float e = __builtin_amdgcn_exp2f(p);
+    // far from 0, where e may be infinite or lo NaN, exp2 alone
+    return fabsf(v) < 80.0f ? fmaf(e, lo * kLn2, e) : e;
+}
+
+// log(1 + exp(v)); above 20 it is v to float32.  log1p(e) = log(w) + (e - (w - 1))/w
+// with w = fl(1 + e); where e >= 1 the second term is below half a unit of the
+// first and is left out, elsewhere w stands for 1 in it (an error below a
+// quarter unit).
+__device__ __forceinline__ float softplus_f(float v) {
+    const float e = exp_f(fminf(v, 20.0f));
+    const float w = 1.0f + e;
+    const float c = e < 1.0f ? e - (w - 1.0f) : 0.0f;
+    const float r = fmaf(__builtin_amdgcn_logf(w), kLn2, c);
+    return v > 20.0f ? v : (v == v ? r : v);
+}
+
+__device__ __forceinline__ float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.0f + exp_f(-v)); }
+__device__ __forceinline__ float silu_f(float v) { return v * sigmoid_f(v); }
+
+// ---- argument blocks ----
+struct ScanArgs {
+    Seqs q;
+    int64_t Bsz, H, N, G;
+    int softplus;
+    View3 u, delta, z, y;  // z.data, y.data nullable
+    View4 B, C;
+    const float* A;
+    const float* D;           // nullable
+    const float* delta_bias;  // nullable
+    const float* x_in;        // [states, H, N] nullable
+    float* x_out;             // nullable
+    float* saved;             // nullable: states every kSaveSteps steps, for the backward pass
+};
+
+struct ScanGradArgs {
+    ScanArgs f;      // the forward call's arguments (y, x_out, saved unused)
+    const float* saved;
+    View3 dy;
+    View3 du, ddelta, dz;
+    View4 dB, dC;
+    float *dA, *dD, *ddelta_bias;  // dD, ddelta_bias nullable
+    const float* dx_out;           // gradient of the final states, nullable
+    float* dx_in;                  // gradient of the initial states, nullable
+};
+
+struct ConvArgs {
+    Seqs q;
+    int64_t H;
+    int width, silu;
+    View3 u, y;
+    const float* weight;   // [H, width]
+    const float* bias;     // [H] nullable
+    const void* state_in;  // [states, H, width - 1] of u's type, oldest first; nullable
+    void* state_out;       // nullable, may be state_in
+};
+
+struct ConvGradArgs {
+    ConvArgs f;  // the forward call's arguments (y, state_out unused; states are per sequence)
+    View3 dy, du;
+    float *dweight, *dbias;    // nullable
+    const float* dstate_out;   // [S, H, width - 1], nullable
+    float* dstate_in;          // nullable
+};
+
+struct StepArgs {
+    int64_t Bsz, H, N, G;
+    int softplus;
+    const int32_t* slots;  // nullable
+    int64_t n_slots;
+    const void *u, *delta, *z, *B, *C;  // [Bsz, H], [Bsz, G, N]; strides of rows (and groups) below
+    void* y;
+    int64_t u_row, delta_row, z_row, y_row, B_row, B_group, C_row, C_group;
+    const float *A, *D, *delta_bias;
+    float* x;  // [states, H, N], updated
+};
+
+struct ConvStepArgs {
+    int64_t Bsz, H;
+    int width, silu;
+    const int32_t* slots;
+    int64_t n_slots;
+    const void* u;
+    void* y;
+    int64_t u_row, y_row;
+    const float *weight, *bias;
+    void* state;  // [states, H, width - 1], updated
+};
+
+// states per channel as the kernels hold them, in blocks of 16 (1, 2 or 4)
+__host__ __device__ inline int64_t padded_states(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+
+// steps between two saved states, and where they lie: sequence s keeps its
+// k-th at row saved_row + k of [rows, H, padded_states(N)]
+constexpr int kSaveSteps = 16;
+__host__ __device__ inline int64_t saved_rows(int64_t S, int64_t L, bool packed) {
+    return packed ? L / kSaveSteps + S : S * ((L + kSaveSteps - 1) / kSaveSteps);
+}
+__device__ __forceinline__ int64_t saved_row(const Seqs& q, const Item& it) {
+    return q.offsets ? (int64_t)(it.beg / kSaveSteps) + it.s
+                     : (int64_t)it.s * ((q.L + kSaveSteps - 1) / kSaveSteps);
+}
+
+}  // namespace ssm

@@ -40,7 +40,53 @@ HIPPO_KINDS = {"legs": HIPPO_LEGS, "legt": HIPPO_LEGT, "lagt": HIPPO_LAGT}
 EXPORTS = ("ssm_workspace_bytes", "ssm_transform_lengths", "ssm_forward_form", "ssm_status_string",
            "ssm_discretize", "ssm_kernel_gen", "ssm_fftconv", "ssm_forward", "ssm_forward_profiled", "ssm_step",
            "ssm_forward_complex", "ssm_hippo_dplr", "ssm_step_prepare", "ssm_step_prepared",
-           "ssm_forward_noalloc")
+           "ssm_forward_noalloc", "ssm_selective_bytes", "ssm_causal_conv", "ssm_causal_conv_backward",
+           "ssm_causal_conv_step", "ssm_selective_scan", "ssm_selective_scan_backward", "ssm_selective_step")
+
+# element types and operation ids of the selective operators
+F32, BF16, F16 = 0, 1, 2
+OP_SELECTIVE_SCAN, OP_SELECTIVE_SCAN_BACKWARD, OP_SELECTIVE_SAVED, OP_CAUSAL_CONV_BACKWARD = 0, 1, 2, 3
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+class View(ctypes.Structure):
+    """ssm_view"""
+    _fields_ = [("data", ctypes.c_void_p)] + [(k, ctypes.c_int64) for k in ("sb", "sh", "sl")]
+
+
+class GroupView(ctypes.Structure):
+    """ssm_group_view"""
+    _fields_ = [("data", ctypes.c_void_p)] + [(k, ctypes.c_int64) for k in ("sb", "sg", "sn", "sl")]
+
+
+class Sequences(ctypes.Structure):
+    """ssm_sequences"""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("Bsz", "L", "S")]
+                + [(k, ctypes.c_void_p) for k in ("offsets", "lengths", "slots")] + [("n_slots", ctypes.c_int64)])
+
+
+class Selective(ctypes.Structure):
+    """ssm_selective"""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("H", "N", "G")] + [(k, ctypes.c_int32) for k in ("dtype", "softplus")]
+                + [(k, View) for k in ("u", "delta", "z")] + [(k, GroupView) for k in ("B", "C")]
+                + [(k, ctypes.c_void_p) for k in ("A", "D", "delta_bias", "x_in")])
+
+
+class SelectiveGrads(ctypes.Structure):
+    """ssm_selective_grads"""
+    _fields_ = ([(k, View) for k in ("du", "ddelta", "dz")] + [(k, GroupView) for k in ("dB", "dC")]
+                + [(k, ctypes.c_void_p) for k in ("dA", "dD", "ddelta_bias", "dx_in")])
+
+
+class SelectiveToken(ctypes.Structure):
+    """ssm_selective_token"""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("Bsz", "H", "N", "G")]
+                + [(k, ctypes.c_int32) for k in ("dtype", "softplus")]
+                + [("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int64)]
+                + [(k, ctypes.c_void_p) for k in ("u", "delta", "z", "B", "C", "y")]
+                + [(k, ctypes.c_int64) for k in ("u_stride", "delta_stride", "z_stride", "y_stride", "B_stride",
+                                                 "B_group", "C_stride", "C_group")]
+                + [(k, ctypes.c_void_p) for k in ("A", "D", "delta_bias", "x")])
 
 
 class SSMError(RuntimeError):
@@ -85,6 +131,23 @@ def _load():
     lib.ssm_forward_noalloc.restype = i32
     lib.ssm_hippo_dplr.argtypes = [i32, i64, ctypes.c_double, i64, vp, i64, vp] + [vp] * 5 + [vp, sz, vp]
     lib.ssm_hippo_dplr.restype = i32
+    view, seqs = ctypes.POINTER(View), ctypes.POINTER(Sequences)
+    lib.ssm_selective_bytes.argtypes = [i32, i64, i64, i64, i64, i64, i64, i32, ctypes.POINTER(sz)]
+    lib.ssm_selective_bytes.restype = i32
+    lib.ssm_causal_conv.argtypes = [i32, seqs, i64, i64, i32, view, vp, vp, vp, vp, view, vp]
+    lib.ssm_causal_conv.restype = i32
+    lib.ssm_causal_conv_backward.argtypes = ([i32, seqs, i64, i64, i32, view, vp, vp, vp, view, vp, view]
+                                             + [vp] * 4 + [sz, vp])
+    lib.ssm_causal_conv_backward.restype = i32
+    lib.ssm_causal_conv_step.argtypes = [i32, i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp]
+    lib.ssm_causal_conv_step.restype = i32
+    lib.ssm_selective_scan.argtypes = [seqs, ctypes.POINTER(Selective), view, vp, vp, sz, vp, sz, vp]
+    lib.ssm_selective_scan.restype = i32
+    lib.ssm_selective_scan_backward.argtypes = [seqs, ctypes.POINTER(Selective), vp, sz, view, vp,
+                                                ctypes.POINTER(SelectiveGrads), vp, sz, vp]
+    lib.ssm_selective_scan_backward.restype = i32
+    lib.ssm_selective_step.argtypes = [ctypes.POINTER(SelectiveToken), vp]
+    lib.ssm_selective_step.restype = i32
     return lib
 
 
@@ -407,6 +470,360 @@ def hippo_dplr(kind, N, theta=1.0, B=None, C=None, want_v=False, device="cuda:0"
     if rc != OK:
         raise SSMError("ssm_hippo_dplr", rc)
     return dict(Lambda=Lam, P=P, V=V, Bt=Bt, Ct=Ct)
+
+
+# ---- selective operators ----
+#
+# Activations are float32, bfloat16 or float16 tensors [Bsz, H, L] (B and C
+# [Bsz, G, N, L]) with any strides: a projection's [Bsz, L, H] output goes in as
+# its .transpose(1, 2), a slice as it is.  Outputs that the call makes are
+# dense, in the order of the input they belong to.
+
+
+def _strides(t):
+    # a dimension of one element has no stride
+    return [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+
+
+def _view(t):
+    return View() if t is None else View(t.data_ptr(), *_strides(t))
+
+
+def _group_view(t):
+    return GroupView(t.data_ptr(), *_strides(t))
+
+
+def _activation(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        got = (None if not isinstance(t, torch.Tensor) else (t.dtype, tuple(t.shape)))
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {got}")
+    if t.device != device:
+        raise ValueError(f"{name}: must be on {device}")
+
+
+def _first(u, dims):
+    if not isinstance(u, torch.Tensor) or u.dim() != dims or u.dtype not in _TYPES or not u.is_cuda:
+        raise ValueError(f"u: expected a float32, bfloat16 or float16 device tensor of {dims} dimensions")
+    if u.numel() == 0:
+        raise ValueError("u: has no elements")
+    return u.device, _TYPES[u.dtype]
+
+
+def _like(t, empty=True):
+    """A dense output for t [Bsz,...,L], with the steps stored last where t's are
+    contiguous and first (behind the batch) elsewhere."""
+    make = torch.empty if empty else torch.zeros
+    if t.stride(-1) == 1:
+        return make(t.shape, dtype=t.dtype, device=t.device)
+    if t.dim() == 3:
+        Bsz, H, L = t.shape
+        return make((Bsz, L, H), dtype=t.dtype, device=t.device).transpose(1, 2)
+    Bsz, G, N, L = t.shape
+    return make((Bsz, L, G, N), dtype=t.dtype, device=t.device).permute(0, 2, 3, 1)
+
+
+class _on:
+    """The device of a call's tensors, made current where it is not."""
+
+    def __init__(self, device):
+        self.switch = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.switch is not None:
+            self.switch.__enter__()
+
+    def __exit__(self, *exc):
+        if self.switch is not None:
+            self.switch.__exit__(*exc)
+
+
+def _sequences(Bsz, L, device, offsets, lengths, slots, n_slots):
+    """(ssm_sequences, the tensors it points to are the caller's)"""
+    S = Bsz
+    if offsets is not None:
+        if lengths is not None:
+            raise ValueError("offsets and lengths: give one of them")
+        if Bsz != 1:
+            raise ValueError("offsets: need one batch row")
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets: expected torch.int32 [S+1]")
+        S = offsets.shape[0] - 1
+        _check(offsets, "offsets", torch.int32, (S + 1,), device)
+    _check(lengths, "lengths", torch.int32, (S,), device)
+    _check(slots, "slots", torch.int32, (S,), device)
+    ptr = [None if t is None else t.data_ptr() for t in (offsets, lengths, slots)]
+    return Sequences(Bsz, L, S, *ptr, 0 if slots is None else n_slots)
+
+
+def _states(t, name, dtype, S, slots, tail, device):
+    """Rows of a state array: S of them, or any number of them with slots."""
+    if t is None:
+        return 0
+    rows = S if slots is None or not isinstance(t, torch.Tensor) or t.dim() < 1 else t.shape[0]
+    _check(t, name, dtype, (rows, *tail), device)
+    return rows
+
+
+def _pool(a, b, names):
+    if a and b and a != b:
+        raise ValueError(f"{names}: must have the same number of rows")
+    return a or b
+
+
+def selective_bytes(op, Bsz, H, N, G, L, S=None, packed=False):
+    """ssm_selective_bytes"""
+    out = ctypes.c_size_t()
+    rc = lib.ssm_selective_bytes(int(op), int(Bsz), int(H), int(N), int(G), int(L), int(Bsz if S is None else S),
+                                 int(bool(packed)), ctypes.byref(out))
+    if rc != OK:
+        raise SSMError("ssm_selective_bytes", rc)
+    return out.value
+
+
+def causal_conv(u, weight, bias=None, silu=False, state=None, state_out=None, want_state=False, offsets=None,
+                lengths=None, slots=None, y=None):
+    """ssm_causal_conv: y_t = act(bias + sum_k weight[:, k] u_{t-W+1+k}) over u
+    [Bsz,H,L], weight float32 [H,W], bias [H].  state: the W - 1 inputs before
+    the first step, [S,H,W-1] of u's type (with slots, a pool [rows,H,W-1]).
+    The inputs before the next step go to state_out (which may be state), or to
+    a new tensor with want_state.  offsets, lengths, slots as in the header.
+    Returns dict(y, state)."""
+    dev, code = _first(u, 3)
+    Bsz, H, L = u.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight: expected torch.float32 [H, W]")
+    W = weight.shape[1]
+    _check(weight, "weight", torch.float32, (H, W), dev)
+    _check(bias, "bias", torch.float32, (H,), dev)
+    S = Bsz if offsets is None else offsets.shape[0] - 1
+    tail = (H, W - 1)
+    if W == 1 and (state is not None or state_out is not None):
+        raise ValueError("state: a convolution of width 1 has none")
+    rows = _pool(_states(state, "state", u.dtype, S, slots, tail, dev),
+                 _states(state_out, "state_out", u.dtype, S, slots, tail, dev), "state and state_out")
+    with _on(dev):
+        if state_out is None and want_state and W > 1:
+            if slots is not None:
+                raise ValueError("want_state: with slots give state_out")
+            state_out = torch.empty((S, *tail), dtype=u.dtype, device=dev)
+        if slots is not None and not rows:
+            rows = S  # no states: slots only say which sequences to skip
+        seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows)
+        if y is None:
+            y = _like(u)
+        _activation(y, "y", u.dtype, (Bsz, H, L), dev)
+        rc = lib.ssm_causal_conv(code, seq, H, W, int(silu), _view(u), _ptr(weight), _ptr(bias), _ptr(state),
+                                 _ptr(state_out), _view(y), _stream(dev))
+    if rc != OK:
+        raise SSMError("ssm_causal_conv", rc)
+    return dict(y=y, state=state_out)
+
+
+def causal_conv_backward(u, weight, dy, bias=None, silu=False, state=None, dstate=None, want_dstate=False,
+                         offsets=None, lengths=None, workspace=None):
+    """ssm_causal_conv_backward: gradients for dy [Bsz,H,L] of y and dstate
+    (float32 [S,H,W-1], or None) of the final state; the other arguments as in
+    the forward call.  Returns dict(du, dweight, dbias (None without bias),
+    dstate (of the initial state, with want_dstate))."""
+    dev, code = _first(u, 3)
+    Bsz, H, L = u.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight: expected torch.float32 [H, W]")
+    W = weight.shape[1]
+    _check(weight, "weight", torch.float32, (H, W), dev)
+    _check(bias, "bias", torch.float32, (H,), dev)
+    _activation(dy, "dy", u.dtype, (Bsz, H, L), dev)
+    if W == 1 and (state is not None or dstate is not None):
+        raise ValueError("state: a convolution of width 1 has none")
+    with _on(dev):
+        seq = _sequences(Bsz, L, dev, offsets, lengths, None, 0)
+        tail = (seq.S, H, W - 1)
+        _check(state, "state", u.dtype, tail, dev)
+        _check(dstate, "dstate", torch.float32, tail, dev)
+        du = _like(u, offsets is None and lengths is None)
+        f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
+        dweight, dbias = f32(H, W), f32(H) if bias is not None else None
+        dstate_in = f32(*tail) if want_dstate and W > 1 else None
+        nbytes = selective_bytes(OP_CAUSAL_CONV_BACKWARD, Bsz, H, W, 1, L, seq.S, offsets is not None)
+        ws = _workspace(nbytes, dev, workspace)
+        rc = lib.ssm_causal_conv_backward(code, seq, H, W, int(silu), _view(u), _ptr(weight), _ptr(bias),
+                                          _ptr(state), _view(dy), _ptr(dstate), _view(du), _ptr(dweight),
+                                          _ptr(dbias), _ptr(dstate_in), _ptr(ws), nbytes, _stream(dev))
+    if rc != OK:
+        raise SSMError("ssm_causal_conv_backward", rc)
+    return dict(du=du, dweight=dweight, dbias=dbias, dstate=dstate_in)
+
+
+def causal_conv_step(u, weight, state, bias=None, silu=False, slots=None, y=None):
+    """ssm_causal_conv_step: the convolution of one token per sequence, u [Bsz,H]
+    (rows any number of elements apart); state [Bsz,H,W-1] (with slots, a pool
+    [rows,H,W-1]) moves on in place.  Returns dict(y, state)."""
+    dev, code = _first(u, 2)
+    Bsz, H = u.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight: expected torch.float32 [H, W]")
+    W = weight.shape[1]
+    _check(weight, "weight", torch.float32, (H, W), dev)
+    _check(bias, "bias", torch.float32, (H,), dev)
+    _check(slots, "slots", torch.int32, (Bsz,), dev)
+    if (state is None) != (W == 1):
+        raise ValueError("state: needed for every width but 1")
+    rows = _states(state, "state", u.dtype, Bsz, slots, (H, W - 1), dev)
+    with _on(dev):
+        if y is None:
+            y = torch.empty((Bsz, H), dtype=u.dtype, device=dev)
+        _activation(y, "y", u.dtype, (Bsz, H), dev)
+        rc = lib.ssm_causal_conv_step(code, Bsz, H, W, int(silu), _ptr(u), _row_stride(u, "u"), _ptr(weight),
+                                      _ptr(bias), _ptr(state), _ptr(slots), rows or Bsz, _ptr(y),
+                                      _row_stride(y, "y"), _stream(dev))
+    if rc != OK:
+        raise SSMError("ssm_causal_conv_step", rc)
+    return dict(y=y, state=state)
+
+
+def _row_stride(t, name):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _selective(u, delta, A, B, C, D, z, delta_bias, softplus, x0):
+    dev, code = _first(u, 3)
+    Bsz, H, L = u.shape
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A: expected torch.float32 [H, N]")
+    if not isinstance(B, torch.Tensor) or B.dim() != 4:
+        raise ValueError("B: expected [Bsz, G, N, L]")
+    N, G = A.shape[1], B.shape[1]
+    _activation(delta, "delta", u.dtype, (Bsz, H, L), dev)
+    _activation(B, "B", u.dtype, (Bsz, G, N, L), dev)
+    _activation(C, "C", u.dtype, (Bsz, G, N, L), dev)
+    if z is not None:
+        _activation(z, "z", u.dtype, (Bsz, H, L), dev)
+    _check(A, "A", torch.float32, (H, N), dev)
+    _check(D, "D", torch.float32, (H,), dev)
+    _check(delta_bias, "delta_bias", torch.float32, (H,), dev)
+    args = Selective(H, N, G, code, int(softplus), _view(u), _view(delta), _view(z), _group_view(B), _group_view(C),
+                     *(None if t is None else t.data_ptr() for t in (A, D, delta_bias, x0)))
+    return dev, Bsz, H, L, N, G, args
+
+
+def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=False, x0=None, x_out=None,
+                   want_state=False, save=False, offsets=None, lengths=None, slots=None, y=None, workspace=None):
+    """ssm_selective_scan: x_t = exp(dt_t A) x_{t-1} + dt_t u_t B_t,
+    y_t = (C_t . x_t + D u_t) silu(z_t), dt = softplus(delta + delta_bias), over
+    u, delta, z [Bsz,H,L], B, C [Bsz,G,N,L], A float32 [H,N], D, delta_bias
+    float32 [H].  x0: the states before the first step, float32 [S,H,N] (with
+    slots, a pool [rows,H,N]); the states after the last go to x_out (which may
+    be x0), or to a new tensor with want_state.  save keeps what
+    selective_scan_backward needs.  offsets, lengths, slots as in the header.
+    Returns dict(y, x, saved)."""
+    dev, Bsz, H, L, N, G, args = _selective(u, delta, A, B, C, D, z, delta_bias, softplus, x0)
+    S = Bsz if offsets is None else offsets.shape[0] - 1
+    rows = _pool(_states(x0, "x0", torch.float32, S, slots, (H, N), dev),
+                 _states(x_out, "x_out", torch.float32, S, slots, (H, N), dev), "x0 and x_out")
+    if slots is not None and (save or (want_state and x_out is None)):
+        raise ValueError("slots: give x_out, and no save")
+    with _on(dev):
+        if x_out is None and want_state:
+            x_out = torch.empty((S, H, N), dtype=torch.float32, device=dev)
+        seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows or S)
+        if y is None:
+            y = _like(u)
+        _activation(y, "y", u.dtype, (Bsz, H, L), dev)
+        nbytes = selective_bytes(OP_SELECTIVE_SCAN, Bsz, H, N, G, L, S, offsets is not None)
+        ws = _workspace(nbytes, dev, workspace) if nbytes else None
+        saved, sbytes = None, 0
+        if save:
+            sbytes = selective_bytes(OP_SELECTIVE_SAVED, Bsz, H, N, G, L, S, offsets is not None)
+            saved = torch.empty(sbytes, dtype=torch.uint8, device=dev)
+        rc = lib.ssm_selective_scan(seq, args, _view(y), _ptr(x_out), _ptr(saved), sbytes, _ptr(ws), nbytes,
+                                    _stream(dev))
+    if rc != OK:
+        raise SSMError("ssm_selective_scan", rc)
+    return dict(y=y, x=x_out, saved=saved)
+
+
+def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, softplus=False, x0=None,
+                            dx=None, saved=None, offsets=None, lengths=None, workspace=None):
+    """ssm_selective_scan_backward: gradients for dy [Bsz,H,L] of y and dx
+    (float32 [S,H,N], or None) of the final states; the other arguments as in the
+    forward call, saved from it (None: the states are computed again).  Returns
+    dict(du, ddelta, dA, dB, dC, dD, dz, ddelta_bias, dx0), None for the
+    gradient of what was not given."""
+    dev, Bsz, H, L, N, G, args = _selective(u, delta, A, B, C, D, z, delta_bias, softplus, x0)
+    _activation(dy, "dy", u.dtype, (Bsz, H, L), dev)
+    with _on(dev):
+        seq = _sequences(Bsz, L, dev, offsets, lengths, None, 0)
+        S, packed = seq.S, offsets is not None
+        _check(x0, "x0", torch.float32, (S, H, N), dev)
+        _check(dx, "dx", torch.float32, (S, H, N), dev)
+        sbytes = selective_bytes(OP_SELECTIVE_SAVED, Bsz, H, N, G, L, S, packed)
+        if saved is None:
+            saved = torch.empty(sbytes, dtype=torch.uint8, device=dev)
+            nbytes = selective_bytes(OP_SELECTIVE_SCAN, Bsz, H, N, G, L, S, packed)
+            ws = _workspace(nbytes, dev) if nbytes else None
+            rc = lib.ssm_selective_scan(seq, args, None, None, _ptr(saved), sbytes, _ptr(ws), nbytes, _stream(dev))
+            if rc != OK:
+                raise SSMError("ssm_selective_scan", rc)
+        elif not (isinstance(saved, torch.Tensor) and saved.dtype == torch.uint8 and saved.device == dev
+                  and saved.is_contiguous()):
+            raise ValueError(f"saved: expected the uint8 tensor of the forward call on {dev}")
+        whole = offsets is None and lengths is None
+        f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
+        du, ddelta, dz = _like(u, whole), _like(delta, whole), _like(z, whole) if z is not None else None
+        dB, dC, dA = _like(B, whole), _like(C, whole), f32(H, N)
+        dD, dbias = f32(H) if D is not None else None, f32(H) if delta_bias is not None else None
+        dx0 = f32(S, H, N) if x0 is not None else None
+        grads = SelectiveGrads(_view(du), _view(ddelta), _view(dz), _group_view(dB), _group_view(dC),
+                               *(None if t is None else t.data_ptr() for t in (dA, dD, dbias, dx0)))
+        nbytes = selective_bytes(OP_SELECTIVE_SCAN_BACKWARD, Bsz, H, N, G, L, S, packed)
+        ws = _workspace(nbytes, dev, workspace)
+        rc = lib.ssm_selective_scan_backward(seq, args, _ptr(saved), saved.numel(), _view(dy), _ptr(dx), grads,
+                                             _ptr(ws), nbytes, _stream(dev))
+    if rc != OK:
+        raise SSMError("ssm_selective_scan_backward", rc)
+    return dict(du=du, ddelta=ddelta, dA=dA, dB=dB, dC=dC, dD=dD, dz=dz, ddelta_bias=dbias, dx0=dx0)
+
+
+def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softplus=False, slots=None, y=None):
+    """ssm_selective_step: the scan of one token per sequence, u, delta, z
+    [Bsz,H], B, C [Bsz,G,N] (rows any number of elements apart); x float32
+    [Bsz,H,N] (with slots, a pool [rows,H,N]) moves on in place.  Returns
+    dict(y, x)."""
+    dev, code = _first(u, 2)
+    Bsz, H = u.shape
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A: expected torch.float32 [H, N]")
+    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("B: expected [Bsz, G, N]")
+    N, G = A.shape[1], B.shape[1]
+    _activation(delta, "delta", u.dtype, (Bsz, H), dev)
+    _activation(B, "B", u.dtype, (Bsz, G, N), dev)
+    _activation(C, "C", u.dtype, (Bsz, G, N), dev)
+    if z is not None:
+        _activation(z, "z", u.dtype, (Bsz, H), dev)
+    _check(A, "A", torch.float32, (H, N), dev)
+    _check(D, "D", torch.float32, (H,), dev)
+    _check(delta_bias, "delta_bias", torch.float32, (H,), dev)
+    _check(slots, "slots", torch.int32, (Bsz,), dev)
+    if x is None:
+        raise ValueError("x: needed")
+    rows = _states(x, "x", torch.float32, Bsz, slots, (H, N), dev)
+    with _on(dev):
+        if y is None:
+            y = torch.empty((Bsz, H), dtype=u.dtype, device=dev)
+        _activation(y, "y", u.dtype, (Bsz, H), dev)
+        group = lambda t: t.stride(1) if G > 1 else 0  # noqa: E731
+        p = [None if t is None else t.data_ptr() for t in (u, delta, z, B, C, y)]
+        strides = [_row_stride(u, "u"), _row_stride(delta, "delta"), 0 if z is None else _row_stride(z, "z"),
+                   _row_stride(y, "y"), _row_stride(B, "B"), group(B), _row_stride(C, "C"), group(C)]
+        args = SelectiveToken(Bsz, H, N, G, code, int(softplus), None if slots is None else slots.data_ptr(), rows,
+                              *p, *strides, *(None if t is None else t.data_ptr() for t in (A, D, delta_bias, x)))
+        rc = lib.ssm_selective_step(args, _stream(dev))
+    if rc != OK:
+        raise SSMError("ssm_selective_step", rc)
+    return dict(y=y, x=x)
 
 
 def to_device(params, device="cuda:0"):
