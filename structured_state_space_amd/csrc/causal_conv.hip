@@ -33,8 +33,9 @@ struct Geometry {
     int blocks;   // channel blocks
 };
 
+template <bool FINE>
 __device__ __forceinline__ float silu_slope(float v) {
-    const float p = sigmoid_f(v);
+    const float p = sigmoid_f<FINE>(v);
     return p * fmaf(v, 1.0f - p, 1.0f);
 }
 
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(256) void conv_tokens_kernel(ConvArgs a, Geometry g
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], past[k][i], acc);
                 acc = fmaf(w[W - 1][i], v[s][i], acc);
-                o[i] = a.silu ? silu_f(acc) : acc;
+                o[i] = a.silu ? silu_f<kFine<T>>(acc) : acc;
 #pragma unroll
                 for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
                 if (W > 1) past[W > 1 ? W - 2 : 0][i] = v[s][i];
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(256) void conv_rows_kernel(ConvArgs a, Geometry geo
         float acc = b;
 #pragma unroll
         for (int k = 0; k < W; ++k) acc = fmaf(w[k], v[i + 4 - (W - 1) + k], acc);
-        o[i] = a.silu ? silu_f(acc) : acc;
+        o[i] = a.silu ? silu_f<kFine<T>>(acc) : acc;
     }
     put_row<T>(o, y, t, it.end);
 }
@@ -273,7 +274,7 @@ __device__ __forceinline__ void grad_old(const ConvGradArgs& a, const Item& it, 
 #pragma unroll
             for (int k = 0; k < W; ++k) pre = fmaf(a.f.weight[h * W + k], line[t + k], pre);
             const float g = to_f(dy[(it.beg + t) * a.dy.sl]);
-            const float dpre = a.f.silu ? g * silu_slope(pre) : g;
+            const float dpre = a.f.silu ? g * silu_slope<kFine<T>>(pre) : g;
 #pragma unroll
             for (int k = 0; k < W; ++k)
                 if (t + k < W - 1) d[t + k < W - 1 ? t + k : 0] += a.f.weight[h * W + k] * dpre;
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(256) void conv_grad_tokens_kernel(ConvGradArgs g, G
 #pragma unroll
                                 for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][i], past[k][i], pre);
                                 pre = fmaf(w[W - 1][i], x, pre);
-                                dpre *= silu_slope(pre);
+                                dpre *= silu_slope<kFine<T>>(pre);
                             }
                             if (mine) {
                                 db[i] += dpre;
@@ -448,7 +449,7 @@ __global__ __launch_bounds__(256) void conv_grad_rows_kernel(ConvGradArgs g, Geo
                     float pre = b;
 #pragma unroll
                     for (int k = 0; k < W; ++k) pre = fmaf(w[k], v[i + 4 - (W - 1) + k], pre);
-                    d[i] = t + i < it.end ? d[i] * silu_slope(pre) : 0.0f;
+                    d[i] = t + i < it.end ? d[i] * silu_slope<kFine<T>>(pre) : 0.0f;
                 }
                 if (i < 8) {
                     db += d[i];

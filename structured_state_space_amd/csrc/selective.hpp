@@ -145,12 +145,29 @@ inline int64_t item_count(const Seqs& q, int64_t Q) {
     return q.S + q.L / Q;
 }
 
-// ---- quad exchanges (v_*_dpp quad_perm) ----
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+// ---- the eight lanes of a channel ----
+// Lane p = 4 half + q of eight neighbours holds S of its channel's 8 S states,
+// n = p S + j.  Of a tile's 32 steps it loads and prepares four: the steps t
+// with t >> 4 == half, of which register reg(t) is in quad position pos(t).
+// "rows" gives a lane four steps in a row (one vector load), "tokens" every
+// fourth step of its half (a wave then reads four neighbouring steps at once).
+constexpr int kTile = 32;
+constexpr int kOwn = 4;
+template <bool ROWS>
+constexpr int pos(int t) { return ROWS ? (t >> 2) & 3 : t & 3; }
+template <bool ROWS>
+constexpr int reg(int t) { return ROWS ? t & 3 : (t >> 2) & 3; }
+// the step in register i of lane p, and the first of them
+template <bool ROWS>
+__device__ __forceinline__ int step_of(int p, int i) { return ROWS ? p * 4 + i : (p >> 2) * 16 + i * 4 + (p & 3); }
+
+// lane exchanges (v_*_dpp): within a quad, and between the two quads of eight
+template <int CTRL, int BANKS = 0xf>
+__device__ __forceinline__ float dpp(float v, float old = 0.0f) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, 0xf, BANKS, BANKS == 0xf));
 }
-// the value of quad lane K in all four lanes (K a compile-time value once unrolled)
+// the value of quad position K in all four lanes (K a compile-time value once unrolled)
 __device__ __forceinline__ float quad_bcast(float v, int K) {
     switch (K) {
         case 0: return dpp<0x00>(v);
@@ -159,24 +176,175 @@ __device__ __forceinline__ float quad_bcast(float v, int K) {
         default: return dpp<0xFF>(v);
     }
 }
-// lane q of each quad gets the sum over the quad of p_q: 9 instructions for four sums
+// quad position q gets the sum over the quad of p_q: 9 instructions for four sums
 __device__ __forceinline__ float quad_sums(float p0, float p1, float p2, float p3, bool odd, bool high) {
     const float a = (odd ? p1 : p0) + dpp<0xB1>(odd ? p0 : p1);
     const float b = (odd ? p3 : p2) + dpp<0xB1>(odd ? p2 : p3);
     return (high ? b : a) + dpp<0x4E>(high ? a : b);
 }
+// both halves' registers in both quads: lo is the lower quad's v, hi the upper one's
+__device__ __forceinline__ void both_halves(float v, float& lo, float& hi) {
+    lo = dpp<0x114, 0xA>(v, v);  // row_shr:4 into the upper quads
+    hi = dpp<0x104, 0x5>(v, v);  // row_shl:4 into the lower quads
+}
+// sum over the two quads of `lo` (wanted in the lower one) and `hi` (in the upper one)
+__device__ __forceinline__ float half_sums(float lo, float hi, bool upper) {
+    const float mine = upper ? hi : lo, give = upper ? lo : hi;
+    return mine + dpp<0x114, 0xA>(give, dpp<0x104, 0x5>(give, give));
+}
+// sum over a channel's lanes of one value, in all of them
+__device__ __forceinline__ float lane_sum(float v) {
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    return v + dpp<0x141>(v);  // row_half_mirror: the other quad's
+}
+
+// the four steps of a tile that lane p owns.  `base` is the same in the whole
+// wave (the tile's first step, the wave's first channel), `off` the lane's
+// distance from it in bytes (its channel and first step), `step4` that of 4 steps.
+template <class T, bool ROWS>
+__device__ __forceinline__ void load_own(T (&r)[kOwn], const char* base, uint32_t off, uint32_t step4) {
+    if constexpr (ROWS) {
+        const Vec4<T> v = *reinterpret_cast<const Vec4<T>*>(base + off);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) r[i] = v.v[i];
+    } else {
+        asm volatile("" : "+v"(off));  // add the steps' distances here: kept over the tiles they cost registers
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) r[i] = *reinterpret_cast<const T*>(base + (off + i * step4));
+    }
+}
+// the same where only the tile's first nt steps exist
+template <class T, bool ROWS>
+__device__ __forceinline__ void load_part(T (&r)[kOwn], const char* base, uint32_t off, uint32_t step4, int nt, int p) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+        r[i] = step_of<ROWS>(p, i) < nt
+                   ? *reinterpret_cast<const T*>(base + (off + i * (ROWS ? (uint32_t)sizeof(T) : step4)))
+                   : from_f<T>(0.0f);
+}
+template <class T, bool ROWS>
+__device__ __forceinline__ void store_own(const float (&v)[kOwn], char* base, uint32_t off, uint32_t step4, int nt,
+                                          int p) {
+    if (nt == kTile) {
+        if constexpr (ROWS) {
+            Vec4<T> w;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) w.v[i] = from_f<T>(v[i]);
+            *reinterpret_cast<Vec4<T>*>(base + off) = w;
+        } else {
+            asm volatile("" : "+v"(off));
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) *reinterpret_cast<T*>(base + (off + i * step4)) = from_f<T>(v[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            if (step_of<ROWS>(p, i) < nt)
+                *reinterpret_cast<T*>(base + (off + i * (ROWS ? (uint32_t)sizeof(T) : step4))) = from_f<T>(v[i]);
+    }
+}
+// a lane's S states of a row [Np] of a workspace
+template <int S>
+__device__ __forceinline__ void load_states(float (&r)[S], const float* p) {
+#pragma unroll
+    for (int k = 0; k < S; k += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p + k);
+        r[k] = v.x, r[k + 1] = v.y;
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_states(const float (&r)[S], float* p) {
+#pragma unroll
+    for (int k = 0; k < S; k += 2) *reinterpret_cast<float2*>(p + k) = make_float2(r[k], r[k + 1]);
+}
+
+// a workgroup of the scan kernels: 64 channels of one group
+constexpr int kChannels = 64;
+constexpr int kScanThreads = kChannels * 8;
+struct Place {
+    int tid, p, wave, g, blk, h, w0;
+    uint32_t dh;  // the lane's channel, counted from its wave's first
+    bool live;    // it has one
+};
+__device__ __forceinline__ Place place_of(int cb, int per_group, int64_t H, int64_t G) {
+    Place l;
+    l.tid = threadIdx.x;
+    l.p = l.tid & 7;
+    l.wave = __builtin_amdgcn_readfirstlane(l.tid >> 6);
+    l.g = cb / per_group;
+    l.blk = cb % per_group;
+    const int Hg = (int)(H / G), c0 = l.blk * kChannels + l.wave * 8, c = c0 + ((l.tid & 63) >> 3);
+    l.live = c < Hg;
+    l.w0 = l.g * Hg + min(c0, Hg - 1);
+    l.h = l.g * Hg + min(c, Hg - 1);
+    l.dh = (uint32_t)(l.h - l.w0);
+    return l;
+}
+
+// B and C of a tile on their way to LDS in float32: row t holds, per pair k of
+// a lane's states, the eight lanes' {B, B, C, C}; a thread brings K elements of either
+template <class T, int S>
+struct Stage {
+    static constexpr int K = kTile * 8 * S / kScanThreads;  // 1, 2 or 4
+    static constexpr int kRow = 16 * S + 4;                 // floats of a row (padded)
+    uint32_t bo[K], co[K];
+    int at[K], st[K];  // place in LDS; step, or kTile for a padded state
+    T b[K], c[K];
+    __device__ __forceinline__ void init(const View4& B, const View4& C, int N, int tid) {
+        const bool by_time = B.sl == 1;  // consecutive threads along B's contiguous axis
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int e = tid + kScanThreads * k;
+            const int t = by_time ? e % kTile : e / (8 * S), n = by_time ? e / kTile : e % (8 * S);
+            at[k] = t * kRow + ((n % S / 2) * 8 + n / S) * 4 + (n & 1);
+            st[k] = n < N ? t : kTile;
+            const uint32_t m = min(n, N - 1);  // padded states read the last one and are zeroed
+            bo[k] = (m * (uint32_t)B.sn + t * (uint32_t)B.sl) * (uint32_t)sizeof(T);
+            co[k] = (m * (uint32_t)C.sn + t * (uint32_t)C.sl) * (uint32_t)sizeof(T);
+        }
+    }
+    template <bool WB, bool WC>
+    __device__ __forceinline__ void load(const char* Bp, const char* Cp) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (WB) b[k] = *reinterpret_cast<const T*>(Bp + bo[k]);
+            if (WC) c[k] = *reinterpret_cast<const T*>(Cp + co[k]);
+        }
+    }
+    // where only the first nt steps exist
+    template <bool WB, bool WC>
+    __device__ __forceinline__ void load_part(const char* Bp, const char* Cp, int nt) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (WB) b[k] = st[k] < nt ? *reinterpret_cast<const T*>(Bp + bo[k]) : from_f<T>(0.0f);
+            if (WC) c[k] = st[k] < nt ? *reinterpret_cast<const T*>(Cp + co[k]) : from_f<T>(0.0f);
+        }
+    }
+    template <bool WB, bool WC>
+    __device__ __forceinline__ void store(float* to) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (WB) to[at[k]] = st[k] < kTile ? to_f(b[k]) : 0.0f;
+            if (WC) to[at[k] + 2] = st[k] < kTile ? to_f(c[k]) : 0.0f;
+        }
+    }
+};
 
 // ---- scalar functions ----
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLo = 1.925963033500717e-08f;  // log2(e) - kLog2e
 constexpr float kLn2 = 0.6931471805599453f;
 
-// exp(v) to about one unit in the last place: the product v log2(e) is carried
-// in two parts (its rounding alone would cost |v| units)
+// exp(v).  FINE: to about one unit in the last place, the product v log2(e) in
+// two parts; else its rounding costs |v| / 2 units more, six instructions fewer.
+// Kernels take FINE for float32 activations; 16-bit ones are coarser by 2^13.
+template <bool FINE>
 __device__ __forceinline__ float exp_f(float v) {
     const float p = v * kLog2e;
-    const float lo = fmaf(v, kLog2eLo, fmaf(v, kLog2e, -p));
     const float e = __builtin_amdgcn_exp2f(p);
+    if (!FINE) return e;
+    const float lo = fmaf(v, kLog2eLo, fmaf(v, kLog2e, -p));
     // far from 0, where e may be infinite or lo NaN, exp2 alone
     return fabsf(v) < 80.0f ? fmaf(e, lo * kLn2, e) : e;
 }
@@ -184,17 +352,27 @@ __device__ __forceinline__ float exp_f(float v) {
 // log(1 + exp(v)); above 20 it is v to float32.  log1p(e) = log(w) + (e - (w - 1))/w
 // with w = fl(1 + e); where e >= 1 the second term is below half a unit of the
 // first and is left out, elsewhere w stands for 1 in it (an error below a
-// quarter unit).
-__device__ __forceinline__ float softplus_f(float v) {
-    const float e = exp_f(fminf(v, 20.0f));
+// quarter unit).  `slope` is e / (1 + e).
+template <bool FINE, bool SLOPE = false>
+__device__ __forceinline__ float softplus_f(float v, float* slope = nullptr) {
+    const float e = exp_f<FINE>(v);
     const float w = 1.0f + e;
     const float c = e < 1.0f ? e - (w - 1.0f) : 0.0f;
     const float r = fmaf(__builtin_amdgcn_logf(w), kLn2, c);
-    return v > 20.0f ? v : (v == v ? r : v);
+    if (SLOPE) *slope = v > 20.0f ? 1.0f : e * __builtin_amdgcn_rcpf(w);
+    return v > 20.0f ? v : r;
 }
 
-__device__ __forceinline__ float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.0f + exp_f(-v)); }
-__device__ __forceinline__ float silu_f(float v) { return v * sigmoid_f(v); }
+template <bool FINE>
+__device__ __forceinline__ float sigmoid_f(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + exp_f<FINE>(-v));
+}
+template <bool FINE>
+__device__ __forceinline__ float silu_f(float v) {
+    return v * sigmoid_f<FINE>(v);
+}
+template <class T>
+constexpr bool kFine = sizeof(T) == 4;
 
 // ---- argument blocks ----
 struct ScanArgs {
@@ -265,12 +443,12 @@ struct ConvStepArgs {
     void* state;  // [states, H, width - 1], updated
 };
 
-// states per channel as the kernels hold them, in blocks of 16 (1, 2 or 4)
+// states per channel as the kernels hold them: 2, 4 or 8 on each of its lanes
 __host__ __device__ inline int64_t padded_states(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 
 // steps between two saved states, and where they lie: sequence s keeps its
 // k-th at row saved_row + k of [rows, H, padded_states(N)]
-constexpr int kSaveSteps = 16;
+constexpr int kSaveSteps = kTile;
 __host__ __device__ inline int64_t saved_rows(int64_t S, int64_t L, bool packed) {
     return packed ? L / kSaveSteps + S : S * ((L + kSaveSteps - 1) / kSaveSteps);
 }

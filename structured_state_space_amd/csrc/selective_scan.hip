@@ -4,12 +4,11 @@
 //   y_t = (sum_n C_t[n] x_t[n] + D u_t) silu(z_t)
 // per (sequence, channel), B and C shared by the channels of a group.
 //
-// Work split.  A quad of lanes holds one channel's states (lane q the states
-// 16 nb + 4 q + j), a wave 16 channels, a workgroup 64 channels of one group.
-// The steps run in order, 32 to a tile: lane q loads and prepares (softplus,
-// gate) 8 of the tile's steps and the quad passes dt and dt u around with
-// quad_perm; B and C of a tile go through LDS in float32, double-buffered, the
-// next tile's loads in flight while this one is computed.
+// Work split.  Eight lanes share a channel, a wave has 8 channels, a workgroup 64
+// of one group.  The steps run in order, 32 to a tile: each lane loads and
+// prepares (softplus, gate) four of a tile's steps, and the channel's lanes pass
+// dt and dt u around by DPP; B and C of a tile go through LDS in float32,
+// double-buffered, the next tile's loads in flight while this one is computed.
 //
 // Where channels and sequences alone leave the GPU idle, the steps are split
 // into chunks of Q as well: a first launch computes every chunk's state from a
@@ -22,57 +21,6 @@ namespace ssm {
 
 namespace {
 
-constexpr int kTile = 32;
-constexpr int kChannels = 64;  // per workgroup
-
-// step t of a tile is owned by quad lane owner(t), in its register reg(t)
-template <bool ROWS>
-constexpr int owner(int t) { return ROWS ? t >> 3 : t & 3; }
-template <bool ROWS>
-constexpr int reg(int t) { return ROWS ? t & 7 : t >> 2; }
-template <bool ROWS>
-__device__ __forceinline__ int step_of(int q, int r) { return ROWS ? q * 8 + r : r * 4 + q; }
-
-// the 8 steps of a tile that lane q owns; `base` is the same in the whole wave
-// (the tile's first step, the wave's first channel), `off` is the lane's
-// offset from it: its channel and its first step
-template <class T, bool ROWS>
-__device__ __forceinline__ void load8(T (&r)[8], const T* base, uint32_t off, int64_t sl, int nt, int q) {
-    if (nt == kTile) {
-        if constexpr (ROWS) {
-            const Vec8<T> v = *reinterpret_cast<const Vec8<T>*>(base + off);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = v.v[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i, base += 4 * sl) r[i] = base[off];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i, base += ROWS ? 1 : 4 * sl)
-            r[i] = step_of<ROWS>(q, i) < nt ? base[off] : from_f<T>(0.0f);
-    }
-}
-
-template <class T, bool ROWS>
-__device__ __forceinline__ void store8(const float (&v)[8], T* base, uint32_t off, int64_t sl, int nt, int q) {
-    if (nt == kTile) {
-        if constexpr (ROWS) {
-            Vec8<T> w;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w.v[i] = from_f<T>(v[i]);
-            *reinterpret_cast<Vec8<T>*>(base + off) = w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i, base += 4 * sl) base[off] = from_f<T>(v[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i, base += ROWS ? 1 : 4 * sl)
-            if (step_of<ROWS>(q, i) < nt) base[off] = from_f<T>(v[i]);
-    }
-}
-
 // what a launch of scan_kernel is for
 enum Mode {
     kEnds,    // every chunk's end state from a zero start, and its sum of dt
@@ -80,42 +28,62 @@ enum Mode {
     kStates,  // the saved states alone
 };
 
-// one tile's recurrence; GUARD: only the first nt steps exist (a branch per step)
-template <int NB, bool ROWS, Mode MODE, bool GUARD>
-__device__ __forceinline__ void run_tile(float (&h)[NB][4], const float (&A2)[NB][4], const float (&dt)[8],
-                                         const float (&dx)[8], const float* lds, int pad, int q, int nt,
-                                         float (&p)[kTile], float* saved, int64_t saved_step) {
+// one tile's recurrence; GUARD: only the first nt steps exist (a branch per step).
+// B and C come from LDS a pair of steps ahead of their use.
+template <int S, bool ROWS, Mode MODE, bool GUARD>
+__device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], const float (&dt)[2][kOwn],
+                                         const float (&dx)[2][kOwn], const float* lds, int nt, bool odd, bool high,
+                                         float (&sums)[2][kOwn]) {
+    constexpr int kRow = Stage<float, S>::kRow, kGroup = S == 2 ? 4 : S == 4 ? 2 : 1;
+    float4 bc[2][kGroup][S / 2];
+    float p[ROWS ? 16 : 4];  // the lanes' shares of y, until a quad's four owners have one each
+    auto fetch = [&](int g) {
 #pragma unroll
-    for (int t = 0; t < kTile; ++t) {
-        if (GUARD && t >= nt) continue;
-        if (MODE != kEnds && t % kSaveSteps == 0 && saved) {
+        for (int i = 0; i < kGroup; ++i)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-                *reinterpret_cast<float4*>(saved + (t / kSaveSteps) * saved_step + nb * 16) =
-                    make_float4(h[nb][0], h[nb][1], h[nb][2], h[nb][3]);
+            for (int k = 0; k < S / 2; ++k)
+                bc[g & 1][i][k] = *reinterpret_cast<const float4*>(lds + (g * kGroup + i) * kRow + k * 32);
+    };
+    auto collect = [&](int t) {  // after step t
+        if (MODE != kFull) return;
+        if (!ROWS && (t & 3) == 3) sums[t >> 4][(t >> 2) & 3] = quad_sums(p[0], p[1], p[2], p[3], odd, high);
+        if (ROWS && (t & 15) == 15) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)
+                sums[t >> 4][i] = quad_sums(p[i], p[(4 + i) & 15], p[(8 + i) & 15], p[(12 + i) & 15], odd, high);
         }
-        const float dtv = quad_bcast(dt[reg<ROWS>(t)], owner<ROWS>(t));
-        const float dxv = quad_bcast(dx[reg<ROWS>(t)], owner<ROWS>(t));
-        float acc = 0.0f;
+    };
+    fetch(0);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const float4 b = *reinterpret_cast<const float4*>(lds + t * pad + (nb * 4 + q) * 8);
-            const float bv[4] = {b.x, b.y, b.z, b.w};
+    for (int g = 0; g < kTile / kGroup; ++g) {
+        if (g + 1 < kTile / kGroup) fetch(g + 1);
+        if (!GUARD) __builtin_amdgcn_sched_barrier(0);  // issue these reads before the steps below
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                h[nb][j] = fmaf(__builtin_amdgcn_exp2f(dtv * A2[nb][j]), h[nb][j], dxv * bv[j]);
-            if (MODE == kFull) {
-                const float4 c = *reinterpret_cast<const float4*>(lds + t * pad + (nb * 4 + q) * 8 + 4);
-                const float cv[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc = fmaf(cv[j], h[nb][j], acc);
+        for (int i = 0; i < kGroup; ++i) {
+            const int t = g * kGroup + i;
+            float& share = p[ROWS ? t & 15 : t & 3];
+            if (GUARD && t >= nt) {
+                share = 0.0f;
+                collect(t);
+                continue;
             }
+            const float dtv = quad_bcast(dt[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
+            const float dxv = quad_bcast(dx[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
+            float acc = 0.0f;
+#pragma unroll
+            for (int k = 0; k < S / 2; ++k) {
+                const float4 v = bc[g & 1][i][k];
+                h[2 * k] = fmaf(__builtin_amdgcn_exp2f(dtv * A2[2 * k]), h[2 * k], dxv * v.x);
+                h[2 * k + 1] = fmaf(__builtin_amdgcn_exp2f(dtv * A2[2 * k + 1]), h[2 * k + 1], dxv * v.y);
+                if (MODE == kFull) acc = fmaf(v.w, h[2 * k + 1], fmaf(v.z, h[2 * k], acc));
+            }
+            // the sum is done here: left alone, the compiler moves the sums of the two
+            // forms of this loop behind both of them and holds every step's states
+            // (hundreds of registers)
+            if (MODE == kFull) asm volatile("" : "+v"(acc));
+            share = acc;
+            collect(t);
         }
-        // the sum is done here: left alone, the compiler moves the sums of the two
-        // forms of this loop behind both of them and holds every step's states
-        // (hundreds of registers)
-        if (MODE == kFull) asm volatile("" : "+v"(acc));
-        p[t] = acc;
     }
 }
 
@@ -128,12 +96,11 @@ struct Split {
     float* starts;    // [S, H, Np]: copy of the initial states (x_out may be x_in)
 };
 
-template <class T, int NB, bool ROWS, Mode MODE>
-__global__ __launch_bounds__(256, NB == 1 ? 3 : 2) void scan_kernel(ScanArgs a, Split sp) {
+template <class T, int S, bool ROWS, Mode MODE>
+__global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, Split sp) {
     constexpr bool ENDS = MODE == kEnds, FULL = MODE == kFull;
-    constexpr int kPad = NB * 32 + 4;
-    constexpr int kStage = NB * 2;  // elements of B (and of C) that a thread stages per tile
-    __shared__ __attribute__((aligned(16))) float lds[2][kTile * kPad];
+    using St = Stage<T, S>;
+    __shared__ __attribute__((aligned(16))) float lds[2][kTile * St::kRow];
 
     const int cb = blockIdx.x % sp.blocks;
     const int64_t item = blockIdx.x / sp.blocks;
@@ -144,196 +111,160 @@ __global__ __launch_bounds__(256, NB == 1 ? 3 : 2) void scan_kernel(ScanArgs a, 
     const int chunks = chunks_of(it.end - it.beg, sp.Q);
     if (it.c >= chunks || (ENDS && it.c + 1 == chunks)) return;
 
-    const int tid = threadIdx.x, lane = tid & 63, q = lane & 3;
-    const bool odd = q & 1, high = q & 2;
-    const int Hg = (int)(a.H / a.G), N = (int)a.N, Np = NB * 16;
-    const int g = cb / sp.per_group;
-    const int c0 = (cb % sp.per_group) * kChannels + __builtin_amdgcn_readfirstlane(tid >> 6) * 16;  // wave's first channel in the group
-    const int lc = lane >> 2;
-    const bool live = c0 + lc < Hg;
-    const int w0 = g * Hg + min(c0, Hg - 1);             // wave's first channel, clamped
-    const int h0 = g * Hg + min(c0 + lc, Hg - 1);        // the lane's
-    const uint32_t dh = (uint32_t)(h0 - w0);
-
-    float A2[NB][4], h[NB][4];
+    const Place l = place_of(cb, sp.per_group, a.H, a.G);
+    const int p = l.p, N = (int)a.N;
+    const bool odd = p & 1, high = p & 2, upper = p & 4;
+    float A2[S], h[S];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = nb * 16 + q * 4 + j;
-            A2[nb][j] = n < N ? a.A[(int64_t)h0 * N + n] * kLog2e : 0.0f;
-            h[nb][j] = 0.0f;
-        }
-    const float bias = a.delta_bias ? a.delta_bias[h0] : 0.0f;
-    const float Dv = a.D ? a.D[h0] : 0.0f;
-    const int64_t wrow = ((int64_t)h0) * Np + q * 4;      // in a workspace row [H, Np]
-    const int64_t wstep = a.H * Np;
+    for (int j = 0; j < S; ++j) {
+        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : 0.0f;
+        h[j] = 0.0f;
+    }
+    const float bias = a.delta_bias ? a.delta_bias[l.h] : 0.0f;
+    const float Dv = a.D ? a.D[l.h] : 0.0f;
+    const int64_t wrow = (int64_t)l.h * (8 * S) + p * S;  // in a workspace row [H, Np]
+    const int64_t wstep = a.H * (8 * S);
 
     // start state
     if (it.c == 0) {
-        if (!ENDS && sp.starts) {
+        if (!ENDS && sp.starts && chunks > 1) {
+            load_states<S>(h, sp.starts + it.s * wstep + wrow);
+        } else if (a.x_in) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const float4 v = *reinterpret_cast<const float4*>(sp.starts + it.s * wstep + wrow + nb * 16);
-                h[nb][0] = v.x, h[nb][1] = v.y, h[nb][2] = v.z, h[nb][3] = v.w;
-            }
+            for (int j = 0; j < S; ++j)
+                if (p * S + j < N) h[j] = a.x_in[(it.state * a.H + l.h) * N + p * S + j];
         }
-        if (ENDS || !sp.starts || chunks == 1) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = nb * 16 + q * 4 + j;
-                    h[nb][j] = a.x_in && n < N ? a.x_in[(it.state * a.H + h0) * N + n] : 0.0f;
-                }
-        }
-        if (ENDS && live) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-                *reinterpret_cast<float4*>(sp.starts + it.s * wstep + wrow + nb * 16) =
-                    make_float4(h[nb][0], h[nb][1], h[nb][2], h[nb][3]);
-        }
+        if (ENDS && l.live) store_states<S>(h, sp.starts + it.s * wstep + wrow);
     } else if (!ENDS) {
         const int64_t first = item - it.c;
-        for (int64_t i = first; i < item; ++i) {
-            const float s = i == first ? 0.0f : sp.sums[i * a.H + h0];
+        load_states<S>(h, sp.ends + first * wstep + wrow);
+        for (int64_t i = first + 1; i < item; ++i) {
+            const float s = sp.sums[i * a.H + l.h];
+            float e[S];
+            load_states<S>(e, sp.ends + i * wstep + wrow);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const float4 v = *reinterpret_cast<const float4*>(sp.ends + i * wstep + wrow + nb * 16);
-                const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    h[nb][j] = i == first ? e[j] : fmaf(__builtin_amdgcn_exp2f(s * A2[nb][j]), h[nb][j], e[j]);
-            }
+            for (int j = 0; j < S; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(s * A2[j]), h[j], e[j]);
         }
     }
 
-    // wave-uniform bases at the tile's first step; lane offsets
-    const T* up = (const T*)a.u.data + it.row * a.u.sb + w0 * a.u.sh + beg * a.u.sl;
-    const T* dp = (const T*)a.delta.data + it.row * a.delta.sb + w0 * a.delta.sh + beg * a.delta.sl;
-    const T* zp = (const T*)a.z.data + it.row * a.z.sb + w0 * a.z.sh + beg * a.z.sl;
-    T* yp = (T*)a.y.data + it.row * a.y.sb + w0 * a.y.sh + beg * a.y.sl;
-    const uint32_t q0 = ROWS ? q * 8 : q;  // the lane's first step
-    const uint32_t uo = dh * (uint32_t)a.u.sh + q0 * (uint32_t)a.u.sl;
-    const uint32_t dof = dh * (uint32_t)a.delta.sh + q0 * (uint32_t)a.delta.sl;
-    const uint32_t zo = dh * (uint32_t)a.z.sh + q0 * (uint32_t)a.z.sl;
-    const uint32_t yo = dh * (uint32_t)a.y.sh + q0 * (uint32_t)a.y.sl;
+    // bases at the tile's first step, the same in the whole wave, and the lanes'
+    // distances from them in bytes (the strides' limits keep these below 2^32)
+    constexpr uint32_t kE = sizeof(T);
+    const uint32_t q0 = step_of<ROWS>(p, 0);
+    auto base = [&](const View3& v) {
+        return (char*)v.data + (it.row * v.sb + l.w0 * v.sh + beg * v.sl) * (int64_t)kE;
+    };
+    auto offset = [&](const View3& v) { return (l.dh * (uint32_t)v.sh + q0 * (uint32_t)v.sl) * kE; };
     const bool gate = FULL && a.z.data;
+    const View3& gv = gate ? a.z : a.u;  // without a gate u once more, unused: the loads need no branch
+    const char *up = base(a.u), *dp = base(a.delta), *zp = base(gv);
+    char* yp = base(a.y);
+    const uint32_t uo = offset(a.u), dof = offset(a.delta), zo = offset(gv), yo = offset(a.y);
+    const uint32_t us = (uint32_t)a.u.sl * 4 * kE, ds = (uint32_t)a.delta.sl * 4 * kE,
+                   zs = (uint32_t)gv.sl * 4 * kE, ys = (uint32_t)a.y.sl * 4 * kE;
+    const char* Bp = (const char*)a.B.data + (it.row * a.B.sb + l.g * a.B.sg + beg * a.B.sl) * (int64_t)kE;
+    const char* Cp = (const char*)a.C.data + (it.row * a.C.sb + l.g * a.C.sg + beg * a.C.sl) * (int64_t)kE;
+    const uint32_t bs = (uint32_t)a.B.sl * 4 * kE, cs = (uint32_t)a.C.sl * 4 * kE;
+    St stage;
+    stage.init(a.B, a.C, N, l.tid);
 
-    const T* Bp = (const T*)a.B.data + it.row * a.B.sb + g * a.B.sg + beg * a.B.sl;
-    const T* Cp = (const T*)a.C.data + it.row * a.C.sb + g * a.C.sg + beg * a.C.sl;
-    const bool by_time = a.B.sl == 1;  // staging order: consecutive threads along B's contiguous axis
-    T sb[kStage], sc[kStage];
-    auto stage_pos = [&](int k, int& t, int& n) {
-        const int e = tid + 256 * k;
-        t = by_time ? e % kTile : e / (NB * 16);
-        n = by_time ? e / kTile : e % (NB * 16);
+    T ur[kOwn], dr[kOwn], zr[kOwn];
+    auto load_tile = [&]() {
+        load_own<T, ROWS>(ur, up, uo, us);
+        load_own<T, ROWS>(dr, dp, dof, ds);
+        if (FULL) load_own<T, ROWS>(zr, zp, zo, zs);
+        stage.template load<true, FULL>(Bp, Cp);
     };
-    auto stage_load = [&](int nt) {
+    auto advance = [&](uint32_t go) {  // by 4 go steps
+        up += (uint64_t)us * go, dp += (uint64_t)ds * go, zp += (uint64_t)zs * go;
+        Bp += (uint64_t)bs * go, Cp += (uint64_t)cs * go;
+    };
+    float dt[2][kOwn], dx[2][kOwn], uf[kOwn], zf[kOwn], sum = 0.0f;
+    auto prepare = [&](int nt) {  // the lane's own steps, then all of the channel's
+        float d[kOwn];
 #pragma unroll
-        for (int k = 0; k < kStage; ++k) {
-            int t, n;
-            stage_pos(k, t, n);
-            const bool in = t < nt && n < N;
-            sb[k] = in ? Bp[(uint32_t)n * (uint32_t)a.B.sn + (uint32_t)t * (uint32_t)a.B.sl] : from_f<T>(0.0f);
-            if (FULL)
-                sc[k] = in ? Cp[(uint32_t)n * (uint32_t)a.C.sn + (uint32_t)t * (uint32_t)a.C.sl] : from_f<T>(0.0f);
+        for (int i = 0; i < kOwn; ++i) {
+            uf[i] = to_f(ur[i]);
+            if (FULL) zf[i] = to_f(zr[i]);
+            d[i] = to_f(dr[i]) + bias;
+        }
+        if (a.softplus) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) d[i] = softplus_f<kFine<T>>(d[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            if (ENDS) sum += step_of<ROWS>(p, i) < nt ? d[i] : 0.0f;
+            both_halves(d[i], dt[0][i], dt[1][i]);
+            both_halves(d[i] * uf[i], dx[0][i], dx[1][i]);
         }
     };
-    auto stage_store = [&](float* to) {
+    auto finish = [&](const float (&s)[2][kOwn], int nt) {  // y of the lane's own steps
+        float yv[kOwn];
 #pragma unroll
-        for (int k = 0; k < kStage; ++k) {
-            int t, n;
-            stage_pos(k, t, n);
-            float* at = to + t * kPad + (n >> 2) * 8 + (n & 3);
-            at[0] = to_f(sb[k]);
-            if (FULL) at[4] = to_f(sc[k]);
+        for (int i = 0; i < kOwn; ++i) yv[i] = fmaf(Dv, uf[i], half_sums(s[0][i], s[1][i], upper));
+        if (gate) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) yv[i] *= silu_f<kFine<T>>(zf[i]);
         }
+        if (l.live) store_own<T, ROWS>(yv, yp, yo, ys, nt, p);
     };
 
-    T ur[8], dr[8], zr[8];
-    int nt = min(kTile, end - beg);
-    if (nt > 0) {
-        load8<T, ROWS>(ur, up, uo, a.u.sl, nt, q);
-        load8<T, ROWS>(dr, dp, dof, a.delta.sl, nt, q);
-        if (gate) load8<T, ROWS>(zr, zp, zo, a.z.sl, nt, q);
-        stage_load(nt);
-        stage_store(lds[0]);
+    float* saved = !ENDS && a.saved && l.live
+                       ? a.saved + (saved_row(a.q, it) + (beg - it.beg) / kTile) * wstep + wrow
+                       : nullptr;
+    const int whole = max(0, end - beg) / kTile, rest = max(0, end - beg) % kTile;
+    int buf = 0;
+    if (whole > 0) {
+        load_tile();
+        stage.template store<true, FULL>(lds[0]);
         __syncthreads();
     }
-    float sum = 0.0f;
-    float* saved = !ENDS && a.saved && live
-                       ? a.saved + (saved_row(a.q, it) + (beg - it.beg) / kSaveSteps) * wstep + wrow
-                       : nullptr;
-    const bool saving = !ENDS && a.saved;
-    int buf = 0;
-    for (int t0 = beg; t0 < end; t0 += kTile) {
-        float dt[8], dx[8], uf[8], zf[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uf[i] = to_f(ur[i]);
-            if (gate) zf[i] = to_f(zr[i]);
-            const float v = to_f(dr[i]) + bias;
-            dt[i] = a.softplus ? softplus_f(v) : v;
-            dx[i] = dt[i] * uf[i];
-            if (ENDS) sum += step_of<ROWS>(q, i) < nt ? dt[i] : 0.0f;
+    for (int k = 0; k < whole; ++k) {
+        prepare(kTile);
+        // the next whole tile's loads fly while this one is computed (the last one
+        // loads itself again: a branch here would make them wait)
+        advance(k + 1 < whole ? kTile / 4 : 0);
+        load_tile();
+        __builtin_amdgcn_sched_barrier(0);  // left alone, the compiler moves the loads behind the tile
+        if (saved) {
+            store_states<S>(h, saved);
+            saved += wstep;
         }
-        const int now = nt, next = min(kTile, end - t0 - kTile);
-        T* yt = yp;
-        if (next > 0) {
-            up += kTile * a.u.sl, dp += kTile * a.delta.sl, zp += kTile * a.z.sl, yp += kTile * a.y.sl;
-            Bp += kTile * a.B.sl, Cp += kTile * a.C.sl;
-            load8<T, ROWS>(ur, up, uo, a.u.sl, next, q);
-            load8<T, ROWS>(dr, dp, dof, a.delta.sl, next, q);
-            if (gate) load8<T, ROWS>(zr, zp, zo, a.z.sl, next, q);
-            stage_load(next);
-        }
-        float p[kTile];
-        if (now == kTile) {
-            run_tile<NB, ROWS, MODE, false>(h, A2, dt, dx, lds[buf], kPad, q, now, p, saved, wstep);
-        } else {
-#pragma unroll
-            for (int t = 0; t < kTile; ++t) p[t] = 0.0f;
-            run_tile<NB, ROWS, MODE, true>(h, A2, dt, dx, lds[buf], kPad, q, now, p, saved, wstep);
-        }
-        if (saving && live) saved += (kTile / kSaveSteps) * wstep;
-        if (FULL) {
-            float yv[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = ROWS ? quad_sums(p[i], p[8 + i], p[16 + i], p[24 + i], odd, high)
-                                     : quad_sums(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3], odd, high);
-                yv[i] = fmaf(Dv, uf[i], s);
-                if (gate) yv[i] *= silu_f(zf[i]);
-            }
-            if (live) store8<T, ROWS>(yv, yt, yo, a.y.sl, now, q);
-        }
-        if (next > 0) {
-            buf ^= 1;
-            stage_store(lds[buf]);
-            __syncthreads();
-            nt = next;
-        }
+        float s[2][kOwn];
+        run_tile<S, ROWS, MODE, false>(h, A2, dt, dx, lds[buf] + p * 4, kTile, odd, high, s);
+        if (FULL) finish(s, kTile);
+        yp += (uint64_t)ys * (kTile / 4);
+        buf ^= 1;
+        stage.template store<true, FULL>(lds[buf]);
+        __syncthreads();
+    }
+    if (rest > 0) {
+        if (whole > 0) advance(kTile / 4);
+        load_part<T, ROWS>(ur, up, uo, us, rest, p);
+        load_part<T, ROWS>(dr, dp, dof, ds, rest, p);
+        if (FULL) load_part<T, ROWS>(zr, zp, zo, zs, rest, p);
+        stage.template load_part<true, FULL>(Bp, Cp, rest);
+        buf ^= 1;
+        stage.template store<true, FULL>(lds[buf]);
+        __syncthreads();
+        prepare(rest);
+        if (saved) store_states<S>(h, saved);
+        float s[2][kOwn];
+        run_tile<S, ROWS, MODE, true>(h, A2, dt, dx, lds[buf] + p * 4, rest, odd, high, s);
+        if (FULL) finish(s, rest);
     }
 
     if (ENDS) {
-        sum += dpp<0xB1>(sum);
-        sum += dpp<0x4E>(sum);
-        if (live) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-                *reinterpret_cast<float4*>(sp.ends + item * wstep + wrow + nb * 16) =
-                    make_float4(h[nb][0], h[nb][1], h[nb][2], h[nb][3]);
-            if (q == 0) sp.sums[item * a.H + h0] = sum;
+        sum = lane_sum(sum);
+        if (l.live) {
+            store_states<S>(h, sp.ends + item * wstep + wrow);
+            if (p == 0) sp.sums[item * a.H + l.h] = sum;
         }
-    } else if (live && a.x_out && it.c + 1 == chunks) {
+    } else if (l.live && a.x_out && it.c + 1 == chunks) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = nb * 16 + q * 4 + j;
-                if (n < N) a.x_out[(it.state * a.H + h0) * N + n] = h[nb][j];
-            }
+        for (int j = 0; j < S; ++j)
+            if (p * S + j < N) a.x_out[(it.state * a.H + l.h) * N + p * S + j] = h[j];
     }
 }
 
@@ -374,23 +305,23 @@ Plan plan(const Seqs& q, int64_t H, int64_t N, int64_t G) {
     return p;
 }
 
-template <class T, int NB, bool ROWS>
+template <class T, int S, bool ROWS>
 hipError_t launch_as(const ScanArgs& a, const Plan& p, hipStream_t s) {
     const int64_t wgs = p.items * p.sp.blocks;
     if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    if (p.split) scan_kernel<T, NB, ROWS, kEnds><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, p.sp);
+    if (p.split) scan_kernel<T, S, ROWS, kEnds><<<dim3((unsigned)wgs), dim3(kScanThreads), 0, s>>>(a, p.sp);
     if (a.y.data)
-        scan_kernel<T, NB, ROWS, kFull><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, p.sp);
+        scan_kernel<T, S, ROWS, kFull><<<dim3((unsigned)wgs), dim3(kScanThreads), 0, s>>>(a, p.sp);
     else
-        scan_kernel<T, NB, ROWS, kStates><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, p.sp);
+        scan_kernel<T, S, ROWS, kStates><<<dim3((unsigned)wgs), dim3(kScanThreads), 0, s>>>(a, p.sp);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_of(const ScanArgs& a, const Plan& p, bool rows, hipStream_t s) {
-    if (a.N <= 16) return rows ? launch_as<T, 1, true>(a, p, s) : launch_as<T, 1, false>(a, p, s);
-    if (a.N <= 32) return rows ? launch_as<T, 2, true>(a, p, s) : launch_as<T, 2, false>(a, p, s);
-    return rows ? launch_as<T, 4, true>(a, p, s) : launch_as<T, 4, false>(a, p, s);
+    if (a.N <= 16) return rows ? launch_as<T, 2, true>(a, p, s) : launch_as<T, 2, false>(a, p, s);
+    if (a.N <= 32) return rows ? launch_as<T, 4, true>(a, p, s) : launch_as<T, 4, false>(a, p, s);
+    return rows ? launch_as<T, 8, true>(a, p, s) : launch_as<T, 8, false>(a, p, s);
 }
 
 }  // namespace

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int blocks) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (at[r] < 0) continue;
-        const float v = dt[r] + bias, s = a.softplus ? softplus_f(v) : v, dx = s * u[r];
+        const float v = dt[r] + bias, s = a.softplus ? softplus_f<kFine<T>>(v) : v, dx = s * u[r];
         float y = 0.0f;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int blocks) {
         y += dpp<0x4E>(y);
         if (q == 0) {
             y = fmaf(D, u[r], y);
-            if (a.z) y *= silu_f(z[r]);
+            if (a.z) y *= silu_f<kFine<T>>(z[r]);
             ((T*)a.y)[(b0 + r) * a.y_row + h] = from_f<T>(y);
         }
     }
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a, int64_t 
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) acc = fmaf(w.v[c * W + k], to_f(line.v[c * (W - 1) + k]), acc);
             acc = fmaf(w.v[c * W + W - 1], to_f(in.v[c]), acc);
-            out.v[c] = from_f<T>(a.silu ? silu_f(acc) : acc);
+            out.v[c] = from_f<T>(a.silu ? silu_f<kFine<T>>(acc) : acc);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
                 next.v[c * (W - 1) + k] = k + 1 < W - 1 ? line.v[c * (W - 1) + (k + 1 < W - 1 ? k + 1 : 0)] : in.v[c];
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a, int64_t 
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) acc = fmaf(a.weight[(h + c) * W + k], to_f(s[k]), acc);
             acc = fmaf(a.weight[(h + c) * W + W - 1], to_f(u[c]), acc);
-            y[c] = from_f<T>(a.silu ? silu_f(acc) : acc);
+            y[c] = from_f<T>(a.silu ? silu_f<kFine<T>>(acc) : acc);
 #pragma unroll
             for (int k = 0; k + 1 < W - 1; ++k) s[k] = s[k + 1];
             if (W > 1) s[W > 1 ? W - 2 : 0] = u[c];
