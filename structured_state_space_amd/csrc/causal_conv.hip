@@ -519,17 +519,6 @@ int pow2_at_least(int64_t v, int most) {
     return p;
 }
 
-enum Order { kRows, kTokens, kAny };
-
-Order order_of(const View3* const* v, int n) {
-    bool rows = true, tokens = true;
-    for (int i = 0; i < n; ++i) {
-        rows = rows && v[i]->sl == 1;
-        tokens = tokens && v[i]->sh == 1;
-    }
-    return rows ? kRows : tokens ? kTokens : kAny;
-}
-
 template <class T>
 constexpr int vec() { return 16 / (int)sizeof(T); }
 
@@ -554,7 +543,7 @@ constexpr int kGradIters = 4;
 template <class T, int W>
 hipError_t forward_as(const ConvArgs& a, hipStream_t s) {
     const View3* views[] = {&a.u, &a.y};
-    const Order o = order_of(views, 2);
+    const Order o = order_of(views, 2, 4);
     const int V = o == kTokens ? vec<T>() : 1;
     const Geometry geo = geometry(o, V, a.H, a.q.L, 1);
     const int64_t wgs = item_count(a.q, geo.Q) * geo.blocks;
@@ -573,7 +562,7 @@ template <class T, int W>
 hipError_t backward_as(const ConvGradArgs& g, float* partial, hipStream_t s) {
     const ConvArgs& a = g.f;
     const View3* views[] = {&a.u, &g.dy, &g.du};
-    const Order o = order_of(views, 3);
+    const Order o = order_of(views, 3, 4);
     const int V = o == kTokens ? vec<T>() : 1;
     const Geometry geo = geometry(o, V, a.H, a.q.L, kGradIters);
     const int64_t items = item_count(a.q, geo.Q), wgs = items * geo.blocks;

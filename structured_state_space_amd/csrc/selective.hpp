@@ -145,103 +145,172 @@ inline int64_t item_count(const Seqs& q, int64_t Q) {
     return q.S + q.L / Q;
 }
 
-// ---- the eight lanes of a channel ----
-// Lane p = 4 half + q of eight neighbours holds S of its channel's 8 S states,
-// n = p S + j.  Of a tile's 32 steps it loads and prepares four: the steps t
-// with t >> 4 == half, of which register reg(t) is in quad position pos(t).
-// "rows" gives a lane four steps in a row (one vector load), "tokens" every
-// fourth step of its half (a wave then reads four neighbouring steps at once).
+// ---- a workgroup of the scan kernels ----
+// 64 channels of one group, 32 steps to a tile, 512 threads in two roles.
+// Moving a tile: thread by thread four elements of every activation, in vector
+// accesses along whichever axis is contiguous; they turn delta into dt and hand
+// the steps' values to the other role, and take its results back, through LDS.
+// Running a tile: eight neighbouring lanes per channel, lane p the S states
+// n = p S + j; a wave has 8 channels.  (Lanes that loaded their own channel's steps
+// made 28 cache accesses per 64-lane load where the vectors make 8.)
 constexpr int kTile = 32;
+constexpr int kChannels = 64;
+constexpr int kScanThreads = kChannels * 8;
 constexpr int kOwn = 4;
-template <bool ROWS>
-constexpr int pos(int t) { return ROWS ? (t >> 2) & 3 : t & 3; }
-template <bool ROWS>
-constexpr int reg(int t) { return ROWS ? t & 3 : (t >> 2) & 3; }
-// the step in register i of lane p, and the first of them
-template <bool ROWS>
-__device__ __forceinline__ int step_of(int p, int i) { return ROWS ? p * 4 + i : (p >> 2) * 16 + i * 4 + (p & 3); }
 
-// lane exchanges (v_*_dpp): within a quad, and between the two quads of eight
-template <int CTRL, int BANKS = 0xf>
-__device__ __forceinline__ float dpp(float v, float old = 0.0f) {
-    return __int_as_float(
-        __builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, 0xf, BANKS, BANKS == 0xf));
+enum Order {
+    kRows,    // steps contiguous: a thread moves four steps of one channel
+    kTokens,  // channels contiguous: four channels of one step
+    kAny,     // neither: the same, element by element
+};
+
+struct Place {
+    int tid, p, wave, c, g, blk, h;  // c, h: the running lane's channel in the block and of all (clamped)
+    int valid;                       // channels of the block
+    int64_t first;                   // the block's first channel
+    bool live;                       // the running lane's channel exists
+};
+__device__ __forceinline__ Place place_of(int cb, int per_group, int64_t H, int64_t G) {
+    Place l;
+    l.tid = threadIdx.x;
+    l.p = l.tid & 7;
+    l.wave = __builtin_amdgcn_readfirstlane(l.tid >> 6);
+    l.g = cb / per_group;
+    l.blk = cb % per_group;
+    const int Hg = (int)(H / G);
+    l.first = (int64_t)l.g * Hg + l.blk * kChannels;
+    l.valid = min(kChannels, Hg - l.blk * kChannels);
+    l.c = l.tid >> 3;
+    l.live = l.c < l.valid;
+    l.h = (int)l.first + min(l.c, l.valid - 1);
+    return l;
 }
-// the value of quad position K in all four lanes (K a compile-time value once unrolled)
-__device__ __forceinline__ float quad_bcast(float v, int K) {
-    switch (K) {
-        case 0: return dpp<0x00>(v);
-        case 1: return dpp<0x55>(v);
-        case 2: return dpp<0xAA>(v);
-        default: return dpp<0xFF>(v);
+
+// the four elements a thread moves: steps t + (kRows ? i : 0), channels
+// c + (kRows ? 0 : i) of the block.  With kTokens a vector that would end behind the
+// last channel is moved back to end with it (c may be negative in a block of fewer
+// than four; a group has at least four), so that some elements are moved twice.
+template <Order O>
+struct Mover {
+    int t, c;
+    __device__ __forceinline__ Mover(int tid, int valid) {
+        t = O == kRows ? (tid & 7) * 4 : tid >> 4;
+        c = O == kRows ? tid >> 3 : (tid & 15) * 4;
+        if (O == kTokens) c = min(c, valid - 4);
     }
+    __device__ __forceinline__ int step(int i) const { return t + (O == kRows ? i : 0); }
+    __device__ __forceinline__ int channel(int i) const { return c + (O == kRows ? 0 : i); }
+    __device__ __forceinline__ bool has(int i, int valid) const {
+        return channel(i) >= 0 && channel(i) < valid;
+    }
+    // the thread's first element in the tile whose first step is `step0`
+    template <class T>
+    __device__ __forceinline__ T* at(const View3& v, int64_t row, const Place& l, int64_t step0) const {
+        const int cc = O == kTokens ? c : min(c, l.valid - 1);
+        return (T*)v.data + row * v.sb + (l.first + cc) * v.sh + (step0 + t) * v.sl;
+    }
+    template <class T>
+    __device__ __forceinline__ void load(T (&r)[kOwn], const T* p, const View3& v, int valid) const {
+        if constexpr (O == kAny) {
+            const int most = max(0, valid - 1 - c);  // channels behind the last one read it again
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) r[i] = p[min(i, most) * v.sh];
+        } else {
+            const Vec4<T> w = *reinterpret_cast<const Vec4<T>*>(p);
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) r[i] = w.v[i];
+        }
+    }
+    // where only the tile's first nt steps exist
+    template <class T>
+    __device__ __forceinline__ void load_part(T (&r)[kOwn], const T* p, const View3& v, int valid, int nt) const {
+        const int most = O == kAny ? max(0, valid - 1 - c) : kOwn;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            r[i] = step(i) < nt ? p[O == kRows ? i : min(i, most) * v.sh] : from_f<T>(0.0f);
+    }
+    template <class T>
+    __device__ __forceinline__ void store(const float (&r)[kOwn], T* p, const View3& v, int valid, int nt) const {
+        if (O != kAny && step(O == kRows ? kOwn - 1 : 0) < nt && (O == kTokens ? c >= 0 : c < valid)) {
+            Vec4<T> w;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) w.v[i] = from_f<T>(r[i]);
+            *reinterpret_cast<Vec4<T>*>(p) = w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)
+                if (step(i) < nt && has(i, valid)) p[O == kRows ? i : i * v.sh] = from_f<T>(r[i]);
+        }
+    }
+};
+
+// B and C of a tile on their way to LDS in float32: row t holds, per pair k of a
+// lane's states, the eight lanes' {B, B, C, C}; a thread brings K elements of either
+template <class T, int S>
+struct Stage {
+    static constexpr int K = kTile * 8 * S / kScanThreads;  // 1, 2 or 4
+    static constexpr int kRow = 16 * S + 4;                 // floats of a row (padded)
+    T b[K], c[K];
+    int N, tid;
+    bool by_time;  // consecutive threads along B's contiguous axis
+    __device__ __forceinline__ Stage(const View4& B, int states, int thread)
+        : N(states), tid(thread), by_time(B.sl == 1) {}
+    __device__ __forceinline__ void place(int k, int& t, int& n) const {
+        const int e = tid + kScanThreads * k;
+        t = by_time ? e % kTile : e / (8 * S);
+        n = by_time ? e / kTile : e % (8 * S);
+    }
+    // the first nt >= 1 steps of the tile at Bp, Cp exist; the others read the last one
+    template <bool WB, bool WC>
+    __device__ __forceinline__ void load(const View4& B, const View4& C, const T* Bp, const T* Cp, int nt) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            int t, n;
+            place(k, t, n);
+            const int64_t s = min(t, nt - 1), m = min(n, N - 1);
+            if (WB) b[k] = Bp[s * B.sl + m * B.sn];
+            if (WC) c[k] = Cp[s * C.sl + m * C.sn];
+        }
+    }
+    // padded states, and steps behind the last one, become zero
+    template <bool WB, bool WC>
+    __device__ __forceinline__ void store(float* to, int nt) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            int t, n;
+            place(k, t, n);
+            float* at = to + t * kRow + ((n % S / 2) * 8 + n / S) * 4 + (n & 1);
+            const bool in = t < nt && n < N;
+            if (WB) at[0] = in ? to_f(b[k]) : 0.0f;
+            if (WC) at[2] = in ? to_f(c[k]) : 0.0f;
+        }
+    }
+};
+
+// lane exchanges (v_*_dpp)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
 }
-// quad position q gets the sum over the quad of p_q: 9 instructions for four sums
+// lane q of a quad gets the sum over the quad of p_q: 9 instructions for four sums
 __device__ __forceinline__ float quad_sums(float p0, float p1, float p2, float p3, bool odd, bool high) {
     const float a = (odd ? p1 : p0) + dpp<0xB1>(odd ? p0 : p1);
     const float b = (odd ? p3 : p2) + dpp<0xB1>(odd ? p2 : p3);
     return (high ? b : a) + dpp<0x4E>(high ? a : b);
 }
-// both halves' registers in both quads: lo is the lower quad's v, hi the upper one's
-__device__ __forceinline__ void both_halves(float v, float& lo, float& hi) {
-    lo = dpp<0x114, 0xA>(v, v);  // row_shr:4 into the upper quads
-    hi = dpp<0x104, 0x5>(v, v);  // row_shl:4 into the lower quads
+// sums over a channel's lanes, by step: lane p leaves its quad's sum of four steps
+// at [step][channel][quad] of `to` (row kSumRow, which spreads a wave's writes over
+// the banks), the mover adds the two quads'
+constexpr int kSumRow = kChannels * 2 + 16;
+__device__ __forceinline__ void put_sums(float* to, int g, float s, int c, int p) {
+    to[(4 * g + (p & 3)) * kSumRow + c * 2 + (p >> 2)] = s;
 }
-// sum over the two quads of `lo` (wanted in the lower one) and `hi` (in the upper one)
-__device__ __forceinline__ float half_sums(float lo, float hi, bool upper) {
-    const float mine = upper ? hi : lo, give = upper ? lo : hi;
-    return mine + dpp<0x114, 0xA>(give, dpp<0x104, 0x5>(give, give));
-}
-// sum over a channel's lanes of one value, in all of them
-__device__ __forceinline__ float lane_sum(float v) {
-    v += dpp<0xB1>(v);
-    v += dpp<0x4E>(v);
-    return v + dpp<0x141>(v);  // row_half_mirror: the other quad's
-}
-
-// the four steps of a tile that lane p owns.  `base` is the same in the whole
-// wave (the tile's first step, the wave's first channel), `off` the lane's
-// distance from it in bytes (its channel and first step), `step4` that of 4 steps.
-template <class T, bool ROWS>
-__device__ __forceinline__ void load_own(T (&r)[kOwn], const char* base, uint32_t off, uint32_t step4) {
-    if constexpr (ROWS) {
-        const Vec4<T> v = *reinterpret_cast<const Vec4<T>*>(base + off);
+template <Order O>
+__device__ __forceinline__ void get_sums(float (&r)[kOwn], const float* from, const Mover<O>& m) {
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) r[i] = v.v[i];
-    } else {
-        asm volatile("" : "+v"(off));  // add the steps' distances here: kept over the tiles they cost registers
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) r[i] = *reinterpret_cast<const T*>(base + (off + i * step4));
-    }
-}
-// the same where only the tile's first nt steps exist
-template <class T, bool ROWS>
-__device__ __forceinline__ void load_part(T (&r)[kOwn], const char* base, uint32_t off, uint32_t step4, int nt, int p) {
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-        r[i] = step_of<ROWS>(p, i) < nt
-                   ? *reinterpret_cast<const T*>(base + (off + i * (ROWS ? (uint32_t)sizeof(T) : step4)))
-                   : from_f<T>(0.0f);
-}
-template <class T, bool ROWS>
-__device__ __forceinline__ void store_own(const float (&v)[kOwn], char* base, uint32_t off, uint32_t step4, int nt,
-                                          int p) {
-    if (nt == kTile) {
-        if constexpr (ROWS) {
-            Vec4<T> w;
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) w.v[i] = from_f<T>(v[i]);
-            *reinterpret_cast<Vec4<T>*>(base + off) = w;
-        } else {
-            asm volatile("" : "+v"(off));
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) *reinterpret_cast<T*>(base + (off + i * step4)) = from_f<T>(v[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-            if (step_of<ROWS>(p, i) < nt)
-                *reinterpret_cast<T*>(base + (off + i * (ROWS ? (uint32_t)sizeof(T) : step4))) = from_f<T>(v[i]);
+    for (int i = 0; i < kOwn; ++i) {
+        const float2 v = *reinterpret_cast<const float2*>(from + m.step(i) * kSumRow + max(m.channel(i), 0) * 2);
+        r[i] = v.x + v.y;
     }
 }
 // a lane's S states of a row [Np] of a workspace
@@ -259,77 +328,16 @@ __device__ __forceinline__ void store_states(const float (&r)[S], float* p) {
     for (int k = 0; k < S; k += 2) *reinterpret_cast<float2*>(p + k) = make_float2(r[k], r[k + 1]);
 }
 
-// a workgroup of the scan kernels: 64 channels of one group
-constexpr int kChannels = 64;
-constexpr int kScanThreads = kChannels * 8;
-struct Place {
-    int tid, p, wave, g, blk, h, w0;
-    uint32_t dh;  // the lane's channel, counted from its wave's first
-    bool live;    // it has one
-};
-__device__ __forceinline__ Place place_of(int cb, int per_group, int64_t H, int64_t G) {
-    Place l;
-    l.tid = threadIdx.x;
-    l.p = l.tid & 7;
-    l.wave = __builtin_amdgcn_readfirstlane(l.tid >> 6);
-    l.g = cb / per_group;
-    l.blk = cb % per_group;
-    const int Hg = (int)(H / G), c0 = l.blk * kChannels + l.wave * 8, c = c0 + ((l.tid & 63) >> 3);
-    l.live = c < Hg;
-    l.w0 = l.g * Hg + min(c0, Hg - 1);
-    l.h = l.g * Hg + min(c, Hg - 1);
-    l.dh = (uint32_t)(l.h - l.w0);
-    return l;
+// how the activations of a call lie, from their views (null ones aside)
+inline Order order_of(const View3* const* v, int n, int64_t per_group) {
+    bool rows = true, tokens = per_group >= 4;
+    for (int i = 0; i < n; ++i) {
+        if (!v[i]->data) continue;
+        rows = rows && v[i]->sl == 1;
+        tokens = tokens && v[i]->sh == 1;
+    }
+    return rows ? kRows : tokens ? kTokens : kAny;
 }
-
-// B and C of a tile on their way to LDS in float32: row t holds, per pair k of
-// a lane's states, the eight lanes' {B, B, C, C}; a thread brings K elements of either
-template <class T, int S>
-struct Stage {
-    static constexpr int K = kTile * 8 * S / kScanThreads;  // 1, 2 or 4
-    static constexpr int kRow = 16 * S + 4;                 // floats of a row (padded)
-    uint32_t bo[K], co[K];
-    int at[K], st[K];  // place in LDS; step, or kTile for a padded state
-    T b[K], c[K];
-    __device__ __forceinline__ void init(const View4& B, const View4& C, int N, int tid) {
-        const bool by_time = B.sl == 1;  // consecutive threads along B's contiguous axis
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int e = tid + kScanThreads * k;
-            const int t = by_time ? e % kTile : e / (8 * S), n = by_time ? e / kTile : e % (8 * S);
-            at[k] = t * kRow + ((n % S / 2) * 8 + n / S) * 4 + (n & 1);
-            st[k] = n < N ? t : kTile;
-            const uint32_t m = min(n, N - 1);  // padded states read the last one and are zeroed
-            bo[k] = (m * (uint32_t)B.sn + t * (uint32_t)B.sl) * (uint32_t)sizeof(T);
-            co[k] = (m * (uint32_t)C.sn + t * (uint32_t)C.sl) * (uint32_t)sizeof(T);
-        }
-    }
-    template <bool WB, bool WC>
-    __device__ __forceinline__ void load(const char* Bp, const char* Cp) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (WB) b[k] = *reinterpret_cast<const T*>(Bp + bo[k]);
-            if (WC) c[k] = *reinterpret_cast<const T*>(Cp + co[k]);
-        }
-    }
-    // where only the first nt steps exist
-    template <bool WB, bool WC>
-    __device__ __forceinline__ void load_part(const char* Bp, const char* Cp, int nt) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (WB) b[k] = st[k] < nt ? *reinterpret_cast<const T*>(Bp + bo[k]) : from_f<T>(0.0f);
-            if (WC) c[k] = st[k] < nt ? *reinterpret_cast<const T*>(Cp + co[k]) : from_f<T>(0.0f);
-        }
-    }
-    template <bool WB, bool WC>
-    __device__ __forceinline__ void store(float* to) const {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (WB) to[at[k]] = st[k] < kTile ? to_f(b[k]) : 0.0f;
-            if (WC) to[at[k] + 2] = st[k] < kTile ? to_f(c[k]) : 0.0f;
-        }
-    }
-};
 
 // ---- scalar functions ----
 constexpr float kLog2e = 1.4426950408889634f;

@@ -8,11 +8,12 @@
 //   dA = sum_{b,t} dt_t a_t g_t x_{t-1}   dD = sum p_t u_t   ddelta_bias = sum ddelta
 //   dz_t = dy_t (sum_n C_t x_t + D u_t) silu'(z_t)          dx_in = a_1 g_1
 //
-// Work split as in the forward scan: eight lanes per channel, 8 channels per
-// wave, 64 per workgroup.  The workgroup takes the tiles of 32 steps from the
-// last to the first, recomputes a tile's states from the one that the forward
-// pass saved at its first step (states and decays stay in registers, for one
-// pair of a lane's states at a time) and walks back through it.
+// Work split as in the forward scan: 64 channels per workgroup, tiles of 32 steps,
+// threads that move elements and eight lanes per channel that run the recurrence,
+// LDS between them.  The tiles go from the last to the first: a tile's states are
+// recomputed from the one that the forward pass saved at its first step (states
+// and decays stay in registers, for one pair of a lane's states at a time), then
+// the lanes walk back through it.
 //
 // dB and dC are sums over all channels of a group: over a wave's 8 channels by
 // lane exchanges, over the workgroup's waves through LDS, over the group's
@@ -30,16 +31,20 @@ namespace ssm {
 
 namespace {
 
-// sums over the 8 channels of a wave (lane bits 3..5) of four values per lane:
-// lane l gets the sum of its lane position's value number l >> 4
+// sums over the 8 channels of a wave (lane bits 3..5) of four values per lane, but
+// for the last addition: lane l gets, of its lane position's value number l >> 4,
+// what the channels with its bit 3 have
 __device__ __forceinline__ float channel_sums(float v0, float v1, float v2, float v3) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v0), __float_as_uint(v2), false, false);
     const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v1), __float_as_uint(v3), false, false);
     const float x = __uint_as_float(a[0]) + __uint_as_float(a[1]);  // v0 below lane 32, v2 above
     const float y = __uint_as_float(b[0]) + __uint_as_float(b[1]);
     const auto c = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
-    const float s = __uint_as_float(c[0]) + __uint_as_float(c[1]);
-    return s + dpp<0x128>(s);  // row_ror:8
+    return __uint_as_float(c[0]) + __uint_as_float(c[1]);
+}
+// that addition for two steps' values: the first's for lanes with bit 3 clear, the second's for the others
+__device__ __forceinline__ float last_sums(float first, float second, bool bit3) {
+    return (bit3 ? second : first) + dpp<0x128>(bit3 ? first : second);  // row_ror:8
 }
 
 struct GradSplit {
@@ -52,21 +57,28 @@ struct GradSplit {
     float* part_d;  // [items, 2, H]: dD, ddelta_bias
 };
 
-template <class T, int S, bool ROWS, bool ENDS>
+// ENDS: the first launch of a split call, what every chunk hands to the one before it
+template <class T, int S, Order O, bool ENDS>
 __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, GradSplit sp) {
     const ScanArgs& a = ga.f;
-    using St = Stage<T, S>;
-    constexpr int kRow = St::kRow;
-    __shared__ __attribute__((aligned(16))) float lds[2][kTile * kRow];
-    __shared__ float red[ENDS ? 1 : 8 * kTile * 32];
+    constexpr int kRow = Stage<T, S>::kRow;
+    __shared__ __attribute__((aligned(16))) float lds[kTile * kRow];
+    // {dt, dt u, p, 0} of every step and channel; p is the gradient behind the gate
+    __shared__ __attribute__((aligned(16))) float4 steps[kTile * kChannels];
+    // sums over a channel's states: of C x, of g B, of A a g x
+    __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kSumRow];
+    __shared__ __attribute__((aligned(16))) float gsum[ENDS ? 4 : kTile * kSumRow];
+    __shared__ __attribute__((aligned(16))) float asum[ENDS ? 4 : kTile * kSumRow];
+    __shared__ float red[ENDS ? 1 : 8 * kTile * 32];  // [wave][step][B or C][16 states]: sums over a wave's channels
 
     const int cb = blockIdx.x % sp.blocks;
     const int64_t item = blockIdx.x / sp.blocks;
     Item it;
     const bool there = find_item(a.q, item, sp.Q, it);
     const Place l = place_of(cb, sp.per_group, a.H, a.G);
+    const Mover<O> m(l.tid, l.valid);
     const int p = l.p, N = (int)a.N, lane = l.tid & 63;
-    const bool odd = p & 1, high = p & 2, upper = p & 4;
+    const bool odd = p & 1, high = p & 2, bit3 = lane & 8;
     const int64_t wrow = (int64_t)l.h * (8 * S) + p * S, wstep = a.H * (8 * S);
 
     float A2[S], carry[S], dA[S];
@@ -75,11 +87,11 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
         A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : 0.0f;
         carry[j] = dA[j] = 0.0f;
     }
-    float dDsum = 0.0f, dbsum = 0.0f, dtsum = 0.0f;
+    float dDsum[kOwn] = {}, dbsum[kOwn] = {}, dtsum[kOwn] = {};
 
     const int chunks = there ? chunks_of(it.end - it.beg, sp.Q) : 0;
-    const int beg = there ? it.beg + it.c * sp.Q : 0;
-    const int end = there ? (int)min((int64_t)it.end, (int64_t)beg + sp.Q) : 0;
+    const int64_t beg = there ? it.beg + (int64_t)it.c * sp.Q : 0;
+    const int64_t end = there ? min((int64_t)it.end, beg + sp.Q) : 0;
     const bool work = there && it.c < chunks && (!ENDS || it.c > 0);
     if (ENDS && !work) return;
     if (work) {
@@ -105,252 +117,253 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
     }
 
     if (work && beg < end) {
-        const float bias = a.delta_bias ? a.delta_bias[l.h] : 0.0f;
-        const float Dv = a.D ? a.D[l.h] : 0.0f;
+        const int tiles = (int)((end - beg + kTile - 1) / kTile);
+        const int64_t last = beg + (int64_t)(tiles - 1) * kTile;  // the last tile's first step
+        int now = (int)(end - last);                              // and its steps; all others are whole
         const bool gate = a.z.data;
-        const int last = beg + (end - 1 - beg) / kTile * kTile;  // the last tile's first step
-        constexpr uint32_t kE = sizeof(T);
-        const uint32_t q0 = step_of<ROWS>(p, 0);
-        auto base = [&](const View3& v) {
-            return (char*)v.data + (it.row * v.sb + l.w0 * v.sh + last * v.sl) * (int64_t)kE;
-        };
-        auto offset = [&](const View3& v) { return (l.dh * (uint32_t)v.sh + q0 * (uint32_t)v.sl) * kE; };
-        auto step4 = [&](const View3& v) { return (uint32_t)v.sl * 4 * kE; };
         const View3& gv = gate ? a.z : a.u;  // without a gate u once more, unused
-        const char *up = base(a.u), *dp = base(a.delta), *zp = base(gv), *gp = base(ga.dy);
-        char *dup = base(ga.du), *ddp = base(ga.ddelta), *dzp = base(ga.dz);
-        const uint32_t uo = offset(a.u), dof = offset(a.delta), zo = offset(gv), go = offset(ga.dy);
-        const uint32_t us = step4(a.u), ds = step4(a.delta), zs = step4(gv), gs = step4(ga.dy);
-        const char* Bp = (const char*)a.B.data + (it.row * a.B.sb + l.g * a.B.sg + last * a.B.sl) * (int64_t)kE;
-        const char* Cp = (const char*)a.C.data + (it.row * a.C.sb + l.g * a.C.sg + last * a.C.sl) * (int64_t)kE;
-        const uint32_t bs = (uint32_t)a.B.sl * 4 * kE, cs = (uint32_t)a.C.sl * 4 * kE;
-        St stage;
-        stage.init(a.B, a.C, N, l.tid);
+        const T* up = m.template at<const T>(a.u, it.row, l, last);
+        const T* dp = m.template at<const T>(a.delta, it.row, l, last);
+        const T* zp = m.template at<const T>(gv, it.row, l, last);
+        const T* gp = m.template at<const T>(ga.dy, it.row, l, last);
+        const T* Bp = (const T*)a.B.data + it.row * a.B.sb + l.g * a.B.sg + last * a.B.sl;
+        const T* Cp = (const T*)a.C.data + it.row * a.C.sb + l.g * a.C.sg + last * a.C.sl;
+        Stage<T, S> stage(a.B, N, l.tid);
         const float* sv = ENDS ? nullptr : ga.saved + (saved_row(a.q, it) + (last - it.beg) / kTile) * wstep + wrow;
+        float bias[kOwn], Dv[kOwn];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int64_t hh = l.first + min(max(m.channel(i), 0), l.valid - 1);
+            bias[i] = a.delta_bias ? a.delta_bias[hh] : 0.0f;
+            Dv[i] = a.D ? a.D[hh] : 0.0f;
+        }
+        if (l.valid < kChannels) {  // channels that are not there: steps of length zero without gradient
+            for (int e = l.tid; e < kTile * kChannels; e += kScanThreads) steps[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            __syncthreads();
+        }
 
         T ur[kOwn], dr[kOwn], zr[kOwn], gr[kOwn];
         float hn[S];
-        // the last tile may be a part of one
-        int now = end - last;
-        load_part<T, ROWS>(ur, up, uo, us, now, p);
-        load_part<T, ROWS>(dr, dp, dof, ds, now, p);
-        load_part<T, ROWS>(gr, gp, go, gs, now, p);
-        load_part<T, ROWS>(zr, zp, zo, zs, now, p);
-        stage.template load_part<!ENDS, true>(Bp, Cp, now);
-        stage.template store<!ENDS, true>(lds[0]);
+        m.template load_part<T>(ur, up, a.u, l.valid, now);
+        m.template load_part<T>(dr, dp, a.delta, l.valid, now);
+        m.template load_part<T>(gr, gp, ga.dy, l.valid, now);
+        m.template load_part<T>(zr, zp, gv, l.valid, now);
+        stage.template load<!ENDS, true>(a.B, a.C, Bp, Cp, now);
         if (!ENDS) load_states<S>(hn, sv);
-        __syncthreads();
-        int buf = 0;
-        for (int t0 = last; t0 >= beg; t0 -= kTile) {
+
+        for (int tile = tiles - 1; tile >= 0; --tile) {
+            const int64_t t0 = beg + (int64_t)tile * kTile;
+            // the loaded tile into LDS
             float u[kOwn], slope[kOwn], zsl[kOwn];
-            float dt[2][kOwn], dx[2][kOwn], pv[2][kOwn];
-            float own[kOwn], po[kOwn];  // dt, and dy behind the gate
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                u[i] = to_f(ur[i]);
-                own[i] = to_f(dr[i]) + bias;
-                po[i] = to_f(gr[i]);
-                slope[i] = 1.0f;
-                zsl[i] = to_f(zr[i]);
-            }
-            if (a.softplus) {
-#pragma unroll
-                for (int i = 0; i < kOwn; ++i) own[i] = softplus_f<kFine<T>, true>(own[i], &slope[i]);
-            }
-            if (gate) {
+            {
+                float dt[kOwn], po[kOwn];
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
-                    const float z = zsl[i], s = sigmoid_f<kFine<T>>(z);
-                    zsl[i] = po[i] * s * fmaf(z, 1.0f - s, 1.0f);  // dz but for the ungated output
-                    po[i] *= z * s;
+                    u[i] = to_f(ur[i]);
+                    dt[i] = to_f(dr[i]) + bias[i];
+                    po[i] = to_f(gr[i]);
+                    slope[i] = 1.0f;
+                    zsl[i] = to_f(zr[i]);
                 }
-            }
+                if (a.softplus) {
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                const bool in = step_of<ROWS>(p, i) < now;
-                own[i] = in ? own[i] : 0.0f;
-                po[i] = in && l.live ? po[i] : 0.0f;
-                if (ENDS) dtsum += own[i];
-                both_halves(own[i], dt[0][i], dt[1][i]);
-                both_halves(po[i], pv[0][i], pv[1][i]);
-                if (!ENDS) both_halves(own[i] * u[i], dx[0][i], dx[1][i]);
+                    for (int i = 0; i < kOwn; ++i) dt[i] = softplus_f<kFine<T>, true>(dt[i], &slope[i]);
+                }
+                if (gate) {
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i) {
+                        const float z = zsl[i], s = sigmoid_f<kFine<T>>(z);
+                        zsl[i] = po[i] * s * fmaf(z, 1.0f - s, 1.0f);  // dz but for the ungated output
+                        po[i] *= z * s;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) {
+                    const bool in = m.step(i) < now;
+                    dt[i] = in ? dt[i] : 0.0f;
+                    po[i] = in ? po[i] : 0.0f;
+                    if (ENDS) dtsum[i] += dt[i];
+                    if (m.has(i, l.valid))
+                        steps[m.step(i) * kChannels + m.channel(i)] = make_float4(dt[i], dt[i] * u[i], po[i], 0.0f);
+                }
+                stage.template store<!ENDS, true>(lds, now);
             }
             float h0[S];
             if (!ENDS) {
 #pragma unroll
                 for (int j = 0; j < S; ++j) h0[j] = hn[j];
             }
-            // the tile before this one, whole, flies while this one is computed (the
-            // first loads a whole tile's worth of itself again where it is one)
-            const uint32_t back = t0 > beg ? kTile / 4 : 0;
-            if (t0 > beg || now == kTile) {
-                up -= (uint64_t)us * back, dp -= (uint64_t)ds * back, zp -= (uint64_t)zs * back;
-                gp -= (uint64_t)gs * back, Bp -= (uint64_t)bs * back, Cp -= (uint64_t)cs * back;
-                load_own<T, ROWS>(ur, up, uo, us);
-                load_own<T, ROWS>(dr, dp, dof, ds);
-                load_own<T, ROWS>(gr, gp, go, gs);
-                load_own<T, ROWS>(zr, zp, zo, zs);
-                stage.template load<!ENDS, true>(Bp, Cp);
+            __syncthreads();
+            // the tile before this one, whole, flies while this one is run (the first
+            // loads itself again where it is a whole one)
+            if (tile > 0 || now == kTile) {
+                const int64_t go = tile > 0 ? kTile : 0;
+                up -= go * a.u.sl, dp -= go * a.delta.sl, zp -= go * gv.sl, gp -= go * ga.dy.sl;
+                Bp -= go * a.B.sl, Cp -= go * a.C.sl;
+                m.template load<T>(ur, up, a.u, l.valid);
+                m.template load<T>(dr, dp, a.delta, l.valid);
+                m.template load<T>(gr, gp, ga.dy, l.valid);
+                m.template load<T>(zr, zp, gv, l.valid);
+                stage.template load<!ENDS, true>(a.B, a.C, Bp, Cp, kTile);
                 if (!ENDS) {
-                    sv -= back ? wstep : 0;
+                    sv -= go ? wstep : 0;
                     load_states<S>(hn, sv);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            const float4* const bc = reinterpret_cast<const float4*>(&lds[0][0]);
-            int bq = buf * (kTile * kRow / 4) + p;  // the lane's B and C in it
+            const float4* const bc = reinterpret_cast<const float4*>(lds) + p;
+            const float4* const mine = steps + l.c;
             if constexpr (ENDS) {
 #pragma unroll
                 for (int t = kTile - 1; t >= 0; --t) {
-                    const float dtv = quad_bcast(dt[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
-                    const float pt = quad_bcast(pv[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
+                    const float4 d = mine[t * kChannels];
 #pragma unroll
                     for (int k = 0; k < S / 2; ++k) {
-                        const float4 v = bc[bq + t * (kRow / 4) + k * 8];
-                        carry[2 * k] = fmaf(v.z, pt, carry[2 * k]) * __builtin_amdgcn_exp2f(dtv * A2[2 * k]);
+                        const float4 v = bc[t * (kRow / 4) + k * 8];
+                        carry[2 * k] = fmaf(v.z, d.z, carry[2 * k]) * __builtin_amdgcn_exp2f(d.x * A2[2 * k]);
                         carry[2 * k + 1] =
-                            fmaf(v.w, pt, carry[2 * k + 1]) * __builtin_amdgcn_exp2f(dtv * A2[2 * k + 1]);
+                            fmaf(v.w, d.z, carry[2 * k + 1]) * __builtin_amdgcn_exp2f(d.x * A2[2 * k + 1]);
                     }
                 }
+                __syncthreads();
             } else {
-                float ys[kOwn] = {}, gxs[kOwn] = {}, dds[kOwn] = {};
+                float ysh[S > 2 ? 8 : 1], gsh[S > 2 ? 8 : 1], ash[S > 2 ? 8 : 1];  // sums of the pairs before
 #pragma unroll
                 for (int k = 0; k < S / 2; ++k) {
                     // this pair of states through the tile and back
-                    float dec[kTile][2], x[kTile + 1][2];
-                    float sums[2][kOwn], share[16];
-                    auto collect = [&](int t) {  // the lanes' shares of the steps up to t (forth) or from t on (back)
-                        if (!ROWS)
-                            sums[t >> 4][(t >> 2) & 3] = quad_sums(share[0], share[1], share[2], share[3], odd, high);
-                        if (ROWS) {
-#pragma unroll
-                            for (int i = 0; i < kOwn; ++i)
-                                sums[t >> 4][i] =
-                                    quad_sums(share[i], share[4 + i], share[8 + i], share[12 + i], odd, high);
-                        }
-                    };
+                    float dec[kTile][2], x[kTile + 1][2], share[4];
                     x[0][0] = h0[2 * k], x[0][1] = h0[2 * k + 1];
 #pragma unroll
                     for (int t = 0; t < kTile; ++t) {
-                        const float dtv = quad_bcast(dt[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
-                        const float dxv = quad_bcast(dx[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
-                        const float4 v = bc[bq + t * (kRow / 4) + k * 8];
-                        dec[t][0] = __builtin_amdgcn_exp2f(dtv * A2[2 * k]);
-                        dec[t][1] = __builtin_amdgcn_exp2f(dtv * A2[2 * k + 1]);
-                        x[t + 1][0] = fmaf(dec[t][0], x[t][0], dxv * v.x);
-                        x[t + 1][1] = fmaf(dec[t][1], x[t][1], dxv * v.y);
+                        const float2 d = *reinterpret_cast<const float2*>(mine + t * kChannels);
+                        const float4 v = bc[t * (kRow / 4) + k * 8];
+                        dec[t][0] = __builtin_amdgcn_exp2f(d.x * A2[2 * k]);
+                        dec[t][1] = __builtin_amdgcn_exp2f(d.x * A2[2 * k + 1]);
+                        x[t + 1][0] = fmaf(dec[t][0], x[t][0], d.y * v.x);
+                        x[t + 1][1] = fmaf(dec[t][1], x[t][1], d.y * v.y);
                         float y = fmaf(v.w, x[t + 1][1], v.z * x[t + 1][0]);
                         asm volatile("" : "+v"(y));  // the sum is done here, not where it is used
-                        share[ROWS ? t & 15 : t & 3] = y;
-                        if (t % (ROWS ? 16 : 4) == (ROWS ? 15 : 3)) collect(t);
+                        share[t & 3] = y;
+                        if ((t & 3) == 3) {
+                            float s = quad_sums(share[0], share[1], share[2], share[3], odd, high);
+                            if (k > 0) s += ysh[t >> 2];
+                            if (k + 1 < S / 2) ysh[S > 2 ? t >> 2 : 0] = s;
+                            else put_sums(ysum, t >> 2, s, l.c, p);
+                        }
                     }
-#pragma unroll
-                    for (int i = 0; i < kOwn; ++i) ys[i] += half_sums(sums[0][i], sums[1][i], upper);
-                    float dsum[2][kOwn], dshare[16];
-                    // on the way back B, C and the passed-on values are read anew: kept
-                    // from the way forth they would take six registers per step
-                    asm volatile("" : "+v"(bq));
-#pragma unroll
-                    for (int i = 0; i < kOwn; ++i)
-                        asm volatile("" : "+v"(dt[0][i]), "+v"(dt[1][i]), "+v"(dx[0][i]), "+v"(dx[1][i]));
+                    // on the way back B, C and the steps are read anew: kept from the way
+                    // forth they would take eight registers per step
+                    int again = 0;
+                    asm volatile("" : "+v"(again));
+                    const float4* const bc2 = bc + again;
+                    float gshare[4], later = 0.0f;
 #pragma unroll
                     for (int t = kTile - 1; t >= 0; --t) {
-                        const float dtv = quad_bcast(dt[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
-                        const float dxv = quad_bcast(dx[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
-                        const float pt = quad_bcast(pv[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
-                        const float4 v = bc[bq + t * (kRow / 4) + k * 8];
-                        const float g0 = fmaf(v.z, pt, carry[2 * k]), g1 = fmaf(v.w, pt, carry[2 * k + 1]);
+                        const float4 d = mine[t * kChannels + again];
+                        const float4 v = bc2[t * (kRow / 4) + k * 8];
+                        const float g0 = fmaf(v.z, d.z, carry[2 * k]), g1 = fmaf(v.w, d.z, carry[2 * k + 1]);
                         float gx = fmaf(g1, v.y, g0 * v.x);
                         carry[2 * k] = g0 * dec[t][0];
                         carry[2 * k + 1] = g1 * dec[t][1];
                         const float b0 = carry[2 * k] * x[t][0], b1 = carry[2 * k + 1] * x[t][1];
                         float dd = fmaf(b1, A2[2 * k + 1], b0 * A2[2 * k]);
-                        dA[2 * k] = fmaf(b0, dtv, dA[2 * k]);
-                        dA[2 * k + 1] = fmaf(b1, dtv, dA[2 * k + 1]);
-                        const float s = channel_sums(g0 * dxv, g1 * dxv, pt * x[t + 1][0], pt * x[t + 1][1]);
-                        // [wave][t][B or C][n]: lane l holds number l >> 4 of {B, B, C, C}
-                        if ((lane & 8) == 0)
-                            red[(l.wave * kTile + t) * 32 + (lane >> 5) * 16 + p * 2 + ((lane >> 4) & 1)] = s;
+                        dA[2 * k] = fmaf(b0, d.x, dA[2 * k]);
+                        dA[2 * k + 1] = fmaf(b1, d.x, dA[2 * k + 1]);
+                        const float s = channel_sums(g0 * d.y, g1 * d.y, d.z * x[t + 1][0], d.z * x[t + 1][1]);
+                        // lane l holds number l >> 4 of {B, B, C, C}; lanes with bit 3 write the later step
+                        if (t & 1) {
+                            later = s;
+                        } else {
+                            red[(l.wave * kTile + t) * 32 + (bit3 ? 32 : 0) + (lane >> 5) * 16 + p * 2 +
+                                ((lane >> 4) & 1)] = last_sums(s, later, bit3);
+                        }
                         // these sums are done here too: their operands are a step's registers
                         asm volatile("" : "+v"(gx), "+v"(dd), "+v"(dA[2 * k]), "+v"(dA[2 * k + 1]));
-                        share[ROWS ? t & 15 : t & 3] = gx;
-                        dshare[ROWS ? t & 15 : t & 3] = dd;
-                        if (t % (ROWS ? 16 : 4) == 0) {
-                            collect(t);
-#pragma unroll
-                            for (int i = 0; i < (ROWS ? kOwn : 1); ++i)
-                                dsum[t >> 4][ROWS ? i : (t >> 2) & 3] =
-                                    ROWS ? quad_sums(dshare[i], dshare[(4 + i) & 15], dshare[(8 + i) & 15],
-                                                     dshare[(12 + i) & 15], odd, high)
-                                         : quad_sums(dshare[0], dshare[1], dshare[2], dshare[3], odd, high);
+                        share[t & 3] = dd;
+                        gshare[t & 3] = gx;
+                        if ((t & 3) == 0) {
+                            float sg = quad_sums(gshare[0], gshare[1], gshare[2], gshare[3], odd, high);
+                            float sa = quad_sums(share[0], share[1], share[2], share[3], odd, high);
+                            if (k > 0) sg += gsh[S > 2 ? t >> 2 : 0], sa += ash[S > 2 ? t >> 2 : 0];
+                            if (k + 1 < S / 2) {
+                                gsh[S > 2 ? t >> 2 : 0] = sg, ash[S > 2 ? t >> 2 : 0] = sa;
+                            } else {
+                                put_sums(gsum, t >> 2, sg, l.c, p);
+                                put_sums(asum, t >> 2, sa, l.c, p);
+                            }
                         }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kOwn; ++i) {
-                        gxs[i] += half_sums(sums[0][i], sums[1][i], upper);
-                        dds[i] += half_sums(dsum[0][i], dsum[1][i], upper);
                     }
                     __syncthreads();
                     // the workgroup's sums of dB and dC: the eight waves' in order
                     constexpr int64_t kOut = S * 16;  // of a step and group
                     float* to = sp.part_bc + ((((int64_t)l.blk * a.Bsz + it.row) * a.q.L + t0) * a.G + l.g) * kOut;
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const int e = l.tid + kScanThreads * m, t = e >> 5;
-                        if (t < now) {
-                            float s = red[e];
+                    for (int mm = 0; mm < 2; ++mm) {
+                        const int e = l.tid + kScanThreads * mm, t = e >> 5;
+                        float s = red[e];
 #pragma unroll
-                            for (int w = 1; w < 8; ++w) s += red[w * kTile * 32 + e];
-                            to[(int64_t)t * a.G * kOut + k * 32 + (e & 31)] = s;
-                        }
+                        for (int w = 1; w < 8; ++w) s += red[w * kTile * 32 + e];
+                        if (t < now) to[(int64_t)t * a.G * kOut + k * 32 + (e & 31)] = s;
                     }
                     if (k + 1 < S / 2) __syncthreads();
                 }
-                float o[kOwn];
-#pragma unroll
-                for (int i = 0; i < kOwn; ++i)
-                    o[i] = fmaf(Dv, upper ? pv[1][i] : pv[0][i], (upper ? dt[1][i] : dt[0][i]) * gxs[i]);
-                if (l.live) store_own<T, ROWS>(o, dup, offset(ga.du), step4(ga.du), now, p);
+                // the tile's gradients
+                float ys[kOwn], gs[kOwn], as[kOwn], o[kOwn];
+                get_sums<O>(ys, ysum, m);
+                get_sums<O>(gs, gsum, m);
+                get_sums<O>(as, asum, m);
+                float dt[kOwn], po[kOwn];
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
-                    o[i] = fmaf(u[i], gxs[i], dds[i] * kLn2) * slope[i];
-                    if (step_of<ROWS>(p, i) < now) {
-                        dbsum += o[i];
-                        dDsum = fmaf(upper ? pv[1][i] : pv[0][i], u[i], dDsum);
-                    }
+                    const float4 d = steps[m.step(i) * kChannels + max(0, min(m.channel(i), l.valid - 1))];
+                    dt[i] = d.x, po[i] = d.z;
+                    o[i] = fmaf(Dv[i], po[i], dt[i] * gs[i]);
                 }
-                if (l.live) store_own<T, ROWS>(o, ddp, offset(ga.ddelta), step4(ga.ddelta), now, p);
+                m.template store<T>(o, m.template at<T>(ga.du, it.row, l, t0), ga.du, l.valid, now);
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) {
+                    o[i] = fmaf(u[i], gs[i], as[i] * kLn2) * slope[i];
+                    dbsum[i] += m.step(i) < now ? o[i] : 0.0f;
+                    dDsum[i] += m.step(i) < now ? po[i] * u[i] : 0.0f;
+                }
+                m.template store<T>(o, m.template at<T>(ga.ddelta, it.row, l, t0), ga.ddelta, l.valid, now);
                 if (gate) {
 #pragma unroll
-                    for (int i = 0; i < kOwn; ++i) o[i] = fmaf(Dv, u[i], ys[i]) * zsl[i];
-                    if (l.live) store_own<T, ROWS>(o, dzp, offset(ga.dz), step4(ga.dz), now, p);
+                    for (int i = 0; i < kOwn; ++i) o[i] = fmaf(Dv[i], u[i], ys[i]) * zsl[i];
+                    m.template store<T>(o, m.template at<T>(ga.dz, it.row, l, t0), ga.dz, l.valid, now);
                 }
-                dup -= (uint64_t)step4(ga.du) * (kTile / 4), ddp -= (uint64_t)step4(ga.ddelta) * (kTile / 4);
-                dzp -= (uint64_t)step4(ga.dz) * (kTile / 4);
+                __syncthreads();  // `steps` is read above and written next
             }
             now = kTile;
-            buf ^= 1;
-            stage.template store<!ENDS, true>(lds[buf]);
-            __syncthreads();
         }
     }
 
-    if (ENDS) {
-        dtsum = lane_sum(dtsum);
-        if (l.live) {
-            store_states<S>(carry, sp.ends + item * wstep + wrow);
-            if (p == 0) sp.sums[item * a.H + l.h] = dtsum;
+    // per channel, over the threads that moved its steps
+    auto per_channel = [&](float (&v)[kOwn], float* out) {
+        float* const part = reinterpret_cast<float*>(steps);
+        constexpr int kParts = O == kRows ? 8 : kTile;
+        __syncthreads();
+#pragma unroll
+        for (int i = 1; i < (O == kRows ? kOwn : 1); ++i) v[0] += v[i];
+#pragma unroll
+        for (int i = 0; i < (O == kRows ? 1 : kOwn); ++i)
+            if (m.has(i, l.valid)) part[(O == kRows ? l.tid & 7 : m.t) * kChannels + m.channel(i)] = v[i];
+        __syncthreads();
+        if (l.tid < l.valid) {
+            float s = 0.0f;
+            for (int k = 0; k < kParts; ++k) s += part[k * kChannels + l.tid];
+            out[l.first + l.tid] = s;
         }
+    };
+    if (ENDS) {
+        per_channel(dtsum, sp.sums + item * a.H);
+        if (l.live) store_states<S>(carry, sp.ends + item * wstep + wrow);
         return;
     }
-    dDsum = lane_sum(dDsum);
-    dbsum = lane_sum(dbsum);
+    per_channel(dDsum, sp.part_d + (item * 2) * a.H);
+    per_channel(dbsum, sp.part_d + (item * 2 + 1) * a.H);
     if (!l.live) return;
     store_states<S>(dA, sp.part_a + item * wstep + wrow);
-    if (p == 0) {
-        sp.part_d[(item * 2) * a.H + l.h] = dDsum;
-        sp.part_d[(item * 2 + 1) * a.H + l.h] = dbsum;
-    }
     if (work && it.c == 0 && ga.dx_in) {
 #pragma unroll
         for (int j = 0; j < S; ++j)
@@ -443,15 +456,15 @@ Plan plan(const Seqs& q, int64_t Bsz, int64_t H, int64_t N, int64_t G) {
     return p;
 }
 
-template <class T, int S, bool ROWS>
+template <class T, int S, Order O>
 hipError_t launch_as(const ScanGradArgs& g, const Plan& p, hipStream_t s) {
     const ScanArgs& a = g.f;
     const int64_t wgs = p.items * p.sp.blocks;
     const int64_t bc = (a.Bsz * a.q.L * a.G * S * 16 + 255) / 256;
     if (wgs >= ((int64_t)1 << 31) || bc >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)wgs), wg(256), lanes(kScanThreads);
-    if (p.split) grad_kernel<T, S, ROWS, true><<<grid, lanes, 0, s>>>(g, p.sp);
-    grad_kernel<T, S, ROWS, false><<<grid, lanes, 0, s>>>(g, p.sp);
+    if (p.split) grad_kernel<T, S, O, true><<<grid, lanes, 0, s>>>(g, p.sp);
+    grad_kernel<T, S, O, false><<<grid, lanes, 0, s>>>(g, p.sp);
     grad_bc_kernel<T><<<dim3((unsigned)bc), wg, 0, s>>>(g, p.sp.part_bc, p.sp.per_group, S);
     auto sum = [&](const float* part, int64_t cols, int64_t stride, int width, int kept, float* out) {
         grad_sum_kernel<<<dim3((unsigned)((cols + kSumCols - 1) / kSumCols)), wg, 0, s>>>(part, p.items, cols, stride,
@@ -463,12 +476,17 @@ hipError_t launch_as(const ScanGradArgs& g, const Plan& p, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <class T, int S>
+hipError_t launch_in(const ScanGradArgs& g, const Plan& p, Order o, hipStream_t s) {
+    return o == kRows ? launch_as<T, S, kRows>(g, p, s)
+         : o == kTokens ? launch_as<T, S, kTokens>(g, p, s) : launch_as<T, S, kAny>(g, p, s);
+}
+
 template <class T>
-hipError_t launch_of(const ScanGradArgs& g, const Plan& p, bool rows, hipStream_t s) {
-    const int64_t N = g.f.N;
-    if (N <= 16) return rows ? launch_as<T, 2, true>(g, p, s) : launch_as<T, 2, false>(g, p, s);
-    if (N <= 32) return rows ? launch_as<T, 4, true>(g, p, s) : launch_as<T, 4, false>(g, p, s);
-    return rows ? launch_as<T, 8, true>(g, p, s) : launch_as<T, 8, false>(g, p, s);
+hipError_t launch_of(const ScanGradArgs& g, const Plan& p, Order o, hipStream_t s) {
+    if (g.f.N <= 16) return launch_in<T, 2>(g, p, o, s);
+    if (g.f.N <= 32) return launch_in<T, 4>(g, p, o, s);
+    return launch_in<T, 8>(g, p, o, s);
 }
 
 }  // namespace
@@ -498,11 +516,10 @@ hipError_t launch_scan_backward(int dtype, const ScanGradArgs& g, void* ws, hipS
     p.sp.part_a = take(p.pa);
     p.sp.part_d = take(p.pd);
     const View3* views[] = {&a.u, &a.delta, &a.z, &g.dy, &g.du, &g.ddelta, &g.dz};
-    bool rows = true;
-    for (const View3* v : views) rows = rows && (!v->data || v->sl == 1);
-    if (dtype == SSM_F32) return launch_of<float>(g, p, rows, s);
-    if (dtype == SSM_BF16) return launch_of<bf16>(g, p, rows, s);
-    return launch_of<f16>(g, p, rows, s);
+    const Order o = order_of(views, 7, a.H / a.G);
+    if (dtype == SSM_F32) return launch_of<float>(g, p, o, s);
+    if (dtype == SSM_BF16) return launch_of<bf16>(g, p, o, s);
+    return launch_of<f16>(g, p, o, s);
 }
 
 }  // namespace ssm

@@ -4,11 +4,11 @@
 //   y_t = (sum_n C_t[n] x_t[n] + D u_t) silu(z_t)
 // per (sequence, channel), B and C shared by the channels of a group.
 //
-// Work split.  Eight lanes share a channel, a wave has 8 channels, a workgroup 64
-// of one group.  The steps run in order, 32 to a tile: each lane loads and
-// prepares (softplus, gate) four of a tile's steps, and the channel's lanes pass
-// dt and dt u around by DPP; B and C of a tile go through LDS in float32,
-// double-buffered, the next tile's loads in flight while this one is computed.
+// Work split.  A workgroup has 64 channels of one group and takes the steps in
+// order, 32 to a tile: its threads move a tile's elements in vectors, prepare them
+// (softplus) and leave dt and dt u in LDS; then eight lanes per channel run the
+// recurrence, B and C in LDS too, and leave their sums for y there; then the movers
+// apply skip term and gate.  The next tile's loads fly while one is run.
 //
 // Where channels and sequences alone leave the GPU idle, the steps are split
 // into chunks of Q as well: a first launch computes every chunk's state from a
@@ -21,36 +21,24 @@ namespace ssm {
 
 namespace {
 
-// what a launch of scan_kernel is for
-enum Mode {
-    kEnds,    // every chunk's end state from a zero start, and its sum of dt
-    kFull,    // y, and the final and saved states where asked for
-    kStates,  // the saved states alone
-};
-
 // one tile's recurrence; GUARD: only the first nt steps exist (a branch per step).
-// B and C come from LDS a pair of steps ahead of their use.
-template <int S, bool ROWS, Mode MODE, bool GUARD>
-__device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], const float (&dt)[2][kOwn],
-                                         const float (&dx)[2][kOwn], const float* lds, int nt, bool odd, bool high,
-                                         float (&sums)[2][kOwn]) {
-    constexpr int kRow = Stage<float, S>::kRow, kGroup = S == 2 ? 4 : S == 4 ? 2 : 1;
-    float4 bc[2][kGroup][S / 2];
-    float p[ROWS ? 16 : 4];  // the lanes' shares of y, until a quad's four owners have one each
+// `bc` is the lane's B and C of the tile, `step` its channel's {dt, dt u}; both come
+// from LDS two steps ahead of their use.
+template <int S, bool ENDS, bool GUARD>
+__device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], const float* bc, const float2* step,
+                                         int nt, float* ysum, int c, int p) {
+    constexpr int kRow = Stage<float, S>::kRow, kGroup = S == 2 ? 2 : 1;
+    const bool odd = p & 1, high = p & 2;
+    float4 v[2][kGroup][S / 2];
+    float2 d[2][kGroup];
+    float share[4];  // the lane's shares of y of four steps
     auto fetch = [&](int g) {
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i)
+        for (int i = 0; i < kGroup; ++i) {
+            d[g & 1][i] = step[(g * kGroup + i) * kChannels];
 #pragma unroll
             for (int k = 0; k < S / 2; ++k)
-                bc[g & 1][i][k] = *reinterpret_cast<const float4*>(lds + (g * kGroup + i) * kRow + k * 32);
-    };
-    auto collect = [&](int t) {  // after step t
-        if (MODE != kFull) return;
-        if (!ROWS && (t & 3) == 3) sums[t >> 4][(t >> 2) & 3] = quad_sums(p[0], p[1], p[2], p[3], odd, high);
-        if (ROWS && (t & 15) == 15) {
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-                sums[t >> 4][i] = quad_sums(p[i], p[(4 + i) & 15], p[(8 + i) & 15], p[(12 + i) & 15], odd, high);
+                v[g & 1][i][k] = *reinterpret_cast<const float4*>(bc + (g * kGroup + i) * kRow + k * 32);
         }
     };
     fetch(0);
@@ -61,28 +49,23 @@ __device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], co
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
             const int t = g * kGroup + i;
-            float& share = p[ROWS ? t & 15 : t & 3];
-            if (GUARD && t >= nt) {
-                share = 0.0f;
-                collect(t);
-                continue;
-            }
-            const float dtv = quad_bcast(dt[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
-            const float dxv = quad_bcast(dx[t >> 4][reg<ROWS>(t)], pos<ROWS>(t));
             float acc = 0.0f;
+            if (!GUARD || t < nt) {
+                const float dt = d[g & 1][i].x, dx = d[g & 1][i].y;
 #pragma unroll
-            for (int k = 0; k < S / 2; ++k) {
-                const float4 v = bc[g & 1][i][k];
-                h[2 * k] = fmaf(__builtin_amdgcn_exp2f(dtv * A2[2 * k]), h[2 * k], dxv * v.x);
-                h[2 * k + 1] = fmaf(__builtin_amdgcn_exp2f(dtv * A2[2 * k + 1]), h[2 * k + 1], dxv * v.y);
-                if (MODE == kFull) acc = fmaf(v.w, h[2 * k + 1], fmaf(v.z, h[2 * k], acc));
+                for (int k = 0; k < S / 2; ++k) {
+                    const float4 w = v[g & 1][i][k];
+                    h[2 * k] = fmaf(__builtin_amdgcn_exp2f(dt * A2[2 * k]), h[2 * k], dx * w.x);
+                    h[2 * k + 1] = fmaf(__builtin_amdgcn_exp2f(dt * A2[2 * k + 1]), h[2 * k + 1], dx * w.y);
+                    if (!ENDS) acc = fmaf(w.w, h[2 * k + 1], k ? fmaf(w.z, h[2 * k], acc) : w.z * h[2 * k]);
+                }
+                // the sum is done here: left alone, the compiler moves the sums of the two
+                // forms of this loop behind both of them and holds every step's states
+                if (!ENDS) asm volatile("" : "+v"(acc));
             }
-            // the sum is done here: left alone, the compiler moves the sums of the two
-            // forms of this loop behind both of them and holds every step's states
-            // (hundreds of registers)
-            if (MODE == kFull) asm volatile("" : "+v"(acc));
-            share = acc;
-            collect(t);
+            share[t & 3] = acc;
+            if (!ENDS && (t & 3) == 3)
+                put_sums(ysum, t >> 2, quad_sums(share[0], share[1], share[2], share[3], odd, high), c, p);
         }
     }
 }
@@ -96,32 +79,32 @@ struct Split {
     float* starts;    // [S, H, Np]: copy of the initial states (x_out may be x_in)
 };
 
-template <class T, int S, bool ROWS, Mode MODE>
+// ENDS: the first launch of a split call, every chunk's end state and sum of dt
+template <class T, int S, Order O, bool ENDS>
 __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, Split sp) {
-    constexpr bool ENDS = MODE == kEnds, FULL = MODE == kFull;
-    using St = Stage<T, S>;
-    __shared__ __attribute__((aligned(16))) float lds[2][kTile * St::kRow];
+    constexpr int kRow = Stage<T, S>::kRow;
+    __shared__ __attribute__((aligned(16))) float lds[kTile * kRow];
+    __shared__ __attribute__((aligned(16))) float2 steps[kTile * kChannels];
+    __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kSumRow];
 
     const int cb = blockIdx.x % sp.blocks;
     const int64_t item = blockIdx.x / sp.blocks;
     Item it;
     if (!find_item(a.q, item, sp.Q, it) || it.state < 0) return;
-    const int beg = it.beg + it.c * sp.Q;
-    const int end = min((int64_t)it.end, (int64_t)beg + sp.Q);
+    const int64_t beg = it.beg + (int64_t)it.c * sp.Q;
+    const int64_t end = min((int64_t)it.end, beg + sp.Q);
     const int chunks = chunks_of(it.end - it.beg, sp.Q);
     if (it.c >= chunks || (ENDS && it.c + 1 == chunks)) return;
 
     const Place l = place_of(cb, sp.per_group, a.H, a.G);
+    const Mover<O> m(l.tid, l.valid);
     const int p = l.p, N = (int)a.N;
-    const bool odd = p & 1, high = p & 2, upper = p & 4;
     float A2[S], h[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
         A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : 0.0f;
         h[j] = 0.0f;
     }
-    const float bias = a.delta_bias ? a.delta_bias[l.h] : 0.0f;
-    const float Dv = a.D ? a.D[l.h] : 0.0f;
     const int64_t wrow = (int64_t)l.h * (8 * S) + p * S;  // in a workspace row [H, Np]
     const int64_t wstep = a.H * (8 * S);
 
@@ -147,46 +130,32 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         }
     }
 
-    // bases at the tile's first step, the same in the whole wave, and the lanes'
-    // distances from them in bytes (the strides' limits keep these below 2^32)
-    constexpr uint32_t kE = sizeof(T);
-    const uint32_t q0 = step_of<ROWS>(p, 0);
-    auto base = [&](const View3& v) {
-        return (char*)v.data + (it.row * v.sb + l.w0 * v.sh + beg * v.sl) * (int64_t)kE;
-    };
-    auto offset = [&](const View3& v) { return (l.dh * (uint32_t)v.sh + q0 * (uint32_t)v.sl) * kE; };
-    const bool gate = FULL && a.z.data;
+    const bool gate = !ENDS && a.z.data;
     const View3& gv = gate ? a.z : a.u;  // without a gate u once more, unused: the loads need no branch
-    const char *up = base(a.u), *dp = base(a.delta), *zp = base(gv);
-    char* yp = base(a.y);
-    const uint32_t uo = offset(a.u), dof = offset(a.delta), zo = offset(gv), yo = offset(a.y);
-    const uint32_t us = (uint32_t)a.u.sl * 4 * kE, ds = (uint32_t)a.delta.sl * 4 * kE,
-                   zs = (uint32_t)gv.sl * 4 * kE, ys = (uint32_t)a.y.sl * 4 * kE;
-    const char* Bp = (const char*)a.B.data + (it.row * a.B.sb + l.g * a.B.sg + beg * a.B.sl) * (int64_t)kE;
-    const char* Cp = (const char*)a.C.data + (it.row * a.C.sb + l.g * a.C.sg + beg * a.C.sl) * (int64_t)kE;
-    const uint32_t bs = (uint32_t)a.B.sl * 4 * kE, cs = (uint32_t)a.C.sl * 4 * kE;
-    St stage;
-    stage.init(a.B, a.C, N, l.tid);
+    const T* up = m.template at<const T>(a.u, it.row, l, beg);
+    const T* dp = m.template at<const T>(a.delta, it.row, l, beg);
+    const T* zp = m.template at<const T>(gv, it.row, l, beg);
+    T* yp = m.template at<T>(a.y, it.row, l, beg);
+    const T* Bp = (const T*)a.B.data + it.row * a.B.sb + l.g * a.B.sg + beg * a.B.sl;
+    const T* Cp = (const T*)a.C.data + it.row * a.C.sb + l.g * a.C.sg + beg * a.C.sl;
+    Stage<T, S> stage(a.B, N, l.tid);
+    float bias[kOwn], Dv[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int64_t hh = l.first + min(max(m.channel(i), 0), l.valid - 1);
+        bias[i] = a.delta_bias ? a.delta_bias[hh] : 0.0f;
+        Dv[i] = a.D ? a.D[hh] : 0.0f;
+    }
 
     T ur[kOwn], dr[kOwn], zr[kOwn];
-    auto load_tile = [&]() {
-        load_own<T, ROWS>(ur, up, uo, us);
-        load_own<T, ROWS>(dr, dp, dof, ds);
-        if (FULL) load_own<T, ROWS>(zr, zp, zo, zs);
-        stage.template load<true, FULL>(Bp, Cp);
-    };
-    auto advance = [&](uint32_t go) {  // by 4 go steps
-        up += (uint64_t)us * go, dp += (uint64_t)ds * go, zp += (uint64_t)zs * go;
-        Bp += (uint64_t)bs * go, Cp += (uint64_t)cs * go;
-    };
-    float dt[2][kOwn], dx[2][kOwn], uf[kOwn], zf[kOwn], sum = 0.0f;
-    auto prepare = [&](int nt) {  // the lane's own steps, then all of the channel's
+    float uf[kOwn], zf[kOwn], sum[kOwn] = {};
+    auto prepare = [&](int nt) {  // the loaded tile into LDS
         float d[kOwn];
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
             uf[i] = to_f(ur[i]);
-            if (FULL) zf[i] = to_f(zr[i]);
-            d[i] = to_f(dr[i]) + bias;
+            if (!ENDS) zf[i] = to_f(zr[i]);
+            d[i] = to_f(dr[i]) + bias[i];
         }
         if (a.softplus) {
 #pragma unroll
@@ -194,72 +163,84 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         }
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
-            if (ENDS) sum += step_of<ROWS>(p, i) < nt ? d[i] : 0.0f;
-            both_halves(d[i], dt[0][i], dt[1][i]);
-            both_halves(d[i] * uf[i], dx[0][i], dx[1][i]);
+            if (ENDS) sum[i] += m.step(i) < nt ? d[i] : 0.0f;
+            if (m.has(i, l.valid)) steps[m.step(i) * kChannels + m.channel(i)] = make_float2(d[i], d[i] * uf[i]);
         }
+        stage.template store<true, !ENDS>(lds, nt);
+        __syncthreads();
     };
-    auto finish = [&](const float (&s)[2][kOwn], int nt) {  // y of the lane's own steps
+    auto finish = [&](int nt) {  // y of the tile
         float yv[kOwn];
+        get_sums<O>(yv, ysum, m);
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) yv[i] = fmaf(Dv, uf[i], half_sums(s[0][i], s[1][i], upper));
+        for (int i = 0; i < kOwn; ++i) yv[i] = fmaf(Dv[i], uf[i], yv[i]);
         if (gate) {
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) yv[i] *= silu_f<kFine<T>>(zf[i]);
         }
-        if (l.live) store_own<T, ROWS>(yv, yp, yo, ys, nt, p);
+        if (a.y.data) m.template store<T>(yv, yp, a.y, l.valid, nt);
     };
 
     float* saved = !ENDS && a.saved && l.live
                        ? a.saved + (saved_row(a.q, it) + (beg - it.beg) / kTile) * wstep + wrow
                        : nullptr;
-    const int whole = max(0, end - beg) / kTile, rest = max(0, end - beg) % kTile;
-    int buf = 0;
+    const int len = (int)max((int64_t)0, end - beg), whole = len / kTile, rest = len % kTile;
     if (whole > 0) {
-        load_tile();
-        stage.template store<true, FULL>(lds[0]);
-        __syncthreads();
+        m.template load<T>(ur, up, a.u, l.valid);
+        m.template load<T>(dr, dp, a.delta, l.valid);
+        if (!ENDS) m.template load<T>(zr, zp, gv, l.valid);
+        stage.template load<true, !ENDS>(a.B, a.C, Bp, Cp, kTile);
     }
     for (int k = 0; k < whole; ++k) {
         prepare(kTile);
-        // the next whole tile's loads fly while this one is computed (the last one
-        // loads itself again: a branch here would make them wait)
-        advance(k + 1 < whole ? kTile / 4 : 0);
-        load_tile();
+        // the next whole tile's loads fly while this one is run (the last one loads
+        // itself again: a branch here would make them wait)
+        const int64_t go = k + 1 < whole ? kTile : 0;
+        up += go * a.u.sl, dp += go * a.delta.sl, zp += go * gv.sl, Bp += go * a.B.sl, Cp += go * a.C.sl;
+        m.template load<T>(ur, up, a.u, l.valid);
+        m.template load<T>(dr, dp, a.delta, l.valid);
+        if (!ENDS) m.template load<T>(zr, zp, gv, l.valid);
+        stage.template load<true, !ENDS>(a.B, a.C, Bp, Cp, kTile);
         __builtin_amdgcn_sched_barrier(0);  // left alone, the compiler moves the loads behind the tile
         if (saved) {
             store_states<S>(h, saved);
             saved += wstep;
         }
-        float s[2][kOwn];
-        run_tile<S, ROWS, MODE, false>(h, A2, dt, dx, lds[buf] + p * 4, kTile, odd, high, s);
-        if (FULL) finish(s, kTile);
-        yp += (uint64_t)ys * (kTile / 4);
-        buf ^= 1;
-        stage.template store<true, FULL>(lds[buf]);
+        run_tile<S, ENDS, false>(h, A2, lds + p * 4, steps + l.c, kTile, ysum, l.c, p);
         __syncthreads();
+        if (!ENDS) finish(kTile);
+        yp += kTile * a.y.sl;
     }
     if (rest > 0) {
-        if (whole > 0) advance(kTile / 4);
-        load_part<T, ROWS>(ur, up, uo, us, rest, p);
-        load_part<T, ROWS>(dr, dp, dof, ds, rest, p);
-        if (FULL) load_part<T, ROWS>(zr, zp, zo, zs, rest, p);
-        stage.template load_part<true, FULL>(Bp, Cp, rest);
-        buf ^= 1;
-        stage.template store<true, FULL>(lds[buf]);
-        __syncthreads();
+        const int64_t go = whole > 0 ? kTile : 0;
+        up += go * a.u.sl, dp += go * a.delta.sl, zp += go * gv.sl, Bp += go * a.B.sl, Cp += go * a.C.sl;
+        m.template load_part<T>(ur, up, a.u, l.valid, rest);
+        m.template load_part<T>(dr, dp, a.delta, l.valid, rest);
+        if (!ENDS) m.template load_part<T>(zr, zp, gv, l.valid, rest);
+        stage.template load<true, !ENDS>(a.B, a.C, Bp, Cp, rest);
         prepare(rest);
         if (saved) store_states<S>(h, saved);
-        float s[2][kOwn];
-        run_tile<S, ROWS, MODE, true>(h, A2, dt, dx, lds[buf] + p * 4, rest, odd, high, s);
-        if (FULL) finish(s, rest);
+        run_tile<S, ENDS, true>(h, A2, lds + p * 4, steps + l.c, rest, ysum, l.c, p);
+        __syncthreads();
+        if (!ENDS) finish(rest);
     }
 
     if (ENDS) {
-        sum = lane_sum(sum);
-        if (l.live) {
-            store_states<S>(h, sp.ends + item * wstep + wrow);
-            if (p == 0) sp.sums[item * a.H + l.h] = sum;
+        if (l.live) store_states<S>(h, sp.ends + item * wstep + wrow);
+        // the channels' sums of dt, over the threads that moved their steps
+        __syncthreads();
+        float* const part = reinterpret_cast<float*>(steps);
+        constexpr int kParts = O == kRows ? 8 : kTile;
+#pragma unroll
+        for (int i = 1; i < (O == kRows ? kOwn : 1); ++i) sum[0] += sum[i];
+#pragma unroll
+        for (int i = 0; i < (O == kRows ? 1 : kOwn); ++i)
+            if (m.has(i, l.valid)) part[(O == kRows ? l.tid & 7 : m.t) * kChannels + m.channel(i)] = sum[i];
+        __syncthreads();
+        if (l.tid < l.valid) {
+            float s = 0.0f;
+            for (int k = 0; k < kParts; ++k) s += part[k * kChannels + l.tid];
+            sp.sums[item * a.H + l.first + l.tid] = s;
         }
     } else if (l.live && a.x_out && it.c + 1 == chunks) {
 #pragma unroll
@@ -305,23 +286,27 @@ Plan plan(const Seqs& q, int64_t H, int64_t N, int64_t G) {
     return p;
 }
 
-template <class T, int S, bool ROWS>
+template <class T, int S, Order O>
 hipError_t launch_as(const ScanArgs& a, const Plan& p, hipStream_t s) {
     const int64_t wgs = p.items * p.sp.blocks;
     if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    if (p.split) scan_kernel<T, S, ROWS, kEnds><<<dim3((unsigned)wgs), dim3(kScanThreads), 0, s>>>(a, p.sp);
-    if (a.y.data)
-        scan_kernel<T, S, ROWS, kFull><<<dim3((unsigned)wgs), dim3(kScanThreads), 0, s>>>(a, p.sp);
-    else
-        scan_kernel<T, S, ROWS, kStates><<<dim3((unsigned)wgs), dim3(kScanThreads), 0, s>>>(a, p.sp);
+    const dim3 grid((unsigned)wgs), wg(kScanThreads);
+    if (p.split) scan_kernel<T, S, O, true><<<grid, wg, 0, s>>>(a, p.sp);
+    scan_kernel<T, S, O, false><<<grid, wg, 0, s>>>(a, p.sp);
     return hipGetLastError();
 }
 
+template <class T, int S>
+hipError_t launch_in(const ScanArgs& a, const Plan& p, Order o, hipStream_t s) {
+    return o == kRows ? launch_as<T, S, kRows>(a, p, s)
+         : o == kTokens ? launch_as<T, S, kTokens>(a, p, s) : launch_as<T, S, kAny>(a, p, s);
+}
+
 template <class T>
-hipError_t launch_of(const ScanArgs& a, const Plan& p, bool rows, hipStream_t s) {
-    if (a.N <= 16) return rows ? launch_as<T, 2, true>(a, p, s) : launch_as<T, 2, false>(a, p, s);
-    if (a.N <= 32) return rows ? launch_as<T, 4, true>(a, p, s) : launch_as<T, 4, false>(a, p, s);
-    return rows ? launch_as<T, 8, true>(a, p, s) : launch_as<T, 8, false>(a, p, s);
+hipError_t launch_of(const ScanArgs& a, const Plan& p, Order o, hipStream_t s) {
+    if (a.N <= 16) return launch_in<T, 2>(a, p, o, s);
+    if (a.N <= 32) return launch_in<T, 4>(a, p, o, s);
+    return launch_in<T, 8>(a, p, o, s);
 }
 
 }  // namespace
@@ -345,11 +330,11 @@ hipError_t launch_scan(int dtype, const ScanArgs& a, void* ws, hipStream_t s) {
     } else {
         p.sp.ends = p.sp.sums = p.sp.starts = nullptr;
     }
-    // steps contiguous in every tensor: the vector loads and stores of "rows"
-    const bool rows = a.u.sl == 1 && a.delta.sl == 1 && (!a.z.data || a.z.sl == 1) && (!a.y.data || a.y.sl == 1);
-    if (dtype == SSM_F32) return launch_of<float>(a, p, rows, s);
-    if (dtype == SSM_BF16) return launch_of<bf16>(a, p, rows, s);
-    return launch_of<f16>(a, p, rows, s);
+    const View3* views[] = {&a.u, &a.delta, &a.z, &a.y};
+    const Order o = order_of(views, 4, a.H / a.G);
+    if (dtype == SSM_F32) return launch_of<float>(a, p, o, s);
+    if (dtype == SSM_BF16) return launch_of<bf16>(a, p, o, s);
+    return launch_of<f16>(a, p, o, s);
 }
 
 }  // namespace ssm

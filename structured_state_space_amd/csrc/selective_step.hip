@@ -9,8 +9,8 @@
 // Both are bound by the state's bytes, read and written once: 8 N bytes per
 // channel for the scan.  A quad of lanes holds a channel's states, four (16
 // bytes) per lane and block of 16, so a wave reads whole lines; a workgroup
-// takes kRows sequences of 64 channels when there are many, which reads A once
-// for all of them and keeps kRows state loads in flight.
+// takes kBatch sequences of 64 channels when there are many, which reads A once
+// for all of them and keeps kBatch state loads in flight.
 #include "selective.hpp"
 
 namespace ssm {
@@ -170,18 +170,18 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a, int64_t 
     }
 }
 
-constexpr int kRows = 4;
+constexpr int kBatch = 4;
 
 template <class T, int NB, bool W4>
 hipError_t step_as(const StepArgs& a, hipStream_t s) {
     const int64_t blocks = (a.H + 63) / 64;
     // four sequences per workgroup once that still gives every CU its workgroups
-    const int R = NB <= 2 && a.Bsz / kRows * blocks >= 1024 ? kRows : 1;
+    const int R = NB <= 2 && a.Bsz / kBatch * blocks >= 1024 ? kBatch : 1;
     const int64_t wgs = (a.Bsz + R - 1) / R * blocks;
     if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     if constexpr (NB <= 2) {
-        if (R == kRows) {
-            step_kernel<T, NB, W4, kRows><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, (int)blocks);
+        if (R == kBatch) {
+            step_kernel<T, NB, W4, kBatch><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, (int)blocks);
             return hipGetLastError();
         }
     }
