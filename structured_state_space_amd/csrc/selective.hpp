@@ -298,19 +298,44 @@ __device__ __forceinline__ float quad_sums(float p0, float p1, float p2, float p
     const float b = (odd ? p3 : p2) + dpp<0xB1>(odd ? p2 : p3);
     return (high ? b : a) + dpp<0x4E>(high ? a : b);
 }
-// sums over a channel's lanes, by step: lane p leaves its quad's sum of four steps
-// at [step][channel][quad] of `to` (row kSumRow, which spreads a wave's writes over
-// the banks), the mover adds the two quads'
-constexpr int kSumRow = kChannels * 2 + 16;
-__device__ __forceinline__ void put_sums(float* to, int g, float s, int c, int p) {
-    to[(4 * g + (p & 3)) * kSumRow + c * 2 + (p >> 2)] = s;
+// Pairs of floats per step and channel in LDS: {dt, dt u} on the way to the
+// running lanes, the two quads' sums over a channel's states on the way back.
+// Four floats of room behind every eighth channel and the row's length keep both
+// roles' accesses (16 bytes of two channels at a time, 16 threads per step; eight
+// bytes of eight channels; four bytes of four steps) off each other's banks.
+constexpr int kPairRow = 176;
+__device__ __forceinline__ int pair_at(int c) { return c * 2 + (c >> 3) * 4; }
+// lane p leaves its quad's sum of step 4 g + (p & 3); the mover adds the two quads'
+__device__ __forceinline__ void put_sums(float* to, int g, float s, int c, int p, bool add = false) {
+    float* at = to + (4 * g + (p & 3)) * kPairRow + pair_at(c) + (p >> 2);
+    *at = add ? *at + s : s;
 }
 template <Order O>
 __device__ __forceinline__ void get_sums(float (&r)[kOwn], const float* from, const Mover<O>& m) {
+    if (O == kTokens && m.c >= 0 && (m.c & 3) == 0) {
+        const float4* v = reinterpret_cast<const float4*>(from + m.t * kPairRow + pair_at(m.c));
+        const float4 x = v[0], y = v[1];
+        r[0] = x.x + x.y, r[1] = x.z + x.w, r[2] = y.x + y.y, r[3] = y.z + y.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-        const float2 v = *reinterpret_cast<const float2*>(from + m.step(i) * kSumRow + max(m.channel(i), 0) * 2);
-        r[i] = v.x + v.y;
+        for (int i = 0; i < kOwn; ++i) {
+            const float2 v = *reinterpret_cast<const float2*>(from + m.step(i) * kPairRow + pair_at(max(m.channel(i), 0)));
+            r[i] = v.x + v.y;
+        }
+    }
+}
+template <Order O>
+__device__ __forceinline__ void put_pairs(float* to, const float (&x)[kOwn], const float (&y)[kOwn], const Mover<O>& m,
+                                          int valid) {
+    if (O == kTokens && m.c >= 0 && (m.c & 3) == 0) {
+        float4* v = reinterpret_cast<float4*>(to + m.t * kPairRow + pair_at(m.c));
+        v[0] = make_float4(x[0], y[0], x[1], y[1]);
+        v[1] = make_float4(x[2], y[2], x[3], y[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            if (m.has(i, valid))
+                *reinterpret_cast<float2*>(to + m.step(i) * kPairRow + pair_at(m.channel(i))) = make_float2(x[i], y[i]);
     }
 }
 // a lane's S states of a row [Np] of a workspace

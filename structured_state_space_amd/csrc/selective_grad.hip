@@ -57,6 +57,10 @@ struct GradSplit {
     float* part_d;  // [items, 2, H]: dD, ddelta_bias
 };
 
+// a row of `steps`: a place free behind every fourth channel, as in the rows of pairs
+constexpr int kStepRow = kChannels / 4 * 5;
+__device__ __forceinline__ int step_at(int c) { return c + (c >> 2); }
+
 // ENDS: the first launch of a split call, what every chunk hands to the one before it
 template <class T, int S, Order O, bool ENDS>
 __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, GradSplit sp) {
@@ -64,12 +68,14 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
     constexpr int kRow = Stage<T, S>::kRow;
     __shared__ __attribute__((aligned(16))) float lds[kTile * kRow];
     // {dt, dt u, p, 0} of every step and channel; p is the gradient behind the gate
-    __shared__ __attribute__((aligned(16))) float4 steps[kTile * kChannels];
+    __shared__ __attribute__((aligned(16))) float4 steps[kTile * kStepRow];
     // sums over a channel's states: of C x, of g B, of A a g x
-    __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kSumRow];
-    __shared__ __attribute__((aligned(16))) float gsum[ENDS ? 4 : kTile * kSumRow];
-    __shared__ __attribute__((aligned(16))) float asum[ENDS ? 4 : kTile * kSumRow];
+    __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kPairRow];
+    __shared__ __attribute__((aligned(16))) float gsum[ENDS ? 4 : kTile * kPairRow];
+    __shared__ __attribute__((aligned(16))) float asum[ENDS ? 4 : kTile * kPairRow];
     __shared__ float red[ENDS ? 1 : 8 * kTile * 32];  // [wave][step][B or C][16 states]: sums over a wave's channels
+
+    __shared__ float2 par[kChannels];  // {delta_bias, D}
 
     const int cb = blockIdx.x % sp.blocks;
     const int64_t item = blockIdx.x / sp.blocks;
@@ -130,15 +136,13 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
         const T* Cp = (const T*)a.C.data + it.row * a.C.sb + l.g * a.C.sg + last * a.C.sl;
         Stage<T, S> stage(a.B, N, l.tid);
         const float* sv = ENDS ? nullptr : ga.saved + (saved_row(a.q, it) + (last - it.beg) / kTile) * wstep + wrow;
-        float bias[kOwn], Dv[kOwn];
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int64_t hh = l.first + min(max(m.channel(i), 0), l.valid - 1);
-            bias[i] = a.delta_bias ? a.delta_bias[hh] : 0.0f;
-            Dv[i] = a.D ? a.D[hh] : 0.0f;
+        if (l.tid < kChannels) {  // (in registers they would take eight)
+            const int64_t hh = l.first + min(l.tid, l.valid - 1);
+            par[l.tid] = make_float2(a.delta_bias ? a.delta_bias[hh] : 0.0f, a.D ? a.D[hh] : 0.0f);
         }
+        __syncthreads();
         if (l.valid < kChannels) {  // channels that are not there: steps of length zero without gradient
-            for (int e = l.tid; e < kTile * kChannels; e += kScanThreads) steps[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int e = l.tid; e < kTile * kStepRow; e += kScanThreads) steps[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             __syncthreads();
         }
 
@@ -160,7 +164,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
                     u[i] = to_f(ur[i]);
-                    dt[i] = to_f(dr[i]) + bias[i];
+                    dt[i] = to_f(dr[i]) + par[min(max(m.channel(i), 0), kChannels - 1)].x;
                     po[i] = to_f(gr[i]);
                     slope[i] = 1.0f;
                     zsl[i] = to_f(zr[i]);
@@ -184,7 +188,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     po[i] = in ? po[i] : 0.0f;
                     if (ENDS) dtsum[i] += dt[i];
                     if (m.has(i, l.valid))
-                        steps[m.step(i) * kChannels + m.channel(i)] = make_float4(dt[i], dt[i] * u[i], po[i], 0.0f);
+                        steps[m.step(i) * kStepRow + step_at(m.channel(i))] = make_float4(dt[i], dt[i] * u[i], po[i], 0.0f);
                 }
                 stage.template store<!ENDS, true>(lds, now);
             }
@@ -212,11 +216,11 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
             }
             __builtin_amdgcn_sched_barrier(0);
             const float4* const bc = reinterpret_cast<const float4*>(lds) + p;
-            const float4* const mine = steps + l.c;
+            const float4* const mine = steps + step_at(l.c);
             if constexpr (ENDS) {
 #pragma unroll
                 for (int t = kTile - 1; t >= 0; --t) {
-                    const float4 d = mine[t * kChannels];
+                    const float4 d = mine[t * kStepRow];
 #pragma unroll
                     for (int k = 0; k < S / 2; ++k) {
                         const float4 v = bc[t * (kRow / 4) + k * 8];
@@ -227,7 +231,6 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                 }
                 __syncthreads();
             } else {
-                float ysh[S > 2 ? 8 : 1], gsh[S > 2 ? 8 : 1], ash[S > 2 ? 8 : 1];  // sums of the pairs before
 #pragma unroll
                 for (int k = 0; k < S / 2; ++k) {
                     // this pair of states through the tile and back
@@ -235,7 +238,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     x[0][0] = h0[2 * k], x[0][1] = h0[2 * k + 1];
 #pragma unroll
                     for (int t = 0; t < kTile; ++t) {
-                        const float2 d = *reinterpret_cast<const float2*>(mine + t * kChannels);
+                        const float2 d = *reinterpret_cast<const float2*>(mine + t * kStepRow);
                         const float4 v = bc[t * (kRow / 4) + k * 8];
                         dec[t][0] = __builtin_amdgcn_exp2f(d.x * A2[2 * k]);
                         dec[t][1] = __builtin_amdgcn_exp2f(d.x * A2[2 * k + 1]);
@@ -244,12 +247,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                         float y = fmaf(v.w, x[t + 1][1], v.z * x[t + 1][0]);
                         asm volatile("" : "+v"(y));  // the sum is done here, not where it is used
                         share[t & 3] = y;
-                        if ((t & 3) == 3) {
-                            float s = quad_sums(share[0], share[1], share[2], share[3], odd, high);
-                            if (k > 0) s += ysh[t >> 2];
-                            if (k + 1 < S / 2) ysh[S > 2 ? t >> 2 : 0] = s;
-                            else put_sums(ysum, t >> 2, s, l.c, p);
-                        }
+                        if ((t & 3) == 3)
+                            put_sums(ysum, t >> 2, quad_sums(share[0], share[1], share[2], share[3], odd, high), l.c, p,
+                                     k > 0);
                     }
                     // on the way back B, C and the steps are read anew: kept from the way
                     // forth they would take eight registers per step
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     float gshare[4], later = 0.0f;
 #pragma unroll
                     for (int t = kTile - 1; t >= 0; --t) {
-                        const float4 d = mine[t * kChannels + again];
+                        const float4 d = mine[t * kStepRow + again];
                         const float4 v = bc2[t * (kRow / 4) + k * 8];
                         const float g0 = fmaf(v.z, d.z, carry[2 * k]), g1 = fmaf(v.w, d.z, carry[2 * k + 1]);
                         float gx = fmaf(g1, v.y, g0 * v.x);
@@ -282,15 +282,10 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                         share[t & 3] = dd;
                         gshare[t & 3] = gx;
                         if ((t & 3) == 0) {
-                            float sg = quad_sums(gshare[0], gshare[1], gshare[2], gshare[3], odd, high);
-                            float sa = quad_sums(share[0], share[1], share[2], share[3], odd, high);
-                            if (k > 0) sg += gsh[S > 2 ? t >> 2 : 0], sa += ash[S > 2 ? t >> 2 : 0];
-                            if (k + 1 < S / 2) {
-                                gsh[S > 2 ? t >> 2 : 0] = sg, ash[S > 2 ? t >> 2 : 0] = sa;
-                            } else {
-                                put_sums(gsum, t >> 2, sg, l.c, p);
-                                put_sums(asum, t >> 2, sa, l.c, p);
-                            }
+                            put_sums(gsum, t >> 2, quad_sums(gshare[0], gshare[1], gshare[2], gshare[3], odd, high),
+                                     l.c, p, k > 0);
+                            put_sums(asum, t >> 2, quad_sums(share[0], share[1], share[2], share[3], odd, high), l.c, p,
+                                     k > 0);
                         }
                     }
                     __syncthreads();
@@ -312,10 +307,11 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                 get_sums<O>(ys, ysum, m);
                 get_sums<O>(gs, gsum, m);
                 get_sums<O>(as, asum, m);
-                float dt[kOwn], po[kOwn];
+                float dt[kOwn], po[kOwn], Dv[kOwn];
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
-                    const float4 d = steps[m.step(i) * kChannels + max(0, min(m.channel(i), l.valid - 1))];
+                    Dv[i] = par[min(max(m.channel(i), 0), kChannels - 1)].y;
+                    const float4 d = steps[m.step(i) * kStepRow + step_at(max(0, min(m.channel(i), l.valid - 1)))];
                     dt[i] = d.x, po[i] = d.z;
                     o[i] = fmaf(Dv[i], po[i], dt[i] * gs[i]);
                 }

@@ -25,7 +25,7 @@ namespace {
 // `bc` is the lane's B and C of the tile, `step` its channel's {dt, dt u}; both come
 // from LDS two steps ahead of their use.
 template <int S, bool ENDS, bool GUARD>
-__device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], const float* bc, const float2* step,
+__device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], const float* bc, const float* step,
                                          int nt, float* ysum, int c, int p) {
     constexpr int kRow = Stage<float, S>::kRow, kGroup = S == 2 ? 2 : 1;
     const bool odd = p & 1, high = p & 2;
@@ -35,7 +35,7 @@ __device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], co
     auto fetch = [&](int g) {
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-            d[g & 1][i] = step[(g * kGroup + i) * kChannels];
+            d[g & 1][i] = *reinterpret_cast<const float2*>(step + (g * kGroup + i) * kPairRow);
 #pragma unroll
             for (int k = 0; k < S / 2; ++k)
                 v[g & 1][i][k] = *reinterpret_cast<const float4*>(bc + (g * kGroup + i) * kRow + k * 32);
@@ -84,8 +84,8 @@ template <class T, int S, Order O, bool ENDS>
 __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(ScanArgs a, Split sp) {
     constexpr int kRow = Stage<T, S>::kRow;
     __shared__ __attribute__((aligned(16))) float lds[kTile * kRow];
-    __shared__ __attribute__((aligned(16))) float2 steps[kTile * kChannels];
-    __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kSumRow];
+    __shared__ __attribute__((aligned(16))) float steps[kTile * kPairRow];
+    __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kPairRow];
 
     const int cb = blockIdx.x % sp.blocks;
     const int64_t item = blockIdx.x / sp.blocks;
@@ -161,11 +161,13 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) d[i] = softplus_f<kFine<T>>(d[i]);
         }
+        float dx[kOwn];
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
             if (ENDS) sum[i] += m.step(i) < nt ? d[i] : 0.0f;
-            if (m.has(i, l.valid)) steps[m.step(i) * kChannels + m.channel(i)] = make_float2(d[i], d[i] * uf[i]);
+            dx[i] = d[i] * uf[i];
         }
+        put_pairs<O>(steps, d, dx, m, l.valid);
         stage.template store<true, !ENDS>(lds, nt);
         __syncthreads();
     };
@@ -206,7 +208,7 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             store_states<S>(h, saved);
             saved += wstep;
         }
-        run_tile<S, ENDS, false>(h, A2, lds + p * 4, steps + l.c, kTile, ysum, l.c, p);
+        run_tile<S, ENDS, false>(h, A2, lds + p * 4, steps + pair_at(l.c), kTile, ysum, l.c, p);
         __syncthreads();
         if (!ENDS) finish(kTile);
         yp += kTile * a.y.sl;
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         stage.template load<true, !ENDS>(a.B, a.C, Bp, Cp, rest);
         prepare(rest);
         if (saved) store_states<S>(h, saved);
-        run_tile<S, ENDS, true>(h, A2, lds + p * 4, steps + l.c, rest, ysum, l.c, p);
+        run_tile<S, ENDS, true>(h, A2, lds + p * 4, steps + pair_at(l.c), rest, ysum, l.c, p);
         __syncthreads();
         if (!ENDS) finish(rest);
     }
@@ -229,7 +231,7 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         if (l.live) store_states<S>(h, sp.ends + item * wstep + wrow);
         // the channels' sums of dt, over the threads that moved their steps
         __syncthreads();
-        float* const part = reinterpret_cast<float*>(steps);
+        float* const part = steps;
         constexpr int kParts = O == kRows ? 8 : kTile;
 #pragma unroll
         for (int i = 1; i < (O == kRows ? kOwn : 1); ++i) sum[0] += sum[i];
