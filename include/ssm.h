@@ -354,8 +354,8 @@ int ssm_hippo_dplr(int kind, int64_t N, double theta,
  *     transpose needs no copy; any non-negative strides work, and two orders are
  *     fast: steps contiguous ([Bsz,H,L] as everywhere in this library) and
  *     channels contiguous ([Bsz,L,H] as a projection writes it).  Strides along
- *     channels and states must be below 2^25 elements, along steps below 2^24
- *     (else SSM_ERR_UNSUPPORTED).  Outputs must not overlap inputs or each other,
+ *     channels, states and steps must be below 2^23 elements (else
+ *     SSM_ERR_UNSUPPORTED).  Outputs must not overlap inputs or each other,
  *     and no two elements of an output may share an address.
  *   - Sequences.  Without `offsets` there are S = Bsz of them, one per batch
  *     row, each of L steps or of lengths[s] <= L (device int32 [S], nullable).

@@ -190,59 +190,83 @@ __device__ __forceinline__ Place place_of(int cb, int per_group, int64_t H, int6
 // c + (kRows ? 0 : i) of the block.  With kTokens a vector that would end behind the
 // last channel is moved back to end with it (c may be negative in a block of fewer
 // than four; a group has at least four), so that some elements are moved twice.
+// A tensor is addressed by a base that is the same in the whole workgroup and
+// moves from tile to tile, and a 32-bit distance in bytes per thread, which the
+// strides' limits keep below 2^32.  (Pointers per thread took twice the registers;
+// the backward pass then kept some in scratch memory, and waiting for those loads
+// meant waiting for the next tile's.)
 template <Order O>
 struct Mover {
-    int t, c;
+    int t, c, low, most;
     __device__ __forceinline__ Mover(int tid, int valid) {
         t = O == kRows ? (tid & 7) * 4 : tid >> 4;
         c = O == kRows ? tid >> 3 : (tid & 15) * 4;
+        low = O == kTokens ? min(0, valid - 4) : 0;
         if (O == kTokens) c = min(c, valid - 4);
+        most = O == kAny ? min(kOwn - 1, max(0, valid - 1 - c)) : kOwn - 1;
+        cc = O == kTokens ? c - low : min(c, valid - 1);
     }
     __device__ __forceinline__ int step(int i) const { return t + (O == kRows ? i : 0); }
     __device__ __forceinline__ int channel(int i) const { return c + (O == kRows ? 0 : i); }
     __device__ __forceinline__ bool has(int i, int valid) const {
         return channel(i) >= 0 && channel(i) < valid;
     }
-    // the thread's first element in the tile whose first step is `step0`
     template <class T>
-    __device__ __forceinline__ T* at(const View3& v, int64_t row, const Place& l, int64_t step0) const {
-        const int cc = O == kTokens ? c : min(c, l.valid - 1);
-        return (T*)v.data + row * v.sb + (l.first + cc) * v.sh + (step0 + t) * v.sl;
+    __device__ __forceinline__ char* base(const View3& v, int64_t row, const Place& l, int64_t step0) const {
+        return (char*)v.data + (row * v.sb + (l.first + low) * v.sh + step0 * v.sl) * (int64_t)sizeof(T);
     }
     template <class T>
-    __device__ __forceinline__ void load(T (&r)[kOwn], const T* p, const View3& v, int valid) const {
-        if constexpr (O == kAny) {
-            const int most = max(0, valid - 1 - c);  // channels behind the last one read it again
+    __device__ __forceinline__ uint32_t offset(const View3& v) const {
+        return ((uint32_t)cc * (uint32_t)v.sh + (uint32_t)t * (uint32_t)v.sl) * (uint32_t)sizeof(T);
+    }
+    template <class T>
+    __device__ __forceinline__ void load(T (&r)[kOwn], const char* p, uint32_t off, const View3& v) const {
+        if constexpr (O == kAny) {  // channels behind the last one read it again
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) r[i] = p[min(i, most) * v.sh];
+            for (int i = 0; i < kOwn; ++i)
+                r[i] = *reinterpret_cast<const T*>(p + (off + min(i, most) * (uint32_t)v.sh * (uint32_t)sizeof(T)));
         } else {
-            const Vec4<T> w = *reinterpret_cast<const Vec4<T>*>(p);
+            const Vec4<T> w = *reinterpret_cast<const Vec4<T>*>(p + off);
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) r[i] = w.v[i];
         }
     }
     // where only the tile's first nt steps exist
     template <class T>
-    __device__ __forceinline__ void load_part(T (&r)[kOwn], const T* p, const View3& v, int valid, int nt) const {
-        const int most = O == kAny ? max(0, valid - 1 - c) : kOwn;
+    __device__ __forceinline__ void load_part(T (&r)[kOwn], const char* p, uint32_t off, const View3& v, int nt) const {
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-            r[i] = step(i) < nt ? p[O == kRows ? i : min(i, most) * v.sh] : from_f<T>(0.0f);
+        for (int i = 0; i < kOwn; ++i) {
+            const uint32_t d = O == kRows ? i * (uint32_t)sizeof(T) : min(i, most) * (uint32_t)v.sh * (uint32_t)sizeof(T);
+            r[i] = step(i) < nt ? *reinterpret_cast<const T*>(p + (off + d)) : from_f<T>(0.0f);
+        }
     }
     template <class T>
-    __device__ __forceinline__ void store(const float (&r)[kOwn], T* p, const View3& v, int valid, int nt) const {
+    __device__ __forceinline__ void store(const float (&r)[kOwn], char* p, uint32_t off, const View3& v, int valid,
+                                          int nt) const {
         if (O != kAny && step(O == kRows ? kOwn - 1 : 0) < nt && (O == kTokens ? c >= 0 : c < valid)) {
             Vec4<T> w;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) w.v[i] = from_f<T>(r[i]);
-            *reinterpret_cast<Vec4<T>*>(p) = w;
+            *reinterpret_cast<Vec4<T>*>(p + off) = w;
         } else {
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
-                if (step(i) < nt && has(i, valid)) p[O == kRows ? i : i * v.sh] = from_f<T>(r[i]);
+                if (step(i) < nt && has(i, valid))
+                    *reinterpret_cast<T*>(p + (off + i * (O == kRows ? 1u : (uint32_t)v.sh) * (uint32_t)sizeof(T))) =
+                        from_f<T>(r[i]);
         }
     }
+
+  private:
+    int cc;
 };
+
+// the thread's number, opaque to the compiler: what is worked out from it is worked
+// out here, and not kept in registers from elsewhere
+__device__ __forceinline__ int anew(int tid) {
+    asm volatile("" : "+v"(tid));
+    return tid;
+}
 
 // B and C of a tile on their way to LDS in float32: row t holds, per pair k of a
 // lane's states, the eight lanes' {B, B, C, C}; a thread brings K elements of either
@@ -250,31 +274,50 @@ template <class T, int S>
 struct Stage {
     static constexpr int K = kTile * 8 * S / kScanThreads;  // 1, 2 or 4
     static constexpr int kRow = 16 * S + 4;                 // floats of a row (padded)
-    T b[K], c[K];
+    uint32_t bo[K], co[K];  // distances from the tile's first step in bytes
     int N, tid;
     bool by_time;  // consecutive threads along B's contiguous axis
-    __device__ __forceinline__ Stage(const View4& B, int states, int thread)
-        : N(states), tid(thread), by_time(B.sl == 1) {}
+    __device__ __forceinline__ Stage(const View4& B, const View4& C, int states, int thread)
+        : N(states), tid(thread), by_time(B.sl == 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            int t, n;
+            place(k, t, n);
+            bo[k] = distance(B, t, n), co[k] = distance(C, t, n);
+        }
+    }
     __device__ __forceinline__ void place(int k, int& t, int& n) const {
         const int e = tid + kScanThreads * k;
         t = by_time ? e % kTile : e / (8 * S);
         n = by_time ? e / kTile : e % (8 * S);
     }
-    // the first nt >= 1 steps of the tile at Bp, Cp exist; the others read the last one
+    __device__ __forceinline__ uint32_t distance(const View4& v, int t, int n) const {  // padded states read the last one
+        return ((uint32_t)t * (uint32_t)v.sl + (uint32_t)min(n, N - 1) * (uint32_t)v.sn) * (uint32_t)sizeof(T);
+    }
     template <bool WB, bool WC>
-    __device__ __forceinline__ void load(const View4& B, const View4& C, const T* Bp, const T* Cp, int nt) {
+    __device__ __forceinline__ void load(T (&b)[K], T (&c)[K], const char* Bp, const char* Cp) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (WB) b[k] = *reinterpret_cast<const T*>(Bp + bo[k]);
+            if (WC) c[k] = *reinterpret_cast<const T*>(Cp + co[k]);
+        }
+    }
+    // where only the tile's first nt steps exist: the others read the last one
+    template <bool WB, bool WC>
+    __device__ __forceinline__ void load_part(T (&b)[K], T (&c)[K], const View4& B, const View4& C, const char* Bp,
+                                              const char* Cp, int nt) const {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             int t, n;
             place(k, t, n);
-            const int64_t s = min(t, nt - 1), m = min(n, N - 1);
-            if (WB) b[k] = Bp[s * B.sl + m * B.sn];
-            if (WC) c[k] = Cp[s * C.sl + m * C.sn];
+            t = min(t, nt - 1);
+            if (WB) b[k] = *reinterpret_cast<const T*>(Bp + distance(B, t, n));
+            if (WC) c[k] = *reinterpret_cast<const T*>(Cp + distance(C, t, n));
         }
     }
     // padded states, and steps behind the last one, become zero
     template <bool WB, bool WC>
-    __device__ __forceinline__ void store(float* to, int nt) const {
+    __device__ __forceinline__ void store(const T (&b)[K], const T (&c)[K], float* to, int nt) const {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             int t, n;
@@ -286,6 +329,11 @@ struct Stage {
         }
     }
 };
+// the base of B or C in a tile
+template <class T>
+__device__ __forceinline__ const char* group_base(const View4& v, int64_t row, int g, int64_t step0) {
+    return (const char*)v.data + (row * v.sb + g * v.sg + step0 * v.sl) * (int64_t)sizeof(T);
+}
 
 // lane exchanges (v_*_dpp)
 template <int CTRL>

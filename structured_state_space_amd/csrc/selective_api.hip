@@ -25,10 +25,9 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxStates = 64;
 constexpr int64_t kMaxWidth = 4;
-// a lane's offset from its wave's first channel and step is 32 bits wide: up to
-// 64 states or 16 channels, and 32 steps
-constexpr int64_t kMaxChannelStride = (int64_t)1 << 25;
-constexpr int64_t kMaxStepStride = (int64_t)1 << 24;
+// a thread's distance from its workgroup's first channel (or state) and step is
+// 32 bits wide in bytes: up to 67 channels or 64 states, and 32 steps, of 4 bytes
+constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool type_known(int dtype) { return dtype == SSM_F32 || dtype == SSM_BF16 || dtype == SSM_F16; }
@@ -76,7 +75,7 @@ Seqs sequences_of(int64_t L, int64_t S, bool packed) {
 
 // an output's dimensions of more than one element must not be broadcast
 bool strides_fit(int64_t sb, int64_t sh, int64_t sl) {
-    return sb < ((int64_t)1 << 40) && sh < kMaxChannelStride && sl < kMaxStepStride;
+    return sb < ((int64_t)1 << 40) && sh < kMaxStride && sl < kMaxStride;
 }
 
 int check_view(const ssm_view* v, int dtype, bool required, bool output, const ssm_sequences* q, int64_t H) {

@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
     const ScanArgs& a = ga.f;
     constexpr int kRow = Stage<T, S>::kRow;
     __shared__ __attribute__((aligned(16))) float lds[kTile * kRow];
-    // {dt, dt u, p, 0} of every step and channel; p is the gradient behind the gate
+    // {dt, dt u, p, slope of softplus} of every step and channel; p is the gradient behind the gate
     __shared__ __attribute__((aligned(16))) float4 steps[kTile * kStepRow];
     // sums over a channel's states: of C x, of g B, of A a g x
     __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kPairRow];
@@ -128,13 +128,16 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
         int now = (int)(end - last);                              // and its steps; all others are whole
         const bool gate = a.z.data;
         const View3& gv = gate ? a.z : a.u;  // without a gate u once more, unused
-        const T* up = m.template at<const T>(a.u, it.row, l, last);
-        const T* dp = m.template at<const T>(a.delta, it.row, l, last);
-        const T* zp = m.template at<const T>(gv, it.row, l, last);
-        const T* gp = m.template at<const T>(ga.dy, it.row, l, last);
-        const T* Bp = (const T*)a.B.data + it.row * a.B.sb + l.g * a.B.sg + last * a.B.sl;
-        const T* Cp = (const T*)a.C.data + it.row * a.C.sb + l.g * a.C.sg + last * a.C.sl;
-        Stage<T, S> stage(a.B, N, l.tid);
+        const char* up = m.template base<T>(a.u, it.row, l, last);
+        const char* dp = m.template base<T>(a.delta, it.row, l, last);
+        const char* zp = m.template base<T>(gv, it.row, l, last);
+        const char* gp = m.template base<T>(ga.dy, it.row, l, last);
+        char* dup = m.template base<T>(ga.du, it.row, l, last);
+        char* ddp = m.template base<T>(ga.ddelta, it.row, l, last);
+        char* dzp = m.template base<T>(ga.dz, it.row, l, last);
+        const char* Bp = group_base<T>(a.B, it.row, l.g, last);
+        const char* Cp = group_base<T>(a.C, it.row, l.g, last);
+        T sb[Stage<T, S>::K], sc[Stage<T, S>::K];
         const float* sv = ENDS ? nullptr : ga.saved + (saved_row(a.q, it) + (last - it.beg) / kTile) * wstep + wrow;
         if (l.tid < kChannels) {  // (in registers they would take eight)
             const int64_t hh = l.first + min(l.tid, l.valid - 1);
@@ -148,19 +151,20 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
 
         T ur[kOwn], dr[kOwn], zr[kOwn], gr[kOwn];
         float hn[S];
-        m.template load_part<T>(ur, up, a.u, l.valid, now);
-        m.template load_part<T>(dr, dp, a.delta, l.valid, now);
-        m.template load_part<T>(gr, gp, ga.dy, l.valid, now);
-        m.template load_part<T>(zr, zp, gv, l.valid, now);
-        stage.template load<!ENDS, true>(a.B, a.C, Bp, Cp, now);
+        m.template load_part<T>(ur, up, m.template offset<T>(a.u), a.u, now);
+        m.template load_part<T>(dr, dp, m.template offset<T>(a.delta), a.delta, now);
+        m.template load_part<T>(gr, gp, m.template offset<T>(ga.dy), ga.dy, now);
+        m.template load_part<T>(zr, zp, m.template offset<T>(gv), gv, now);
+        Stage<T, S>(a.B, a.C, N, l.tid).template load_part<!ENDS, true>(sb, sc, a.B, a.C, Bp, Cp, now);
         if (!ENDS) load_states<S>(hn, sv);
 
         for (int tile = tiles - 1; tile >= 0; --tile) {
             const int64_t t0 = beg + (int64_t)tile * kTile;
             // the loaded tile into LDS
-            float u[kOwn], slope[kOwn], zsl[kOwn];
+            float u[kOwn], zsl[kOwn];
             {
-                float dt[kOwn], po[kOwn];
+                const Mover<O> m(anew(l.tid), l.valid);
+                float dt[kOwn], po[kOwn], slope[kOwn];
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
                     u[i] = to_f(ur[i]);
@@ -188,9 +192,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     po[i] = in ? po[i] : 0.0f;
                     if (ENDS) dtsum[i] += dt[i];
                     if (m.has(i, l.valid))
-                        steps[m.step(i) * kStepRow + step_at(m.channel(i))] = make_float4(dt[i], dt[i] * u[i], po[i], 0.0f);
+                        steps[m.step(i) * kStepRow + step_at(m.channel(i))] = make_float4(dt[i], dt[i] * u[i], po[i], slope[i]);
                 }
-                stage.template store<!ENDS, true>(lds, now);
+                Stage<T, S>(a.B, a.C, N, anew(l.tid)).template store<!ENDS, true>(sb, sc, lds, now);
             }
             float h0[S];
             if (!ENDS) {
@@ -201,16 +205,17 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
             // the tile before this one, whole, flies while this one is run (the first
             // loads itself again where it is a whole one)
             if (tile > 0 || now == kTile) {
-                const int64_t go = tile > 0 ? kTile : 0;
-                up -= go * a.u.sl, dp -= go * a.delta.sl, zp -= go * gv.sl, gp -= go * ga.dy.sl;
-                Bp -= go * a.B.sl, Cp -= go * a.C.sl;
-                m.template load<T>(ur, up, a.u, l.valid);
-                m.template load<T>(dr, dp, a.delta, l.valid);
-                m.template load<T>(gr, gp, ga.dy, l.valid);
-                m.template load<T>(zr, zp, gv, l.valid);
-                stage.template load<!ENDS, true>(a.B, a.C, Bp, Cp, kTile);
+                const int64_t back = tile > 0 ? kTile * (int64_t)sizeof(T) : 0;
+                up -= back * a.u.sl, dp -= back * a.delta.sl, zp -= back * gv.sl, gp -= back * ga.dy.sl;
+                Bp -= back * a.B.sl, Cp -= back * a.C.sl;
+                const Mover<O> m(anew(l.tid), l.valid);
+                m.template load<T>(ur, up, m.template offset<T>(a.u), a.u);
+                m.template load<T>(dr, dp, m.template offset<T>(a.delta), a.delta);
+                m.template load<T>(gr, gp, m.template offset<T>(ga.dy), ga.dy);
+                m.template load<T>(zr, zp, m.template offset<T>(gv), gv);
+                Stage<T, S>(a.B, a.C, N, anew(l.tid)).template load<!ENDS, true>(sb, sc, Bp, Cp);
                 if (!ENDS) {
-                    sv -= go ? wstep : 0;
+                    sv -= back ? wstep : 0;
                     load_states<S>(hn, sv);
                 }
             }
@@ -218,12 +223,24 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
             const float4* const bc = reinterpret_cast<const float4*>(lds) + p;
             const float4* const mine = steps + step_at(l.c);
             if constexpr (ENDS) {
+                float4 dn = mine[(kTile - 1) * kStepRow], vn[S / 2];
+#pragma unroll
+                for (int k = 0; k < S / 2; ++k) vn[k] = bc[(kTile - 1) * (kRow / 4) + k * 8];
 #pragma unroll
                 for (int t = kTile - 1; t >= 0; --t) {
-                    const float4 d = mine[t * kStepRow];
+                    const float4 d = dn;
+                    float4 vt[S / 2];
+#pragma unroll
+                    for (int k = 0; k < S / 2; ++k) vt[k] = vn[k];
+                    if (t > 0) {
+                        dn = mine[(t - 1) * kStepRow];
+#pragma unroll
+                        for (int k = 0; k < S / 2; ++k) vn[k] = bc[(t - 1) * (kRow / 4) + k * 8];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int k = 0; k < S / 2; ++k) {
-                        const float4 v = bc[t * (kRow / 4) + k * 8];
+                        const float4 v = vt[k];
                         carry[2 * k] = fmaf(v.z, d.z, carry[2 * k]) * __builtin_amdgcn_exp2f(d.x * A2[2 * k]);
                         carry[2 * k + 1] =
                             fmaf(v.w, d.z, carry[2 * k + 1]) * __builtin_amdgcn_exp2f(d.x * A2[2 * k + 1]);
@@ -236,10 +253,19 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     // this pair of states through the tile and back
                     float dec[kTile][2], x[kTile + 1][2], share[4];
                     x[0][0] = h0[2 * k], x[0][1] = h0[2 * k + 1];
+                    // LDS is read a step ahead of its use; without the barriers to scheduling
+                    // the compiler puts the reads right before it, and waits every step
+                    float2 dn = *reinterpret_cast<const float2*>(mine);
+                    float4 vn = bc[k * 8];
 #pragma unroll
                     for (int t = 0; t < kTile; ++t) {
-                        const float2 d = *reinterpret_cast<const float2*>(mine + t * kStepRow);
-                        const float4 v = bc[t * (kRow / 4) + k * 8];
+                        const float2 d = dn;
+                        const float4 v = vn;
+                        if (t + 1 < kTile) {
+                            dn = *reinterpret_cast<const float2*>(mine + (t + 1) * kStepRow);
+                            vn = bc[(t + 1) * (kRow / 4) + k * 8];
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                         dec[t][0] = __builtin_amdgcn_exp2f(d.x * A2[2 * k]);
                         dec[t][1] = __builtin_amdgcn_exp2f(d.x * A2[2 * k + 1]);
                         x[t + 1][0] = fmaf(dec[t][0], x[t][0], d.y * v.x);
@@ -256,11 +282,18 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     int again = 0;
                     asm volatile("" : "+v"(again));
                     const float4* const bc2 = bc + again;
+                    const float4* const mine2 = mine + again;
                     float gshare[4], later = 0.0f;
+                    float4 en = mine2[(kTile - 1) * kStepRow];
+                    vn = bc2[(kTile - 1) * (kRow / 4) + k * 8];
 #pragma unroll
                     for (int t = kTile - 1; t >= 0; --t) {
-                        const float4 d = mine[t * kStepRow + again];
-                        const float4 v = bc2[t * (kRow / 4) + k * 8];
+                        const float4 d = en, v = vn;
+                        if (t > 0) {
+                            en = mine2[(t - 1) * kStepRow];
+                            vn = bc2[(t - 1) * (kRow / 4) + k * 8];
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                         const float g0 = fmaf(v.z, d.z, carry[2 * k]), g1 = fmaf(v.w, d.z, carry[2 * k + 1]);
                         float gx = fmaf(g1, v.y, g0 * v.x);
                         carry[2 * k] = g0 * dec[t][0];
@@ -303,31 +336,34 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     if (k + 1 < S / 2) __syncthreads();
                 }
                 // the tile's gradients
+                const Mover<O> m(anew(l.tid), l.valid);
                 float ys[kOwn], gs[kOwn], as[kOwn], o[kOwn];
                 get_sums<O>(ys, ysum, m);
                 get_sums<O>(gs, gsum, m);
                 get_sums<O>(as, asum, m);
-                float dt[kOwn], po[kOwn], Dv[kOwn];
+                float dt[kOwn], po[kOwn], slope[kOwn], Dv[kOwn];
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
                     Dv[i] = par[min(max(m.channel(i), 0), kChannels - 1)].y;
                     const float4 d = steps[m.step(i) * kStepRow + step_at(max(0, min(m.channel(i), l.valid - 1)))];
-                    dt[i] = d.x, po[i] = d.z;
+                    dt[i] = d.x, po[i] = d.z, slope[i] = d.w;
                     o[i] = fmaf(Dv[i], po[i], dt[i] * gs[i]);
                 }
-                m.template store<T>(o, m.template at<T>(ga.du, it.row, l, t0), ga.du, l.valid, now);
+                m.template store<T>(o, dup, m.template offset<T>(ga.du), ga.du, l.valid, now);
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
                     o[i] = fmaf(u[i], gs[i], as[i] * kLn2) * slope[i];
                     dbsum[i] += m.step(i) < now ? o[i] : 0.0f;
                     dDsum[i] += m.step(i) < now ? po[i] * u[i] : 0.0f;
                 }
-                m.template store<T>(o, m.template at<T>(ga.ddelta, it.row, l, t0), ga.ddelta, l.valid, now);
+                m.template store<T>(o, ddp, m.template offset<T>(ga.ddelta), ga.ddelta, l.valid, now);
                 if (gate) {
 #pragma unroll
                     for (int i = 0; i < kOwn; ++i) o[i] = fmaf(Dv[i], u[i], ys[i]) * zsl[i];
-                    m.template store<T>(o, m.template at<T>(ga.dz, it.row, l, t0), ga.dz, l.valid, now);
+                    m.template store<T>(o, dzp, m.template offset<T>(ga.dz), ga.dz, l.valid, now);
                 }
+                constexpr int64_t kBack = kTile * (int64_t)sizeof(T);
+                dup -= kBack * ga.du.sl, ddp -= kBack * ga.ddelta.sl, dzp -= kBack * ga.dz.sl;
                 __syncthreads();  // `steps` is read above and written next
             }
             now = kTile;

@@ -132,13 +132,27 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 
     const bool gate = !ENDS && a.z.data;
     const View3& gv = gate ? a.z : a.u;  // without a gate u once more, unused: the loads need no branch
-    const T* up = m.template at<const T>(a.u, it.row, l, beg);
-    const T* dp = m.template at<const T>(a.delta, it.row, l, beg);
-    const T* zp = m.template at<const T>(gv, it.row, l, beg);
-    T* yp = m.template at<T>(a.y, it.row, l, beg);
-    const T* Bp = (const T*)a.B.data + it.row * a.B.sb + l.g * a.B.sg + beg * a.B.sl;
-    const T* Cp = (const T*)a.C.data + it.row * a.C.sb + l.g * a.C.sg + beg * a.C.sl;
-    Stage<T, S> stage(a.B, N, l.tid);
+    T ur[kOwn], dr[kOwn], zr[kOwn];
+    const char* up = m.template base<T>(a.u, it.row, l, beg);
+    const char* dp = m.template base<T>(a.delta, it.row, l, beg);
+    const char* zp = m.template base<T>(gv, it.row, l, beg);
+    char* yp = m.template base<T>(a.y, it.row, l, beg);
+    const uint32_t uo = m.template offset<T>(a.u), dof = m.template offset<T>(a.delta),
+                   zo = m.template offset<T>(gv), yo = m.template offset<T>(a.y);
+    const char* Bp = group_base<T>(a.B, it.row, l.g, beg);
+    const char* Cp = group_base<T>(a.C, it.row, l.g, beg);
+    const Stage<T, S> stage(a.B, a.C, N, l.tid);
+    T sb[Stage<T, S>::K], sc[Stage<T, S>::K];
+    auto advance = [&](int64_t steps_on) {
+        const int64_t e = steps_on * (int64_t)sizeof(T);
+        up += e * a.u.sl, dp += e * a.delta.sl, zp += e * gv.sl, Bp += e * a.B.sl, Cp += e * a.C.sl;
+    };
+    auto load_tile = [&]() {
+        m.template load<T>(ur, up, uo, a.u);
+        m.template load<T>(dr, dp, dof, a.delta);
+        if (!ENDS) m.template load<T>(zr, zp, zo, gv);
+        stage.template load<true, !ENDS>(sb, sc, Bp, Cp);
+    };
     float bias[kOwn], Dv[kOwn];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
@@ -147,7 +161,6 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         Dv[i] = a.D ? a.D[hh] : 0.0f;
     }
 
-    T ur[kOwn], dr[kOwn], zr[kOwn];
     float uf[kOwn], zf[kOwn], sum[kOwn] = {};
     auto prepare = [&](int nt) {  // the loaded tile into LDS
         float d[kOwn];
@@ -168,7 +181,7 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             dx[i] = d[i] * uf[i];
         }
         put_pairs<O>(steps, d, dx, m, l.valid);
-        stage.template store<true, !ENDS>(lds, nt);
+        stage.template store<true, !ENDS>(sb, sc, lds, nt);
         __syncthreads();
     };
     auto finish = [&](int nt) {  // y of the tile
@@ -180,29 +193,20 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) yv[i] *= silu_f<kFine<T>>(zf[i]);
         }
-        if (a.y.data) m.template store<T>(yv, yp, a.y, l.valid, nt);
+        if (a.y.data) m.template store<T>(yv, yp, yo, a.y, l.valid, nt);
     };
 
     float* saved = !ENDS && a.saved && l.live
                        ? a.saved + (saved_row(a.q, it) + (beg - it.beg) / kTile) * wstep + wrow
                        : nullptr;
     const int len = (int)max((int64_t)0, end - beg), whole = len / kTile, rest = len % kTile;
-    if (whole > 0) {
-        m.template load<T>(ur, up, a.u, l.valid);
-        m.template load<T>(dr, dp, a.delta, l.valid);
-        if (!ENDS) m.template load<T>(zr, zp, gv, l.valid);
-        stage.template load<true, !ENDS>(a.B, a.C, Bp, Cp, kTile);
-    }
+    if (whole > 0) load_tile();
     for (int k = 0; k < whole; ++k) {
         prepare(kTile);
         // the next whole tile's loads fly while this one is run (the last one loads
         // itself again: a branch here would make them wait)
-        const int64_t go = k + 1 < whole ? kTile : 0;
-        up += go * a.u.sl, dp += go * a.delta.sl, zp += go * gv.sl, Bp += go * a.B.sl, Cp += go * a.C.sl;
-        m.template load<T>(ur, up, a.u, l.valid);
-        m.template load<T>(dr, dp, a.delta, l.valid);
-        if (!ENDS) m.template load<T>(zr, zp, gv, l.valid);
-        stage.template load<true, !ENDS>(a.B, a.C, Bp, Cp, kTile);
+        advance(k + 1 < whole ? kTile : 0);
+        load_tile();
         __builtin_amdgcn_sched_barrier(0);  // left alone, the compiler moves the loads behind the tile
         if (saved) {
             store_states<S>(h, saved);
@@ -211,15 +215,14 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         run_tile<S, ENDS, false>(h, A2, lds + p * 4, steps + pair_at(l.c), kTile, ysum, l.c, p);
         __syncthreads();
         if (!ENDS) finish(kTile);
-        yp += kTile * a.y.sl;
+        yp += kTile * a.y.sl * (int64_t)sizeof(T);
     }
     if (rest > 0) {
-        const int64_t go = whole > 0 ? kTile : 0;
-        up += go * a.u.sl, dp += go * a.delta.sl, zp += go * gv.sl, Bp += go * a.B.sl, Cp += go * a.C.sl;
-        m.template load_part<T>(ur, up, a.u, l.valid, rest);
-        m.template load_part<T>(dr, dp, a.delta, l.valid, rest);
-        if (!ENDS) m.template load_part<T>(zr, zp, gv, l.valid, rest);
-        stage.template load<true, !ENDS>(a.B, a.C, Bp, Cp, rest);
+        advance(whole > 0 ? kTile : 0);
+        m.template load_part<T>(ur, up, uo, a.u, rest);
+        m.template load_part<T>(dr, dp, dof, a.delta, rest);
+        if (!ENDS) m.template load_part<T>(zr, zp, zo, gv, rest);
+        stage.template load_part<true, !ENDS>(sb, sc, a.B, a.C, Bp, Cp, rest);
         prepare(rest);
         if (saved) store_states<S>(h, saved);
         run_tile<S, ENDS, true>(h, A2, lds + p * 4, steps + pair_at(l.c), rest, ysum, l.c, p);

@@ -91,7 +91,7 @@ BAD_SEQ = [
 ]
 BAD_VIEW = [
     (dict(data=None), INVALID), (dict(data=FAKE + 1), INVALID), (dict(sl=-1), INVALID), (dict(sh=-1), INVALID),
-    (dict(sh=1 << 25), UNSUPPORTED), (dict(sl=1 << 24), UNSUPPORTED), (dict(sb=1 << 40), UNSUPPORTED),
+    (dict(sh=1 << 23), UNSUPPORTED), (dict(sl=1 << 23), UNSUPPORTED), (dict(sb=1 << 40), UNSUPPORTED),
 ]
 BAD_OUT = BAD_VIEW + [(dict(sb=0), INVALID), (dict(sh=0), INVALID), (dict(sl=0), INVALID)]
 
@@ -148,8 +148,8 @@ BAD_SELECTIVE = [
     (dict(dtype=3), INVALID), (dict(H=0), INVALID), (dict(N=0), INVALID), (dict(G=3), INVALID), (dict(G=0), INVALID),
     (dict(N=65), UNSUPPORTED), (dict(A=None), INVALID), (dict(A=FAKE + 2), INVALID), (dict(D=FAKE + 1), INVALID),
     (dict(delta_bias=FAKE + 2), INVALID), (dict(x_in=FAKE + 2), INVALID),
-    (dict(B=_group(data=None)), INVALID), (dict(C=_group(sn=-1)), INVALID), (dict(C=_group(sn=1 << 25)), UNSUPPORTED),
-    (dict(B=_group(sg=1 << 40)), UNSUPPORTED), (dict(B=_group(sl=1 << 24)), UNSUPPORTED),
+    (dict(B=_group(data=None)), INVALID), (dict(C=_group(sn=-1)), INVALID), (dict(C=_group(sn=1 << 23)), UNSUPPORTED),
+    (dict(B=_group(sg=1 << 40)), UNSUPPORTED), (dict(B=_group(sl=1 << 23)), UNSUPPORTED),
 ] + [(dict(u=_view(**k)), c) for k, c in BAD_VIEW] + [(dict(delta=_view(**k)), c) for k, c in BAD_VIEW] \
   + [(dict(z=_view(**k)), c) for k, c in BAD_VIEW[1:]]
 
