@@ -463,7 +463,7 @@ typedef struct ssm_selective {
 /*
  * Selective scan.  y: view [Bsz,H,L], nullable where x_out or saved is given
  * (the states alone).  x_out [S or n_slots, H, N] nullable.
- * saved (nullable, SSM_OP_SELECTIVE_SAVED bytes): the states at every 16th step,
+ * saved (nullable, SSM_OP_SELECTIVE_SAVED bytes): the states at every 32nd step,
  * for ssm_selective_scan_backward; not with slots.  Workspace:
  * SSM_OP_SELECTIVE_SCAN.
  */

@@ -6,7 +6,7 @@
 // Both directions read and write each element once and are bound by HBM; the
 // arithmetic per element is 2 W operations and one exponential.
 //   tokens  channels contiguous: a thread holds V channels (16 bytes) and walks
-//           kWalk steps with the W - 1 last inputs in registers; 64 lanes read
+//           up to kMaxWalk steps with the W - 1 last inputs in registers; 64 lanes read
 //           1 KB of one step.  Any other strides take V = 1.
 //   rows    steps contiguous: a thread holds 8 steps of one channel and reads the
 //           steps around them again (an L1 hit).
@@ -20,7 +20,8 @@ namespace ssm {
 
 namespace {
 
-constexpr int kWalk = 32;  // steps a thread walks ("tokens")
+constexpr int kMaxWalk = 64;  // steps a thread walks at most ("tokens"); see geometry()
+constexpr int kAhead = 8;     // of them loaded together
 
 template <class T, int V>
 struct __attribute__((packed, aligned(sizeof(T)))) VecN {
@@ -30,6 +31,7 @@ struct __attribute__((packed, aligned(sizeof(T)))) VecN {
 struct Geometry {
     int Q;        // steps of an item
     int cx;       // threads along the channels (tokens) or along the steps (rows); 256 / cx along the other
+    int walk;     // steps a thread walks (tokens)
     int blocks;   // channel blocks
 };
 
@@ -62,6 +64,30 @@ __device__ __forceinline__ void store_v(const float (&r)[V], T* p, int64_t sh, i
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (i < n) p[i * sh] = from_f<T>(r[i]);
+    }
+}
+
+// V channels' weights and biases
+template <int W, int V>
+__device__ __forceinline__ void load_weights(float (&w)[W][V], float (&b)[V], const float* weight, const float* bias,
+                                             int64_t h, int n) {
+    if (n == V) {
+        const VecN<float, W * V> x = *reinterpret_cast<const VecN<float, W * V>*>(weight + h * W);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = x.v[i * W + k];
+        VecN<float, V> y = {};
+        if (bias) y = *reinterpret_cast<const VecN<float, V>*>(bias + h);
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = y.v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            b[i] = bias && i < n ? bias[h + i] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = i < n ? weight[(h + i) * W + k] : 0.0f;
+        }
     }
 }
 
@@ -103,16 +129,11 @@ __global__ __launch_bounds__(256) void conv_tokens_kernel(ConvArgs a, Geometry g
     const int64_t h = ((int64_t)cb * geo.cx + cx) * V;
     if (h >= a.H) return;
     const int n = (int)min((int64_t)V, a.H - h);
-    const int64_t first = (int64_t)it.beg + (int64_t)it.c * geo.Q + seg * kWalk;  // this thread's steps
-    const int last = (int)min((int64_t)it.end, first + kWalk);
+    const int64_t first = (int64_t)it.beg + (int64_t)it.c * geo.Q + seg * geo.walk;  // this thread's steps
+    const int64_t last = min((int64_t)it.end, first + geo.walk);
 
     float w[W][V], b[V], past[W > 1 ? W - 1 : 1][V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        b[i] = a.bias && i < n ? a.bias[h + i] : 0.0f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) w[k][i] = i < n ? a.weight[(h + i) * W + k] : 0.0f;
-    }
+    load_weights<W, V>(w, b, a.weight, a.bias, h, n);
     const T* u = (const T*)a.u.data + it.row * a.u.sb + h * a.u.sh;
     T* y = (T*)a.y.data + it.row * a.y.sb + h * a.y.sh;
 #pragma unroll
@@ -133,29 +154,48 @@ __global__ __launch_bounds__(256) void conv_tokens_kernel(ConvArgs a, Geometry g
         for (int i = 0; i < V; ++i)
             if (i < n) hand_on<T, W>(a, it, (int)h + i);
     }
-    constexpr int kAhead = 8;  // steps loaded together
-    for (int64_t t0 = first; t0 < last; t0 += kAhead) {
-        float v[kAhead][V];
+    auto step = [&](const float (&x)[V], float (&o)[V]) {
 #pragma unroll
-        for (int s = 0; s < kAhead; ++s)
-            if (t0 + s < last) load_v<T, V>(v[s], u + (t0 + s) * a.u.sl, a.u.sh, n);
+        for (int i = 0; i < V; ++i) {
+            float acc = b[i];
 #pragma unroll
-        for (int s = 0; s < kAhead; ++s) {
-            if (t0 + s >= last) break;
-            float o[V];
+            for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], past[k][i], acc);
+            o[i] = fmaf(w[W - 1][i], x[i], acc);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float acc = b[i];
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], past[k][i], acc);
-                acc = fmaf(w[W - 1][i], v[s][i], acc);
-                o[i] = a.silu ? silu_f<kFine<T>>(acc) : acc;
-#pragma unroll
-                for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
-                if (W > 1) past[W > 1 ? W - 2 : 0][i] = v[s][i];
-            }
-            store_v<T, V>(o, y + (t0 + s) * a.y.sl, a.y.sh, n);
+            for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
+            if (W > 1) past[W > 1 ? W - 2 : 0][i] = x[i];
         }
+        if (a.silu) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = silu_f<kFine<T>>(o[i]);
+        }
+    };
+    int64_t t = first;
+    if (V > 1 && n == V) {
+        const T* from = u + first * a.u.sl;
+        T* to = y + first * a.y.sl;
+        for (; t + kAhead <= last; t += kAhead) {
+            VecN<T, V> raw[kAhead];
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s, from += a.u.sl) raw[s] = *reinterpret_cast<const VecN<T, V>*>(from);
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s, to += a.y.sl) {
+                float x[V], o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[i] = to_f(raw[s].v[i]);
+                step(x, o);
+                VecN<T, V> out;
+#pragma unroll
+                for (int i = 0; i < V; ++i) out.v[i] = from_f<T>(o[i]);
+                *reinterpret_cast<VecN<T, V>*>(to) = out;
+            }
+        }
+    }
+    for (; t < last; ++t) {
+        float x[V], o[V];
+        load_v<T, V>(x, u + t * a.u.sl, a.u.sh, n);
+        step(x, o);
+        store_v<T, V>(o, y + t * a.y.sl, a.y.sh, n);
     }
 }
 
@@ -269,12 +309,11 @@ __device__ __forceinline__ void grad_old(const ConvGradArgs& a, const Item& it, 
         for (int i = 0; i < W - 1; ++i) d[i] = from_final<W>(a, it, h, i - (W - 1));
 #pragma unroll
         for (int t = 0; t < W - 1; ++t) {  // the steps whose window reaches back over the start
-            if (t >= len) break;
             float pre = a.f.bias ? a.f.bias[h] : 0.0f;
 #pragma unroll
             for (int k = 0; k < W; ++k) pre = fmaf(a.f.weight[h * W + k], line[t + k], pre);
-            const float g = to_f(dy[(it.beg + t) * a.dy.sl]);
-            const float dpre = a.f.silu ? g * silu_slope<kFine<T>>(pre) : g;
+            const float g = t < len ? to_f(dy[(it.beg + t) * a.dy.sl]) : 0.0f;
+            const float dpre = t < len ? (a.f.silu ? g * silu_slope<kFine<T>>(pre) : g) : 0.0f;
 #pragma unroll
             for (int k = 0; k < W; ++k)
                 if (t + k < W - 1) d[t + k < W - 1 ? t + k : 0] += a.f.weight[h * W + k] * dpre;
@@ -297,21 +336,19 @@ __global__ __launch_bounds__(256) void conv_grad_tokens_kernel(ConvGradArgs g, G
     const int n = (int)max((int64_t)0, min((int64_t)V, a.H - h));
     float dw[W][V] = {}, db[V] = {};
     if (there && n > 0) {
-        const int64_t first = (int64_t)it.beg + (int64_t)it.c * geo.Q + seg * kWalk;
-        const int64_t last = min((int64_t)it.end, first + kWalk);
+        const int64_t first = (int64_t)it.beg + (int64_t)it.c * geo.Q + seg * geo.walk;
+        const int64_t last = min((int64_t)it.end, first + geo.walk);
         const T* u = (const T*)a.u.data + it.row * a.u.sb + h * a.u.sh;
         const T* dy = (const T*)g.dy.data + it.row * g.dy.sb + h * g.dy.sh;
         T* du = (T*)g.du.data + it.row * g.du.sb + h * g.du.sh;
-        if (it.c == 0 && seg == 0)
-            for (int i = 0; i < n; ++i) grad_old<T, W>(g, it, h + i);
+        if (it.c == 0 && seg == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) grad_old<T, W>(g, it, h + i);
+        }
         if (first < last) {
             float w[W][V], b[V], past[W > 1 ? W - 1 : 1][V], ahead[W][V] = {};
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                b[i] = a.bias && i < n ? a.bias[h + i] : 0.0f;
-#pragma unroll
-                for (int k = 0; k < W; ++k) w[k][i] = i < n ? a.weight[(h + i) * W + k] : 0.0f;
-            }
+            load_weights<W, V>(w, b, a.weight, a.bias, h, n);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) {
                 const int64_t t = first - (W - 1) + k;
@@ -327,56 +364,85 @@ __global__ __launch_bounds__(256) void conv_grad_tokens_kernel(ConvGradArgs g, G
             }
             // ahead[j]: the gradient collected so far for input t - (W - 1) + j; the
             // walk goes W - 1 steps past `last` so that the own inputs get all theirs
-            const int64_t stop = last + W - 1;
-            constexpr int kAhead = 4;
-            for (int64_t t0 = first; t0 < stop; t0 += kAhead) {
-                float v[kAhead][V], d[kAhead][V];
+            const int64_t stop = last + W - 1, there_to = min(stop, (int64_t)it.end);
+            // one step: `x` and `d` the input and the gradient of y at step t (0 behind the sequence)
+            auto step = [&](int64_t t, const float (&x)[V], float (&d)[V]) {
+                const bool mine = t < last;
+                float o[V];
+                if (a.silu) {
 #pragma unroll
-                for (int s = 0; s < kAhead; ++s) {
-                    const int64_t t = t0 + s;
-                    if (t < stop && t < it.end) {
-                        load_v<T, V>(v[s], u + t * a.u.sl, a.u.sh, n);
-                        load_v<T, V>(d[s], dy + t * g.dy.sl, g.dy.sh, n);
+                    for (int i = 0; i < V; ++i) {
+                        float pre = b[i];
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][i], past[k][i], pre);
+                        pre = fmaf(w[W - 1][i], x[i], pre);
+                        d[i] *= silu_slope<kFine<T>>(pre);
                     }
                 }
 #pragma unroll
-                for (int s = 0; s < kAhead; ++s) {
-                    const int64_t t = t0 + s;
-                    if (t >= stop) break;
-                    const bool inside = t < it.end;
-                    const bool mine = t < last;
+                for (int i = 0; i < V; ++i) {
+                    if (mine) {
+                        db[i] += d[i];
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) dw[k][i] = fmaf(d[i], past[k][i], dw[k][i]);
+                        dw[W - 1][i] = fmaf(d[i], x[i], dw[W - 1][i]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < W; ++j) ahead[j][i] = fmaf(w[j][i], d[i], ahead[j][i]);
+                    o[i] = ahead[0][i];
+#pragma unroll
+                    for (int j = 0; j + 1 < W; ++j) ahead[j][i] = ahead[j + 1][i];
+                    ahead[W - 1][i] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
+                    if (W > 1) past[W > 1 ? W - 2 : 0][i] = x[i];
+                }
+                const int64_t done = t - (W - 1);  // this input's gradient is whole
+                if (done >= first) {
+                    if (g.dstate_out && done >= it.end - (W - 1)) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            if (i < n) o[i] += from_final<W>(g, it, h + i, done - it.beg);
+                    }
+                    store_v<T, V>(o, du + done * g.du.sl, g.du.sh, n);
+                }
+            };
+            int64_t t = first;
+            if (V > 1 && n == V) {
+                const T *fu = u + first * a.u.sl, *fd = dy + first * g.dy.sl;
+                for (; t + kAhead <= there_to; t += kAhead) {
+                    VecN<T, V> ru[kAhead], rd[kAhead];
+#pragma unroll
+                    for (int s = 0; s < kAhead; ++s, fu += a.u.sl, fd += g.dy.sl) {
+                        ru[s] = *reinterpret_cast<const VecN<T, V>*>(fu);
+                        rd[s] = *reinterpret_cast<const VecN<T, V>*>(fd);
+                    }
+#pragma unroll
+                    for (int s = 0; s < kAhead; ++s) {
+                        float x[V], d[V];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) x[i] = to_f(ru[s].v[i]), d[i] = to_f(rd[s].v[i]);
+                        step(t + s, x, d);
+                    }
+                }
+            }
+            for (; t < stop; ++t) {
+                float x[V] = {}, d[V] = {};
+                if (t < it.end) {
+                    load_v<T, V>(x, u + t * a.u.sl, a.u.sh, n);
+                    load_v<T, V>(d, dy + t * g.dy.sl, g.dy.sh, n);
+                    step(t, x, d);
+                } else {
+                    // behind the sequence nothing is added; the gradients collected come out
+                    const int64_t done = t - (W - 1);
                     float o[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        float dpre = 0.0f, x = 0.0f;
-                        if (inside) {
-                            x = v[s][i];
-                            dpre = d[s][i];
-                            if (a.silu) {
-                                float pre = b[i];
-#pragma unroll
-                                for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][i], past[k][i], pre);
-                                pre = fmaf(w[W - 1][i], x, pre);
-                                dpre *= silu_slope<kFine<T>>(pre);
-                            }
-                            if (mine) {
-                                db[i] += dpre;
-#pragma unroll
-                                for (int k = 0; k < W - 1; ++k) dw[k][i] = fmaf(dpre, past[k][i], dw[k][i]);
-                                dw[W - 1][i] = fmaf(dpre, x, dw[W - 1][i]);
-                            }
-                        }
-#pragma unroll
-                        for (int j = 0; j < W; ++j) ahead[j][i] = fmaf(w[j][i], dpre, ahead[j][i]);
                         o[i] = ahead[0][i];
 #pragma unroll
                         for (int j = 0; j + 1 < W; ++j) ahead[j][i] = ahead[j + 1][i];
                         ahead[W - 1][i] = 0.0f;
-#pragma unroll
-                        for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
-                        if (W > 1) past[W > 1 ? W - 2 : 0][i] = x;
                     }
-                    const int64_t done = t - (W - 1);  // this input's gradient is whole
                     if (done >= first) {
                         if (g.dstate_out && done >= it.end - (W - 1)) {
 #pragma unroll
@@ -522,8 +588,10 @@ int pow2_at_least(int64_t v, int most) {
 template <class T>
 constexpr int vec() { return 16 / (int)sizeof(T); }
 
-Geometry geometry(Order o, int V, int64_t H, int64_t L, int iters) {
+// `rows`: batch rows (one when packed)
+Geometry geometry(Order o, int V, int64_t H, int64_t L, int64_t rows, int iters) {
     Geometry g;
+    g.walk = 0;
     if (o == kRows) {
         g.cx = pow2_at_least((L + 7) / 8, 64);
         g.Q = g.cx * 8 * iters;
@@ -532,22 +600,32 @@ Geometry geometry(Order o, int V, int64_t H, int64_t L, int iters) {
     } else {
         const int64_t n = (H + V - 1) / V;
         g.cx = pow2_at_least(n, 64);
-        g.Q = 256 / g.cx * kWalk;
         g.blocks = (int)((n + g.cx - 1) / g.cx);
+        // a walk reads W - 1 steps more than it has: the longest that still gives
+        // kMany workgroups, and no shorter than what is loaded together
+        constexpr int64_t kMany = 1024;
+        g.walk = kMaxWalk;
+        while (g.walk > kAhead && rows * g.blocks * ((L + 256 / g.cx * g.walk - 1) / (256 / g.cx * g.walk)) < kMany)
+            g.walk >>= 1;
+        g.Q = 256 / g.cx * g.walk;
     }
     return g;
 }
 
+// batch rows for geometry()
+int64_t rows_of(const Seqs& q) { return q.offsets ? 1 : q.S; }
+
 constexpr int kGradIters = 4;
+constexpr int kGradV = 2;  // 96 registers, 5 waves per SIMD (4 channels: 151 and 3)
 
 template <class T, int W>
 hipError_t forward_as(const ConvArgs& a, hipStream_t s) {
     const View3* views[] = {&a.u, &a.y};
     const Order o = order_of(views, 2, 4);
     const int V = o == kTokens ? vec<T>() : 1;
-    const Geometry geo = geometry(o, V, a.H, a.q.L, 1);
+    const Geometry geo = geometry(o, V, a.H, a.q.L, rows_of(a.q), 1);
     const int64_t wgs = item_count(a.q, geo.Q) * geo.blocks;
-    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(wgs, 256)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)wgs), wg(256);
     if (o == kRows)
         conv_rows_kernel<T, W><<<grid, wg, 0, s>>>(a, geo);
@@ -563,16 +641,16 @@ hipError_t backward_as(const ConvGradArgs& g, float* partial, hipStream_t s) {
     const ConvArgs& a = g.f;
     const View3* views[] = {&a.u, &g.dy, &g.du};
     const Order o = order_of(views, 3, 4);
-    const int V = o == kTokens ? vec<T>() : 1;
-    const Geometry geo = geometry(o, V, a.H, a.q.L, kGradIters);
+    const int V = o == kTokens ? kGradV : 1;
+    const Geometry geo = geometry(o, V, a.H, a.q.L, rows_of(a.q), kGradIters);
     const int64_t items = item_count(a.q, geo.Q), wgs = items * geo.blocks;
-    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(wgs, 256)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)wgs), wg(256);
     float* to = g.dweight || g.dbias ? partial : nullptr;
     if (o == kRows)
         conv_grad_rows_kernel<T, W><<<grid, wg, 0, s>>>(g, geo, to);
     else if (o == kTokens)
-        conv_grad_tokens_kernel<T, W, vec<T>()><<<grid, wg, 0, s>>>(g, geo, to);
+        conv_grad_tokens_kernel<T, W, kGradV><<<grid, wg, 0, s>>>(g, geo, to);
     else
         conv_grad_tokens_kernel<T, W, 1><<<grid, wg, 0, s>>>(g, geo, to);
     if (to) {
@@ -608,21 +686,21 @@ hipError_t backward_of(const ConvGradArgs& g, float* partial, hipStream_t s) {
 size_t conv_grad_workspace_bytes(const Seqs& q, int64_t H, int width) {
     int64_t items = 0;
     for (Order o : {kRows, kTokens, kAny})
-        for (int V : {1, 4, 8}) {
-            const int64_t n = item_count(q, geometry(o, V, H, q.L, kGradIters).Q);
+        for (int V : {1, kGradV}) {
+            const int64_t n = item_count(q, geometry(o, V, H, q.L, rows_of(q), kGradIters).Q);
             items = n > items ? n : items;
         }
     return (size_t)items * H * (width + 1) * sizeof(float);
 }
 
-// whether every storage order's launch stays below 2^31 workgroups
+// whether every storage order's launch can be made
 bool conv_fits(const Seqs& q, int64_t H) {
     for (Order o : {kRows, kTokens, kAny})
-        for (int V : {1, 4, 8}) {
-            const Geometry g = geometry(o, V, H, q.L, 1);
-            if (item_count(q, g.Q) * g.blocks >= ((int64_t)1 << 31)) return false;
+        for (int V : {1, kGradV, 4, 8}) {
+            const Geometry g = geometry(o, V, H, q.L, rows_of(q), 1);
+            if (!grid_fits(item_count(q, g.Q) * g.blocks, 256)) return false;
         }
-    return true;
+    return grid_fits((H * (4 + 1) + kSumCols - 1) / kSumCols, 256);
 }
 
 hipError_t launch_causal_conv(int dtype, const ConvArgs& a, hipStream_t s) {

@@ -145,6 +145,9 @@ inline int64_t item_count(const Seqs& q, int64_t Q) {
     return q.S + q.L / Q;
 }
 
+// a launch has less than 2^32 threads in all
+inline bool grid_fits(int64_t wgs, int threads) { return wgs < ((int64_t)1 << 32) / threads; }
+
 // ---- a workgroup of the scan kernels ----
 // 64 channels of one group, 32 steps to a tile, 512 threads in two roles.
 // Moving a tile: thread by thread four elements of every activation, in vector

@@ -322,7 +322,9 @@ int ssm_selective_scan_backward(const ssm_sequences* seq, const ssm_selective* p
 int ssm_selective_step(const ssm_selective_token* p, void* stream) {
     if (!p || !type_known(p->dtype) || p->Bsz < 1 || p->H < 1) return SSM_ERR_INVALID_ARGUMENT;
     SSM_TRY(check_scan_sizes(p->H, p->N, p->G));
-    if (p->Bsz >= kMaxDim || p->H >= kMaxDim || p->Bsz * p->H >= kMaxDim) return SSM_ERR_UNSUPPORTED;
+    if (p->Bsz >= kMaxDim || p->H >= kMaxDim || p->Bsz * p->H >= kMaxDim ||
+        !grid_fits(p->Bsz * ((p->H + 63) / 64), 256))
+        return SSM_ERR_UNSUPPORTED;
     if (!p->u || !p->delta || !p->B || !p->C || !p->y || !p->A || !p->x || (p->slots && p->n_slots < 1))
         return SSM_ERR_INVALID_ARGUMENT;
     const size_t e = type_bytes(p->dtype);

@@ -53,9 +53,9 @@ struct GradSplit {
     float* ends;    // [items, H, Np]: gradient a chunk hands to the chunk before it, from a zero end
     float* sums;    // [items, H]: sum of dt over a chunk
     float* part_bc; // [per_group, Bsz, L, G, S/2, 2, 16]: a workgroup's dB and dC by pairs of lane states
-    float* part_a;  // [items, H, Np]
-    float* part_d;  // [items, 2, H]: dD, ddelta_bias
+    float* part;    // [items, part_cols]: dA [H, Np], dD [H], ddelta_bias [H]
 };
+__host__ __device__ inline int64_t part_cols(int64_t H, int64_t Np) { return (H * (Np + 2) + 3) & ~(int64_t)3; }
 
 // a row of `steps`: a place free behind every fourth channel, as in the rows of pairs
 constexpr int kStepRow = kChannels / 4 * 5;
@@ -392,10 +392,11 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
         if (l.live) store_states<S>(carry, sp.ends + item * wstep + wrow);
         return;
     }
-    per_channel(dDsum, sp.part_d + (item * 2) * a.H);
-    per_channel(dbsum, sp.part_d + (item * 2 + 1) * a.H);
+    float* sums = sp.part + item * part_cols(a.H, 8 * S);
+    per_channel(dDsum, sums + wstep);
+    per_channel(dbsum, sums + wstep + a.H);
     if (!l.live) return;
-    store_states<S>(dA, sp.part_a + item * wstep + wrow);
+    store_states<S>(dA, sums + wrow);
     if (work && it.c == 0 && ga.dx_in) {
 #pragma unroll
         for (int j = 0; j < S; ++j)
@@ -403,19 +404,18 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
     }
 }
 
-// dB and dC from the workgroups' sums; steps outside every sequence stay as they were
+// dB and dC: the sums of a group's workgroups, four values a thread; steps
+// outside every sequence stay as they were.  It reads per_group rows of 64 G S
+// bytes per step and writes little, so HBM bounds it; sixteen loads a thread are in flight.
 template <class T>
-__global__ __launch_bounds__(256) void grad_bc_kernel(ScanGradArgs ga, const float* part, int per_group, int S) {
+__device__ __forceinline__ void finish_bc(const ScanGradArgs& ga, const float* part, int per_group, int S, int64_t i) {
     const ScanArgs& a = ga.f;
-    const int64_t row = (int64_t)S * 16, total = a.Bsz * a.q.L * a.G * row;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int row = S * 4;
+    const int64_t total = a.Bsz * a.q.L * a.G * row;
     if (i >= total) return;
-    const int v = (int)(i % row);
-    const int g = (int)(i / row % a.G);
-    const int64_t bl = i / (row * a.G);
-    const int64_t b = bl / a.q.L;
-    const int t = (int)(bl % a.q.L), n = ((v & 15) >> 1) * S + (v >> 5) * 2 + (v & 1);
-    if (n >= a.N) return;
+    const int v = (int)(i & (row - 1)) * 4;
+    const int64_t step = i / row, g = step % a.G, bl = step / a.G, b = bl / a.q.L;
+    const int t = (int)(bl - b * a.q.L);
     int64_t r0;
     int beg, end, e0;
     if (a.q.offsets) {
@@ -425,31 +425,60 @@ __global__ __launch_bounds__(256) void grad_bc_kernel(ScanGradArgs ga, const flo
         seq_bounds(a.q, (int)b, r0, beg, end);
     }
     if (t < beg || t >= end) return;
-    float s = part[i];
-    for (int k = 1; k < per_group; ++k) s += part[(int64_t)k * total + i];
+    float s[4] = {};
+    const float4* from = (const float4*)part + i;
+    int k = 0;
+    for (; k + 16 <= per_group; k += 16) {
+        float4 x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = from[(k + j) * total];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[0] += x[j].x, s[1] += x[j].y, s[2] += x[j].z, s[3] += x[j].w;
+    }
+    for (; k < per_group; ++k) {
+        const float4 x = from[k * total];
+        s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+    }
     const View4& o = v & 16 ? ga.dC : ga.dB;
-    ((T*)o.data)[b * o.sb + g * o.sg + n * o.sn + t * o.sl] = from_f<T>(s);
+    T* to = (T*)o.data + b * o.sb + g * o.sg + t * o.sl;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int w = v + j, n = ((w & 15) >> 1) * S + (w >> 5) * 2 + (w & 1);
+        if (n < a.N) to[n * o.sn] = from_f<T>(s[j]);
+    }
 }
 
-// dA, dD and ddelta_bias: the workgroups' rows added in float64
+// dA, dD and ddelta_bias: the items' rows added in float64
 constexpr int kSumCols = 32, kSumRows = 8;
-__global__ __launch_bounds__(256) void grad_sum_kernel(const float* part, int64_t rows, int64_t cols, int64_t stride,
-                                                       int width, int kept, float* out) {
-    // columns are [cols / width] runs of `width`, of which the first `kept` go to `out`
+__device__ __forceinline__ void finish_sums(const ScanGradArgs& ga, const GradSplit& sp, int64_t Np, int64_t block) {
     __shared__ double red[kSumRows][kSumCols];
+    const ScanArgs& a = ga.f;
     const int c = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
-    const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
+    const int64_t cols = part_cols(a.H, Np), col = block * kSumCols + c;
     double s = 0.0;
     if (col < cols)
-        for (int64_t i = r; i < rows; i += kSumRows) s += (double)part[i * stride + col];
+        for (int64_t i = r; i < sp.items; i += kSumRows) s += (double)sp.part[i * cols + col];
     red[r][c] = s;
     __syncthreads();
-    if (r == 0 && col < cols) {
+    if (r != 0 || col >= cols) return;
 #pragma unroll
-        for (int i = 1; i < kSumRows; ++i) s += red[i][c];
-        const int64_t h = col / width, n = col % width;
-        if (n < kept) out[h * kept + n] = (float)s;
+    for (int i = 1; i < kSumRows; ++i) s += red[i][c];
+    if (col < a.H * Np) {
+        const int64_t h = col / Np, n = col % Np;
+        if (n < a.N) ga.dA[h * a.N + n] = (float)s;
+    } else if (col < a.H * (Np + 1)) {
+        if (ga.dD) ga.dD[col - a.H * Np] = (float)s;
+    } else if (ga.ddelta_bias && col < a.H * (Np + 2)) {
+        ga.ddelta_bias[col - a.H * (Np + 1)] = (float)s;
     }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void grad_finish_kernel(ScanGradArgs ga, GradSplit sp, int S, unsigned sum_blocks) {
+    if (blockIdx.x < sum_blocks)
+        finish_sums(ga, sp, S * 8, blockIdx.x);
+    else
+        finish_bc<T>(ga, sp.part_bc, sp.per_group, S, (int64_t)(blockIdx.x - sum_blocks) * 256 + threadIdx.x);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -458,7 +487,7 @@ struct Plan {
     GradSplit sp;
     int64_t items, Np;
     bool split;
-    size_t ends, sums, bc, pa, pd;
+    size_t ends, sums, bc, part;
 };
 
 Plan plan(const Seqs& q, int64_t Bsz, int64_t H, int64_t N, int64_t G) {
@@ -483,28 +512,24 @@ Plan plan(const Seqs& q, int64_t Bsz, int64_t H, int64_t N, int64_t G) {
     p.ends = p.split ? up256((size_t)p.items * H * p.Np * 4) : 0;
     p.sums = p.split ? up256((size_t)p.items * H * 4) : 0;
     p.bc = up256((size_t)p.sp.per_group * Bsz * q.L * G * p.Np * 2 * 4);
-    p.pa = up256((size_t)p.items * H * p.Np * 4);
-    p.pd = up256((size_t)p.items * H * 2 * 4);
+    p.part = up256((size_t)p.items * part_cols(H, p.Np) * 4);
     return p;
 }
+
+// workgroups of the last launch: dA, dD, ddelta_bias, then dB and dC
+int64_t sum_blocks(int64_t H, int64_t Np) { return (part_cols(H, Np) + kSumCols - 1) / kSumCols; }
+int64_t bc_blocks(int64_t Bsz, int64_t L, int64_t G, int64_t Np) { return (Bsz * L * G * (Np / 2) + 255) / 256; }
 
 template <class T, int S, Order O>
 hipError_t launch_as(const ScanGradArgs& g, const Plan& p, hipStream_t s) {
     const ScanArgs& a = g.f;
-    const int64_t wgs = p.items * p.sp.blocks;
-    const int64_t bc = (a.Bsz * a.q.L * a.G * S * 16 + 255) / 256;
-    if (wgs >= ((int64_t)1 << 31) || bc >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)wgs), wg(256), lanes(kScanThreads);
+    const int64_t wgs = p.items * p.sp.blocks, sums = sum_blocks(a.H, p.Np);
+    const int64_t finish = sums + bc_blocks(a.Bsz, a.q.L, a.G, p.Np);
+    if (!grid_fits(wgs, kScanThreads) || !grid_fits(finish, 256)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)wgs), lanes(kScanThreads);
     if (p.split) grad_kernel<T, S, O, true><<<grid, lanes, 0, s>>>(g, p.sp);
     grad_kernel<T, S, O, false><<<grid, lanes, 0, s>>>(g, p.sp);
-    grad_bc_kernel<T><<<dim3((unsigned)bc), wg, 0, s>>>(g, p.sp.part_bc, p.sp.per_group, S);
-    auto sum = [&](const float* part, int64_t cols, int64_t stride, int width, int kept, float* out) {
-        grad_sum_kernel<<<dim3((unsigned)((cols + kSumCols - 1) / kSumCols)), wg, 0, s>>>(part, p.items, cols, stride,
-                                                                                        width, kept, out);
-    };
-    sum(p.sp.part_a, a.H * p.Np, a.H * p.Np, (int)p.Np, (int)a.N, g.dA);
-    if (g.dD) sum(p.sp.part_d, a.H, 2 * a.H, 1, 1, g.dD);
-    if (g.ddelta_bias) sum(p.sp.part_d + a.H, a.H, 2 * a.H, 1, 1, g.ddelta_bias);
+    grad_finish_kernel<T><<<dim3((unsigned)finish), dim3(256), 0, s>>>(g, p.sp, S, (unsigned)sums);
     return hipGetLastError();
 }
 
@@ -525,12 +550,13 @@ hipError_t launch_of(const ScanGradArgs& g, const Plan& p, Order o, hipStream_t 
 
 size_t scan_grad_workspace_bytes(const Seqs& q, int64_t Bsz, int64_t H, int64_t N, int64_t G) {
     const Plan p = plan(q, Bsz, H, N, G);
-    return p.ends + p.sums + p.bc + p.pa + p.pd;
+    return p.ends + p.sums + p.bc + p.part;
 }
 
 bool scan_grad_fits(const Seqs& q, int64_t Bsz, int64_t H, int64_t N, int64_t G) {
     const Plan p = plan(q, Bsz, H, N, G);
-    return p.items * p.sp.blocks < ((int64_t)1 << 31) && Bsz * q.L * G * p.Np * 2 / 256 < ((int64_t)1 << 31) - 1;
+    return grid_fits(p.items * p.sp.blocks, kScanThreads) &&
+           grid_fits(sum_blocks(H, p.Np) + bc_blocks(Bsz, q.L, G, p.Np), 256);
 }
 
 hipError_t launch_scan_backward(int dtype, const ScanGradArgs& g, void* ws, hipStream_t s) {
@@ -545,8 +571,7 @@ hipError_t launch_scan_backward(int dtype, const ScanGradArgs& g, void* ws, hipS
     p.sp.ends = take(p.ends);
     p.sp.sums = take(p.sums);
     p.sp.part_bc = take(p.bc);
-    p.sp.part_a = take(p.pa);
-    p.sp.part_d = take(p.pd);
+    p.sp.part = take(p.part);
     const View3* views[] = {&a.u, &a.delta, &a.z, &g.dy, &g.du, &g.ddelta, &g.dz};
     const Order o = order_of(views, 7, a.H / a.G);
     if (dtype == SSM_F32) return launch_of<float>(g, p, o, s);

@@ -294,7 +294,7 @@ Plan plan(const Seqs& q, int64_t H, int64_t N, int64_t G) {
 template <class T, int S, Order O>
 hipError_t launch_as(const ScanArgs& a, const Plan& p, hipStream_t s) {
     const int64_t wgs = p.items * p.sp.blocks;
-    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(wgs, kScanThreads)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)wgs), wg(kScanThreads);
     if (p.split) scan_kernel<T, S, O, true><<<grid, wg, 0, s>>>(a, p.sp);
     scan_kernel<T, S, O, false><<<grid, wg, 0, s>>>(a, p.sp);
@@ -323,7 +323,7 @@ size_t scan_workspace_bytes(const Seqs& q, int64_t H, int64_t N, int64_t G) {
 
 bool scan_fits(const Seqs& q, int64_t H, int64_t N, int64_t G) {
     const Plan p = plan(q, H, N, G);
-    return p.items * p.sp.blocks < ((int64_t)1 << 31);
+    return grid_fits(p.items * p.sp.blocks, kScanThreads);
 }
 
 hipError_t launch_scan(int dtype, const ScanArgs& a, void* ws, hipStream_t s) {

@@ -178,7 +178,7 @@ hipError_t step_as(const StepArgs& a, hipStream_t s) {
     // four sequences per workgroup once that still gives every CU its workgroups
     const int R = NB <= 2 && a.Bsz / kBatch * blocks >= 1024 ? kBatch : 1;
     const int64_t wgs = (a.Bsz + R - 1) / R * blocks;
-    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(wgs, 256)) return hipErrorInvalidValue;
     if constexpr (NB <= 2) {
         if (R == kBatch) {
             step_kernel<T, NB, W4, kBatch><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, (int)blocks);
@@ -201,7 +201,7 @@ template <class T, int W>
 hipError_t conv_step_as(const ConvStepArgs& a, hipStream_t s) {
     constexpr int V = 4;
     const int64_t per_row = (a.H + V - 1) / V, wgs = (a.Bsz * per_row + 255) / 256;
-    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (!grid_fits(wgs, 256)) return hipErrorInvalidValue;
     conv_step_kernel<T, W, V><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, per_row);
     return hipGetLastError();
 }

@@ -188,6 +188,10 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -195,7 +199,7 @@ def _stream(device):
 def _check(t, name, dtype, shape, device):
     if t is None:
         return
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != tuple(shape):
         got = (None if not isinstance(t, torch.Tensor) else (t.dtype, tuple(t.shape)))
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {got}")
     if not t.is_cuda or t.device != device:
@@ -494,7 +498,8 @@ def _group_view(t):
 
 
 def _activation(t, name, dtype, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    # shape: a tuple
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
         got = (None if not isinstance(t, torch.Tensor) else (t.dtype, tuple(t.shape)))
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {got}")
     if t.device != device:
@@ -669,22 +674,25 @@ def causal_conv_step(u, weight, state, bias=None, silu=False, slots=None, y=None
     if (state is None) != (W == 1):
         raise ValueError("state: needed for every width but 1")
     rows = _states(state, "state", u.dtype, Bsz, slots, (H, W - 1), dev)
+    u_row = _row_stride(u, "u")
     with _on(dev):
         if y is None:
-            y = torch.empty((Bsz, H), dtype=u.dtype, device=dev)
-        _activation(y, "y", u.dtype, (Bsz, H), dev)
-        rc = lib.ssm_causal_conv_step(code, Bsz, H, W, int(silu), _ptr(u), _row_stride(u, "u"), _ptr(weight),
-                                      _ptr(bias), _ptr(state), _ptr(slots), rows or Bsz, _ptr(y),
-                                      _row_stride(y, "y"), _stream(dev))
+            y = torch.empty_like(u, memory_format=torch.contiguous_format)
+        else:
+            _activation(y, "y", u.dtype, (Bsz, H), dev)
+        rc = lib.ssm_causal_conv_step(code, Bsz, H, W, int(silu), u.data_ptr(), u_row, weight.data_ptr(),
+                                      _address(bias), _address(state), _address(slots), rows or Bsz, y.data_ptr(),
+                                      _row_stride(y, "y"), torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != OK:
         raise SSMError("ssm_causal_conv_step", rc)
     return dict(y=y, state=state)
 
 
 def _row_stride(t, name):
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    strides, shape = t.stride(), t.shape
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return strides[0] if shape[0] > 1 else 0
 
 
 def _selective(u, delta, A, B, C, D, z, delta_bias, softplus, x0):
@@ -810,17 +818,19 @@ def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softpl
     if x is None:
         raise ValueError("x: needed")
     rows = _states(x, "x", torch.float32, Bsz, slots, (H, N), dev)
+    u_row, delta_row, z_row = _row_stride(u, "u"), _row_stride(delta, "delta"), 0 if z is None else _row_stride(z, "z")
+    B_row, C_row = _row_stride(B, "B"), _row_stride(C, "C")
     with _on(dev):
         if y is None:
-            y = torch.empty((Bsz, H), dtype=u.dtype, device=dev)
-        _activation(y, "y", u.dtype, (Bsz, H), dev)
-        group = lambda t: t.stride(1) if G > 1 else 0  # noqa: E731
-        p = [None if t is None else t.data_ptr() for t in (u, delta, z, B, C, y)]
-        strides = [_row_stride(u, "u"), _row_stride(delta, "delta"), 0 if z is None else _row_stride(z, "z"),
-                   _row_stride(y, "y"), _row_stride(B, "B"), group(B), _row_stride(C, "C"), group(C)]
-        args = SelectiveToken(Bsz, H, N, G, code, int(softplus), None if slots is None else slots.data_ptr(), rows,
-                              *p, *strides, *(None if t is None else t.data_ptr() for t in (A, D, delta_bias, x)))
-        rc = lib.ssm_selective_step(args, _stream(dev))
+            y = torch.empty_like(u, memory_format=torch.contiguous_format)
+        else:
+            _activation(y, "y", u.dtype, (Bsz, H), dev)
+        args = SelectiveToken(Bsz, H, N, G, code, int(softplus), _address(slots), rows, u.data_ptr(),
+                              delta.data_ptr(), _address(z), B.data_ptr(), C.data_ptr(), y.data_ptr(), u_row,
+                              delta_row, z_row, _row_stride(y, "y"), B_row, B.stride(1) if G > 1 else 0, C_row,
+                              C.stride(1) if G > 1 else 0, A.data_ptr(), _address(D), _address(delta_bias),
+                              x.data_ptr())
+        rc = lib.ssm_selective_step(args, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != OK:
         raise SSMError("ssm_selective_step", rc)
     return dict(y=y, x=x)

@@ -35,10 +35,10 @@ def test_struct_layouts_match_the_header(tmp_path):
 
 def test_bytes():
     B = ssm.selective_bytes
-    # states every 16 steps, a row of H x 16 floats each
-    assert B(ssm.OP_SELECTIVE_SAVED, 2, 48, 16, 1, 33) == 2 * 3 * 48 * 16 * 4
-    assert B(ssm.OP_SELECTIVE_SAVED, 2, 48, 40, 1, 33) == 2 * 3 * 48 * 64 * 4
-    assert B(ssm.OP_SELECTIVE_SAVED, 1, 48, 16, 1, 33, 5, True) == (2 + 5) * 48 * 16 * 4
+    # states every 32 steps, a row of H x 16 floats each
+    assert B(ssm.OP_SELECTIVE_SAVED, 2, 48, 16, 1, 33) == 2 * 2 * 48 * 16 * 4
+    assert B(ssm.OP_SELECTIVE_SAVED, 2, 48, 40, 1, 33) == 2 * 2 * 48 * 64 * 4
+    assert B(ssm.OP_SELECTIVE_SAVED, 1, 48, 16, 1, 33, 5, True) == (1 + 5) * 48 * 16 * 4
     # enough sequences and channels: no chunks, no workspace
     assert B(ssm.OP_SELECTIVE_SCAN, 16, 4096, 16, 1, 2048) == 0
     assert B(ssm.OP_SELECTIVE_SCAN, 1, 64, 16, 1, 4096) > 0
@@ -63,6 +63,9 @@ def test_bytes():
     ((0, 1, 8, 16, 1, 1 << 31, 1, 0), UNSUPPORTED),
     ((3, 1, 8, 0, 1, 8, 1, 0), INVALID),
     ((3, 1, 8, 5, 1, 8, 1, 0), UNSUPPORTED),
+    ((0, 1 << 23, 64, 16, 1, 8, 1 << 23, 0), UNSUPPORTED),   # 2^32 threads in a launch
+    ((2, 1 << 23, 64, 16, 1, 8, 1 << 23, 0), UNSUPPORTED),
+    ((3, 1 << 24, 64, 4, 1, 8, 1 << 24, 0), UNSUPPORTED),
 ])
 def test_bytes_rejects(args, code):
     out = ctypes.c_size_t(123)
@@ -210,7 +213,7 @@ def _token(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(Bsz=0), INVALID), (dict(H=0), INVALID), (dict(N=0), INVALID), (dict(G=5), INVALID), (dict(dtype=4), INVALID),
-    (dict(N=65), UNSUPPORTED), (dict(Bsz=1 << 30), UNSUPPORTED), (dict(u=None), INVALID), (dict(x=None), INVALID),
+    (dict(N=65), UNSUPPORTED), (dict(Bsz=1 << 30), UNSUPPORTED), (dict(Bsz=1 << 24), UNSUPPORTED), (dict(u=None), INVALID), (dict(x=None), INVALID),
     (dict(y=FAKE + 1), INVALID), (dict(x=FAKE + 2), INVALID), (dict(slots=FAKE, n_slots=0), INVALID),
     (dict(slots=FAKE + 2), INVALID), (dict(u_stride=-1), INVALID), (dict(y_stride=0), INVALID),
     (dict(B_stride=1 << 32), UNSUPPORTED), (dict(slots=FAKE, n_slots=1 << 40), UNSUPPORTED),
