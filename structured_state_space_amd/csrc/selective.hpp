@@ -271,6 +271,24 @@ __device__ __forceinline__ int anew(int tid) {
     return tid;
 }
 
+// a kernel's first argument, read anew from where a launch leaves its arguments:
+// what a tile needs of it once is loaded then (scalar loads that hit their cache).
+// Kept in scalar registers it would spill, to be read back lane by lane from a
+// vector register, an instruction for each.
+template <class A>
+__device__ __forceinline__ A arguments() {
+    using Words = const __attribute__((address_space(4))) uint64_t*;
+    static_assert(sizeof(A) % 8 == 0, "whole words");
+    Words p = (Words)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    uint64_t w[sizeof(A) / 8];
+#pragma unroll
+    for (size_t i = 0; i < sizeof(A) / 8; ++i) w[i] = p[i];
+    A a;
+    __builtin_memcpy(&a, w, sizeof(A));
+    return a;
+}
+
 // B and C of a tile on their way to LDS in float32: row t holds, per pair k of a
 // lane's states, the eight lanes' {B, B, C, C}; a thread brings K elements of either
 template <class T, int S>

@@ -205,6 +205,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
             // the tile before this one, whole, flies while this one is run (the first
             // loads itself again where it is a whole one)
             if (tile > 0 || now == kTile) {
+                const ScanGradArgs ga = arguments<ScanGradArgs>();
+                const ScanArgs& a = ga.f;
+                const View3& gv = a.z.data ? a.z : a.u;
                 const int64_t back = tile > 0 ? kTile * (int64_t)sizeof(T) : 0;
                 up -= back * a.u.sl, dp -= back * a.delta.sl, zp -= back * gv.sl, gp -= back * ga.dy.sl;
                 Bp -= back * a.B.sl, Cp -= back * a.C.sl;
@@ -324,6 +327,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     __syncthreads();
                     // the workgroup's sums of dB and dC: the eight waves' in order
                     constexpr int64_t kOut = S * 16;  // of a step and group
+                    const ScanArgs a = arguments<ScanArgs>();
                     float* to = sp.part_bc + ((((int64_t)l.blk * a.Bsz + it.row) * a.q.L + t0) * a.G + l.g) * kOut;
 #pragma unroll
                     for (int mm = 0; mm < 2; ++mm) {
@@ -336,6 +340,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                     if (k + 1 < S / 2) __syncthreads();
                 }
                 // the tile's gradients
+                const ScanGradArgs ga = arguments<ScanGradArgs>();
                 const Mover<O> m(anew(l.tid), l.valid);
                 float ys[kOwn], gs[kOwn], as[kOwn], o[kOwn];
                 get_sums<O>(ys, ysum, m);
