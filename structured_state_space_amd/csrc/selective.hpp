@@ -148,6 +148,33 @@ inline int64_t item_count(const Seqs& q, int64_t Q) {
 // a launch has less than 2^32 threads in all
 inline bool grid_fits(int64_t wgs, int threads) { return wgs < ((int64_t)1 << 32) / threads; }
 
+// Steps of a chunk, a multiple of kTile, for `blocks` workgroups along the
+// channels; q.L or more: no chunks.  Chunks cost a launch over nearly all of the
+// steps more (0.65 of the forward pass, 0.25 of the backward), so they are made
+// where 512 workgroups, two to a CU, come out of `least` chunks or more.
+// Measured at 1024 channels (16 workgroups a row), N = 16, 4096 steps bf16, forward:
+// 8 rows 337 us whole, 249 in 4 chunks; 10 rows 337 and 311 in 3; 12 rows 338 and
+// 454 in 2.  Both directions, 2048 steps: 9 rows 738 whole and 669 with the backward
+// pass in 3, 12 rows 720 and 859 in 2.
+// N = 64 forward, whose workgroups have a CU to themselves: 8 rows 422 and 380 in 4,
+// 10 rows 422 and 502 in 3.
+// A chunk has four tiles where 256 workgroups come out of that (256 channels in 2
+// groups, N = 64, 8 rows x 1024 steps: 74 us against 87 with two tiles), else two
+// at least (256 channels, N = 64, 1 row x 2048 steps: 49 us against 66 with four).
+// Packed sequences count as one long one: they may be that.
+constexpr int kTile = 32;
+inline int64_t chunk_steps(const Seqs& q, int64_t blocks, int least) {
+    const int64_t total = blocks * (q.offsets ? 1 : q.S), chunks = 512 / total;
+    int64_t Q = q.L;
+    if (chunks >= (q.offsets ? 2 : least)) {
+        Q = (q.L + chunks - 1) / chunks;
+        const int64_t few = q.L / (4 * kTile) * total >= 256 ? 4 * kTile : 2 * kTile;
+        if (Q < few) Q = few;
+    }
+    Q = (Q + kTile - 1) / kTile * kTile;
+    return Q < ((int64_t)1 << 30) ? Q : (int64_t)1 << 30;
+}
+
 // ---- a workgroup of the scan kernels ----
 // 64 channels of one group, 32 steps to a tile, 512 threads in two roles.
 // Moving a tile: thread by thread four elements of every activation, in vector
@@ -156,7 +183,6 @@ inline bool grid_fits(int64_t wgs, int threads) { return wgs < ((int64_t)1 << 32
 // Running a tile: eight neighbouring lanes per channel, lane p the S states
 // n = p S + j; a wave has 8 channels.  (Lanes that loaded their own channel's steps
 // made 28 cache accesses per 64-lane load where the vectors make 8.)
-constexpr int kTile = 32;
 constexpr int kChannels = 64;
 constexpr int kScanThreads = kChannels * 8;
 constexpr int kOwn = 4;

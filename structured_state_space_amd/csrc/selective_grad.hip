@@ -496,20 +496,11 @@ struct Plan {
 };
 
 Plan plan(const Seqs& q, int64_t Bsz, int64_t H, int64_t N, int64_t G) {
-    constexpr int64_t kFew = 256, kMany = 512;
     Plan p;
     const int64_t Hg = H / G;
     p.sp.per_group = (int)((Hg + kChannels - 1) / kChannels);
     p.sp.blocks = (int)(G * p.sp.per_group);
-    const int64_t rows = q.offsets ? 1 : q.S;
-    int64_t Q = q.L;
-    if (q.offsets || rows * p.sp.blocks < kFew) {
-        const int64_t share = (q.L * rows * p.sp.blocks + kMany - 1) / kMany;
-        Q = share < q.L ? share : q.L;
-        if (Q < 2 * kTile) Q = 2 * kTile;
-    }
-    Q = (Q + kTile - 1) / kTile * kTile;
-    if (Q > ((int64_t)1 << 30)) Q = (int64_t)1 << 30;
+    const int64_t Q = chunk_steps(q, p.sp.blocks, 3);
     p.sp.Q = (int)Q;
     p.split = Q < q.L;
     p.items = p.sp.items = item_count(q, Q);
