@@ -188,10 +188,6 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -484,9 +480,26 @@ def hippo_dplr(kind, N, theta=1.0, B=None, C=None, want_v=False, device="cuda:0"
 # dense, in the order of the input they belong to.
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _queue(device):
+    # the current stream's handle, without the Stream object around it (1.9 us)
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _strides(t):
     # a dimension of one element has no stride
-    return [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    return [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)] if 1 in t.shape else t.stride()
+
+
+def _scratch(nbytes, device, workspace):
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    return _workspace(nbytes, device, workspace)
 
 
 def _view(t):
@@ -517,14 +530,15 @@ def _first(u, dims):
 def _like(t, empty=True):
     """A dense output for t [Bsz,...,L], with the steps stored last where t's are
     contiguous and first (behind the batch) elsewhere."""
-    make = torch.empty if empty else torch.zeros
     if t.stride(-1) == 1:
-        return make(t.shape, dtype=t.dtype, device=t.device)
-    if t.dim() == 3:
+        out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    elif t.dim() == 3:
         Bsz, H, L = t.shape
-        return make((Bsz, L, H), dtype=t.dtype, device=t.device).transpose(1, 2)
-    Bsz, G, N, L = t.shape
-    return make((Bsz, L, G, N), dtype=t.dtype, device=t.device).permute(0, 2, 3, 1)
+        out = torch.empty_strided((Bsz, H, L), (H * L, 1, H), dtype=t.dtype, device=t.device)
+    else:
+        Bsz, G, N, L = t.shape
+        out = torch.empty_strided((Bsz, G, N, L), (G * N * L, N, 1, G * N), dtype=t.dtype, device=t.device)
+    return out if empty else out.zero_()
 
 
 class _on:
@@ -616,9 +630,10 @@ def causal_conv(u, weight, bias=None, silu=False, state=None, state_out=None, wa
         seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows)
         if y is None:
             y = _like(u)
-        _activation(y, "y", u.dtype, (Bsz, H, L), dev)
-        rc = lib.ssm_causal_conv(code, seq, H, W, int(silu), _view(u), _ptr(weight), _ptr(bias), _ptr(state),
-                                 _ptr(state_out), _view(y), _stream(dev))
+        else:
+            _activation(y, "y", u.dtype, (Bsz, H, L), dev)
+        rc = lib.ssm_causal_conv(code, seq, H, W, int(silu), _view(u), _address(weight), _address(bias), _address(state),
+                                 _address(state_out), _view(y), _queue(dev))
     if rc != OK:
         raise SSMError("ssm_causal_conv", rc)
     return dict(y=y, state=state_out)
@@ -650,10 +665,10 @@ def causal_conv_backward(u, weight, dy, bias=None, silu=False, state=None, dstat
         dweight, dbias = f32(H, W), f32(H) if bias is not None else None
         dstate_in = f32(*tail) if want_dstate and W > 1 else None
         nbytes = selective_bytes(OP_CAUSAL_CONV_BACKWARD, Bsz, H, W, 1, L, seq.S, offsets is not None)
-        ws = _workspace(nbytes, dev, workspace)
-        rc = lib.ssm_causal_conv_backward(code, seq, H, W, int(silu), _view(u), _ptr(weight), _ptr(bias),
-                                          _ptr(state), _view(dy), _ptr(dstate), _view(du), _ptr(dweight),
-                                          _ptr(dbias), _ptr(dstate_in), _ptr(ws), nbytes, _stream(dev))
+        ws = _scratch(nbytes, dev, workspace)
+        rc = lib.ssm_causal_conv_backward(code, seq, H, W, int(silu), _view(u), _address(weight), _address(bias),
+                                          _address(state), _view(dy), _address(dstate), _view(du), _address(dweight),
+                                          _address(dbias), _address(dstate_in), _address(ws), nbytes, _queue(dev))
     if rc != OK:
         raise SSMError("ssm_causal_conv_backward", rc)
     return dict(du=du, dweight=dweight, dbias=dbias, dstate=dstate_in)
@@ -682,7 +697,7 @@ def causal_conv_step(u, weight, state, bias=None, silu=False, slots=None, y=None
             _activation(y, "y", u.dtype, (Bsz, H), dev)
         rc = lib.ssm_causal_conv_step(code, Bsz, H, W, int(silu), u.data_ptr(), u_row, weight.data_ptr(),
                                       _address(bias), _address(state), _address(slots), rows or Bsz, y.data_ptr(),
-                                      _row_stride(y, "y"), torch._C._cuda_getCurrentRawStream(dev.index))
+                                      _row_stride(y, "y"), _queue(dev))
     if rc != OK:
         raise SSMError("ssm_causal_conv_step", rc)
     return dict(y=y, state=state)
@@ -738,15 +753,16 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
         seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows or S)
         if y is None:
             y = _like(u)
-        _activation(y, "y", u.dtype, (Bsz, H, L), dev)
+        else:
+            _activation(y, "y", u.dtype, (Bsz, H, L), dev)
         nbytes = selective_bytes(OP_SELECTIVE_SCAN, Bsz, H, N, G, L, S, offsets is not None)
-        ws = _workspace(nbytes, dev, workspace) if nbytes else None
+        ws = _scratch(nbytes, dev, workspace) if nbytes else None
         saved, sbytes = None, 0
         if save:
             sbytes = selective_bytes(OP_SELECTIVE_SAVED, Bsz, H, N, G, L, S, offsets is not None)
             saved = torch.empty(sbytes, dtype=torch.uint8, device=dev)
-        rc = lib.ssm_selective_scan(seq, args, _view(y), _ptr(x_out), _ptr(saved), sbytes, _ptr(ws), nbytes,
-                                    _stream(dev))
+        rc = lib.ssm_selective_scan(seq, args, _view(y), _address(x_out), _address(saved), sbytes, _address(ws), nbytes,
+                                    _queue(dev))
     if rc != OK:
         raise SSMError("ssm_selective_scan", rc)
     return dict(y=y, x=x_out, saved=saved)
@@ -770,8 +786,8 @@ def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, delta_bias=No
         if saved is None:
             saved = torch.empty(sbytes, dtype=torch.uint8, device=dev)
             nbytes = selective_bytes(OP_SELECTIVE_SCAN, Bsz, H, N, G, L, S, packed)
-            ws = _workspace(nbytes, dev) if nbytes else None
-            rc = lib.ssm_selective_scan(seq, args, None, None, _ptr(saved), sbytes, _ptr(ws), nbytes, _stream(dev))
+            ws = _scratch(nbytes, dev, None) if nbytes else None
+            rc = lib.ssm_selective_scan(seq, args, None, None, _address(saved), sbytes, _address(ws), nbytes, _queue(dev))
             if rc != OK:
                 raise SSMError("ssm_selective_scan", rc)
         elif not (isinstance(saved, torch.Tensor) and saved.dtype == torch.uint8 and saved.device == dev
@@ -786,9 +802,9 @@ def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, delta_bias=No
         grads = SelectiveGrads(_view(du), _view(ddelta), _view(dz), _group_view(dB), _group_view(dC),
                                *(None if t is None else t.data_ptr() for t in (dA, dD, dbias, dx0)))
         nbytes = selective_bytes(OP_SELECTIVE_SCAN_BACKWARD, Bsz, H, N, G, L, S, packed)
-        ws = _workspace(nbytes, dev, workspace)
-        rc = lib.ssm_selective_scan_backward(seq, args, _ptr(saved), saved.numel(), _view(dy), _ptr(dx), grads,
-                                             _ptr(ws), nbytes, _stream(dev))
+        ws = _scratch(nbytes, dev, workspace)
+        rc = lib.ssm_selective_scan_backward(seq, args, _address(saved), saved.numel(), _view(dy), _address(dx), grads,
+                                             _address(ws), nbytes, _queue(dev))
     if rc != OK:
         raise SSMError("ssm_selective_scan_backward", rc)
     return dict(du=du, ddelta=ddelta, dA=dA, dB=dB, dC=dC, dD=dD, dz=dz, ddelta_bias=dbias, dx0=dx0)
@@ -830,7 +846,7 @@ def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softpl
                               delta_row, z_row, _row_stride(y, "y"), B_row, B.stride(1) if G > 1 else 0, C_row,
                               C.stride(1) if G > 1 else 0, A.data_ptr(), _address(D), _address(delta_bias),
                               x.data_ptr())
-        rc = lib.ssm_selective_step(args, torch._C._cuda_getCurrentRawStream(dev.index))
+        rc = lib.ssm_selective_step(args, _queue(dev))
     if rc != OK:
         raise SSMError("ssm_selective_step", rc)
     return dict(y=y, x=x)
