@@ -78,6 +78,15 @@ def test_conv(name, order, Bsz, H, L, W, act, bias, state):
     _check_conv(a, name, order, act, S.dense_spans(Bsz, L))
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [8, 9])
+def test_conv_long_walks(name, H):
+    # enough rows that a thread walks 64 steps and then part of the next 64
+    a = K.conv_inputs(45, name, 1030, H, 107, 4, state=True)
+    _check_conv(a, name, "tokens", True, S.dense_spans(1030, 107))
+    _check_conv_backward(a, name, "tokens", True, S.dense_spans(1030, 107))
+
+
 @pytest.mark.parametrize("name,order", [("bf16", "tokens"), ("f32", "rows"), ("f16", "mixed")])
 def test_conv_packed_and_ragged(name, order):
     offs = [3, 3, 4, 40, 42, 42, 300, 301]   # empty ones, one step, shorter than the window; steps on both sides in none
@@ -150,7 +159,7 @@ def _check_conv_backward(a, name, order, act, spans, **kw):
     want = S.conv_grad(a["u"], a["w"], a["bias"], act, a["state"], dy, dlast, spans)
     mag = S.conv_grad(a["u"], a["w"], a["bias"], act, a["state"], dy, dlast, spans, mag=True)
     # the slope's argument carries 2 W roundings of |w||u|, a slope's change is below
-    # half the argument's; then W or, for the parameters, at most 64 sums in float32
+    # half the argument's; then W or, for the parameters, at most 66 sums in float32 (64 of a walk, and the walks)
     rnd = 16 * W + 160
     amp = 1.0 + np.abs(a["w"]).sum(1).max() * np.abs(a["u"]).max()
     K.assert_near(_np(out["du"]), want["du"], amp * mag["du"], name, rnd, "du")
@@ -213,6 +222,9 @@ SCANS = [
     (2, 20, 50, 24, 1, True, True, True, True, True),       # two blocks of states
     (1, 9, 150, 40, 3, True, True, True, True, True),       # four blocks, the third half full
     (2, 33, 66, 64, 1, True, True, True, False, True),
+    (2, 10, 33, 33, 5, True, True, True, True, True),       # groups of fewer channels than a vector, 33 states
+    (1, 66, 64, 47, 1, True, True, True, True, False),      # two channels in the second block, whole tiles
+    (1, 8, 31, 17, 8, False, True, True, True, True),       # a group per channel
 ]
 
 
@@ -558,7 +570,85 @@ def test_training_step_against_differences():
     assert abs(diff - slope) <= 1e-3 * abs(slope), (diff, slope)
 
 
+def test_broadcast_inputs():
+    """Inputs that repeat along the batch, the channels, the states or the steps
+    (stride 0) give what their copies give, and so do the gradients."""
+    ssm = _ssm()
+    Bsz, H, N, L = 3, 12, 16, 70
+    g = torch.Generator(device=DEV).manual_seed(46)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    u, delta, z = r(1, H, L).expand(Bsz, H, L), r(Bsz, 1, L).expand(Bsz, H, L), r(Bsz, H, 1).expand(Bsz, H, L)
+    B, C = r(Bsz, 1, 1, L).expand(Bsz, 2, N, L), r(1, 2, N, 1).expand(Bsz, 2, N, L)
+    A, dy = -torch.rand((H, N), generator=g, device=DEV), r(Bsz, 1, 1).expand(Bsz, H, L)
+    w = torch.randn((H, 4), generator=g, device=DEV)
+
+    def step(f):
+        v = [f(t) for t in (u, delta, A, B, C)]
+        fw = ssm.selective_scan(*v, z=f(z), softplus=True, want_state=True)
+        bw = ssm.selective_scan_backward(*v, f(dy), z=f(z), softplus=True)
+        cv = ssm.causal_conv(f(u), w, silu=True)
+        cb = ssm.causal_conv_backward(f(delta), w, f(dy), silu=True)
+        dw = cb.pop("dweight")
+        return [t for d in (fw, bw, cv, cb) for t in d.values() if t is not None], dw
+
+    (got, dw), (want, dw_want) = step(lambda t: t), step(lambda t: t.contiguous())
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    # the two storage orders add a weight's 210 terms d_t u_t in different orders: at
+    # most 80 float32 additions in a row on either side (a row's 70 steps and the
+    # threads' sums; rows are added in float64), each off by half a step of at most
+    # the terms' magnitudes, |d| <= 1.1 |dy|
+    most = 1.1 * (dy.double().abs() * delta.double().abs().max()).sum((0, 2))
+    assert ((dw.double() - dw_want.double()).abs() <= 2 * 80 * 2.0 ** -24 * most[:, None]).all()
+    with pytest.raises(ssm.SSMError):   # an output must not repeat
+        ssm.causal_conv(u.contiguous(), w, y=torch.empty((1, H, L), dtype=u.dtype, device=DEV).expand(Bsz, H, L))
+
+
+def test_workspace_is_checked():
+    ssm = _ssm()
+    a = K.scan_inputs(47, "f32", 1, 6, 400, 16)
+    args, more = _scan_args(a, "f32", "rows")
+    n = ssm.selective_bytes(ssm.OP_SELECTIVE_SCAN, 1, 6, 16, 1, 400)
+    assert n > 0
+    ref = ssm.selective_scan(*args, **more)["y"]
+    for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2],
+                torch.empty(n - 1, dtype=torch.uint8, device=DEV)):
+        with pytest.raises(ValueError):
+            ssm.selective_scan(*args, **more, workspace=bad)
+    with pytest.raises(ssm.SSMError):   # not on a multiple of 256 bytes
+        ssm.selective_scan(*args, **more, workspace=torch.empty(n + 4, dtype=torch.uint8, device=DEV)[4:])
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    assert torch.equal(ssm.selective_scan(*args, **more, workspace=ws)["y"], ref)
+
+
 # ------------------------------------------------------ streams and graphs ----
+
+def test_two_streams_at_once():
+    """Calls with workspaces in flight on two streams keep to their own."""
+    ssm = _ssm()
+    sets = [_scan_args(K.scan_inputs(48 + i, "bf16", 1, 200, 3000, 16), "bf16", "tokens") for i in range(2)]
+
+    def step(args, more):
+        f = ssm.selective_scan(*args, **more, want_state=True, save=True)
+        b = ssm.selective_scan_backward(*args, args[0], **more, saved=f["saved"])
+        c = ssm.causal_conv_backward(args[0], W, args[1], silu=True)
+        return [v for d in (f, b, c) for k, v in d.items() if v is not None and k != "saved"]
+
+    W = torch.randn((200, 4), generator=torch.Generator(device=DEV).manual_seed(50), device=DEV)
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            for p, q in zip(g, want[i]):
+                assert torch.equal(p, q)
+
 
 def test_on_another_stream():
     ssm = _ssm()
