@@ -90,7 +90,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
     float A2[S], carry[S], dA[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : 0.0f;
+        // (behind the last state not 0: a chunk's sum of dt may be infinite)
+        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : -1.0f;
         carry[j] = dA[j] = 0.0f;
     }
     float dDsum[kOwn] = {}, dbsum[kOwn] = {}, dtsum[kOwn] = {};

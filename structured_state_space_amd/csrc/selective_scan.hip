@@ -102,7 +102,8 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     float A2[S], h[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : 0.0f;
+        // (behind the last state not 0: a chunk's sum of dt may be infinite)
+        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : -1.0f;
         h[j] = 0.0f;
     }
     const int64_t wrow = (int64_t)l.h * (8 * S) + p * S;  // in a workspace row [H, Np]

@@ -294,6 +294,33 @@ def test_scan_extreme_values():
     assert torch.equal(y, ref)
 
 
+def test_scan_of_huge_steps():
+    # a chunk's sum of dt passes float32's range: full decays, and nothing else
+    a = K.scan_inputs(52, "f32", 1, 5, 700, 3, gate=False, soft=False, bias=False, state=True)
+    a["delta"] = K.rounded(np.full_like(a["delta"], 1e37), "f32")
+    a["u"] = K.rounded(a["u"] * 1e-36, "f32")
+    spans = S.dense_spans(1, 700)
+    for order in ("rows", "tokens"):
+        args, more = _scan_args(a, "f32", order)
+        out = _ssm().selective_scan(*args, **more, want_state=True)
+        want, last, _ = K.oracle_scan(a, spans)
+        mag, mlast, _ = K.oracle_scan(a, spans, mag=True)
+        K.assert_near(_np(out["y"]), want, mag, "f32", K.steps_bound(1, 3), "y")
+        K.assert_near(_np(out["x"]), last, mlast, "f32", K.steps_bound(1, 3), "x")
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+def test_scan_backward_extreme_values(name):
+    # steps of length zero (delta -inf or the type's lowest value) hand gradients on
+    # and have none of their own; a step past softplus's threshold has slope one
+    a = K.scan_inputs(51, name, 2, 5, 70, 16, state=True)
+    a["delta"][0, :, 10:14] = -np.inf
+    a["delta"][:, 1, 30:66] = float(torch.finfo(K.torch_type(name)).min)
+    a["delta"][1, 0, 40] = 50.0
+    with np.errstate(over="ignore"):
+        _check_scan_backward(a, name, "tokens", S.dense_spans(2, 70))
+
+
 def test_scan_slots_and_state_in_place():
     ssm = _ssm()
     a = K.scan_inputs(20, "f32", 4, 6, 150, 16)
