@@ -493,7 +493,7 @@ int ssm_selective_scan_backward(const ssm_sequences* seq, const ssm_selective* p
 /*
  * The scan of one token per sequence, on states kept in x.
  *   u, delta, z, y [Bsz,H], rows u_stride, ... elements apart; z nullable
- *   B, C [Bsz,G,N], rows and groups B_stride, B_group, ... elements apart
+ *   B, C [Bsz,G,N], rows, groups and states B_stride, B_group, B_state, ... elements apart
  *   A [H,N], D, delta_bias [H] as above; x [Bsz or n_slots, H, N], updated
  * No workspace.
  */
@@ -504,7 +504,7 @@ typedef struct ssm_selective_token {
     int64_t n_slots;
     const void *u, *delta, *z, *B, *C;
     void* y;
-    int64_t u_stride, delta_stride, z_stride, y_stride, B_stride, B_group, C_stride, C_group;
+    int64_t u_stride, delta_stride, z_stride, y_stride, B_stride, B_group, B_state, C_stride, C_group, C_state;
     const float *A, *D, *delta_bias;
     float* x;
 } ssm_selective_token;

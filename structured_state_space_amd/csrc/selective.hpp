@@ -552,9 +552,9 @@ struct StepArgs {
     int softplus;
     const int32_t* slots;  // nullable
     int64_t n_slots;
-    const void *u, *delta, *z, *B, *C;  // [Bsz, H], [Bsz, G, N]; strides of rows (and groups) below
+    const void *u, *delta, *z, *B, *C;  // [Bsz, H], [Bsz, G, N]; strides of rows (groups, states) below
     void* y;
-    int64_t u_row, delta_row, z_row, y_row, B_row, B_group, C_row, C_group;
+    int64_t u_row, delta_row, z_row, y_row, B_row, B_group, B_state, C_row, C_group, C_state;
     const float *A, *D, *delta_bias;
     float* x;  // [states, H, N], updated
 };

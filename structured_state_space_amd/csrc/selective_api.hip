@@ -334,8 +334,8 @@ int ssm_selective_step(const ssm_selective_token* p, void* stream) {
     const void* words[] = {p->slots, p->A, p->D, p->delta_bias, p->x};
     for (const void* v : words)
         if (!aligned(v, 4)) return SSM_ERR_INVALID_ARGUMENT;
-    const int64_t strides[] = {p->u_stride, p->delta_stride, p->z_stride, p->y_stride,
-                               p->B_stride, p->B_group,      p->C_stride, p->C_group};
+    const int64_t strides[] = {p->u_stride, p->delta_stride, p->z_stride, p->y_stride, p->B_stride,
+                               p->B_group,  p->B_state,      p->C_stride, p->C_group,  p->C_state};
     for (int64_t s : strides)
         if (s < 0) return SSM_ERR_INVALID_ARGUMENT;
     if (p->y_stride == 0 && p->Bsz > 1) return SSM_ERR_INVALID_ARGUMENT;
@@ -352,7 +352,8 @@ int ssm_selective_step(const ssm_selective_token* p, void* stream) {
     a.n_slots = p->slots ? p->n_slots : p->Bsz;
     a.u = p->u, a.delta = p->delta, a.z = p->z, a.B = p->B, a.C = p->C, a.y = p->y;
     a.u_row = p->u_stride, a.delta_row = p->delta_stride, a.z_row = p->z_stride, a.y_row = p->y_stride;
-    a.B_row = p->B_stride, a.B_group = p->B_group, a.C_row = p->C_stride, a.C_group = p->C_group;
+    a.B_row = p->B_stride, a.B_group = p->B_group, a.B_state = p->B_state;
+    a.C_row = p->C_stride, a.C_group = p->C_group, a.C_state = p->C_state;
     a.A = p->A, a.D = p->D, a.delta_bias = p->delta_bias, a.x = p->x;
     return device_status(launch_selective_step(p->dtype, a, (hipStream_t)stream));
 }

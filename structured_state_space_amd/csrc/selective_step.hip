@@ -50,6 +50,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int blocks) {
     const int64_t h = cb * 64 + (threadIdx.x >> 2);
     if (h >= a.H) return;
     const int64_t g = h / (a.H / a.G);
+    const bool dense = a.B_state == 1 && a.C_state == 1;
     float x[R][NB][4], bv[R][NB][4], cv[R][NB][4], u[R], dt[R], z[R];
     int64_t at[R];
 #pragma unroll
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int blocks) {
         for (int nb = 0; nb < NB; ++nb) {
             const int n0 = nb * 16 + q * 4;
             load_states<W4>(x[r][nb], a.x + at[r], n0, N);
-            if (n0 + 4 <= N) {
+            if (dense && n0 + 4 <= N) {
                 const Vec4<T> vb = *reinterpret_cast<const Vec4<T>*>(Bp + n0);
                 const Vec4<T> vc = *reinterpret_cast<const Vec4<T>*>(Cp + n0);
 #pragma unroll
@@ -76,8 +77,8 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int blocks) {
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    bv[r][nb][j] = n0 + j < N ? to_f(Bp[n0 + j]) : 0.0f;
-                    cv[r][nb][j] = n0 + j < N ? to_f(Cp[n0 + j]) : 0.0f;
+                    bv[r][nb][j] = n0 + j < N ? to_f(Bp[(n0 + j) * a.B_state]) : 0.0f;
+                    cv[r][nb][j] = n0 + j < N ? to_f(Cp[(n0 + j) * a.C_state]) : 0.0f;
                 }
             }
         }

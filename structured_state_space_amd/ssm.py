@@ -85,7 +85,7 @@ class SelectiveToken(ctypes.Structure):
                 + [("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int64)]
                 + [(k, ctypes.c_void_p) for k in ("u", "delta", "z", "B", "C", "y")]
                 + [(k, ctypes.c_int64) for k in ("u_stride", "delta_stride", "z_stride", "y_stride", "B_stride",
-                                                 "B_group", "C_stride", "C_group")]
+                                                 "B_group", "B_state", "C_stride", "C_group", "C_state")]
                 + [(k, ctypes.c_void_p) for k in ("A", "D", "delta_bias", "x")])
 
 
@@ -812,7 +812,7 @@ def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, delta_bias=No
 
 def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softplus=False, slots=None, y=None):
     """ssm_selective_step: the scan of one token per sequence, u, delta, z
-    [Bsz,H], B, C [Bsz,G,N] (rows any number of elements apart); x float32
+    [Bsz,H] (rows any number of elements apart), B, C [Bsz,G,N] (any strides); x float32
     [Bsz,H,N] (with slots, a pool [rows,H,N]) moves on in place.  Returns
     dict(y, x)."""
     dev, code = _first(u, 2)
@@ -835,7 +835,7 @@ def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softpl
         raise ValueError("x: needed")
     rows = _states(x, "x", torch.float32, Bsz, slots, (H, N), dev)
     u_row, delta_row, z_row = _row_stride(u, "u"), _row_stride(delta, "delta"), 0 if z is None else _row_stride(z, "z")
-    B_row, C_row = _row_stride(B, "B"), _row_stride(C, "C")
+    B_strides, C_strides = _strides(B), _strides(C)
     with _on(dev):
         if y is None:
             y = torch.empty_like(u, memory_format=torch.contiguous_format)
@@ -843,9 +843,8 @@ def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softpl
             _activation(y, "y", u.dtype, (Bsz, H), dev)
         args = SelectiveToken(Bsz, H, N, G, code, int(softplus), _address(slots), rows, u.data_ptr(),
                               delta.data_ptr(), _address(z), B.data_ptr(), C.data_ptr(), y.data_ptr(), u_row,
-                              delta_row, z_row, _row_stride(y, "y"), B_row, B.stride(1) if G > 1 else 0, C_row,
-                              C.stride(1) if G > 1 else 0, A.data_ptr(), _address(D), _address(delta_bias),
-                              x.data_ptr())
+                              delta_row, z_row, _row_stride(y, "y"), *B_strides, *C_strides, A.data_ptr(),
+                              _address(D), _address(delta_bias), x.data_ptr())
         rc = lib.ssm_selective_step(args, _queue(dev))
     if rc != OK:
         raise SSMError("ssm_selective_step", rc)

@@ -463,6 +463,20 @@ def test_selective_step(name, Bsz, H, N, G, gate):
     assert out["x"] is x
 
 
+@pytest.mark.parametrize("Bsz,H,N,G", [(3, 130, 16, 2), (2, 12, 24, 4), (300, 1030, 16, 2), (2, 5, 1, 1)])
+def test_selective_step_strides(Bsz, H, N, G):
+    # B and C with the groups stored last, or one B for all states: what their copies give
+    ssm = _ssm()
+    g = torch.Generator(device=DEV).manual_seed(53)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    u, delta, B, C, b1 = r(Bsz, H), r(Bsz, H), r(Bsz, N, G).transpose(1, 2), r(Bsz, N, G).transpose(1, 2), r(Bsz, G, 1)
+    A, x = -torch.rand((H, N), generator=g, device=DEV), torch.randn((Bsz, H, N), generator=g, device=DEV)
+    for B in (B, b1.expand(Bsz, G, N)):
+        got = ssm.selective_step(u, delta, A, B, C, x.clone(), softplus=True)
+        want = ssm.selective_step(u, delta, A, B.contiguous(), C.contiguous(), x.clone(), softplus=True)
+        assert torch.equal(got["y"], want["y"]) and torch.equal(got["x"], want["x"])
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("Bsz,H,W,act,bias", [(1, 1, 4, True, True), (3, 67, 4, True, True), (5, 130, 3, False, False),
                                              (2, 48, 2, True, True), (2, 9, 1, True, True), (300, 1030, 4, True, True)])

@@ -207,7 +207,7 @@ def test_scan_backward_rejects(kw, code):
 def _token(**kw):
     base = dict(Bsz=2, H=8, N=16, G=2, dtype=ssm.F16, softplus=1, slots=None, n_slots=2, u=FAKE, delta=FAKE, z=FAKE,
                 B=FAKE, C=FAKE, y=FAKE, u_stride=8, delta_stride=8, z_stride=8, y_stride=8, B_stride=32, B_group=16,
-                C_stride=32, C_group=16, A=FAKE, D=FAKE, delta_bias=FAKE, x=FAKE)
+                B_state=1, C_stride=32, C_group=16, C_state=1, A=FAKE, D=FAKE, delta_bias=FAKE, x=FAKE)
     return ssm.lib.ssm_selective_step(ssm.SelectiveToken(**{**base, **kw}), None)
 
 
@@ -215,7 +215,7 @@ def _token(**kw):
     (dict(Bsz=0), INVALID), (dict(H=0), INVALID), (dict(N=0), INVALID), (dict(G=5), INVALID), (dict(dtype=4), INVALID),
     (dict(N=65), UNSUPPORTED), (dict(Bsz=1 << 30), UNSUPPORTED), (dict(Bsz=1 << 24), UNSUPPORTED), (dict(u=None), INVALID), (dict(x=None), INVALID),
     (dict(y=FAKE + 1), INVALID), (dict(x=FAKE + 2), INVALID), (dict(slots=FAKE, n_slots=0), INVALID),
-    (dict(slots=FAKE + 2), INVALID), (dict(u_stride=-1), INVALID), (dict(y_stride=0), INVALID),
+    (dict(slots=FAKE + 2), INVALID), (dict(u_stride=-1), INVALID), (dict(B_state=-1), INVALID), (dict(C_state=1 << 32), UNSUPPORTED), (dict(y_stride=0), INVALID),
     (dict(B_stride=1 << 32), UNSUPPORTED), (dict(slots=FAKE, n_slots=1 << 40), UNSUPPORTED),
 ])
 def test_step_rejects(kw, code):
