@@ -67,6 +67,28 @@ __device__ __forceinline__ void store_v(const float (&r)[V], T* p, int64_t sh, i
     }
 }
 
+// the first n of N consecutive elements
+template <class T, int N>
+__device__ __forceinline__ void load_line(VecN<T, N>& r, const T* p, int n) {
+    if (n == N) {
+        r = *reinterpret_cast<const VecN<T, N>*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) r.v[i] = p[i];
+    }
+}
+template <class T, int N>
+__device__ __forceinline__ void store_line(T* p, const VecN<T, N>& r, int n) {
+    if (n == N) {
+        *reinterpret_cast<VecN<T, N>*>(p) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = r.v[i];
+    }
+}
+
 // V channels' weights and biases
 template <int W, int V>
 __device__ __forceinline__ void load_weights(float (&w)[W][V], float (&b)[V], const float* weight, const float* bias,
@@ -132,27 +154,54 @@ __global__ __launch_bounds__(256) void conv_tokens_kernel(ConvArgs a, Geometry g
     const int64_t first = (int64_t)it.beg + (int64_t)it.c * geo.Q + seg * geo.walk;  // this thread's steps
     const int64_t last = min((int64_t)it.end, first + geo.walk);
 
-    float w[W][V], b[V], past[W > 1 ? W - 1 : 1][V];
+    float w[W][V], b[V], past[W > 1 ? W - 1 : 1][V] = {};
     load_weights<W, V>(w, b, a.weight, a.bias, h, n);
     const T* u = (const T*)a.u.data + it.row * a.u.sb + h * a.u.sh;
     T* y = (T*)a.y.data + it.row * a.y.sb + h * a.y.sh;
+    // past[k]: the input W - 1 - k steps before `first`; a walk is longer than W - 1
+    // steps, so it is in u for every thread but the sequence's first
+    if constexpr (W > 1) {
+        if (it.c == 0 && seg == 0) {
+            VecN<T, V*(W - 1)> old, next;
+            const int64_t at = (it.state * a.H + h) * (W - 1);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {  // past[k]: the input W - 1 - k steps before `first`
-        const int64_t t = first - (W - 1) + k;
-        if (first < last && t >= it.beg) {
-            load_v<T, V>(past[k], u + t * a.u.sl, a.u.sh, n);
-        } else {
+            for (int i = 0; i < V * (W - 1); ++i) old.v[i] = from_f<T>(0.0f);
+            if (a.state_in) load_line<T, V*(W - 1)>(old, (const T*)a.state_in + at, n * (W - 1));
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                past[k][i] = first < last && i < n
-                                 ? old_input<T, W>((const T*)a.state_in, it.state, a.H, (int)h + i, (int)(it.beg - t))
-                                 : 0.0f;
+            for (int i = 0; i < V * (W - 1); ++i) past[i % (W - 1)][i / (W - 1)] = to_f(old.v[i]);
+            if (a.state_out) {  // (read above: it may be state_in)
+                const int len = it.end - it.beg;
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    const int t = len - (W - 1) + j;
+                    if (t >= 0) {
+                        const T* from = u + (it.beg + t) * a.u.sl;
+                        if (V > 1 && n == V) {
+                            const VecN<T, V> x = *reinterpret_cast<const VecN<T, V>*>(from);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) next.v[i * (W - 1) + j] = x.v[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                next.v[i * (W - 1) + j] = i < n ? from[i * a.u.sh] : from_f<T>(0.0f);
+                        }
+                    } else {  // t + W - 1 = len + j
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            next.v[i * (W - 1) + j] = old.v[i * (W - 1)];
+#pragma unroll
+                            for (int k = 1; k < W - 1; ++k)
+                                if (t + W - 1 == k) next.v[i * (W - 1) + j] = old.v[i * (W - 1) + k];
+                        }
+                    }
+                }
+                store_line<T, V*(W - 1)>((T*)a.state_out + at, next, n * (W - 1));
+            }
+        } else if (first < last) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+                load_v<T, V>(past[k], u + (first - (W - 1) + k) * a.u.sl, a.u.sh, n);
         }
-    }
-    if (it.c == 0 && seg == 0) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) hand_on<T, W>(a, it, (int)h + i);
     }
     auto step = [&](const float (&x)[V], float (&o)[V]) {
 #pragma unroll
