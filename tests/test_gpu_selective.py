@@ -645,6 +645,65 @@ def test_broadcast_inputs():
         ssm.causal_conv(u.contiguous(), w, y=torch.empty((1, H, L), dtype=u.dtype, device=DEV).expand(Bsz, H, L))
 
 
+def _far(t, stride):
+    """`t` [Bsz, ..., L] with batch rows, or its steps if it has one row, `stride` elements apart."""
+    moved = t.movedim(-1, 1).contiguous()                          # [Bsz, L, ...]
+    apart = list(moved.stride())
+    apart[0 if t.shape[0] > 1 else 1] = stride
+    n = sum((d - 1) * v for d, v in zip(moved.shape, apart)) + 1
+    out = torch.empty(n, dtype=t.dtype, device=DEV).as_strided(moved.shape, apart)
+    return out.copy_(moved).movedim(1, -1)
+
+
+@pytest.mark.parametrize("Bsz,L,stride", [(2, 70, 2**31 + 64), (1, 600, 2**22)])
+def test_offsets_past_32_bits(Bsz, L, stride):
+    """Rows further apart than 2^31 elements, and steps that end there: what dense
+    copies give, bit for bit."""
+    ssm = _ssm()
+    a = K.scan_inputs(54, "bf16", Bsz, 72, L, 16, state=True)
+    c = K.conv_inputs(55, "bf16", Bsz, 72, L, 4, state=True)
+    args, more = _scan_args(a, "bf16", "tokens")
+    u0, w, cb, state = _conv_args(c, "bf16", "tokens")
+
+    def step(f):
+        fw = ssm.selective_scan(f(args[0]), f(args[1]), args[2], *args[3:], **more, want_state=True, y=f(args[0]))
+        bw = ssm.selective_scan_backward(f(args[0]), *args[1:], f(args[1]), **more)
+        cv = ssm.causal_conv(f(u0), w, cb, silu=True, state=state, want_state=True, y=f(u0))
+        cg = ssm.causal_conv_backward(f(u0), w, f(args[1]), cb, silu=True, state=state)
+        return [t.contiguous() for d in (fw, bw, cv, cg) for t in d.values() if t is not None]
+
+    for p, q in zip(step(lambda t: _far(t, stride)), step(lambda t: t.clone())):
+        assert torch.equal(p, q)
+
+
+def test_pool_past_32_bits():
+    ssm = _ssm()
+    H, N = 4096, 16
+    rows = 2**31 // (H * N) + 3
+    g = torch.Generator(device=DEV).manual_seed(56)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    x = torch.empty((rows, H, N), device=DEV)
+    conv = torch.empty((2**31 // (H * 3) + 3, H, 3), dtype=torch.bfloat16, device=DEV)
+    sx, sc = _int([rows - 1, 5]), _int([conv.shape[0] - 1, 5])
+    first, cfirst = torch.randn((2, H, N), generator=g, device=DEV), r(2, H, 3)
+    x[sx.long()], conv[sc.long()] = first, cfirst
+    u, delta, B, C, w = r(2, H), r(2, H), r(2, 1, N), r(2, 1, N), torch.randn((H, 4), generator=g, device=DEV)
+    A = -torch.rand((H, N), generator=g, device=DEV)
+    for args in ((u, delta, A, B, C), tuple(t if t is A else t[..., None] for t in (u, delta, A, B, C))):
+        if args[0].dim() == 2:
+            y = ssm.selective_step(*args, x, softplus=True, slots=sx)["y"]
+            want = ssm.selective_step(*args, first, softplus=True)
+        else:
+            y = ssm.selective_scan(*args, softplus=True, x0=x, x_out=x, slots=sx)["y"]
+            want = ssm.selective_scan(*args, softplus=True, x0=first, x_out=first)
+        assert torch.equal(y, want["y"]) and torch.equal(x[sx.long()], first)
+    y = ssm.causal_conv_step(u, w, conv, slots=sc)["y"]
+    assert torch.equal(y, ssm.causal_conv_step(u, w, cfirst)["y"]) and torch.equal(conv[sc.long()], cfirst)
+    y = ssm.causal_conv(u[..., None], w, state=conv, state_out=conv, slots=sc)["y"]
+    assert torch.equal(y, ssm.causal_conv(u[..., None], w, state=cfirst, state_out=cfirst)["y"])
+    assert torch.equal(conv[sc.long()], cfirst)
+
+
 def test_workspace_is_checked():
     ssm = _ssm()
     a = K.scan_inputs(47, "f32", 1, 6, 400, 16)
