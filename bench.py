@@ -16,6 +16,7 @@ this host.  --gpus N > 1 exits: the benchmark measures one GPU.
 from __future__ import annotations
 
 import argparse
+import gc
 import hashlib
 import json
 import math
@@ -639,6 +640,7 @@ def main():
         ssm.forward(d["Lambda"], d["P"], d["Q"], d["B"], Ct, d["dt"], d["D"], ut, y=y, status=status,
                     workspace=ws, events=events)
 
+    gc.collect()  # a full collection takes 35 ms here: not one that falls due in the timed steps
     for _ in range(args.warmup):
         step()
     torch.cuda.synchronize()
