@@ -10,9 +10,9 @@
 // for the sums, 4.1 TB/s; by rows, float32, 16 x 512 x 3000, width 3, 70 us and 5,
 // 3.9 TB/s.  A small call waits for its few loads: 1536 channels x 5096 packed steps,
 // f16, 13 us.
-//   tokens  channels contiguous: a thread holds V channels (16 bytes) and walks
-//           up to kMaxWalk steps with the W - 1 last inputs in registers; 64 lanes read
-//           1 KB of one step.  Any other strides take V = 1.
+//   tokens  channels contiguous: a thread holds 16 bytes of channels (backward two
+//           channels) and walks up to kMaxWalk steps with the W - 1 last inputs in
+//           registers; 64 lanes read 1 KB of one step.  Any other strides take one channel.
 //   rows    steps contiguous: a thread holds 8 steps of one channel and reads the
 //           steps around them again (an L1 hit).
 // Backward: dpre_t = dy_t silu'(pre_t) is recomputed, du_t sums W of them, so a
