@@ -502,6 +502,12 @@ __device__ __forceinline__ float silu_f(float v) {
 template <class T>
 constexpr bool kFine = sizeof(T) == 4;
 
+// a chunk's sum of dt, which may pass float32 where no dt does: times an A of 0 it has to be 0
+__device__ __forceinline__ float finite(float v) {
+    constexpr float kMost = 3.402823466e38f;
+    return __builtin_amdgcn_fmed3f(v, -kMost, kMost);
+}
+
 // ---- argument blocks ----
 struct ScanArgs {
     Seqs q;

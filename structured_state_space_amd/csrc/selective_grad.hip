@@ -97,8 +97,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
     float A2[S], carry[S], dA[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-        // (behind the last state not 0: a chunk's sum of dt may be infinite)
-        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : -1.0f;
+        // behind the last state nothing decays or grows, whatever the sign of dt
+        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : 0.0f;
         carry[j] = dA[j] = 0.0f;
     }
     float dDsum[kOwn] = {}, dbsum[kOwn] = {}, dtsum[kOwn] = {};
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
             const int64_t from = min(item + (chunks - 1 - it.c), sp.items - 1);
             if (from > item) load_states<S>(carry, sp.ends + from * wstep + wrow);  // with dx_out's part
             for (int64_t i = from - 1; i > item; --i) {
-                const float s = sp.sums[i * a.H + l.h];
+                const float s = finite(sp.sums[i * a.H + l.h]);
                 float e[S];
                 load_states<S>(e, sp.ends + i * wstep + wrow);
 #pragma unroll

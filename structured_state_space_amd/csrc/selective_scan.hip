@@ -112,8 +112,8 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     float A2[S], h[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-        // (behind the last state not 0: a chunk's sum of dt may be infinite)
-        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : -1.0f;
+        // behind the last state nothing decays or grows, whatever the sign of dt
+        A2[j] = p * S + j < N ? a.A[(int64_t)l.h * N + p * S + j] * kLog2e : 0.0f;
         h[j] = 0.0f;
     }
     const int64_t wrow = (int64_t)l.h * (8 * S) + p * S;  // in a workspace row [H, Np]
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         const int64_t first = item - it.c;
         load_states<S>(h, sp.ends + first * wstep + wrow);
         for (int64_t i = first + 1; i < item; ++i) {
-            const float s = sp.sums[i * a.H + l.h];
+            const float s = finite(sp.sums[i * a.H + l.h]);
             float e[S];
             load_states<S>(e, sp.ends + i * wstep + wrow);
 #pragma unroll
