@@ -502,10 +502,15 @@ __device__ __forceinline__ float silu_f(float v) {
 template <class T>
 constexpr bool kFine = sizeof(T) == 4;
 
-// a chunk's sum of dt, which may pass float32 where no dt does: times an A of 0 it has to be 0
-__device__ __forceinline__ float finite(float v) {
-    constexpr float kMost = 3.402823466e38f;
-    return __builtin_amdgcn_fmed3f(v, -kMost, kMost);
+// x exp2(s A2): a state (or gradient) over a chunk whose steps add up to s.  The sum may
+// pass float32 where no step does (with an A of 0 the factor stays 1), and so may the
+// factor where x is small or zero, so it is put together as a fraction of one step and
+// a power of two, which ldexp applies over x's whole range.
+__device__ __forceinline__ float over_chunk(float x, float s, float A2) {
+    constexpr float kMost = 3.402823466e38f, kFar = 1024.0f;  // 2^1024 takes any float out of range
+    const float e = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(s, -kMost, kMost) * A2, -kFar, kFar);
+    const float whole = rintf(e);
+    return __builtin_amdgcn_ldexpf(x * __builtin_amdgcn_exp2f(e - whole), (int)whole);
 }
 
 // ---- argument blocks ----

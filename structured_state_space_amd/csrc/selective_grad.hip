@@ -121,11 +121,11 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
             const int64_t from = min(item + (chunks - 1 - it.c), sp.items - 1);
             if (from > item) load_states<S>(carry, sp.ends + from * wstep + wrow);  // with dx_out's part
             for (int64_t i = from - 1; i > item; --i) {
-                const float s = finite(sp.sums[i * a.H + l.h]);
+                const float s = sp.sums[i * a.H + l.h];
                 float e[S];
                 load_states<S>(e, sp.ends + i * wstep + wrow);
 #pragma unroll
-                for (int j = 0; j < S; ++j) carry[j] = fmaf(__builtin_amdgcn_exp2f(s * A2[j]), carry[j], e[j]);
+                for (int j = 0; j < S; ++j) carry[j] = over_chunk(carry[j], s, A2[j]) + e[j];
             }
         }
     }

@@ -133,11 +133,11 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
         const int64_t first = item - it.c;
         load_states<S>(h, sp.ends + first * wstep + wrow);
         for (int64_t i = first + 1; i < item; ++i) {
-            const float s = finite(sp.sums[i * a.H + l.h]);
+            const float s = sp.sums[i * a.H + l.h];
             float e[S];
             load_states<S>(e, sp.ends + i * wstep + wrow);
 #pragma unroll
-            for (int j = 0; j < S; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(s * A2[j]), h[j], e[j]);
+            for (int j = 0; j < S; ++j) h[j] = over_chunk(h[j], s, A2[j]) + e[j];
         }
     }
 

@@ -31,3 +31,34 @@ def test_negative_steps(order, N, L):
     a["A"] = K.rounded(-1e-3 * (1.0 + np.arange(N)) / N * np.exp(0.1 * r.standard_normal((5, N))), "f32")
     _check_scan(a, "f32", order, S.dense_spans(1, L))
     _check_scan_backward(a, "f32", order, S.dense_spans(1, L))
+
+
+# Growing states (dt A > 0): over a chunk of 64 steps they grow by e^96, more than
+# float32 holds, while every state and gradient stays in its range.
+
+@pytest.mark.parametrize("order", ["rows", "tokens", "mixed"])
+@pytest.mark.parametrize("N", [1, 16, 20, 40])
+def test_zero_states_through_growing_chunks(order, N):
+    # inputs in the last 20 of 700 steps only: the states before them are zero
+    a = _plain_inputs(63, 1, 5, 700, N)
+    a["delta"][...], a["A"][...], a["x0"][...] = 0.125, 12.0, 0.0
+    a["u"][..., :680] = 0.0
+    _check_scan(a, "f32", order, S.dense_spans(1, 700))
+    # from the end: C in the first 20 steps only, and no input at all
+    a["u"][...] = 0.0
+    a["C"][..., 20:] = 0.0
+    _check_scan_backward(a, "f32", order, S.dense_spans(1, 700), dlast=False)
+
+
+@pytest.mark.parametrize("order", ["rows", "tokens", "mixed"])
+@pytest.mark.parametrize("N", [1, 16, 20, 40])
+def test_small_states_through_a_growing_chunk(order, N):
+    # states of 2^-80 (e^-55) that grow by e^96 in the second chunk and shrink by e^-78
+    # in the third; gradients go through the same from the end
+    a = _plain_inputs(64, 1, 5, 180, N)
+    a["A"][...], a["u"][...] = 12.0, 0.0
+    a["delta"][..., :64], a["delta"][..., 64:128], a["delta"][..., 128:] = 2.0 ** -13, 0.125, -0.125
+    a["x0"] = K.rounded(a["x0"] * 2.0 ** -80, "f32")
+    a["C"][..., 64:] = 0.0
+    _check_scan(a, "f32", order, S.dense_spans(1, 180))
+    _check_scan_backward(a, "f32", order, S.dense_spans(1, 180))
