@@ -502,15 +502,20 @@ __device__ __forceinline__ float silu_f(float v) {
 template <class T>
 constexpr bool kFine = sizeof(T) == 4;
 
-// x exp2(s A2): a state (or gradient) over a chunk whose steps add up to s.  The sum may
-// pass float32 where no step does (with an A of 0 the factor stays 1), and so may the
-// factor where x is small or zero, so it is put together as a fraction of one step and
-// a power of two, which ldexp applies over x's whole range.
-__device__ __forceinline__ float over_chunk(float x, float s, float A2) {
-    constexpr float kMost = 3.402823466e38f, kFar = 1024.0f;  // 2^1024 takes any float out of range
-    const float e = __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(s, -kMost, kMost) * A2, -kFar, kFar);
-    const float whole = rintf(e);
-    return __builtin_amdgcn_ldexpf(x * __builtin_amdgcn_exp2f(e - whole), (int)whole);
+// x <- x exp2(s A2) + e: states (or gradients) over a chunk whose steps add up to s and
+// which ends in e from zero.  The sum may pass float32 where no step does (with an A of
+// 0 the factor stays 1), and so may the factor where x is zero, small or infinite: x
+// takes its square root twice, which is held finite and above zero.  (Factors beyond
+// 2^254 or below 2^-252 are cut there: normal x become infinite, or less than 2^-123.)
+template <int S>
+__device__ __forceinline__ void over_chunk(float (&x)[S], float s, const float (&A2)[S], const float (&e)[S]) {
+    constexpr float kMost = 3.402823466e38f;
+    const float half = 0.5f * __builtin_amdgcn_fmed3f(s, -kMost, kMost);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        const float root = __builtin_amdgcn_exp2f(__builtin_amdgcn_fmed3f(half * A2[j], -126.0f, 127.0f));
+        x[j] = fmaf(x[j] * root, root, e[j]);
+    }
 }
 
 // ---- argument blocks ----

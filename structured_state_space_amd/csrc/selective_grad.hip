@@ -124,8 +124,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void grad_kernel(ScanGradArgs ga, 
                 const float s = sp.sums[i * a.H + l.h];
                 float e[S];
                 load_states<S>(e, sp.ends + i * wstep + wrow);
-#pragma unroll
-                for (int j = 0; j < S; ++j) carry[j] = over_chunk(carry[j], s, A2[j]) + e[j];
+                over_chunk<S>(carry, s, A2, e);
             }
         }
     }

@@ -136,8 +136,7 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             const float s = sp.sums[i * a.H + l.h];
             float e[S];
             load_states<S>(e, sp.ends + i * wstep + wrow);
-#pragma unroll
-            for (int j = 0; j < S; ++j) h[j] = over_chunk(h[j], s, A2[j]) + e[j];
+            over_chunk<S>(h, s, A2, e);
         }
     }
 
