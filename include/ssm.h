@@ -371,6 +371,10 @@ int ssm_hippo_dplr(int kind, int64_t N, double theta,
  *     state: its sequence is skipped and its outputs are left as they were (the
  *     padding rows of a captured decode batch).  No two sequences of a call may
  *     name the same slot.
+ *   - An infinite or NaN input reaches its own channel from its step on, and the
+ *     others only where they share it (B, C; dB, dC of the group).  The scan's
+ *     outputs and states are infinite where the formulas give an infinity; that
+ *     channel's gradients are infinite or NaN.
  *   - The calls use no atomics: a repeated call gives the same bits.
  * ---------------------------------------------------------------------- */
 

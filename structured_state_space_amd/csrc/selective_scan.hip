@@ -31,12 +31,14 @@ namespace ssm {
 
 namespace {
 
-// one tile's recurrence; GUARD: only the first nt steps exist (a branch per step).
+// one tile's recurrence; GUARD: only the first nt steps exist (a branch per step), and
+// the lane's states from the real-th on are held at zero (where dt and dt u are finite,
+// they stay so by themselves).
 // `bc` is the lane's B and C of the tile, `step` its channel's {dt, dt u}; both come
 // from LDS two steps ahead of their use.
 template <int S, bool ENDS, bool GUARD>
 __device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], const float* bc, const float* step,
-                                         int nt, float* ysum, int c, int p) {
+                                         int nt, int real, float* ysum, int c, int p) {
     constexpr int kRow = Stage<float, S>::kRow, kGroup = S == 2 ? 2 : 1;
     const bool odd = p & 1, high = p & 2;
     float4 v[2][kGroup][S / 2];
@@ -67,6 +69,10 @@ __device__ __forceinline__ void run_tile(float (&h)[S], const float (&A2)[S], co
                     const float4 w = v[g & 1][i][k];
                     h[2 * k] = fmaf(__builtin_amdgcn_exp2f(dt * A2[2 * k]), h[2 * k], dx * w.x);
                     h[2 * k + 1] = fmaf(__builtin_amdgcn_exp2f(dt * A2[2 * k + 1]), h[2 * k + 1], dx * w.y);
+                    if (GUARD && !ENDS) {
+                        h[2 * k] = 2 * k < real ? h[2 * k] : 0.0f;
+                        h[2 * k + 1] = 2 * k + 1 < real ? h[2 * k + 1] : 0.0f;
+                    }
                     if (!ENDS) acc = fmaf(w.w, h[2 * k + 1], k ? fmaf(w.z, h[2 * k], acc) : w.z * h[2 * k]);
                 }
                 // the sum is done here: left alone, the compiler moves the sums of the two
@@ -96,6 +102,12 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     __shared__ __attribute__((aligned(16))) float lds[kTile * kRow];
     __shared__ __attribute__((aligned(16))) float steps[kTile * kPairRow];
     __shared__ __attribute__((aligned(16))) float ysum[ENDS ? 4 : kTile * kPairRow];
+    // an infinite or NaN dt u has come: its product with a padded state's B of zero is NaN,
+    // which the sum over states would take for the channel's.  From that tile on the
+    // guarded form runs, which holds padded states at zero (held in every tile, they
+    // would cost two of 22 instructions per step); watching for it costs 1 to 2% with
+    // padded states, nothing without.
+    __shared__ int beyond;
 
     const int cb = blockIdx.x % sp.blocks;
     const int64_t item = blockIdx.x / sp.blocks;
@@ -108,7 +120,8 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
 
     const Place l = place_of(cb, sp.per_group, a.H, a.G);
     const Mover<O> m(l.tid, l.valid);
-    const int p = l.p, N = (int)a.N;
+    const int p = l.p, N = (int)a.N, real = N - p * S;
+    const bool padded = N != 8 * S;  // some lanes have states that do not exist
     float A2[S], h[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
@@ -118,6 +131,11 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     }
     const int64_t wrow = (int64_t)l.h * (8 * S) + p * S;  // in a workspace row [H, Np]
     const int64_t wstep = a.H * (8 * S);
+
+    if (!ENDS && padded) {
+        if (l.tid == 0) beyond = 0;
+        __syncthreads();
+    }
 
     // start state
     if (it.c == 0) {
@@ -137,6 +155,10 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             float e[S];
             load_states<S>(e, sp.ends + i * wstep + wrow);
             over_chunk<S>(h, s, A2, e);
+        }
+        if (padded) {
+#pragma unroll
+            for (int j = 0; j < S; ++j) h[j] = j < real ? h[j] : 0.0f;
         }
     }
 
@@ -190,6 +212,12 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             if (ENDS) sum[i] += m.step(i) < nt ? d[i] : 0.0f;
             dx[i] = d[i] * uf[i];
         }
+        if (!ENDS && padded) {
+            bool in = true;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) in = in && fabsf(dx[i]) < __builtin_inff();
+            if (!in) beyond = 1;
+        }
         put_pairs<O>(steps, d, dx, m, l.valid);
         stage.template store<true, !ENDS>(sb, sc, lds, nt);
         __syncthreads();
@@ -209,10 +237,12 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     float* saved = !ENDS && a.saved && l.live
                        ? a.saved + (saved_row(a.q, it) + (beg - it.beg) / kTile) * wstep + wrow
                        : nullptr;
-    const int len = (int)max((int64_t)0, end - beg), whole = len / kTile, rest = len % kTile;
+    const int len = (int)max((int64_t)0, end - beg), whole = len / kTile;
+    int k = 0;
     if (whole > 0) load_tile();
-    for (int k = 0; k < whole; ++k) {
+    for (; k < whole; ++k) {
         prepare(kTile);
+        if (!ENDS && padded && __builtin_amdgcn_readfirstlane(beyond)) break;
         // the next whole tile's loads fly while this one is run (the last one loads
         // itself again: a branch here would make them wait)
         advance(k + 1 < whole ? kTile : 0);
@@ -222,22 +252,28 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
             store_states<S>(h, saved);
             saved += wstep;
         }
-        run_tile<S, ENDS, false>(h, A2, lds + p * 4, steps + pair_at(l.c), kTile, ysum, l.c, p);
+        run_tile<S, ENDS, false>(h, A2, lds + p * 4, steps + pair_at(l.c), kTile, real, ysum, l.c, p);
         __syncthreads();
         if (!ENDS) finish(kTile);
         yp += kTile * a.y.sl * (int64_t)sizeof(T);
     }
-    if (rest > 0) {
-        advance(whole > 0 ? kTile : 0);
-        m.template load_part<T>(ur, up, uo, a.u, rest);
-        m.template load_part<T>(dr, dp, dof, a.delta, rest);
-        if (!ENDS) m.template load_part<T>(zr, zp, zo, gv, rest);
-        stage.template load_part<true, !ENDS>(sb, sc, a.B, a.C, Bp, Cp, rest);
-        prepare(rest);
-        if (saved) store_states<S>(h, saved);
-        run_tile<S, ENDS, true>(h, A2, lds + p * 4, steps + pair_at(l.c), rest, ysum, l.c, p);
+    // the steps behind the last whole tile, and the tile left above with all behind it
+    for (bool on = k == whole && whole > 0; k * kTile < len; ++k, on = true) {
+        const int nt = min(kTile, len - k * kTile);
+        advance(on ? kTile : 0);
+        m.template load_part<T>(ur, up, uo, a.u, nt);
+        m.template load_part<T>(dr, dp, dof, a.delta, nt);
+        if (!ENDS) m.template load_part<T>(zr, zp, zo, gv, nt);
+        stage.template load_part<true, !ENDS>(sb, sc, a.B, a.C, Bp, Cp, nt);
+        prepare(nt);
+        if (saved) {
+            store_states<S>(h, saved);
+            saved += wstep;
+        }
+        run_tile<S, ENDS, true>(h, A2, lds + p * 4, steps + pair_at(l.c), nt, real, ysum, l.c, p);
         __syncthreads();
-        if (!ENDS) finish(rest);
+        if (!ENDS) finish(nt);
+        yp += kTile * a.y.sl * (int64_t)sizeof(T);
     }
 
     if (ENDS) {

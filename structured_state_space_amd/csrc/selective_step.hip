@@ -87,7 +87,8 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int blocks) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             x[nb][j] = fmaf(__builtin_amdgcn_exp2f(s * (A2[nb][j] * kLog2e)), x[nb][j], dx * bv[nb][j]);
-            y = fmaf(cv[nb][j], x[nb][j], y);
+            // (behind the last state 0, also where dt u is infinite)
+            y = fmaf(cv[nb][j], nb * 16 + q * 4 + j < N ? x[nb][j] : 0.0f, y);
         }
         store_states<W4>(x[nb], state, nb * 16 + q * 4, N);
     }

@@ -6,7 +6,7 @@ import pytest
 
 import oracle.selective_oracle as S
 from tests import selective_cases as K
-from tests.test_gpu_selective import _check_scan, _check_scan_backward
+from tests.test_gpu_selective import DEV, _check_scan, _check_scan_backward, _f32, _np, _scan_args, _ssm
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,50 @@ def test_small_states_through_a_growing_chunk(order, N):
     a["C"][..., 64:] = 0.0
     _check_scan(a, "f32", order, S.dense_spans(1, 180))
     _check_scan_backward(a, "f32", order, S.dense_spans(1, 180))
+
+
+def _assert_like_definition(got, want, mag, name, roundings, what):
+    """Infinities where the definition has them, with their signs; near it elsewhere."""
+    inf = np.isinf(want)
+    assert not np.isnan(want).any() and np.array_equal(got[inf], want[inf]), what
+    K.assert_near(np.where(inf, 0.0, got), np.where(inf, 0.0, want), np.where(inf, 0.0, mag), name, roundings, what)
+
+
+def _infinite_inputs(name, Bsz, L, N, at, value):
+    # all of one sign but u's and the gate's: every infinite sum has a sign
+    a = K.scan_inputs(65, name, Bsz, 5, L, N, gate=True, state=True)
+    for k in ("B", "C", "D"):
+        a[k] = np.abs(a[k]) + 0.5
+    a = {k: K.rounded(v, name) if k in ("B", "C") else K.rounded(v, "f32") if k == "D" else v for k, v in a.items()}
+    a["u"][0, 1, at], a["u"][0, 3, at] = value, -value
+    return a
+
+
+@pytest.mark.parametrize("name,order", [("f32", "rows"), ("bf16", "tokens"), ("f32", "mixed")])
+@pytest.mark.parametrize("L,at", [(40, 3), (40, 33), (200, 70), (200, 199)])
+@pytest.mark.parametrize("N", [1, 2, 3, 8, 16, 20, 33, 40])
+def test_infinite_inputs(name, order, L, at, N):
+    # an infinite u makes its channel's states and outputs infinite from its step on,
+    # however the state count fills the lanes, and leaves the other channels alone
+    a = _infinite_inputs(name, 1, L, N, at, np.inf)
+    args, more = _scan_args(a, name, order)
+    out = _ssm().selective_scan(*args, **more, want_state=True)
+    want, last, _ = K.oracle_scan(a, S.dense_spans(1, L))
+    mag, mlast, _ = K.oracle_scan(a, S.dense_spans(1, L), mag=True)
+    assert np.isinf(want).sum() == 2 * (L - at)
+    _assert_like_definition(_np(out["y"]), want, mag, name, K.steps_bound(L, N), "y")
+    _assert_like_definition(_np(out["x"]), last, mlast, "f32", K.steps_bound(L, N), "x")
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 2, 3, 8, 16, 20, 33, 40])
+def test_infinite_token(name, N):
+    a = _infinite_inputs(name, 2, 1, N, 0, np.inf)
+    tok = lambda v: torch.from_numpy(v[..., 0]).to(K.torch_type(name)).to(DEV)  # noqa: E731
+    x = _f32(a["x0"])
+    y = _ssm().selective_step(tok(a["u"]), tok(a["delta"]), _f32(a["A"]), tok(a["B"]), tok(a["C"]), x, D=_f32(a["D"]),
+                              z=tok(a["z"]), delta_bias=_f32(a["bias"]), softplus=True)["y"]
+    want, last, _ = K.oracle_scan(a, S.dense_spans(2, 1))
+    mag, mlast, _ = K.oracle_scan(a, S.dense_spans(2, 1), mag=True)
+    _assert_like_definition(_np(y), want[..., 0], mag[..., 0], name, K.steps_bound(1, N), "y")
+    _assert_like_definition(_np(x), last, mlast, "f32", K.steps_bound(1, N), "x")
