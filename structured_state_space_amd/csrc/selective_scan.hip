@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kScanThreads, S <= 4 ? 4 : 2) void scan_kernel(Scan
     // an infinite or NaN dt u has come: its product with a padded state's B of zero is NaN,
     // which the sum over states would take for the channel's.  From that tile on the
     // guarded form runs, which holds padded states at zero (held in every tile, they
-    // would cost two of 22 instructions per step); watching for it costs 1 to 2% with
+    // would cost two of 17 instructions per step); watching for it costs 1 to 2% with
     // padded states, nothing without.
     __shared__ int beyond;
 

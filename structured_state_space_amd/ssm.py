@@ -589,6 +589,12 @@ def _pool(a, b, names):
     return a or b
 
 
+def _any_slot(H):
+    # no state array: a slot only says whether its sequence runs, and any row that a
+    # pool of H channels can have does (the library takes pools up to 2^40 / H rows)
+    return min(2 ** 31, 2 ** 40 // H)
+
+
 def selective_bytes(op, Bsz, H, N, G, L, S=None, packed=False):
     """ssm_selective_bytes"""
     out = ctypes.c_size_t()
@@ -625,9 +631,7 @@ def causal_conv(u, weight, bias=None, silu=False, state=None, state_out=None, wa
             if slots is not None:
                 raise ValueError("want_state: with slots give state_out")
             state_out = torch.empty((S, *tail), dtype=u.dtype, device=dev)
-        if slots is not None and not rows:
-            rows = S  # no states: slots only say which sequences to skip
-        seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows)
+        seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows or _any_slot(H))
         if y is None:
             y = _like(u)
         else:
@@ -696,7 +700,7 @@ def causal_conv_step(u, weight, state, bias=None, silu=False, slots=None, y=None
         else:
             _activation(y, "y", u.dtype, (Bsz, H), dev)
         rc = lib.ssm_causal_conv_step(code, Bsz, H, W, int(silu), u.data_ptr(), u_row, weight.data_ptr(),
-                                      _address(bias), _address(state), _address(slots), rows or Bsz, y.data_ptr(),
+                                      _address(bias), _address(state), _address(slots), rows or _any_slot(H), y.data_ptr(),
                                       _row_stride(y, "y"), _queue(dev))
     if rc != OK:
         raise SSMError("ssm_causal_conv_step", rc)
@@ -750,7 +754,7 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     with _on(dev):
         if x_out is None and want_state:
             x_out = torch.empty((S, H, N), dtype=torch.float32, device=dev)
-        seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows or S)
+        seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows or _any_slot(H))
         if y is None:
             y = _like(u)
         else:
