@@ -556,17 +556,23 @@ class _on:
             self.switch.__exit__(*exc)
 
 
+def _count(Bsz, offsets):
+    """The number of sequences."""
+    if offsets is None:
+        return Bsz
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets: expected torch.int32 [S+1]")
+    return offsets.shape[0] - 1
+
+
 def _sequences(Bsz, L, device, offsets, lengths, slots, n_slots):
     """(ssm_sequences, the tensors it points to are the caller's)"""
-    S = Bsz
+    S = _count(Bsz, offsets)
     if offsets is not None:
         if lengths is not None:
             raise ValueError("offsets and lengths: give one of them")
         if Bsz != 1:
             raise ValueError("offsets: need one batch row")
-        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
-            raise ValueError("offsets: expected torch.int32 [S+1]")
-        S = offsets.shape[0] - 1
         _check(offsets, "offsets", torch.int32, (S + 1,), device)
     _check(lengths, "lengths", torch.int32, (S,), device)
     _check(slots, "slots", torch.int32, (S,), device)
@@ -580,6 +586,8 @@ def _states(t, name, dtype, S, slots, tail, device):
         return 0
     rows = S if slots is None or not isinstance(t, torch.Tensor) or t.dim() < 1 else t.shape[0]
     _check(t, name, dtype, (rows, *tail), device)
+    if rows == 0:
+        raise ValueError(f"{name}: has no rows")
     return rows
 
 
@@ -620,7 +628,7 @@ def causal_conv(u, weight, bias=None, silu=False, state=None, state_out=None, wa
     W = weight.shape[1]
     _check(weight, "weight", torch.float32, (H, W), dev)
     _check(bias, "bias", torch.float32, (H,), dev)
-    S = Bsz if offsets is None else offsets.shape[0] - 1
+    S = _count(Bsz, offsets)
     tail = (H, W - 1)
     if W == 1 and (state is not None or state_out is not None):
         raise ValueError("state: a convolution of width 1 has none")
@@ -730,6 +738,8 @@ def _selective(u, delta, A, B, C, D, z, delta_bias, softplus, x0):
     _check(A, "A", torch.float32, (H, N), dev)
     _check(D, "D", torch.float32, (H,), dev)
     _check(delta_bias, "delta_bias", torch.float32, (H,), dev)
+    if x0 is not None and not isinstance(x0, torch.Tensor):
+        raise ValueError("x0: expected a torch.float32 tensor")
     args = Selective(H, N, G, code, int(softplus), _view(u), _view(delta), _view(z), _group_view(B), _group_view(C),
                      *(None if t is None else t.data_ptr() for t in (A, D, delta_bias, x0)))
     return dev, Bsz, H, L, N, G, args
@@ -746,7 +756,7 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     selective_scan_backward needs.  offsets, lengths, slots as in the header.
     Returns dict(y, x, saved)."""
     dev, Bsz, H, L, N, G, args = _selective(u, delta, A, B, C, D, z, delta_bias, softplus, x0)
-    S = Bsz if offsets is None else offsets.shape[0] - 1
+    S = _count(Bsz, offsets)
     rows = _pool(_states(x0, "x0", torch.float32, S, slots, (H, N), dev),
                  _states(x_out, "x_out", torch.float32, S, slots, (H, N), dev), "x0 and x_out")
     if slots is not None and (save or (want_state and x_out is None)):

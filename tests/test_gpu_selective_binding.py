@@ -36,3 +36,32 @@ def test_slots_without_states():
     t = u[..., 0].contiguous()
     check(ssm.causal_conv_step(t, w[:, :1].contiguous(), None, slots=slots, y=y)["y"],
           ssm.causal_conv_step(t, w[:, :1].contiguous(), None)["y"])
+
+
+def test_refusals_name_the_argument():
+    ssm, r = _ssm(), _random(72)
+    u, w, A = r(1, 8, 20), r(8, 4), -torch.rand((8, 16), device=DEV)
+    B = r(1, 1, 16, 20)
+    scan = lambda **kw: ssm.selective_scan(u, u, A, B, B, **kw)  # noqa: E731
+    back = lambda **kw: ssm.selective_scan_backward(u, u, A, B, B, u, **kw)  # noqa: E731
+    conv = lambda **kw: ssm.causal_conv(u, w, **kw)  # noqa: E731
+    none = torch.empty((0, 8, 16), device=DEV), torch.empty((0, 8, 3), device=DEV)
+    for call, kw, name in [
+        (scan, dict(offsets=[0, 20]), "offsets"), (conv, dict(offsets=[0, 20]), "offsets"),
+        (scan, dict(offsets=torch.tensor(20, dtype=torch.int32, device=DEV)), "offsets"),
+        (conv, dict(offsets=_int([20])), "offsets"), (back, dict(offsets=[0, 20]), "offsets"),
+        (scan, dict(offsets=torch.tensor([0, 20], device=DEV)), "offsets"),      # int64
+        (scan, dict(x0=0.0), "x0"), (back, dict(x0=0.0), "x0"), (scan, dict(x_out=1), "x_out"),
+        (conv, dict(state=0.0), "state"), (scan, dict(lengths=[20]), "lengths"), (scan, dict(slots=[0]), "slots"),
+        # a pool without rows
+        (scan, dict(x0=none[0], x_out=none[0], slots=_int([0])), "x0"),
+        (scan, dict(x_out=none[0], slots=_int([0])), "x_out"),
+        (conv, dict(state=none[1], state_out=none[1], slots=_int([0])), "state"),
+    ]:
+        with pytest.raises(ValueError, match=f"^{name}"):
+            call(**kw)
+    t = u[..., 0].contiguous()
+    with pytest.raises(ValueError, match="^state"):
+        ssm.causal_conv_step(t, w, none[1], slots=_int([0]))
+    with pytest.raises(ValueError, match="^x"):
+        ssm.selective_step(t, t, A, B[..., 0].contiguous(), B[..., 0].contiguous(), none[0], slots=_int([0]))
