@@ -478,6 +478,15 @@ def hippo_dplr(kind, N, theta=1.0, B=None, C=None, want_v=False, device="cuda:0"
 # [Bsz, G, N, L]) with any strides: a projection's [Bsz, L, H] output goes in as
 # its .transpose(1, 2), a slice as it is.  Outputs that the call makes are
 # dense, in the order of the input they belong to.
+#
+# As everywhere in this binding, autograd does not see the calls: outputs never
+# require gradients, also where inputs do.  The gradients are the *_backward
+# calls, for use in a torch.autograd.Function or by hand.
+#
+# Where no sequence runs (steps that offsets or lengths leave out, rows whose slot
+# names no state) a y that is given stays as it was, and one that the call makes
+# holds what its memory held: give y=torch.zeros_like(u) where such places are read.
+# Gradients that a call makes are zero there.
 
 
 def _address(t):
@@ -619,8 +628,9 @@ def causal_conv(u, weight, bias=None, silu=False, state=None, state_out=None, wa
     [Bsz,H,L], weight float32 [H,W], bias [H].  state: the W - 1 inputs before
     the first step, [S,H,W-1] of u's type (with slots, a pool [rows,H,W-1]).
     The inputs before the next step go to state_out (which may be state), or to
-    a new tensor with want_state.  offsets, lengths, slots as in the header.
-    Returns dict(y, state)."""
+    a new tensor with want_state.  offsets, lengths, slots as in the header
+    (slots without states: a negative one skips its sequence).  y is not written
+    where no sequence runs, and not seen by autograd.  Returns dict(y, state)."""
     dev, code = _first(u, 3)
     Bsz, H, L = u.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
@@ -689,7 +699,8 @@ def causal_conv_backward(u, weight, dy, bias=None, silu=False, state=None, dstat
 def causal_conv_step(u, weight, state, bias=None, silu=False, slots=None, y=None):
     """ssm_causal_conv_step: the convolution of one token per sequence, u [Bsz,H]
     (rows any number of elements apart); state [Bsz,H,W-1] (with slots, a pool
-    [rows,H,W-1]) moves on in place.  Returns dict(y, state)."""
+    [rows,H,W-1]) moves on in place.  y's rows whose slot names no state are not
+    written.  Returns dict(y, state)."""
     dev, code = _first(u, 2)
     Bsz, H = u.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
@@ -753,8 +764,9 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     float32 [H].  x0: the states before the first step, float32 [S,H,N] (with
     slots, a pool [rows,H,N]); the states after the last go to x_out (which may
     be x0), or to a new tensor with want_state.  save keeps what
-    selective_scan_backward needs.  offsets, lengths, slots as in the header.
-    Returns dict(y, x, saved)."""
+    selective_scan_backward needs.  offsets, lengths, slots as in the header
+    (slots without states: a negative one skips its sequence).  y is not written
+    where no sequence runs, and not seen by autograd.  Returns dict(y, x, saved)."""
     dev, Bsz, H, L, N, G, args = _selective(u, delta, A, B, C, D, z, delta_bias, softplus, x0)
     S = _count(Bsz, offsets)
     rows = _pool(_states(x0, "x0", torch.float32, S, slots, (H, N), dev),
@@ -827,8 +839,8 @@ def selective_scan_backward(u, delta, A, B, C, dy, D=None, z=None, delta_bias=No
 def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softplus=False, slots=None, y=None):
     """ssm_selective_step: the scan of one token per sequence, u, delta, z
     [Bsz,H] (rows any number of elements apart), B, C [Bsz,G,N] (any strides); x float32
-    [Bsz,H,N] (with slots, a pool [rows,H,N]) moves on in place.  Returns
-    dict(y, x)."""
+    [Bsz,H,N] (with slots, a pool [rows,H,N]) moves on in place.  y's rows whose
+    slot names no state are not written.  Returns dict(y, x)."""
     dev, code = _first(u, 2)
     Bsz, H = u.shape
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
