@@ -151,22 +151,31 @@ inline bool grid_fits(int64_t wgs, int threads) { return wgs < ((int64_t)1 << 32
 // Steps of a chunk, a multiple of kTile, for `blocks` workgroups along the
 // channels; q.L or more: no chunks.  Chunks cost a launch over nearly all of the
 // steps more (0.65 of the forward pass, 0.25 of the backward), so they are made
-// where 512 workgroups, two to a CU, come out of `least` chunks or more.
+// where 512 workgroups come out of `least` chunks or more.
 // Measured at 1024 channels (16 workgroups a row), N = 16, 4096 steps bf16, forward:
 // 8 rows 337 us whole, 249 in 4 chunks; 10 rows 337 and 311 in 3; 12 rows 338 and
 // 454 in 2.  Both directions, 2048 steps: 9 rows 738 whole and 669 with the backward
 // pass in 3, 12 rows 720 and 859 in 2.
 // N = 64 forward, whose workgroups have a CU to themselves: 8 rows 422 and 380 in 4,
 // 10 rows 422 and 502 in 3.
+// The backward pass's second launch has one workgroup to a CU and takes 512 in two
+// rounds.  256 in its place, N = 16, that pass alone: 9 rows of 1024 x 2048 545 us
+// against 468 with 512, 1 x 2048 x 8192 375 and 355, 4 rows of 1024 x 2048 191 and 187;
+// but 1 x 256 x 16384 124 and 149.
 // A chunk has four tiles where 256 workgroups come out of that (256 channels in 2
 // groups, N = 64, 8 rows x 1024 steps: 74 us against 87 with two tiles), else two
-// at least (256 channels, N = 64, 1 row x 2048 steps: 49 us against 66 with four).
-// Packed sequences count as one long one: they may be that.
+// at least (256 channels, N = 64, 1 row x 2048 steps: 49 us against 66 with four;
+// but 64 channels, N = 16, x 16384: 87 and 60).
+// Packed sequences count as one long one: the host does not know their lengths.  4096
+// steps forward, N = 16, whole and in chunks, of one sequence, two (2100 and 1996)
+// and eight of 512: 8192 channels in 4 chunks 340 and 238, 183 and 245, 146 and 151 us;
+// 10240 channels in 3 342 and 313, 279 and 313, 194 and 188; 12288 in 2 341 and 387,
+// 280 and 392, 225 and 233.
 constexpr int kTile = 32;
 inline int64_t chunk_steps(const Seqs& q, int64_t blocks, int least) {
     const int64_t total = blocks * (q.offsets ? 1 : q.S), chunks = 512 / total;
     int64_t Q = q.L;
-    if (chunks >= (q.offsets ? 2 : least)) {
+    if (chunks >= least) {
         Q = (q.L + chunks - 1) / chunks;
         const int64_t few = q.L / (4 * kTile) * total >= 256 ? 4 * kTile : 2 * kTile;
         if (Q < few) Q = few;

@@ -250,3 +250,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         ssm.selective_step(u[..., 0], u[..., 0], torch.zeros(4, 16), torch.zeros(1, 1, 16), torch.zeros(1, 1, 16), None)
     with pytest.raises(ValueError):
         ssm.causal_conv_step(u, torch.zeros(4, 4), None)
+
+
+def test_packed_calls_are_split_by_the_same_rule():
+    B = ssm.selective_bytes
+    for op in (ssm.OP_SELECTIVE_SCAN, ssm.OP_SELECTIVE_SCAN_BACKWARD):
+        size = lambda H, S, packed, N=16: B(op, 1, H, N, 1, 4096, S, packed)  # noqa: E731
+        parts = lambda H, S: 4096 * (H // 64) * 32 * 4 + (S + 1) * H * 18 * 4  # noqa: E731  of the backward pass
+        whole = lambda H, S: 0 if op == ssm.OP_SELECTIVE_SCAN else parts(H, S)  # noqa: E731
+        # 64 channels a workgroup: three chunks of 10240 are worth it, two of 12288 are not
+        for H in (10240, 8192):
+            assert size(H, 2, True) > whole(H, 2) and size(H, 1, False) > whole(H, 0)
+        for H in (12288, 16384):
+            assert size(H, 2, True) == whole(H, 2) and size(H, 1, False) == whole(H, 0)
