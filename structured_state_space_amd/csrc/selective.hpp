@@ -473,8 +473,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLo = 1.925963033500717e-08f;  // log2(e) - kLog2e
 constexpr float kLn2 = 0.6931471805599453f;
 
-// exp(v).  FINE: to about one unit in the last place, the product v log2(e) in
-// two parts; else its rounding costs |v| / 2 units more, six instructions fewer.
+// exp(v).  FINE: to about one unit in the last place up to |v| = 80, the product
+// v log2(e) in two parts; else, and beyond 80 (where only results below 2e-35 or
+// their reciprocals show it), its rounding costs |v| / 2 units more, for six
+// instructions fewer.
 // Kernels take FINE for float32 activations; 16-bit ones are coarser by 2^13.
 template <bool FINE>
 __device__ __forceinline__ float exp_f(float v) {
@@ -487,9 +489,9 @@ __device__ __forceinline__ float exp_f(float v) {
 }
 
 // log(1 + exp(v)); above 20 it is v to float32.  log1p(e) = log(w) + (e - (w - 1))/w
-// with w = fl(1 + e); where e >= 1 the second term is below half a unit of the
-// first and is left out, elsewhere w stands for 1 in it (an error below a
-// quarter unit).  `slope` is e / (1 + e).
+// with w = fl(1 + e); where e >= 1 the second term, up to one unit of the result, is
+// left out, elsewhere w stands for 1 in it (up to 0.9 units, at e near 0.6).  With
+// exact exp and log the result is within 3.1 units.  `slope` is e / (1 + e).
 template <bool FINE, bool SLOPE = false>
 __device__ __forceinline__ float softplus_f(float v, float* slope = nullptr) {
     const float e = exp_f<FINE>(v);

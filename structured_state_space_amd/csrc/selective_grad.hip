@@ -29,9 +29,11 @@
 // The vector ALU bounds it: 27 instructions per step and state, of which the two
 // walks take 20, the sums over lanes included, and moving the elements the rest.  bf16,
 // N = 16, with gate, 4 x 4096 x 2048: 590 us and 18 for the last launch, vector
-// instructions issuing in 76% of the busy cycles at one workgroup (146 KB of LDS, two
-// waves per SIMD) per CU, 0.75 TB/s.  float32, N = 64, 8 x 256 x 1024 by rows: 37 us
-// for the ends, 131, and 17.
+// instructions issuing in 76% of the busy cycles at one workgroup (146 KB of LDS, 208
+// to 256 registers, two waves per SIMD) per CU, 0.75 TB/s.  What does not fit there: 21
+// to 49 scalars lie in vector registers, and with N > 32 some forms keep 8 to 36 bytes a
+// lane in scratch.  float32, N = 64, 8 x 256 x 1024 by rows: 37 us for the ends, 134,
+// and 17.
 #include "selective.hpp"
 
 namespace ssm {

@@ -21,7 +21,8 @@
 // moving and the sums over lanes.  bf16, N = 16, with gate: 1 row of 2048 channels x
 // 16384 steps 106 us for the ends and 163 for the rest, vector instructions issuing in
 // 97% of the busy cycles, 1.7 TB/s; 4 x 4096 x 2048 with its states saved, one workgroup
-// per CU, 192 us, 76%.
+// per CU, 192 us, 76%.  With N = 17 to 32, any strides (float32: by tokens too) keep 12
+// to 24 bytes a lane in scratch.
 // (Both launches of the first case, call for call: 332 us with four lanes per
 // channel, 308 with eight whose lanes loaded their own channels' steps, 280 with
 // the roles apart, 235 with LDS layouts off each other's banks and 32-bit distances.)
