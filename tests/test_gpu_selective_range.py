@@ -109,3 +109,25 @@ def test_infinite_token(name, N):
     mag, mlast, _ = K.oracle_scan(a, S.dense_spans(2, 1), mag=True)
     _assert_like_definition(_np(y), want[..., 0], mag[..., 0], name, K.steps_bound(1, N), "y")
     _assert_like_definition(_np(x), last, mlast, "f32", K.steps_bound(1, N), "x")
+
+
+@pytest.mark.parametrize("name,order", [("f32", "rows"), ("bf16", "tokens"), ("f32", "mixed")])
+@pytest.mark.parametrize("L,at", [(40, 3), (200, 70)])
+@pytest.mark.parametrize("N", [1, 3, 8, 16, 20, 40])
+def test_gradients_beside_infinite_inputs(name, order, L, at, N):
+    # an infinite u leaves the gradients of the other channels as they are, bit for bit,
+    # and its own channel's du, which holds no u
+    grads = []
+    for value in (1.0, np.inf):
+        a = _infinite_inputs(name, 1, L, N, at, value)
+        args, more = _scan_args(a, name, order)
+        dy = K.on_device(K.rounded(np.random.default_rng(66).standard_normal(a["u"].shape), name), name, order)
+        f = _ssm().selective_scan(*args, **more, save=True)
+        grads.append(_ssm().selective_scan_backward(*args, dy, **more, saved=f["saved"]))
+    others = [0, 2, 4]
+    for k in ("ddelta", "dz", "dx0"):
+        assert torch.equal(grads[0][k][:, others], grads[1][k][:, others]), k
+    for k in ("dA", "dD", "ddelta_bias"):
+        assert torch.equal(grads[0][k][others], grads[1][k][others]), k
+    assert torch.equal(grads[0]["du"], grads[1]["du"])
+    assert bool(torch.isfinite(grads[0]["du"]).all())
