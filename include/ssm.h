@@ -514,6 +514,136 @@ typedef struct ssm_selective_token {
 } ssm_selective_token;
 int ssm_selective_step(const ssm_selective_token* p, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the selective scan with one
+ * decay per head and step, on a state of N x P per head (its keys k, queries q
+ * and weights beta are the scan's B, C and dt, its values v the input u):
+ *   x_t = exp(g_t) x_{t-1} + beta_t k_t v_t^T
+ *   y_t = scale x_t^T q_t + D v_t
+ * q and k are shared by the H/G heads of a group.  Conventions as for the
+ * selective operators above (views, sequences, slots, outputs, no atomics), and
+ *   - q, k, v, y and their gradients are activations; g, beta, D, states and their
+ *     gradients are float.  g and beta may be broadcast (stride 0: a fixed decay
+ *     for each head); their gradients are those of every single element.
+ *   - g is the logarithm of the decay, at most 0; minus infinity resets the state.
+ *     Positive values are growth: products of exp(g) over 64 steps must then fit the
+ *     activations' type with room (float32 and bfloat16: sums of positive g up to 40
+ *     over 64 steps, float16 up to 4; beyond, the forward pass goes step by step and
+ *     the backward pass may overflow).
+ *   - Results of 16-bit types are rounded from sums of products whose one factor (the
+ *     weight of a pair of steps, the state) was rounded to the type; states, dg, dbeta
+ *     and dD come from float32 numbers or from two parts of 16 bits.
+ *   - An infinite or NaN input makes its own head (or, of q and k, its group) infinite
+ *     or NaN from its step on, and nothing before; the head's (group's) gradients are
+ *     infinite or NaN.
+ * Sizes: those of the selective operators, N <= 256, P <= 256.
+ * ---------------------------------------------------------------------- */
+
+/* Operation ids for ssm_linear_bytes. */
+#define SSM_OP_LINEAR_ATTENTION 0           /* workspace of ssm_linear_attention */
+#define SSM_OP_LINEAR_ATTENTION_BACKWARD 1  /* workspace of ssm_linear_attention_backward */
+#define SSM_OP_LINEAR_SAVED 2               /* the states ssm_linear_attention keeps for the backward pass */
+
+/* Bytes that a call needs beside its arguments, as ssm_selective_bytes. */
+int ssm_linear_bytes(int op, int dtype, int64_t Bsz, int64_t H, int64_t N, int64_t P, int64_t G, int64_t L, int64_t S,
+                     int packed, size_t* bytes);
+
+/* The arguments of ssm_linear_attention, and of its backward pass. */
+typedef struct ssm_linear {
+    int64_t H, G, N, P;       /* G divides H */
+    int32_t dtype;
+    float scale;              /* finite */
+    ssm_group_view q, k;      /* [Bsz,G,N,L] */
+    ssm_group_view v;         /* [Bsz,H,P,L]: head, value, step */
+    ssm_view g, beta;         /* float [Bsz,H,L]; beta.data nullable (= 1) */
+    const float* D;           /* [H], nullable (= 0) */
+    const float* x_in;        /* [S or n_slots, H, N, P], nullable (= 0) */
+} ssm_linear;
+
+/*
+ * Linear attention.  y: view [Bsz,H,P,L], nullable where x_out or saved is given.
+ * x_out [S or n_slots, H, N, P] nullable, may be x_in.  saved (nullable,
+ * SSM_OP_LINEAR_SAVED bytes): the states before every 64th step (float32: 32nd), for
+ * ssm_linear_attention_backward; not with slots.  Workspace: SSM_OP_LINEAR_ATTENTION.
+ */
+int ssm_linear_attention(const ssm_sequences* seq, const ssm_linear* p, const ssm_group_view* y, float* x_out,
+                         void* saved, size_t saved_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradients that ssm_linear_attention_backward writes. */
+typedef struct ssm_linear_grads {
+    ssm_group_view dq, dk;    /* [Bsz,G,N,L], summed over a group's heads */
+    ssm_group_view dv;        /* [Bsz,H,P,L] */
+    ssm_view dg, dbeta;       /* float [Bsz,H,L]; dbeta nullable, with beta only */
+    float* dD;                /* [H], nullable, with D only */
+    float* dx_in;             /* [S,H,N,P], nullable */
+} ssm_linear_grads;
+
+/*
+ * Gradients of ssm_linear_attention for the gradient dy of y and (nullable) dx_out of
+ * the final states, float [S,H,N,P].  p as in the forward call, saved as it wrote it for
+ * the same p and seq (no slots).  Gradients of steps outside every sequence are left as
+ * they were.  Workspace: SSM_OP_LINEAR_ATTENTION_BACKWARD.
+ */
+int ssm_linear_attention_backward(const ssm_sequences* seq, const ssm_linear* p, const void* saved, size_t saved_bytes,
+                                  const ssm_group_view* dy, const float* dx_out, const ssm_linear_grads* grads,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Linear attention of one token per sequence, on states kept in x.
+ *   q, k [Bsz,G,N], v, y [Bsz,H,P], g, beta [Bsz,H] with any strides (elements);
+ *   beta nullable; D [H] nullable; x [Bsz or n_slots, H, N, P], updated
+ * No workspace.
+ */
+typedef struct ssm_linear_token {
+    int64_t Bsz, H, G, N, P;
+    int32_t dtype;
+    float scale;
+    const int32_t* slots;  /* [Bsz], nullable */
+    int64_t n_slots;
+    const void *q, *k, *v;
+    void* y;
+    const float *g, *beta;
+    int64_t q_stride, q_group, q_key, k_stride, k_group, k_key, v_stride, v_head, v_value, y_stride, y_head, y_value;
+    int64_t g_stride, g_head, beta_stride, beta_head;
+    const float* D;
+    float* x;
+} ssm_linear_token;
+int ssm_linear_attention_step(const ssm_linear_token* p, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm over the channels of a group at every step, with a gate:
+ *   a = u  or (SSM_GATE_BEFORE)  u silu(z)
+ *   n = (a - mean a) / sqrt(var a + eps)  or (rms)  a / sqrt(mean a^2 + eps)
+ *   y = n weight + bias,  or (SSM_GATE_AFTER)  (n weight + bias) silu(z)
+ * u, z, y and their gradients are activations, views [Bsz,H,L] as above; a group
+ * has H/G channels.  Means, variances and sums are float32 (the parameters' gradients
+ * float64 over the workgroups), the mean is taken before the squares.  A call with L = 1
+ * is the form for single tokens.  An infinite or NaN input reaches its own step and group.
+ * ---------------------------------------------------------------------- */
+#define SSM_GATE_NONE 0
+#define SSM_GATE_BEFORE 1
+#define SSM_GATE_AFTER 2
+
+typedef struct ssm_norm {
+    int64_t Bsz, H, L, G;         /* G divides H */
+    int32_t dtype, rms, gate;
+    float eps;                    /* >= 0, finite */
+    ssm_view u, z;                /* [Bsz,H,L]; z with a gate only */
+    const float *weight, *bias;   /* [H], nullable (= 1, = 0) */
+} ssm_norm;
+
+int ssm_layer_norm(const ssm_norm* p, const ssm_view* y, void* stream);
+
+/*
+ * Gradients for the gradient dy of y, p as in the forward call: du, and dz with a gate
+ * only, views [Bsz,H,L]; dweight, dbias [H] float, each nullable (dbias is the sum
+ * over bias's place, also where bias is null).  Workspace where one of them is given:
+ * ssm_layer_norm_bytes.
+ */
+int ssm_layer_norm_bytes(int64_t Bsz, int64_t H, int64_t L, int64_t G, size_t* bytes);
+int ssm_layer_norm_backward(const ssm_norm* p, const ssm_view* dy, const ssm_view* du, const ssm_view* dz,
+                            float* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -41,11 +41,15 @@ EXPORTS = ("ssm_workspace_bytes", "ssm_transform_lengths", "ssm_forward_form", "
            "ssm_discretize", "ssm_kernel_gen", "ssm_fftconv", "ssm_forward", "ssm_forward_profiled", "ssm_step",
            "ssm_forward_complex", "ssm_hippo_dplr", "ssm_step_prepare", "ssm_step_prepared",
            "ssm_forward_noalloc", "ssm_selective_bytes", "ssm_causal_conv", "ssm_causal_conv_backward",
-           "ssm_causal_conv_step", "ssm_selective_scan", "ssm_selective_scan_backward", "ssm_selective_step")
+           "ssm_causal_conv_step", "ssm_selective_scan", "ssm_selective_scan_backward", "ssm_selective_step",
+           "ssm_linear_bytes", "ssm_linear_attention", "ssm_linear_attention_backward", "ssm_linear_attention_step",
+           "ssm_layer_norm_bytes", "ssm_layer_norm", "ssm_layer_norm_backward")
 
 # element types and operation ids of the selective operators
 F32, BF16, F16 = 0, 1, 2
 OP_SELECTIVE_SCAN, OP_SELECTIVE_SCAN_BACKWARD, OP_SELECTIVE_SAVED, OP_CAUSAL_CONV_BACKWARD = 0, 1, 2, 3
+OP_LINEAR_ATTENTION, OP_LINEAR_ATTENTION_BACKWARD, OP_LINEAR_SAVED = 0, 1, 2
+GATES = {"none": 0, "before": 1, "after": 2}
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
@@ -87,6 +91,38 @@ class SelectiveToken(ctypes.Structure):
                 + [(k, ctypes.c_int64) for k in ("u_stride", "delta_stride", "z_stride", "y_stride", "B_stride",
                                                  "B_group", "B_state", "C_stride", "C_group", "C_state")]
                 + [(k, ctypes.c_void_p) for k in ("A", "D", "delta_bias", "x")])
+
+
+class Linear(ctypes.Structure):
+    """ssm_linear"""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("H", "G", "N", "P")]
+                + [("dtype", ctypes.c_int32), ("scale", ctypes.c_float)] + [(k, GroupView) for k in ("q", "k", "v")]
+                + [(k, View) for k in ("g", "beta")] + [(k, ctypes.c_void_p) for k in ("D", "x_in")])
+
+
+class LinearGrads(ctypes.Structure):
+    """ssm_linear_grads"""
+    _fields_ = ([(k, GroupView) for k in ("dq", "dk", "dv")] + [(k, View) for k in ("dg", "dbeta")]
+                + [(k, ctypes.c_void_p) for k in ("dD", "dx_in")])
+
+
+class LinearToken(ctypes.Structure):
+    """ssm_linear_token"""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("Bsz", "H", "G", "N", "P")]
+                + [("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+                + [("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int64)]
+                + [(k, ctypes.c_void_p) for k in ("q", "k", "v", "y", "g", "beta")]
+                + [(k, ctypes.c_int64) for k in ("q_stride", "q_group", "q_key", "k_stride", "k_group", "k_key",
+                                                 "v_stride", "v_head", "v_value", "y_stride", "y_head", "y_value",
+                                                 "g_stride", "g_head", "beta_stride", "beta_head")]
+                + [(k, ctypes.c_void_p) for k in ("D", "x")])
+
+
+class Norm(ctypes.Structure):
+    """ssm_norm"""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("Bsz", "H", "L", "G")]
+                + [(k, ctypes.c_int32) for k in ("dtype", "rms", "gate")] + [("eps", ctypes.c_float)]
+                + [(k, View) for k in ("u", "z")] + [(k, ctypes.c_void_p) for k in ("weight", "bias")])
 
 
 class SSMError(RuntimeError):
@@ -148,6 +184,22 @@ def _load():
     lib.ssm_selective_scan_backward.restype = i32
     lib.ssm_selective_step.argtypes = [ctypes.POINTER(SelectiveToken), vp]
     lib.ssm_selective_step.restype = i32
+    group, linear = ctypes.POINTER(GroupView), ctypes.POINTER(Linear)
+    lib.ssm_linear_bytes.argtypes = [i32, i32] + [i64] * 7 + [i32, ctypes.POINTER(sz)]
+    lib.ssm_linear_bytes.restype = i32
+    lib.ssm_linear_attention.argtypes = [seqs, linear, group, vp, vp, sz, vp, sz, vp]
+    lib.ssm_linear_attention.restype = i32
+    lib.ssm_linear_attention_backward.argtypes = [seqs, linear, vp, sz, group, vp, ctypes.POINTER(LinearGrads), vp, sz, vp]
+    lib.ssm_linear_attention_backward.restype = i32
+    lib.ssm_linear_attention_step.argtypes = [ctypes.POINTER(LinearToken), vp]
+    lib.ssm_linear_attention_step.restype = i32
+    norm = ctypes.POINTER(Norm)
+    lib.ssm_layer_norm_bytes.argtypes = [i64] * 4 + [ctypes.POINTER(sz)]
+    lib.ssm_layer_norm_bytes.restype = i32
+    lib.ssm_layer_norm.argtypes = [norm, view, vp]
+    lib.ssm_layer_norm.restype = i32
+    lib.ssm_layer_norm_backward.argtypes = [norm, view, view, view, vp, vp, vp, sz, vp]
+    lib.ssm_layer_norm_backward.restype = i32
     return lib
 
 
@@ -875,6 +927,233 @@ def selective_step(u, delta, A, B, C, x, D=None, z=None, delta_bias=None, softpl
     if rc != OK:
         raise SSMError("ssm_selective_step", rc)
     return dict(y=y, x=x)
+
+
+# ---- linear attention and layer norm ----
+
+
+def _first_of(t, name, dims):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims or t.dtype not in _TYPES or not t.is_cuda:
+        raise ValueError(f"{name}: expected a float32, bfloat16 or float16 device tensor of {dims} dimensions")
+    if t.numel() == 0:
+        raise ValueError(f"{name}: has no elements")
+    return t.device, _TYPES[t.dtype]
+
+
+def linear_bytes(op, dtype, Bsz, H, N, P, G, L, S=None, packed=False):
+    """ssm_linear_bytes; dtype is a torch type"""
+    out = ctypes.c_size_t()
+    rc = lib.ssm_linear_bytes(int(op), _TYPES[dtype], int(Bsz), int(H), int(N), int(P), int(G), int(L),
+                              int(Bsz if S is None else S), int(bool(packed)), ctypes.byref(out))
+    if rc != OK:
+        raise SSMError("ssm_linear_bytes", rc)
+    return out.value
+
+
+def _linear(q, k, v, g, beta, D, scale, x0):
+    dev, code = _first_of(v, "v", 4)
+    Bsz, H, P, L = v.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q: expected [Bsz, G, N, L]")
+    G, N = q.shape[1], q.shape[2]
+    _activation(q, "q", v.dtype, (Bsz, G, N, L), dev)
+    _activation(k, "k", v.dtype, (Bsz, G, N, L), dev)
+    _activation(g, "g", torch.float32, (Bsz, H, L), dev)
+    if beta is not None:
+        _activation(beta, "beta", torch.float32, (Bsz, H, L), dev)
+    _check(D, "D", torch.float32, (H,), dev)
+    if x0 is not None and not isinstance(x0, torch.Tensor):
+        raise ValueError("x0: expected a torch.float32 tensor")
+    args = Linear(H, G, N, P, code, float(scale), _group_view(q), _group_view(k), _group_view(v), _view(g), _view(beta),
+                  _address(D), _address(x0))
+    return dev, Bsz, H, L, N, P, G, args
+
+
+def linear_attention(q, k, v, g, beta=None, D=None, scale=1.0, x0=None, x_out=None, want_state=False, save=False,
+                     offsets=None, lengths=None, slots=None, y=None, workspace=None):
+    """ssm_linear_attention: x_t = exp(g_t) x_{t-1} + beta_t k_t v_t^T,
+    y_t = scale x_t^T q_t + D v_t per head, over v [Bsz,H,P,L], q, k [Bsz,G,N,L]
+    (shared by H/G heads), g, beta float32 [Bsz,H,L] (any strides, also of 0), D
+    float32 [H].  x0: the states before the first step, float32 [S,H,N,P] (with
+    slots, a pool [rows,H,N,P]); the states after the last go to x_out (which may
+    be x0), or to a new tensor with want_state.  save keeps what
+    linear_attention_backward needs.  offsets, lengths, slots as for
+    selective_scan.  y is not written where no sequence runs, and not seen by
+    autograd.  Returns dict(y, x, saved)."""
+    dev, Bsz, H, L, N, P, G, args = _linear(q, k, v, g, beta, D, scale, x0)
+    S = _count(Bsz, offsets)
+    rows = _pool(_states(x0, "x0", torch.float32, S, slots, (H, N, P), dev),
+                 _states(x_out, "x_out", torch.float32, S, slots, (H, N, P), dev), "x0 and x_out")
+    if slots is not None and (save or (want_state and x_out is None)):
+        raise ValueError("slots: give x_out, and no save")
+    with _on(dev):
+        if x_out is None and want_state:
+            x_out = torch.empty((S, H, N, P), dtype=torch.float32, device=dev)
+        seq = _sequences(Bsz, L, dev, offsets, lengths, slots, rows or _any_slot(H))
+        if y is None:
+            y = _like(v)
+        else:
+            _activation(y, "y", v.dtype, (Bsz, H, P, L), dev)
+        sizes = (v.dtype, Bsz, H, N, P, G, L, S, offsets is not None)
+        nbytes = linear_bytes(OP_LINEAR_ATTENTION, *sizes)
+        ws = _scratch(nbytes, dev, workspace) if nbytes else None
+        saved, sbytes = None, 0
+        if save:
+            sbytes = linear_bytes(OP_LINEAR_SAVED, *sizes)
+            saved = torch.empty(sbytes, dtype=torch.uint8, device=dev)
+        rc = lib.ssm_linear_attention(seq, args, _group_view(y), _address(x_out), _address(saved), sbytes, _address(ws),
+                                      nbytes, _queue(dev))
+    if rc != OK:
+        raise SSMError("ssm_linear_attention", rc)
+    return dict(y=y, x=x_out, saved=saved)
+
+
+def linear_attention_backward(q, k, v, g, dy, beta=None, D=None, scale=1.0, x0=None, dx=None, saved=None, offsets=None,
+                              lengths=None, workspace=None):
+    """ssm_linear_attention_backward: gradients for dy [Bsz,H,P,L] of y and dx
+    (float32 [S,H,N,P], or None) of the final states; the other arguments as in the
+    forward call, saved from it (None: the states are computed again).  dg and
+    dbeta are [Bsz,H,L] also where g and beta are broadcast.  Returns dict(dq, dk,
+    dv, dg, dbeta, dD, dx0), None for the gradient of what was not given."""
+    dev, Bsz, H, L, N, P, G, args = _linear(q, k, v, g, beta, D, scale, x0)
+    _activation(dy, "dy", v.dtype, (Bsz, H, P, L), dev)
+    with _on(dev):
+        seq = _sequences(Bsz, L, dev, offsets, lengths, None, 0)
+        S = seq.S
+        _check(x0, "x0", torch.float32, (S, H, N, P), dev)
+        _check(dx, "dx", torch.float32, (S, H, N, P), dev)
+        sizes = (v.dtype, Bsz, H, N, P, G, L, S, offsets is not None)
+        sbytes = linear_bytes(OP_LINEAR_SAVED, *sizes)
+        if saved is None:
+            saved = torch.empty(sbytes, dtype=torch.uint8, device=dev)
+            nbytes = linear_bytes(OP_LINEAR_ATTENTION, *sizes)
+            ws = _scratch(nbytes, dev, None) if nbytes else None
+            rc = lib.ssm_linear_attention(seq, args, None, None, _address(saved), sbytes, _address(ws), nbytes, _queue(dev))
+            if rc != OK:
+                raise SSMError("ssm_linear_attention", rc)
+        elif not (isinstance(saved, torch.Tensor) and saved.dtype == torch.uint8 and saved.device == dev
+                  and saved.is_contiguous()):
+            raise ValueError(f"saved: expected the uint8 tensor of the forward call on {dev}")
+        whole = offsets is None and lengths is None
+        dq, dk, dv = _like(q, whole), _like(k, whole), _like(v, whole)
+        f32 = lambda *shape: (torch.empty if whole else torch.zeros)(shape, dtype=torch.float32, device=dev)  # noqa: E731
+        dg, dbeta = f32(Bsz, H, L), f32(Bsz, H, L) if beta is not None else None
+        dD, dx0 = f32(H) if D is not None else None, f32(S, H, N, P) if x0 is not None else None
+        grads = LinearGrads(_group_view(dq), _group_view(dk), _group_view(dv), _view(dg), _view(dbeta), _address(dD),
+                            _address(dx0))
+        nbytes = linear_bytes(OP_LINEAR_ATTENTION_BACKWARD, *sizes)
+        ws = _scratch(nbytes, dev, workspace)
+        rc = lib.ssm_linear_attention_backward(seq, args, _address(saved), saved.numel(), _group_view(dy), _address(dx),
+                                               grads, _address(ws), nbytes, _queue(dev))
+    if rc != OK:
+        raise SSMError("ssm_linear_attention_backward", rc)
+    return dict(dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta, dD=dD, dx0=dx0)
+
+
+def linear_attention_step(q, k, v, g, x, beta=None, D=None, scale=1.0, slots=None, y=None):
+    """ssm_linear_attention_step: one token per sequence, v [Bsz,H,P], q, k
+    [Bsz,G,N], g, beta float32 [Bsz,H] (any strides); x float32 [Bsz,H,N,P] (with
+    slots, a pool [rows,H,N,P]) moves on in place.  y's rows whose slot names no
+    state are not written.  Returns dict(y, x)."""
+    dev, code = _first_of(v, "v", 3)
+    Bsz, H, P = v.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected [Bsz, G, N]")
+    G, N = q.shape[1], q.shape[2]
+    _activation(q, "q", v.dtype, (Bsz, G, N), dev)
+    _activation(k, "k", v.dtype, (Bsz, G, N), dev)
+    _activation(g, "g", torch.float32, (Bsz, H), dev)
+    if beta is not None:
+        _activation(beta, "beta", torch.float32, (Bsz, H), dev)
+    _check(D, "D", torch.float32, (H,), dev)
+    _check(slots, "slots", torch.int32, (Bsz,), dev)
+    if x is None:
+        raise ValueError("x: needed")
+    rows = _states(x, "x", torch.float32, Bsz, slots, (H, N, P), dev)
+    with _on(dev):
+        if y is None:
+            y = torch.empty((Bsz, H, P), dtype=v.dtype, device=dev)
+        else:
+            _activation(y, "y", v.dtype, (Bsz, H, P), dev)
+        args = LinearToken(Bsz, H, G, N, P, code, float(scale), _address(slots), rows, q.data_ptr(), k.data_ptr(),
+                           v.data_ptr(), y.data_ptr(), g.data_ptr(), _address(beta), *_strides(q), *_strides(k),
+                           *_strides(v), *_strides(y), *_strides(g), *((0, 0) if beta is None else _strides(beta)),
+                           _address(D), x.data_ptr())
+        rc = lib.ssm_linear_attention_step(args, _queue(dev))
+    if rc != OK:
+        raise SSMError("ssm_linear_attention_step", rc)
+    return dict(y=y, x=x)
+
+
+def _steps_of(t):
+    """[Bsz,H] as [Bsz,H,1]"""
+    return t.unsqueeze(-1) if isinstance(t, torch.Tensor) and t.dim() == 2 else t
+
+
+def _norm(u, weight, bias, z, gate, rms, groups, eps):
+    if gate not in GATES:
+        raise ValueError("gate: expected 'before' or 'after'")
+    if isinstance(u, torch.Tensor) and u.dim() == 2:
+        u, z = _steps_of(u), _steps_of(z)
+    dev, code = _first(u, 3)
+    Bsz, H, L = u.shape
+    if z is not None:
+        _activation(z, "z", u.dtype, (Bsz, H, L), dev)
+    _check(weight, "weight", torch.float32, (H,), dev)
+    _check(bias, "bias", torch.float32, (H,), dev)
+    args = Norm(Bsz, H, L, int(groups), code, int(bool(rms)), 0 if z is None else GATES[gate], float(eps), _view(u),
+                _view(z), _address(weight), _address(bias))
+    return dev, u, args
+
+
+def layer_norm(u, weight=None, bias=None, z=None, gate="after", rms=False, groups=1, eps=1e-5, y=None):
+    """ssm_layer_norm: over the channels of each of `groups` groups of u [Bsz,H,L]
+    (or [Bsz,H], one token each), y = n weight + bias with n = (u - mean) /
+    sqrt(var + eps), or with rms u / sqrt(mean u^2 + eps); weight, bias float32 [H].
+    z (like u) gates with silu(z): the result (gate "after") or u itself
+    ("before").  Not seen by autograd.  Returns dict(y)."""
+    dev, steps, args = _norm(u, weight, bias, z, gate, rms, groups, eps)
+    with _on(dev):
+        if y is None:
+            out = _like(steps)
+            y = out.squeeze(-1) if u.dim() == 2 else out
+        else:
+            _activation(y, "y", u.dtype, tuple(u.shape), dev)
+            out = _steps_of(y)
+        rc = lib.ssm_layer_norm(args, _view(out), _queue(dev))
+    if rc != OK:
+        raise SSMError("ssm_layer_norm", rc)
+    return dict(y=y)
+
+
+def layer_norm_backward(u, dy, weight=None, bias=None, z=None, gate="after", rms=False, groups=1, eps=1e-5,
+                        workspace=None):
+    """ssm_layer_norm_backward: gradients for dy of y, the other arguments as in
+    the forward call (whose results are not needed).  Returns dict(du, dz, dweight,
+    dbias), None for the gradient of what was not given."""
+    dev, steps, args = _norm(u, weight, bias, z, gate, rms, groups, eps)
+    _activation(dy, "dy", u.dtype, tuple(u.shape), dev)
+    Bsz, H, L = steps.shape
+    with _on(dev):
+        du = _like(steps)
+        dz = _like(_steps_of(z)) if z is not None else None
+        f32 = lambda t: torch.empty((H,), dtype=torch.float32, device=dev) if t is not None else None  # noqa: E731
+        dweight, dbias = f32(weight), f32(bias)
+        ws, nbytes = None, 0
+        if weight is not None or bias is not None:
+            size = ctypes.c_size_t()
+            rc = lib.ssm_layer_norm_bytes(Bsz, H, L, int(groups), ctypes.byref(size))
+            if rc != OK:
+                raise SSMError("ssm_layer_norm_bytes", rc)
+            nbytes = size.value
+            ws = _scratch(nbytes, dev, workspace)
+        rc = lib.ssm_layer_norm_backward(args, _view(_steps_of(dy)), _view(du), _view(dz), _address(dweight),
+                                         _address(dbias), _address(ws), nbytes, _queue(dev))
+    if rc != OK:
+        raise SSMError("ssm_layer_norm_backward", rc)
+    if u.dim() == 2:
+        du, dz = du.squeeze(-1), None if dz is None else dz.squeeze(-1)
+    return dict(du=du, dz=dz, dweight=dweight, dbias=dbias)
 
 
 def to_device(params, device="cuda:0"):
