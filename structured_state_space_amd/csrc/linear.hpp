@@ -14,6 +14,12 @@ using i16x8 = short __attribute__((ext_vector_type(8)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 using u16x2 = unsigned short __attribute__((ext_vector_type(2)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+// 16 bytes anywhere that the element's alignment allows
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Words {
+    u32x4 v;
+};
 
 constexpr int64_t kMaxKeys = 256;
 constexpr int64_t kMaxValues = 256;
@@ -74,28 +80,28 @@ template <>
 __device__ __forceinline__ float frag_get<float>(const Frag<float>& f, int j) {
     return f.v[j];
 }
-// x = hi + lo to 16 (bf16) or 22 bits (f16); in float32 hi is x itself
+// Float32 numbers as sums of operands of the type: one in float32, two in f16 (22 bits), three
+// in bf16 (24 bits; two, 16 bits, left errors of 2.4e-6 in the states).
 template <class T>
-__device__ __forceinline__ void split(const float (&x)[8], Frag<T>& hi, Frag<T>& lo) {
-    float y[8], r[8];
+constexpr int kParts = sizeof(T) == 4 ? 1 : std::is_same<T, f16>::value ? 2 : 3;
+template <class T>
+__device__ __forceinline__ void split(const float (&x)[8], Frag<T> (&part)[kParts<T>]) {
+    float r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        // one number for both parts: a product would be rounded to f16 in one step for the
+        // one number for all parts: a product would be rounded to f16 in one step for the
         // first and by way of float32 for the second
-        y[j] = x[j];
-        asm("" : "+v"(y[j]));
+        r[j] = x[j];
+        if (kParts<T> > 1) asm("" : "+v"(r[j]));
     }
-    hi = frag_of<T>(y);
+    part[0] = frag_of<T>(r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = y[j] - frag_get<T>(hi, j);
-    lo = frag_of<T>(r);
+    for (int i = 1; i < kParts<T>; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] -= frag_get<T>(part[i - 1], j);
+        part[i] = frag_of<T>(r);
+    }
 }
-template <>
-__device__ __forceinline__ void split<float>(const float (&x)[8], Frag<float>& hi, Frag<float>&) {
-    hi = frag_of<float>(x);
-}
-template <class T>
-constexpr bool kSplit = sizeof(T) == 2;
 
 // ---- tiles of a chunk in LDS: one row per step, 16 bytes of room behind each ----
 template <class T>
@@ -152,19 +158,39 @@ __device__ __forceinline__ Frag<float> column_frag<float>(const float* p, int st
     return f;
 }
 
-// how a tensor [steps, columns] lies
-enum Lay : int { kByColumn, kByStep, kElement };  // columns contiguous, steps contiguous, neither
-inline Lay lay_of(const View4& v) { return v.sn == 1 ? kByColumn : v.sl == 1 ? kByStep : kElement; }
+// How a tensor [steps, columns] is read: vectors of 16 bytes of neighbouring columns (a whole
+// number of them), vectors of neighbouring steps (in whole chunks), or element by element.
+enum Lay : int { kByColumn, kByStep, kElement };
+// a tile of a call's tensors: strides in bytes where vectors are read
+struct Source {
+    const char* data = nullptr;
+    int64_t sb = 0, sg = 0, sn = 0, sl = 0;  // bytes
+    Lay lay = kElement;
+};
+inline Source source_of(const View4& v, int64_t columns, int64_t size) {
+    Source s;
+    s.data = (const char*)v.data;
+    s.sb = v.sb * size, s.sg = v.sg * size, s.sn = v.sn * size, s.sl = v.sl * size;
+    // distances within a chunk are 32 bits wide
+    if (v.sn == 1 && columns % (16 / size) == 0) s.lay = kByColumn;
+    else if (v.sl == 1 && s.sn < ((int64_t)1 << 24)) s.lay = kByStep;
+    return s;
+}
 
 // A chunk's tile on its way from memory to LDS: columns CP (those behind the last one and
-// steps behind the chunk's `nt` are zero), TH threads, each with vectors of 16 bytes along
-// whichever axis is contiguous.
-template <class T, int CP, int TH>
+// steps behind the chunk's `nt` become zero), TH threads, each with vectors of 16 bytes.
+// The loads are unconditional, at clamped places, and what does not exist is cleared when
+// the tile is stored, a chunk later: conditions around the loads, vector by vector, took
+// thousands of scalar instructions, and clearing at once would wait for the data.
+// FAST: vectors of columns, known when the kernel is compiled.
+template <class T, int CP, int TH, bool FAST>
 struct Carrier {
-    static constexpr int Q = kChunk<T>, V = kRoom<T>, K = Q * CP / (TH * V), kStride = CP + kRoom<T>;
-    static_assert(Q * CP % (TH * V) == 0, "whole vectors");
-    using Vec = typename std::conditional<sizeof(T) == 2, Vec8<T>, Vec4<T>>::type;
-    Vec r[K];
+    static constexpr int Q = kChunk<T>, V = kRoom<T>, kVectors = Q * CP / V, kStride = CP + kRoom<T>;
+    static constexpr int K = kVectors > TH ? kVectors / TH : 1;
+    static_assert(kVectors % TH == 0 || kVectors < TH, "a vector each, or some threads none");
+    u32x4 r[K] = {};  // (whole words: element by element they took a register each)
+
+    static __device__ __forceinline__ bool idle(int tid) { return kVectors < TH && tid >= kVectors; }
 
     static __device__ __forceinline__ void place(Lay lay, int tid, int k, int& step, int& col) {
         const int e = tid + TH * k;
@@ -176,61 +202,108 @@ struct Carrier {
             col = e % (CP / V) * V;
         }
     }
-    // `p`: the chunk's first step, column 0; C columns exist
-    __device__ __forceinline__ void load(const T* p, Lay lay, int64_t sn, int64_t sl, int C, int nt, int tid) {
+    // `p`: the chunk's first step, column 0; C columns and nt >= 1 steps exist
+    __device__ __forceinline__ void load(const char* p, const Source& s, int C, int nt, int tid) {
+        constexpr uint32_t E = sizeof(T);
+        if (idle(tid)) return;
+        if (FAST || s.lay == kByColumn) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                int step, col;
+                place(kByColumn, tid, k, step, col);
+                r[k] = reinterpret_cast<const Words<T>*>(p + ((uint32_t)min(step, nt - 1) * (uint32_t)s.sl + (uint32_t)min(col, C - V) * E))->v;
+            }
+        } else if (s.lay == kByStep && nt == Q) {
+            const int t = anew(tid);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                int step, col;
+                place(kByStep, t, k, step, col);
+                r[k] = reinterpret_cast<const Words<T>*>(p + ((uint32_t)step * E + (uint32_t)min(col, C - 1) * (uint32_t)s.sn))->v;
+            }
+        } else {
+            const int t = anew(tid);  // the addresses are worked out here, and not kept from chunk to chunk
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                int step, col;
+                place(s.lay, t, k, step, col);
+                const bool by_step = s.lay == kByStep;
+                const char* at[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    at[i] = p + min(step + (by_step ? i : 0), nt - 1) * s.sl + min(col + (by_step ? 0 : i), C - 1) * s.sn;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (sizeof(T) == 4) r[k][i] = *reinterpret_cast<const uint32_t*>(at[i]);
+                    else
+                        r[k][i] = *reinterpret_cast<const uint16_t*>(at[2 * i]) |
+                                  (uint32_t)*reinterpret_cast<const uint16_t*>(at[2 * i + 1]) << 16;
+                }
+            }
+        }
+    }
+    // what does not exist becomes zero
+    __device__ __forceinline__ void clear(Lay lay, int C, int nt, int tid) {
+        if (FAST) lay = kByColumn;
+        if (__builtin_expect(nt == Q && C >= CP, 1)) return;
+        const int t = anew(tid);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             int step, col;
-            place(lay, tid, k, step, col);
-            const T* at = p + step * sl + col * sn;
-            const bool by_step = lay == kByStep;
-            const int there = by_step ? (col < C ? nt - step : 0) : (step < nt ? C - col : 0);
-            if (there >= V && lay != kElement) {
-                r[k] = *reinterpret_cast<const Vec*>(at);
-            } else {
-                const int64_t d = by_step ? 1 : sn;
+            place(lay, t, k, step, col);
+            if (lay == kByColumn) {
+                const uint32_t m = step < nt && col < C ? ~0u : 0u;
 #pragma unroll
-                for (int i = 0; i < V; ++i) r[k].v[i] = i < there ? at[i * d] : from_f<T>(0.0f);
+                for (int i = 0; i < 4; ++i) r[k][i] &= m;
+            } else {
+                const int there = lay == kByStep ? (col < C ? nt - step : 0) : (step < nt ? C - col : 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (sizeof(T) == 4) r[k][i] &= i < there ? ~0u : 0u;
+                    else r[k][i] &= 2 * i + 1 < there ? ~0u : 2 * i < there ? 0xffffu : 0u;
+                }
             }
         }
     }
     // row of step i: i, or from the chunk's end
     template <bool REVERSE>
     __device__ __forceinline__ void store(T* to, Lay lay, int tid) const {
+        if (FAST) lay = kByColumn;
+        const int t = anew(tid);
+        if (idle(t)) return;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             int step, col;
-            place(lay, tid, k, step, col);
+            place(lay, t, k, step, col);
             if (lay == kByStep) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) to[(REVERSE ? Q - 1 - step - i : step + i) * kStride + col] = r[k].v[i];
+                for (int i = 0; i < V; ++i) {
+                    T* at = to + (REVERSE ? Q - 1 - step - i : step + i) * kStride + col;
+                    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(at) = r[k][i];
+                    else *reinterpret_cast<uint16_t*>(at) = (uint16_t)(r[k][i / 2] >> (16 * (i & 1)));
+                }
             } else {
-                *reinterpret_cast<f32x4*>(to + (REVERSE ? Q - 1 - step : step) * kStride + col) =
-                    __builtin_bit_cast(f32x4, r[k]);
+                *reinterpret_cast<u32x4*>(to + (REVERSE ? Q - 1 - step : step) * kStride + col) = r[k];
             }
         }
     }
     // the largest magnitude as bits: at or above kInf<T> where one is infinite or NaN
     __device__ __forceinline__ uint32_t most() const {
-        uint32_t m = 0;
         if constexpr (sizeof(T) == 2) {
             u16x2 w = {0, 0};
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                struct Words { uint32_t w[4]; };
-                const Words x = __builtin_bit_cast(Words, r[k]);
+            for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w = __builtin_elementwise_max(w, __builtin_bit_cast(u16x2, x.w[i] & 0x7fff7fffu));
-            }
-            m = max((uint32_t)w[0], (uint32_t)w[1]);
+                for (int i = 0; i < 4; ++i) w = __builtin_elementwise_max(w, __builtin_bit_cast(u16x2, r[k][i] & 0x7fff7fffu));
+            return max((uint32_t)w[0], (uint32_t)w[1]);
         } else {
+            uint32_t m = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(to_f(r[k].v[i])) & 0x7fffffffu);
+                for (int i = 0; i < 4; ++i) m = max(m, r[k][i] & 0x7fffffffu);
+            return m;
         }
-        return m;
     }
 };
 template <class T>
@@ -336,47 +409,36 @@ __device__ __forceinline__ void put_decays(Decays<T>& d, float g, float in, floa
         if (lane == 0) d.most_in = a, d.most_out = b;
     }
 }
-// the weights out_t E in_s of lane's elements of tile (ti, si): t = 16 ti + (lane & 15),
-// s = 16 si + 4 (lane >> 4) + i; zero for s > t
+// The weights out_t E in_s of the lane's elements of tile (ti, si): t = 16 ti + (lane & 15),
+// s = 16 si + 4 (lane >> 4) + i.  Across blocks:
 template <class T>
-__device__ __forceinline__ f32x4 pair_weights(const Decays<T>& d, int ti, int si, int lane) {
-    const int tl = lane & 15, gl = lane >> 4, t = 16 * ti + tl, s = 16 * si + 4 * gl;
-    f32x4 r;
-    if (ti != si) {
-        const float b = d.between[ti][si];
-        const f32x4 v = *reinterpret_cast<const f32x4*>(&d.tail[s]);
-        const float h = d.head[t] * b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = h * v[i];
-        return r;
-    }
-    f32x4 q[4];
-    float sums[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        q[b] = *reinterpret_cast<const f32x4*>(&d.g[16 * ti + 4 * b]);
-        sums[b] = (q[b][0] + q[b][1]) + (q[b][2] + q[b][3]);
-    }
+__device__ __forceinline__ f32x4 weights_across(const Decays<T>& d, int ti, int si, int lane) {
+    const float h = d.head[16 * ti + (lane & 15)] * d.between[ti][si];
+    return *reinterpret_cast<const f32x4*>(&d.tail[16 * si + 4 * (lane >> 4)]) * h;
+}
+// within block ti (zero for s > t): sums of t's own four steps up to t, of s's four behind s
+// (up to t where both are the same) and of the fours between
+template <class T>
+__device__ __forceinline__ f32x4 weights_within(const Decays<T>& d, int ti, int lane) {
+    const int tl = lane & 15, gl = lane >> 4;
     const int tb = tl >> 2, tr = tl & 3;
     const bool same = tb == gl;
-    // t's own four up to t, s's four behind s (up to t where both are the same), those between
-    const f32x4 qt = tb == 0 ? q[0] : tb == 1 ? q[1] : tb == 2 ? q[2] : q[3];
-    f32x4 qs = gl == 0 ? q[0] : gl == 1 ? q[1] : gl == 2 ? q[2] : q[3];
+    const f32x4 q1 = *reinterpret_cast<const f32x4*>(&d.g[16 * ti + 4]);
+    const f32x4 q2 = *reinterpret_cast<const f32x4*>(&d.g[16 * ti + 8]);
+    const f32x4 qt = *reinterpret_cast<const f32x4*>(&d.g[16 * ti + 4 * tb]);
+    f32x4 qs = *reinterpret_cast<const f32x4*>(&d.g[16 * ti + 4 * gl]);
     float rest = qt[0] + (tr > 0 ? qt[1] : 0.0f) + (tr > 1 ? qt[2] : 0.0f) + (tr > 2 ? qt[3] : 0.0f);
-    rest += (gl < 1 && tb > 1 ? sums[1] : 0.0f) + (gl < 2 && tb > 2 ? sums[2] : 0.0f);
+    rest += gl < 1 && tb > 1 ? (q1[0] + q1[1]) + (q1[2] + q1[3]) : 0.0f;
+    rest += gl < 2 && tb > 2 ? (q2[0] + q2[1]) + (q2[2] + q2[3]) : 0.0f;
     rest = same ? 0.0f : rest;
 #pragma unroll
     for (int i = 1; i < 4; ++i) qs[i] = same && i > tr ? 0.0f : qs[i];
-    float e[4];
-    e[3] = rest;
-    e[2] = rest + qs[3];
-    e[1] = rest + (qs[2] + qs[3]);
-    e[0] = rest + (qs[1] + (qs[2] + qs[3]));
-    const float o = d.out[t];
-    const f32x4 w = *reinterpret_cast<const f32x4*>(&d.in[s]);
+    const float e[4] = {rest + (qs[1] + (qs[2] + qs[3])), rest + (qs[2] + qs[3]), rest + qs[3], rest};
+    const float o = d.out[16 * ti + tl];
+    const f32x4 w = *reinterpret_cast<const f32x4*>(&d.in[16 * ti + 4 * gl]);
+    f32x4 r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r[i] = s + i <= t ? exp_f<kFine<T>>(e[i]) * (o * w[i]) : 0.0f;
+    for (int i = 0; i < 4; ++i) r[i] = 4 * gl + i <= tl ? exp_f<kFine<T>>(e[i]) * (o * w[i]) : 0.0f;
     return r;
 }
 
@@ -388,8 +450,9 @@ __device__ __forceinline__ f32x4 pair_weights(const Decays<T>& d, int ti, int si
 struct WalkArgs {
     Seqs q;
     int64_t H, G, N, P;
-    View4 key, query, value, result;  // result.data null: the states alone
-    Lay key_lay, query_lay, value_lay;
+    Source key, query, value;
+    bool fast;                        // all three vectors of columns, and results stored four values at once
+    View4 result;                     // result.data null: the states alone
     View3 g, beta;                    // float; beta.data nullable
     float scale;
     const float* D;                   // [H] nullable
@@ -421,13 +484,14 @@ struct LinearGradArgs {
 };
 
 // what the pairs' kernel takes: the forward call's tensors, the states before every chunk
-// and the gradients of the states behind them, both [rows, H, N, padded P]
+// and the gradients of the states behind them, both as kept (below)
 struct PairArgs {
     Seqs q;
     int64_t Bsz, H, G, N, P;
     float scale;
-    View4 qv, k, v, dy, dq, dk;
-    Lay q_lay, k_lay, v_lay, dy_lay;
+    Source qv, k, v, dy;
+    bool fast;                 // all four vectors of columns
+    View4 dq, dk;
     View3 g, beta, dg, dbeta;  // beta, dbeta nullable
     const float *states, *ahead;
     int heads, blocks;         // heads of a workgroup, workgroups of a group
@@ -452,8 +516,9 @@ struct LinearStepArgs {
 };
 
 // The states kept for the backward pass, one before every chunk: row (first of the
-// sequence + chunk) of [rows, H, N, padded P]
-inline int64_t padded_values(int64_t P) { return (P + 31) / 32 * 32; }
+// sequence + chunk) of [rows, H, padded N, padded P], zero where there is none
+__host__ __device__ inline int64_t padded_keys(int64_t N) { return (N + 15) / 16 * 16; }
+__host__ __device__ inline int64_t padded_values(int64_t P) { return (P + 31) / 32 * 32; }
 __host__ __device__ inline int64_t linear_rows(int64_t S, int64_t L, bool packed, int Q) {
     return packed ? L / Q + S : S * ((L + Q - 1) / Q);
 }

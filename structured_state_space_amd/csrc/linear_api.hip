@@ -54,8 +54,8 @@ size_t walk_bytes(const Seqs& q, const Sizes& z) {
     return rounded((size_t)(items * z.H) * z.N * z.P * sizeof(float)) + rounded((size_t)(items * z.H) * sizeof(float));
 }
 size_t saved_bytes(const Seqs& q, const Sizes& z) {
-    return (size_t)(linear_rows(q.S, q.L, q.offsets != nullptr, chunk_of(z.dtype)) * z.H) * z.N * padded_values(z.P) *
-           sizeof(float);
+    return (size_t)(linear_rows(q.S, q.L, q.offsets != nullptr, chunk_of(z.dtype)) * z.H) * padded_keys(z.N) *
+           padded_values(z.P) * sizeof(float);
 }
 // workgroups that share a group's heads in the pairs' kernel, and their heads
 int64_t head_blocks(const Seqs& q, const Sizes& z, int* heads) {
@@ -88,10 +88,9 @@ int check_linear_sizes(int64_t H, int64_t N, int64_t P, int64_t G) {
 }
 bool grids_fit(const Seqs& q, const Sizes& z) {
     const int64_t chunks = item_count(q, chunk_of(z.dtype));
-    int heads;
-    return grid_fits(item_count(q, segment_steps(q, z)) * z.H * value_blocks(z.P), 256) &&
-           grid_fits(chunks * z.G * head_blocks(q, z, &heads) + z.H, 512) &&
-           chunks * z.H < ((int64_t)1 << 40) / (z.N * padded_values(z.P));
+    return grid_fits(item_count(q, segment_steps(q, z)) * z.H * value_blocks(z.P), 512) &&
+           grid_fits(chunks * z.G * 8 + z.H, 512) &&
+           chunks * z.H < ((int64_t)1 << 40) / (padded_keys(z.N) * padded_values(z.P));
 }
 
 int check_linear(const ssm_sequences* seq, const ssm_linear* p, bool slots_allowed, LinearArgs* a, Sizes* z) {
@@ -129,9 +128,10 @@ hipError_t walk(const LinearArgs& a, const Sizes& z, const View4& value, const V
     WalkArgs w;
     w.q = a.q;
     w.H = a.H, w.G = a.G, w.N = a.N, w.P = a.P;
-    w.key = REVERSE ? a.qv : a.k, w.query = REVERSE ? a.k : a.qv;
-    w.value = value, w.result = result;
-    w.key_lay = lay_of(w.key), w.query_lay = lay_of(w.query), w.value_lay = lay_of(value);
+    const int64_t size = type_bytes(z.dtype);
+    w.key = source_of(REVERSE ? a.qv : a.k, a.N, size), w.query = source_of(REVERSE ? a.k : a.qv, a.N, size);
+    w.value = source_of(value, a.P, size), w.result = result;
+    w.fast = w.key.lay == kByColumn && w.query.lay == kByColumn && w.value.lay == kByColumn && (!result.data || result.sn == 1);
     w.g = a.g, w.beta = a.beta;
     w.scale = a.scale;
     w.D = a.D;
@@ -210,9 +210,11 @@ int ssm_linear_attention_backward(const ssm_sequences* seq, const ssm_linear* p,
     r.q = a.q;
     r.Bsz = a.Bsz, r.H = a.H, r.G = a.G, r.N = a.N, r.P = a.P;
     r.scale = a.scale;
-    r.qv = a.qv, r.k = a.k, r.v = a.v, r.dy = view_of(*dy);
+    const int64_t size = type_bytes(z.dtype);
+    r.qv = source_of(a.qv, a.N, size), r.k = source_of(a.k, a.N, size);
+    r.v = source_of(a.v, a.P, size), r.dy = source_of(view_of(*dy), a.P, size);
     r.dq = view_of(grads->dq), r.dk = view_of(grads->dk);
-    r.q_lay = lay_of(r.qv), r.k_lay = lay_of(r.k), r.v_lay = lay_of(r.v), r.dy_lay = lay_of(r.dy);
+    r.fast = r.qv.lay == kByColumn && r.k.lay == kByColumn && r.v.lay == kByColumn && r.dy.lay == kByColumn;
     r.g = a.g, r.beta = a.beta, r.dg = view_of(&grads->dg), r.dbeta = view_of(&grads->dbeta);
     r.states = (const float*)saved, r.ahead = ahead;
     r.blocks = (int)head_blocks(a.q, z, &r.heads);

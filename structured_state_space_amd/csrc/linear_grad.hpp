@@ -8,8 +8,7 @@
 namespace ssm {
 
 constexpr int kPairValues = 64;
-template <int NP>
-constexpr int kPairThreads = NP > 128 ? 512 : 256;
+constexpr int kPairThreads = 512;
 
 // A workgroup has one chunk of a sequence and some of a group's heads, whose gradients of
 // the shared queries and keys it adds up in registers.  Per head, with E_ts as in the walk,
@@ -21,31 +20,37 @@ constexpr int kPairThreads = NP > 128 ? 512 : 256;
 //   dg_r = sum over pairs t >= r > s of beta_s W_ts, over t >= r of q_t . before_t, over s < r of
 //          beta_s k_s . behind_s, and E <x, X>:
 // a step's decay takes part in every product over it.  All of dg and dbeta are sums in
-// float32 of float32 numbers: x and X are split into two operands of the activations' type,
-// and only u beta dM is rounded to it, for dq and dk, which are of that type.
+// float32 of float32 numbers: x and X are split (kParts), and only u beta dM is rounded to the
+// activations' type, for dq and dk, which are of that type.
 // Values beyond 64 go block by block; every sum is linear in them.  q_t . k_s is formed
-// once for all heads.  Results lie transposed (lane: step, registers: four keys), so that
-// rows of four keys are multiplied with q and k and stored at once.
-template <class T, int NP>
-__global__ __launch_bounds__(kPairThreads<NP>) void linear_pairs_kernel(const PairArgs a) {
-    constexpr int TH = kPairThreads<NP>, W = TH / 64;
+// once for all heads.  A wave has 16 keys (or more), and all steps or some of them; results
+// lie transposed (lane: step, registers: four keys), so that rows of four keys are
+// multiplied with q and k at once.  The sums over pairs and keys go through LDS, of two
+// blocks in turn, and become dg and dbeta a block later, beside the other waves' work; so do
+// the next head's decays.
+template <class T, int NP, bool FAST>
+__global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const PairArgs a) {
+    constexpr int TH = kPairThreads, W = TH / 64;
     constexpr int Q = kChunk<T>, TT = Q / 16, KK = NP / 32, SS = Q / 32, PK = kPairValues / 32;
-    constexpr int NT = NP / 16 < W ? 1 : NP / 16 / W;             // tiles of keys of a wave
-    constexpr int OWN = TT * TT < W ? 1 : TT * TT / W, STEP = W / TT;  // tiles of pairs of a wave
+    constexpr int TILES = NP / 16, NT = TILES > W ? TILES / W : 1;  // tiles of keys, and those of a wave
+    constexpr int GROUPS = TILES >= W ? 1 : W / TILES < TT ? W / TILES : TT, TW = TT / GROUPS;  // of the steps; tiles of one
     constexpr int KS = NP + kRoom<T>, VS = kPairValues + kRoom<T>, MS = Q + kRoom<T>;
+    constexpr bool F16 = std::is_same<T, f16>::value;
+    struct Sums {  // of W over the pairs of a tile's rows and columns, and on the diagonal
+        float rows[TT][Q], columns[TT][Q], diagonal[Q];
+        float before[TILES][Q], behind[TILES][Q], whole[TILES], skip[TT];
+    };
     struct __attribute__((aligned(16))) Shared {
         T q[Q * KS], k[Q * KS], v[Q * VS], dy[Q * VS], m[Q * MS];
-        Decays<T> d;
-        float beta[Q];
-        float rows[STEP][Q], columns[TT][Q], diagonal[Q], skip[TT];  // sums of W over its rows and columns
-        float before[W][Q], behind[W][Q], whole[W];
-        float next, most_beta;  // the decay from the chunk's last step to the next one
+        Decays<T> d[2];
+        float beta[2][Q];
+        float next[2], across[2], most_beta[2];  // the decay to the next chunk's first step; over the chunk and it
+        Sums sums[2];
         uint32_t most[2][W];
     };
     __shared__ Shared sh;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tl = lane & 15, gl = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t bid = blockIdx.x;
     const int blk = (int)(bid % a.blocks), grp = (int)(bid / a.blocks % a.G);
     const int64_t item = bid / a.blocks / a.G;
@@ -54,98 +59,93 @@ __global__ __launch_bounds__(kPairThreads<NP>) void linear_pairs_kernel(const Pa
     const bool found = find_item(a.q, item, Q, it);
     const int t0 = found ? it.beg + it.c * Q : 0, nt = found ? min(Q, it.end - t0) : 0;
     if (nt <= 0) {
-        if (a.skips && h0 + tid < h1)
-            for (int h = h0 + tid; h < h1; h += TH) a.skips[item * a.H + h] = 0.0f;
+        if (a.skips)
+            for (int h = h0 + (int)threadIdx.x; h < h1; h += TH) a.skips[item * a.H + h] = 0.0f;
         return;
     }
     const int N = (int)a.N, P = (int)a.P, values = (P + kPairValues - 1) / kPairValues;
-    const int64_t Pp = (a.P + 31) / 32 * 32, row = linear_row(a.q, it, Q) + it.c;
+    const int Np = (int)padded_keys(a.N), Pp = (int)padded_values(a.P);
+    const int64_t row = (linear_row(a.q, it, Q) + it.c) * a.H;
 
     {
-        Carrier<T, NP, TH> c;
-        c.load((const T*)a.qv.data + it.row * a.qv.sb + grp * a.qv.sg + t0 * a.qv.sl, a.q_lay, a.qv.sn, a.qv.sl, N, nt, tid);
-        c.template store<false>(sh.q, a.q_lay, tid);
-        c.load((const T*)a.k.data + it.row * a.k.sb + grp * a.k.sg + t0 * a.k.sl, a.k_lay, a.k.sn, a.k.sl, N, nt, tid);
-        c.template store<false>(sh.k, a.k_lay, tid);
+        const int tid = threadIdx.x;
+        Carrier<T, NP, TH, FAST> cq, ck;
+        cq.load(a.qv.data + it.row * a.qv.sb + grp * a.qv.sg + t0 * a.qv.sl, a.qv, N, nt, tid);
+        ck.load(a.k.data + it.row * a.k.sb + grp * a.k.sg + t0 * a.k.sl, a.k, N, nt, tid);
+        cq.clear(a.qv.lay, N, nt, tid);
+        ck.clear(a.k.lay, N, nt, tid);
+        cq.template store<false>(sh.q, a.qv.lay, tid);
+        ck.template store<false>(sh.k, a.k.lay, tid);
+        for (int i = tid; i < Q * MS; i += TH) sh.m[i] = from_f<T>(0.0f);  // pairs s > t stay zero
     }
-    Carrier<T, kPairValues, TH> cv, cy;
-    float g = 0.0f, beta = 0.0f, g_next = 0.0f;
+    Carrier<T, kPairValues, TH, FAST> cv, cy;
     auto load = [&](int h, int pb) {
-        const int p0 = pb * kPairValues;
-        cv.load((const T*)a.v.data + it.row * a.v.sb + h * a.v.sg + t0 * a.v.sl + p0 * a.v.sn, a.v_lay, a.v.sn, a.v.sl, P - p0,
-                nt, tid);
-        cy.load((const T*)a.dy.data + it.row * a.dy.sb + h * a.dy.sg + t0 * a.dy.sl + p0 * a.dy.sn, a.dy_lay, a.dy.sn, a.dy.sl,
-                P - p0, nt, tid);
-        if (wave == 0) {
-            const float* gs = (const float*)a.g.data + it.row * a.g.sb + h * a.g.sh;
-            g = beta = 0.0f;
-            if (lane < nt) {
-                g = gs[(t0 + lane) * a.g.sl];
-                beta = a.beta.data ? ((const float*)a.beta.data)[it.row * a.beta.sb + h * a.beta.sh + (t0 + lane) * a.beta.sl] : 1.0f;
-            }
-            // what lies between the chunk and the state behind the next step
-            g_next = t0 + nt < it.end ? gs[(t0 + nt) * a.g.sl] : 0.0f;
+        const int p0 = pb * kPairValues, tid = threadIdx.x;
+        cv.load(a.v.data + it.row * a.v.sb + h * a.v.sg + t0 * a.v.sl + p0 * a.v.sn, a.v, P - p0, nt, tid);
+        cy.load(a.dy.data + it.row * a.dy.sb + h * a.dy.sg + t0 * a.dy.sl + p0 * a.dy.sn, a.dy, P - p0, nt, tid);
+    };
+    // the last wave: the decays of a head
+    float g = 0.0f, beta = 0.0f, g_next = 0.0f;
+    auto load_decays = [&](int h) {
+        const int lane = threadIdx.x & 63;
+        const float* gs = (const float*)a.g.data + it.row * a.g.sb + h * a.g.sh;
+        g = beta = 0.0f;
+        if (lane < nt) {
+            g = gs[(t0 + lane) * a.g.sl];
+            beta = a.beta.data ? ((const float*)a.beta.data)[it.row * a.beta.sb + h * a.beta.sh + (t0 + lane) * a.beta.sl] : 1.0f;
+        }
+        g_next = t0 + nt < it.end ? gs[(t0 + nt) * a.g.sl] : 0.0f;
+    };
+    auto keep_decays = [&](int i) {
+        const int lane = anew(threadIdx.x) & 63;
+        put_decays<T>(sh.d[i], g, lane < nt ? 1.0f : 0.0f, lane < nt ? a.scale : 0.0f, lane);
+        if (lane < Q) sh.beta[i][lane] = beta;
+        const float all = across_rows(row_sum(g));
+        if (lane == 0) sh.across[i] = exp_f<kFine<T>>(all + g_next), sh.next[i] = exp_f<kFine<T>>(g_next);
+        if constexpr (F16) {
+            float m = fabsf(beta);
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+            if (lane == 0) sh.most_beta[i] = m;
         }
     };
-    load(h0, 0);
-    __syncthreads();
-
-    const int ti = wave % TT, si0 = wave / TT;
-    f32x4 qk[OWN];
-#pragma unroll
-    for (int j = 0; j < OWN; ++j) {
-        const int si = si0 + j * STEP;
-        qk[j] = f32x4{0, 0, 0, 0};
-        if (si <= ti) {
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                qk[j] = mma<T>(row_frag<T>(sh.k + (16 * si + tl) * KS + 32 * kk + 8 * gl),
-                               row_frag<T>(sh.q + (16 * ti + tl) * KS + 32 * kk + 8 * gl), qk[j]);
-        }
-    }
-    f32x4 dq[NT][TT], dk[NT][TT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) dq[n][t] = dk[n][t] = f32x4{0, 0, 0, 0};
-    const int n0 = 16 * NT * wave;  // the wave's first key
-
-    // wave 0, lane r: sums over the blocks of a head's values
+    // the wave before it, lane r: a head's sums over its blocks of values
     float sum_row = 0.0f, sum_column = 0.0f, sum_diagonal = 0.0f, sum_before = 0.0f, sum_behind = 0.0f, sum_whole = 0.0f,
           sum_skip = 0.0f;
-    float g_own = 0.0f, beta_own = 0.0f, across = 1.0f;
-    auto collect = [&]() {
+    auto collect = [&](const Sums& s) {
+        const int lane = anew(threadIdx.x) & 63;
         if (lane < Q) {
+            const int own = lane >> 4;
 #pragma unroll
-            for (int i = 0; i < STEP; ++i) sum_row += sh.rows[i][lane];
+            for (int i = 0; i < TT; ++i) {
+                sum_row += i <= own ? s.rows[i][lane] : 0.0f;
+                sum_column += i >= own ? s.columns[i][lane] : 0.0f;
+            }
+            sum_diagonal += s.diagonal[lane];
 #pragma unroll
-            for (int i = 0; i < TT; ++i) sum_column += sh.columns[i][lane];
-            sum_diagonal += sh.diagonal[lane];
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                if (16 * NT * i < NP) sum_before += sh.before[i][lane], sum_behind += sh.behind[i][lane];
+            for (int i = 0; i < TILES; ++i) sum_before += s.before[i][lane], sum_behind += s.behind[i][lane];
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (16 * NT * i < NP) sum_whole += sh.whole[i];
+        for (int i = 0; i < TILES; ++i) sum_whole += s.whole[i];
 #pragma unroll
-        for (int i = 0; i < TT; ++i) sum_skip += sh.skip[i];
+        for (int i = 0; i < TT; ++i) sum_skip += s.skip[i];
     };
-    auto finish = [&](int h) {
+    auto finish = [&](int h, int i) {  // of head h, whose decays are in place i
+        const int lane = anew(threadIdx.x) & 63, r = min(lane, Q - 1);
+        const float b = sh.beta[i][r], own = b * sum_behind;
         // sums over the steps from r on, and before r
-        float from = sum_row + sum_before - beta_own * sum_column, till = beta_own * sum_behind;
-        const float own = till;
+        float from = sum_row + sum_before - b * sum_column, till = own;
 #pragma unroll
         for (int d = 1; d < Q; d <<= 1) {
-            const float f = __shfl_down(from, d), b = __shfl_up(till, d);
+            const float f = __shfl_down(from, d), e = __shfl_up(till, d);
             if (lane + d < Q) from += f;
-            if (lane >= d) till += b;
+            if (lane >= d) till += e;
         }
-        const float dg = from + (till - own) + across * sum_whole;
+        const float dg = from + (till - own) + sh.across[i] * sum_whole;
         if (lane < nt) {
             // a reset takes part in no product, and the sums' rounding is not left in its place
             ((float*)a.dg.data)[it.row * a.dg.sb + h * a.dg.sh + (t0 + lane) * a.dg.sl] =
-                exp_f<kFine<T>>(g_own) == 0.0f ? 0.0f : dg;
+                exp_f<kFine<T>>(sh.d[i].g[r]) == 0.0f ? 0.0f : dg;
             if (a.dbeta.data)
                 ((float*)a.dbeta.data)[it.row * a.dbeta.sb + h * a.dbeta.sh + (t0 + lane) * a.dbeta.sl] =
                     sum_column + sum_diagonal + sum_behind;
@@ -154,143 +154,165 @@ __global__ __launch_bounds__(kPairThreads<NP>) void linear_pairs_kernel(const Pa
         sum_row = sum_column = sum_diagonal = sum_before = sum_behind = sum_whole = sum_skip = 0.0f;
     };
 
+    load(h0, 0);
+    if (wave == W - 1) {
+        load_decays(h0);
+        keep_decays(0);
+        if (h0 + 1 < h1) load_decays(h0 + 1);
+    }
+    __syncthreads();
+
+    // the wave's pairs: a tile on the diagonal, or one or two below it
+    constexpr int BELOW = TT * (TT - 1) / 2, OWN = BELOW > 4 ? 2 : 1;
+    auto below = [](int j, int& ti, int& si) {
+        ti = j < 1 ? 1 : j < 3 ? 2 : 3;
+        si = j - ti * (ti - 1) / 2;
+    };
+    const bool diagonal = wave < TT;
+    const int first = diagonal ? 0 : wave < 4 ? BELOW : wave - 4;
+    f32x4 qk[OWN];
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+        qk[j] = f32x4{0, 0, 0, 0};
+        int ti = wave, si = wave;
+        if (!diagonal) below(first + 4 * j, ti, si);
+        if (diagonal ? j == 0 : first + 4 * j < BELOW) {
+            const int lane = threadIdx.x & 63;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                qk[j] = mma<T>(row_frag<T>(sh.k + (16 * si + (lane & 15)) * KS + 32 * kk + 8 * (lane >> 4)),
+                               row_frag<T>(sh.q + (16 * ti + (lane & 15)) * KS + 32 * kk + 8 * (lane >> 4)), qk[j]);
+        }
+    }
+    // the wave's keys and steps
+    const int tile = TILES >= W ? wave * NT : wave % TILES, n0 = 16 * tile, group = TILES >= W ? 0 : wave / TILES;
+    const bool live = group < GROUPS;
+    f32x4 dq[NT][TW], dk[NT][TW];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < TW; ++t) dq[n][t] = dk[n][t] = f32x4{0, 0, 0, 0};
+
     const int count = (h1 - h0) * values;
     int h = h0, pb = 0;
     for (int k = 0; k < count; ++k) {
+        const int tid = FAST ? threadIdx.x : anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;
+        const int p0 = pb * kPairValues, turn = (h - h0) & 1;
+        const Decays<T>& d = sh.d[turn];
+        Sums& sums = sh.sums[k & 1];
+        if (k) __syncthreads();  // the last block's tiles have been read
+        cv.clear(a.v.lay, P - p0, nt, tid);
+        cy.clear(a.dy.lay, P - p0, nt, tid);
+        cv.template store<false>(sh.v, a.v.lay, tid);
+        cy.template store<false>(sh.dy, a.dy.lay, tid);
+        if constexpr (F16) {
+            uint32_t mv = cv.most(), my = cy.most();
+#pragma unroll
+            for (int i = 1; i < 64; i <<= 1)
+                mv = max(mv, (uint32_t)__shfl_xor((int)mv, i)), my = max(my, (uint32_t)__shfl_xor((int)my, i));
+            if (lane == 0) sh.most[0][wave] = mv, sh.most[1][wave] = my;
+        }
         // the states' fragments: keys n0 + 16 n + tl, values 32 kk + 8 gl .. + 7
-        float x[NT][PK][8], X[NT][PK][8];
-        const int p0 = pb * kPairValues;
+        f32x4 x[NT][PK][2], X[NT][PK][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int kk = 0; kk < PK; ++kk) {
-                const int key = n0 + 16 * n + tl, p = p0 + 32 * kk + 8 * gl;
-                f32x4 v[4] = {};
-                if (key < N && p < Pp) {
-                    const int64_t at = ((row * a.H + h) * N + key) * Pp + p;
+                x[n][kk][0] = x[n][kk][1] = X[n][kk][0] = X[n][kk][1] = f32x4{0, 0, 0, 0};
+                if (live && n0 + 16 * n < Np && p0 + 32 * kk < Pp) {
+                    const int64_t at = (row + h) * Np * Pp + ((n0 + 16 * n + tl) * Pp + p0 + 32 * kk + 8 * gl);
                     const f32x4* s = reinterpret_cast<const f32x4*>(a.states + at);
                     const f32x4* e = reinterpret_cast<const f32x4*>(a.ahead + at);
-                    v[0] = s[0], v[1] = s[1], v[2] = e[0], v[3] = e[1];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[n][kk][i] = v[0][i], x[n][kk][4 + i] = v[1][i], X[n][kk][i] = v[2][i], X[n][kk][4 + i] = v[3][i];
-            }
-        if (k) __syncthreads();  // the last block's tiles have been read, its sums are there
-        cv.template store<false>(sh.v, a.v_lay, tid);
-        cy.template store<false>(sh.dy, a.dy_lay, tid);
-        if constexpr (std::is_same<T, f16>::value) {
-            uint32_t mv = cv.most(), my = cy.most();
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1)
-                mv = max(mv, (uint32_t)__shfl_xor((int)mv, d)), my = max(my, (uint32_t)__shfl_xor((int)my, d));
-            if (lane == 0) sh.most[0][wave] = mv, sh.most[1][wave] = my;
-        }
-        if (wave == 0) {
-            if (k) {
-                collect();
-                if (pb == 0) finish(h - 1);
-            }
-            if (pb == 0) {
-                put_decays<T>(sh.d, g, lane < nt ? 1.0f : 0.0f, lane < nt ? a.scale : 0.0f, lane);
-                if (lane < Q) sh.beta[lane] = beta;
-                g_own = g, beta_own = beta;
-                across = exp_f<kFine<T>>(across_rows(row_sum(g)) + g_next);
-                if (lane == 0) sh.next = exp_f<kFine<T>>(g_next);
-                if constexpr (std::is_same<T, f16>::value) {
-                    float m = fabsf(beta);
-#pragma unroll
-                    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-                    if (lane == 0) sh.most_beta = m;
+                    x[n][kk][0] = s[0], x[n][kk][1] = s[1], X[n][kk][0] = e[0], X[n][kk][1] = e[1];
                 }
             }
-        }
         __syncthreads();
-        if (++pb == values) pb = 0, ++h;
-        if (k + 1 < count) load(h, pb);
+        const int h_next = pb + 1 == values ? h + 1 : h, pb_next = pb + 1 == values ? 0 : pb + 1;
+        if (k + 1 < count) load(h_next, pb_next);
 
         float sm = 1.0f;
-        if constexpr (std::is_same<T, f16>::value) {
+        if constexpr (F16) {
             uint32_t mv = 0, my = 0;
 #pragma unroll
             for (int i = 0; i < W; ++i) mv = max(mv, sh.most[0][i]), my = max(my, sh.most[1][i]);
-            sm = to_range<T>(fabsf(a.scale) * sh.d.grow * sh.most_beta * (float)kPairValues *
+            sm = to_range<T>(fabsf(a.scale) * d.grow * sh.most_beta[turn] * (float)kPairValues *
                              to_f(__builtin_bit_cast(f16, (uint16_t)mv)) * to_f(__builtin_bit_cast(f16, (uint16_t)my)));
         }
         // the pairs
-        float row_part = 0.0f, skip = 0.0f;
-        {
-            Frag<T> yf[PK];
+        auto pairs = [&](int ti, int si, const f32x4& u, const f32x4& kq, bool on) {
+            f32x4 dm = {0, 0, 0, 0};
 #pragma unroll
-            for (int kk = 0; kk < PK; ++kk) yf[kk] = row_frag<T>(sh.dy + (16 * ti + tl) * VS + 32 * kk + 8 * gl);
+            for (int kk = 0; kk < PK; ++kk)
+                dm = mma<T>(row_frag<T>(sh.v + (16 * si + tl) * VS + 32 * kk + 8 * gl),
+                            row_frag<T>(sh.dy + (16 * ti + tl) * VS + 32 * kk + 8 * gl), dm);
+            const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.beta[turn][16 * si + 4 * gl]);
+            struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
+            float column[4], part = 0.0f, skip = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float um = u[i] * dm[i], wt = um * kq[i];
+                const bool own = on && 4 * gl + i == tl;
+                if (own) sums.diagonal[16 * ti + tl] = wt;
+                column[i] = own ? 0.0f : wt;
+                skip = own ? dm[i] : skip;
+                part = fmaf(column[i], b[i], part);
+                w.v[i] = from_f<T>(um * b[i] * sm);
+            }
+            *reinterpret_cast<Four*>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl) = w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) column[i] = row_sum(column[i]);
+            if (tl == 0)
+                *reinterpret_cast<f32x4*>(&sums.columns[ti][16 * si + 4 * gl]) = f32x4{column[0], column[1], column[2], column[3]};
+            part = across_rows(part);
+            if (gl == 0) sums.rows[si][16 * ti + tl] = part;
+            if (on) {
+                skip = across_rows(row_sum(skip));
+                if (lane == 0) sums.skip[ti] = skip;
+            }
+        };
+        if (diagonal) {
+            pairs(wave, wave, weights_within<T>(d, wave, lane), qk[0], true);
+        } else {
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
-                const int si = si0 + j * STEP;
-                if (si >= TT) break;
-                struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
-                float column[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(0.0f);
-                if (si <= ti) {
-                    f32x4 dm = {0, 0, 0, 0};
-#pragma unroll
-                    for (int kk = 0; kk < PK; ++kk)
-                        dm = mma<T>(row_frag<T>(sh.v + (16 * si + tl) * VS + 32 * kk + 8 * gl), yf[kk], dm);
-                    const f32x4 u = pair_weights<T>(sh.d, ti, si, lane);
-                    const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.beta[16 * si + 4 * gl]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float um = u[i] * dm[i], wt = um * qk[j][i];
-                        const bool diagonal = si == ti && 4 * gl + i == tl;
-                        if (diagonal) {
-                            sh.diagonal[16 * ti + tl] = wt;
-                            skip = dm[i];
-                        } else {
-                            row_part = fmaf(wt, b[i], row_part);
-                            column[i] = wt;
-                        }
-                        w.v[i] = from_f<T>(um * b[i] * sm);
-                    }
-                }
-                *reinterpret_cast<Four*>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl) = w;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) column[i] = row_sum(column[i]);
-                if (tl == 0) *reinterpret_cast<f32x4*>(&sh.columns[ti][16 * si + 4 * gl]) = f32x4{column[0], column[1], column[2], column[3]};
+                int ti, si;
+                below(first + 4 * j, ti, si);
+                if (first + 4 * j < BELOW) pairs(ti, si, weights_across<T>(d, ti, si, lane), qk[j], false);
             }
-            row_part = across_rows(row_part);
-            skip = across_rows(row_sum(skip));
-            if (gl == 0) sh.rows[si0][16 * ti + tl] = row_part;
-            if (lane == 0 && si0 <= ti && (ti - si0) % STEP == 0) sh.skip[ti] = skip;  // it has the diagonal's tile
+        }
+        if (wave == W - 2 && k) {
+            collect(sh.sums[(k - 1) & 1]);
+            if (pb == 0) finish(h - 1, turn ^ 1);
         }
         __syncthreads();
-        if (n0 >= NP) continue;
+        if (wave == W - 1 && h_next > h && h_next < h1) {
+            keep_decays(turn ^ 1);
+            if (h_next + 1 < h1) load_decays(h_next + 1);
+        }
+        h = h_next, pb = pb_next;
+        if (!live) continue;
 
         // keys by steps: dq and dk
-        float before[TT], behind[TT], whole = 0.0f;
-#pragma unroll
-        for (int t = 0; t < TT; ++t) before[t] = behind[t] = 0.0f;
-        const float um = reciprocal_of_power(sm);
+        const float um = reciprocal_of_power(sm), next = sh.next[turn];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int key = n0 + 16 * n;
-            Frag<T> kf[SS], qf[SS], xh[PK], xl[PK], Xh[PK], Xl[PK];
+            float whole = 0.0f;
+            f32x4 in[TW], out[TW];
 #pragma unroll
-            for (int s = 0; s < SS; ++s) {
-                kf[s] = column_frag<T>(sh.k + 32 * s * KS + key, KS, lane);
-                qf[s] = column_frag<T>(sh.q + 32 * s * KS + key, KS, lane);
-            }
+            for (int t = 0; t < TW; ++t) in[t] = out[t] = f32x4{0, 0, 0, 0};
             float sx = 1.0f, sX = 1.0f;
-            if constexpr (std::is_same<T, f16>::value) {
+            if constexpr (F16) {
                 float mx = 0.0f, mX = 0.0f;
 #pragma unroll
                 for (int kk = 0; kk < PK; ++kk)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float u = fabsf(x[n][kk][i]), v = fabsf(X[n][kk][i]);
+                        const float u = fabsf(x[n][kk][i / 4][i % 4]), v = fabsf(X[n][kk][i / 4][i % 4]);
                         mx = fmaxf(mx, u < INFINITY ? u : 0.0f), mX = fmaxf(mX, v < INFINITY ? v : 0.0f);
                     }
 #pragma unroll
-                for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d)), mX = fmaxf(mX, __shfl_xor(mX, d));
+                for (int i = 1; i < 64; i <<= 1) mx = fmaxf(mx, __shfl_xor(mx, i)), mX = fmaxf(mX, __shfl_xor(mX, i));
                 sx = to_range<T>(mx), sX = to_range<T>(mX);
             }
 #pragma unroll
@@ -298,63 +320,73 @@ __global__ __launch_bounds__(kPairThreads<NP>) void linear_pairs_kernel(const Pa
                 float u[8], v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    whole = fmaf(x[n][kk][i], X[n][kk][i], whole);
-                    u[i] = x[n][kk][i] * sx, v[i] = X[n][kk][i] * sX;
+                    whole = fmaf(x[n][kk][i / 4][i % 4], X[n][kk][i / 4][i % 4], whole);
+                    u[i] = x[n][kk][i / 4][i % 4] * sx, v[i] = X[n][kk][i / 4][i % 4] * sX;
                 }
-                split<T>(u, xh[kk], xl[kk]);
-                split<T>(v, Xh[kk], Xl[kk]);
+                Frag<T> part[kParts<T>];
+                split<T>(u, part);
+#pragma unroll
+                for (int t = 0; t < TW; ++t) {
+                    const Frag<T> f = row_frag<T>(sh.dy + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+#pragma unroll
+                    for (int i = 0; i < kParts<T>; ++i) in[t] = mma<T>(part[i], f, in[t]);
+                }
+                split<T>(v, part);
+#pragma unroll
+                for (int t = 0; t < TW; ++t) {
+                    const Frag<T> f = row_frag<T>(sh.v + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+#pragma unroll
+                    for (int i = 0; i < kParts<T>; ++i) out[t] = mma<T>(part[i], f, out[t]);
+                }
             }
             const float ux = reciprocal_of_power(sx), uX = reciprocal_of_power(sX);
+            Frag<T> kf[SS], qf[SS];
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                f32x4 in = {0, 0, 0, 0}, out = {0, 0, 0, 0};
+            for (int s = 0; s < SS; ++s) {
+                kf[s] = column_frag<T>(sh.k + 32 * s * KS + key, KS, lane);
+                qf[s] = column_frag<T>(sh.q + 32 * s * KS + key, KS, lane);
+            }
 #pragma unroll
-                for (int kk = 0; kk < PK; ++kk) {
-                    const Frag<T> yf = row_frag<T>(sh.dy + (16 * t + tl) * VS + 32 * kk + 8 * gl);
-                    const Frag<T> vf = row_frag<T>(sh.v + (16 * t + tl) * VS + 32 * kk + 8 * gl);
-                    in = mma<T>(xh[kk], yf, in), out = mma<T>(Xh[kk], vf, out);
-                    if (kSplit<T>) in = mma<T>(xl[kk], yf, in), out = mma<T>(Xl[kk], vf, out);
-                }
+            for (int t = 0; t < TW; ++t) {
+                const int tt = TW * group + t, r = 16 * tt + tl;
                 f32x4 wq = {0, 0, 0, 0}, wk = {0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < SS; ++s) {
-                    if (s <= t / 2) wq = mma<T>(kf[s], row_frag<T>(sh.m + (16 * t + tl) * MS + 32 * s + 8 * gl), wq);
-                    if (s >= t / 2) wk = mma<T>(qf[s], column_frag<T>(sh.m + 32 * s * MS + 16 * t, MS, lane), wk);
+                    if (s <= tt / 2) wq = mma<T>(kf[s], row_frag<T>(sh.m + r * MS + 32 * s + 8 * gl), wq);
+                    if (s >= tt / 2) wk = mma<T>(qf[s], column_frag<T>(sh.m + 32 * s * MS + 16 * tt, MS, lane), wk);
                 }
-                const int r = 16 * t + tl;
-                const float from = sh.d.from[r] * ux, to = sh.d.to[r] * sh.next * uX, b = sh.beta[r];
+                const float from = d.from[r] * ux, to = d.to[r] * next * uX, b = sh.beta[turn][r];
                 struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; };
                 const Four q4 = *reinterpret_cast<const Four*>(sh.q + r * KS + key + 4 * gl);
                 const Four k4 = *reinterpret_cast<const Four*>(sh.k + r * KS + key + 4 * gl);
+                float before = 0.0f, behind = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float u = in[i] * from, v = out[i] * to;
-                    before[t] = fmaf(u, to_f(q4.v[i]), before[t]);
-                    behind[t] = fmaf(v, to_f(k4.v[i]), behind[t]);
+                    const float u = in[t][i] * from, v = out[t][i] * to;
+                    before = fmaf(u, to_f(q4.v[i]), before);
+                    behind = fmaf(v, to_f(k4.v[i]), behind);
                     dq[n][t][i] += fmaf(wq[i], um, u);
                     dk[n][t][i] += fmaf(wk[i], um, v * b);
                 }
+                before = across_rows(before), behind = across_rows(behind);
+                if (gl == 0) sums.before[tile + n][r] = before, sums.behind[tile + n][r] = behind;
             }
+            whole = across_rows(row_sum(whole));
+            if (lane == 0) sums.whole[tile + n] = whole;
         }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            before[t] = across_rows(before[t]), behind[t] = across_rows(behind[t]);
-            if (gl == 0) sh.before[wave][16 * t + tl] = before[t], sh.behind[wave][16 * t + tl] = behind[t];
-        }
-        whole = across_rows(row_sum(whole));
-        if (lane == 0) sh.whole[wave] = whole;
     }
     __syncthreads();
-    if (wave == 0) {
-        collect();
-        finish(h1 - 1);
+    if (wave == W - 2) {
+        collect(sh.sums[(count - 1) & 1]);
+        finish(h1 - 1, (h1 - 1 - h0) & 1);
     }
-    if (n0 >= NP) return;
+    if (!live) return;
+    const int lane = anew(threadIdx.x) & 63, tl = lane & 15, gl = lane >> 4;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int r = 16 * t + tl, key = n0 + 16 * n + 4 * gl, there = N - key;
+        for (int t = 0; t < TW; ++t) {
+            const int r = 16 * (TW * group + t) + tl, key = n0 + 16 * n + 4 * gl, there = N - key;
             if (r >= nt || there <= 0) continue;
             if (a.blocks > 1) {
                 const int64_t all = a.Bsz * a.G * a.q.L * N;
@@ -392,9 +424,11 @@ __global__ __launch_bounds__(256) void linear_sums_kernel(const PairArgs a, int6
         return;
     }
     const int grp = (int)(blockIdx.x % a.G);
+    constexpr int R = 8;  // steps of a workgroup
+    const int64_t part = blockIdx.x / a.G;
     Item it;
-    if (!find_item(a.q, blockIdx.x / a.G, Q, it)) return;
-    const int t0 = it.beg + it.c * Q, nt = min(Q, it.end - t0), N = (int)a.N;
+    if (!find_item(a.q, part / (Q / R), Q, it)) return;
+    const int t0 = it.beg + it.c * Q + (int)(part % (Q / R)) * R, nt = min(R, it.end - t0), N = (int)a.N;
     const int64_t all = a.Bsz * a.G * a.q.L * N;
     const float* from = a.parts + (((int64_t)it.row * a.G + grp) * a.q.L + t0) * N;
     const bool by_step = a.dq.sl == 1 && a.dk.sl == 1;
@@ -410,14 +444,19 @@ __global__ __launch_bounds__(256) void linear_sums_kernel(const PairArgs a, int6
     }
 }
 
+template <class T, int NP>
+static void launch_pairs_keys(const PairArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)(a.items * a.G * a.blocks)), wg(kPairThreads);
+    if (a.fast) hipLaunchKernelGGL((linear_pairs_kernel<T, NP, true>), grid, wg, 0, s, a);
+    else hipLaunchKernelGGL((linear_pairs_kernel<T, NP, false>), grid, wg, 0, s, a);
+}
 template <class T>
 hipError_t launch_pairs(const PairArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.items * a.G * a.blocks));
-    if (a.N <= 32) hipLaunchKernelGGL((linear_pairs_kernel<T, 32>), grid, dim3(kPairThreads<32>), 0, s, a);
-    else if (a.N <= 64) hipLaunchKernelGGL((linear_pairs_kernel<T, 64>), grid, dim3(kPairThreads<64>), 0, s, a);
-    else if (a.N <= 128) hipLaunchKernelGGL((linear_pairs_kernel<T, 128>), grid, dim3(kPairThreads<128>), 0, s, a);
-    else hipLaunchKernelGGL((linear_pairs_kernel<T, 256>), grid, dim3(kPairThreads<256>), 0, s, a);
-    const int64_t tokens = a.blocks > 1 ? a.items * a.G : 0, heads = a.skips ? a.H : 0;
+    if (a.N <= 32) launch_pairs_keys<T, 32>(a, s);
+    else if (a.N <= 64) launch_pairs_keys<T, 64>(a, s);
+    else if (a.N <= 128) launch_pairs_keys<T, 128>(a, s);
+    else launch_pairs_keys<T, 256>(a, s);
+    const int64_t tokens = a.blocks > 1 ? a.items * (kChunk<T> / 8) * a.G : 0, heads = a.skips ? a.H : 0;
     if (tokens + heads)
         hipLaunchKernelGGL((linear_sums_kernel<T>), dim3((unsigned)(tokens + heads)), dim3(256), 0, s, a, tokens);
     return hipGetLastError();

@@ -6,43 +6,50 @@
 
 namespace ssm {
 
-constexpr int kWalkThreads = 256;
-constexpr int kWalkValues = 64;  // values of a workgroup: 16 to a wave
+constexpr int kWalkThreads = 512;
+constexpr int kWalkWaves = kWalkThreads / 64;
+constexpr int kWalkValues = 64;  // values of a workgroup
 
 // A workgroup has one head, 64 of its values and one segment of a sequence, and takes a
 // chunk of rows at a time.  With the pairs' weights M_ts = out_t (q_t . k_s) E_ts in_s
 // (s <= t, D on the diagonal) the chunk's results are
 //   result_t = sum_s M_ts value_s + out_t E_t x^T q_t,
-// and the state becomes E x + sum_s E'_s in_s k_s value_s^T: four matrix products.  A wave
-// has the whole state of its 16 values in float32 in registers, in the order in which the
-// matrix instruction leaves it and in which, rounded, it is the next chunk's operand: the
-// state goes through no memory.  M goes through LDS once, a tile of rows from each wave.
+// and the state becomes E x + sum_s E'_s in_s k_s value_s^T: four matrix products.  The state
+// stays in float32 in registers, as the matrix instruction leaves it: a wave has 16 values and
+// half of the keys, and of the results those values and half of the steps.  Rounded, the state
+// goes through LDS once a chunk, and so does M, a tile of 16 x 16 pairs from a wave.
+// (Four waves with all keys and steps of their values needed no exchange of the state, but
+// one wave to a SIMD waited half of the time: 265 us at 256 heads of 2048 steps, 128 keys
+// and 64 values, bf16.)
 // Rounding to the activations' type: M and the state as operands for the results, which
-// are rounded to it anyway.  What is added to the state is split into two parts of that
-// type, so that the state has 16 (bf16) or 22 (f16) bits of every product.
+// are rounded to it anyway.  What is added to the state is split (kParts).
 // ENDS: the first of two passes, which finds each segment's end state for the second.
-// OUT: results wanted.
-template <class T, int NP, bool OUT, bool REVERSE, bool ENDS>
-__global__ __launch_bounds__(kWalkThreads) void linear_walk_kernel(const WalkArgs a) {
-    constexpr int Q = kChunk<T>, TT = Q / 16, KK = NP / 32, SS = Q / 32, NT = NP / 16;
+// OUT: results wanted.  FAST: the tensors' usual layout (WalkArgs), without the code for others
+// between what runs: 8 kB of instructions instead of 50.
+template <class T, int NP, bool OUT, bool REVERSE, bool ENDS, bool FAST>
+__global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void linear_walk_kernel(const WalkArgs a) {
+    constexpr int Q = kChunk<T>, TT = Q / 16, HT = TT / 2, KK = NP / 32, SS = Q / 32, NT = NP / 32;  // NT: of a wave
     constexpr int KS = NP + kRoom<T>, VS = kWalkValues + kRoom<T>, MS = Q + kRoom<T>;
+    constexpr bool F16 = std::is_same<T, f16>::value;
     struct __attribute__((aligned(16))) Shared {
         T k[Q * KS];
         T v[Q * VS];
         T q[OUT ? Q * KS : 8];
+        T x[OUT ? kWalkValues * KS : 8];  // a row per value
         T m[OUT ? Q * MS : 8];
-        Decays<T> d;
-        uint32_t most[3][4];
-        int odd[4];
+        Decays<T> d[2];
+        uint32_t most[3][kWalkWaves];
+        float most_x[kWalkWaves];
+        int odd[kWalkWaves];
+        float sums[2][2][kWalkValues];
     };
     __shared__ Shared sh;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tl = lane & 15, gl = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int pq = wave & 3, half = wave >> 2;
     const int blocks = (int)((a.P + kWalkValues - 1) / kWalkValues);
-    const int64_t bid = blockIdx.x;
-    const int pb = (int)(bid % blocks), h = (int)(bid / blocks % a.H);
-    const int64_t item = bid / blocks / a.H;
+    const int pb = (int)(blockIdx.x % blocks), h = (int)(blockIdx.x / blocks % (int)a.H);
+    const int64_t item = (int64_t)(blockIdx.x / blocks) / a.H;
     Item it;
     if (!find_item(a.q, item, (int)a.segment, it) || it.state < 0) return;
     const int len = it.end - it.beg, segments = chunks_of(len, (int)a.segment);
@@ -52,30 +59,29 @@ __global__ __launch_bounds__(kWalkThreads) void linear_walk_kernel(const WalkArg
     const int c0 = it.c * per, c1 = min(c0 + per, chunks);
 
     const int N = (int)a.N, P = (int)a.P;
-    const int p0 = pb * kWalkValues, p = p0 + 16 * wave + tl;
-    const bool live = p0 + 16 * wave < P;
+    const int p0 = pb * kWalkValues;
+    const bool live = p0 + 16 * pq < P;
     f32x4 x[NT];
-    // the lane's states of a row of a [rows, H, N, P] array: n = 16 tile + 4 gl + i, value p
-    auto place = [&](int64_t r) { return ((r * a.H + h) * N + 4 * gl) * P + p; };
-    auto get = [&](const float* from) {
-        const float* f = from + (p < P ? 0 : P - 1 - p);
+    // the lane's states of a row of a [rows, H, N, P] array: n = 16 (NT half + tile) + 4 gl + i, value p
+    auto exchange = [&](auto* base, int64_t r, auto&& each) {
+        const int lane = anew(threadIdx.x) & 63, p = p0 + 16 * pq + (lane & 15), n0 = 16 * NT * half + 4 * (lane >> 4);
+        auto* at = base + ((r * a.H + h) * N + n0) * P + p;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[n][i] = 16 * n + 4 * gl + i < N && p < P ? f[(int64_t)(16 * n + i) * P] : 0.0f;
+            for (int i = 0; i < 4; ++i) x[n][i] = each(x[n][i], at + (16 * n + i) * P, n0 + 16 * n + i < N && p < P);
     };
-    auto put = [&](float* to, float factor) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (16 * n + 4 * gl + i < N && p < P) to[(int64_t)(16 * n + i) * P] = x[n][i] * factor;
+    auto get = [&](const float* base, int64_t r) {
+        exchange(base, r, [](float, const float* at, bool there) { return there ? *at : 0.0f; });
     };
-    auto clear = [&]() {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) x[n] = f32x4{0, 0, 0, 0};
+    auto put = [&](float* base, int64_t r, float factor) {
+        exchange(base, r, [=](float v, float* at, bool there) {
+            if (there) *at = v * factor;
+            return v;
+        });
     };
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n] = f32x4{0, 0, 0, 0};
     // the item of the segment at a place of the walk
     auto item_at = [&](int j) { return item - it.c + (REVERSE ? segments - 1 - j : j); };
     float decay = 1.0f;  // of the segment
@@ -84,91 +90,129 @@ __global__ __launch_bounds__(kWalkThreads) void linear_walk_kernel(const WalkArg
         if (pos == 0 || pos == segments - 1) {
             // the last one's end is not needed: its place keeps the initial state, which the
             // final state may overwrite while the second pass still needs it
-            if (a.x_in) get(a.x_in + place(it.state));
-            else clear();
+            if (a.x_in) get(a.x_in, it.state);
             if (pos != 0) {
-                put(a.seg_x + place(item), 1.0f);
+                put(a.seg_x, item, 1.0f);
                 return;
             }
-        } else {
-            clear();
         }
     } else if (segments == 1) {
-        if (a.x_in) get(a.x_in + place(it.state));
-        else clear();
+        if (a.x_in) get(a.x_in, it.state);
     } else {
-        get(a.seg_x + place(item_at(pos == 0 ? segments - 1 : 0)));
+        get(a.seg_x, item_at(pos == 0 ? segments - 1 : 0));
         for (int j = 1; j < pos; ++j) {
             const int64_t before = item_at(j);
             const float e = a.seg_decay[before * a.H + h];
-            f32x4 y[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) y[n] = x[n];
-            get(a.seg_x + place(before));
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][i] = fmaf(y[n][i], e, x[n][i]);
+            exchange(a.seg_x, before, [=](float v, const float* at, bool there) { return fmaf(v, e, there ? *at : 0.0f); });
         }
     }
 
-    const int grp = (int)(h / (a.H / a.G));
-    const T* key = (const T*)a.key.data + it.row * a.key.sb + grp * a.key.sg;
-    const T* query = (const T*)a.query.data + it.row * a.query.sb + grp * a.query.sg;
-    const T* value = (const T*)a.value.data + it.row * a.value.sb + h * a.value.sg + p0 * a.value.sn;
-    T* result = (T*)a.result.data + it.row * a.result.sb + h * a.result.sg;
+    const int grp = h / (int)(a.H / a.G);
+    // the next chunk's first step
+    const int first = it.beg + (REVERSE ? c1 - 1 : c0) * Q;
+    const char* key = a.key.data + it.row * a.key.sb + grp * a.key.sg + first * a.key.sl;
+    const char* query = a.query.data + it.row * a.query.sb + grp * a.query.sg + first * a.query.sl;
+    const char* value = a.value.data + it.row * a.value.sb + h * a.value.sg + p0 * a.value.sn + first * a.value.sl;
+    T* result = (T*)a.result.data + it.row * a.result.sb + h * a.result.sg + (int64_t)(p0 + 16 * pq) * a.result.sn + first * a.result.sl;
     const float* gs = (const float*)a.g.data + it.row * a.g.sb + h * a.g.sh;
     const float* bs = a.beta.data ? (const float*)a.beta.data + it.row * a.beta.sb + h * a.beta.sh : nullptr;
     const float skip = a.D ? a.D[h] : 0.0f;
-    const int64_t Pp = (a.P + 31) / 32 * 32;
-    float* saved = a.saved && !ENDS ? a.saved + ((linear_row(a.q, it, Q) * a.H + h) * N + 4 * gl) * Pp + p : nullptr;
-
-    Carrier<T, NP, kWalkThreads> ck, cq;
-    Carrier<T, kWalkValues, kWalkThreads> cv;
-    float g = 0.0f, in = 0.0f, out = 0.0f;
-    auto load = [&](int c) {
-        const int t0 = it.beg + c * Q, nt = min(Q, it.end - t0);
-        ck.load(key + t0 * a.key.sl, a.key_lay, a.key.sn, a.key.sl, N, nt, tid);
-        cv.load(value + t0 * a.value.sl, a.value_lay, a.value.sn, a.value.sl, P - p0, nt, tid);
-        if (OUT) cq.load(query + t0 * a.query.sl, a.query_lay, a.query.sn, a.query.sl, N, nt, tid);
-        if (wave == 0) {
-            const int o = REVERSE ? Q - 1 - lane : lane, t = t0 + o;
-            g = in = out = 0.0f;
-            if (lane < Q && o < nt) {
-                const float b = bs ? bs[t * a.beta.sl] : 1.0f;
-                const int tg = REVERSE ? t + 1 : t;
-                g = tg < it.end ? gs[tg * a.g.sl] : 0.0f;
-                in = REVERSE ? a.scale : b;
-                out = REVERSE ? b : a.scale;
-            }
-        }
-    };
+    const bool vectors = FAST || (a.result.sn == 1 && P % 4 == 0);  // four values are stored at once
+    const int Np = (int)padded_keys(a.N), Pp = (int)padded_values(a.P);
+    float* saved = a.saved && !ENDS ? a.saved + (linear_row(a.q, it, Q) * a.H + h) * Np * Pp : nullptr;
 
     const int count = c1 - c0;
-    if (count > 0) load(REVERSE ? c1 - 1 : c0);
+    auto chunk = [&](int k) { return REVERSE ? c1 - 1 - k : c0 + k; };
+    Carrier<T, NP, kWalkThreads, FAST> ck, cq;
+    Carrier<T, kWalkValues, kWalkThreads, FAST> cv;
+    auto load = [&](int k) {
+        const int nt = min(Q, it.end - it.beg - chunk(k) * Q), tid = threadIdx.x;
+        ck.load(key, a.key, N, nt, tid);
+        cv.load(value, a.value, P - p0, nt, tid);
+        if (OUT) cq.load(query, a.query, N, nt, tid);
+        constexpr int64_t D = REVERSE ? -Q : Q;
+        key += D * a.key.sl, value += D * a.value.sl, query += D * a.query.sl;
+    };
+    // The decays are worked out a chunk ahead by the last wave, from what it loaded a chunk before.
+    float g = 0.0f, in = 0.0f, out = 0.0f;
+    auto load_decays = [&](int k) {
+        const int lane = threadIdx.x & 63, t0 = it.beg + chunk(k) * Q, o = REVERSE ? Q - 1 - lane : lane, t = t0 + o;
+        g = in = out = 0.0f;
+        if (lane < Q && t < it.end) {
+            const float b = bs ? bs[t * a.beta.sl] : 1.0f;
+            const int tg = REVERSE ? t + 1 : t;
+            g = tg < it.end ? gs[tg * a.g.sl] : 0.0f;
+            in = REVERSE ? a.scale : b;
+            out = REVERSE ? b : a.scale;
+        }
+    };
+    auto most_state = [&]() {  // float16: the largest finite magnitude of the wave's states
+        float m = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = fabsf(x[n][i]);
+                m = fmaxf(m, v < INFINITY ? v : 0.0f);
+            }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        if ((threadIdx.x & 63) == 0) sh.most_x[wave] = m;
+    };
+    if (count > 0) {
+        load(0);
+        if (wave == kWalkWaves - 1) {
+            load_decays(0);
+            put_decays<T>(sh.d[0], g, in, out, threadIdx.x & 63);
+            if (count > 1) load_decays(1);
+        }
+        if (OUT) {
+            if (F16) most_state();
+            // pairs s > t within two blocks of a product stay zero
+            for (int i = threadIdx.x; i < Q * MS; i += kWalkThreads) sh.m[i] = from_f<T>(0.0f);
+        }
+    }
     for (int k = 0; k < count; ++k) {
-        const int c = REVERSE ? c1 - 1 - k : c0 + k;
-        const int t0 = it.beg + c * Q, nt = min(Q, it.end - t0);
-        if (saved && p < Pp) {
+        const int c = chunk(k), t0 = it.beg + c * Q, nt = min(Q, it.end - t0);
+        const int tid = FAST ? threadIdx.x : anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;
+        const Decays<T>& d = sh.d[k & 1];
+        if (saved && p0 + 16 * pq < Pp) {
+            float* at = saved + (int64_t)c * a.H * Np * Pp + (16 * NT * half + 4 * gl) * Pp + p0 + 16 * pq + tl;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
+                if (16 * (NT * half + n) < Np) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (16 * n + 4 * gl + i < N)
-                        saved[(int64_t)c * a.H * N * Pp + (16 * n + i) * Pp] = p < P ? x[n][i] : 0.0f;
+                    for (int i = 0; i < 4; ++i) at[(16 * n + i) * Pp] = x[n][i];
+                }
         }
         __syncthreads();  // the last chunk's tiles have been read
-        ck.template store<REVERSE>(sh.k, a.key_lay, tid);
-        cv.template store<REVERSE>(sh.v, a.value_lay, tid);
-        if (OUT) cq.template store<REVERSE>(sh.q, a.query_lay, tid);
-        if (wave == 0) put_decays<T>(sh.d, g, in, out, lane);
+        ck.clear(a.key.lay, N, nt, tid);
+        cv.clear(a.value.lay, P - p0, nt, tid);
+        ck.template store<REVERSE>(sh.k, a.key.lay, tid);
+        cv.template store<REVERSE>(sh.v, a.value.lay, tid);
+        float sx = 1.0f;
+        if (OUT) {
+            cq.clear(a.query.lay, N, nt, tid);
+            cq.template store<REVERSE>(sh.q, a.query.lay, tid);
+            if (F16) sx = to_range<T>(fmaxf(sh.most_x[pq], sh.most_x[pq + 4]));
+            if (live) {
+                T* to = sh.x + (16 * pq + tl) * KS + 16 * NT * half + 4 * gl;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(x[n][i] * sx);
+                    *reinterpret_cast<Four*>(to + 16 * n) = w;
+                }
+            }
+        }
         {
             uint32_t mk = ck.most(), mv = cv.most(), mq = OUT ? cq.most() : 0;
-            if constexpr (std::is_same<T, f16>::value) {
+            if constexpr (F16) {
 #pragma unroll
-                for (int d = 1; d < 64; d <<= 1) {
-                    mk = max(mk, (uint32_t)__shfl_xor((int)mk, d)), mv = max(mv, (uint32_t)__shfl_xor((int)mv, d));
-                    if (OUT) mq = max(mq, (uint32_t)__shfl_xor((int)mq, d));
+                for (int i = 1; i < 64; i <<= 1) {
+                    mk = max(mk, (uint32_t)__shfl_xor((int)mk, i)), mv = max(mv, (uint32_t)__shfl_xor((int)mv, i));
+                    if (OUT) mq = max(mq, (uint32_t)__shfl_xor((int)mq, i));
                 }
                 if (lane == 0) sh.most[0][wave] = mk, sh.most[1][wave] = mv, sh.most[2][wave] = mq;
             }
@@ -176,174 +220,181 @@ __global__ __launch_bounds__(kWalkThreads) void linear_walk_kernel(const WalkArg
             if (lane == 0) sh.odd[wave] = any;
         }
         __syncthreads();
-        if (k + 1 < count) load(REVERSE ? c - 1 : c + 1);
+        if (k + 1 < count) load(k + 1);
+        if (wave == kWalkWaves - 1 && k + 1 < count) {
+            put_decays<T>(sh.d[(k + 1) & 1], g, in, out, lane);
+            if (k + 2 < count) load_decays(k + 2);
+        }
 
-        const float whole = sh.d.whole;
+        const float whole = d.whole;
         decay *= whole;
-        if (sh.d.odd | sh.odd[0] | sh.odd[1] | sh.odd[2] | sh.odd[3]) {
+        int odd = d.odd;
+#pragma unroll
+        for (int i = 0; i < kWalkWaves; ++i) odd |= sh.odd[i];
+        if (__builtin_expect(odd, 0)) {
             // An infinity or NaN among the inputs would reach earlier rows through the products'
             // zeros: the chunk goes row by row, as the formula says.
             for (int r = REVERSE ? Q - nt : 0; r < (REVERSE ? Q : nt); ++r) {
-                const float e = exp_f<kFine<T>>(sh.d.g[r]), in_r = sh.d.in[r];
-                const float v = to_f(sh.v[r * VS + 16 * wave + tl]);
+                const float e = exp_f<kFine<T>>(d.g[r]), in_r = d.in[r];
+                const float v = to_f(sh.v[r * VS + 16 * pq + tl]);
                 float sum = 0.0f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int at = 16 * n + 4 * gl + i;
-                        if (at < N) {
+                        const int at = 16 * (NT * half + n) + 4 * gl + i;
+                        if (at < N && p0 + 16 * pq + tl < P) {  // (what does not exist stays zero)
                             x[n][i] = fmaf(x[n][i], e, in_r * to_f(sh.k[r * KS + at]) * v);
                             if (OUT) sum = fmaf(x[n][i], to_f(sh.q[r * KS + at]), sum);
                         }
                     }
                 if (OUT) {
-                    sum = across_rows(sum) * sh.d.out[r];
-                    if (a.D) sum = fmaf(skip, v, sum);
-                    const int t = t0 + (REVERSE ? Q - 1 - r : r);
-                    if (gl == 0 && p < P) result[t * a.result.sl + p * a.result.sn] = from_f<T>(sum);
+                    sum = across_rows(sum);
+                    if (gl == 0) sh.sums[r & 1][half][16 * pq + tl] = sum;
+                    __syncthreads();
+                    if (half == 0 && gl == 0 && p0 + 16 * pq + tl < P) {
+                        sum = (sum + sh.sums[r & 1][1][16 * pq + tl]) * d.out[r];
+                        if (a.D) sum = fmaf(skip, v, sum);
+                        const int o = REVERSE ? Q - 1 - r : r;
+                        result[o * a.result.sl + tl * a.result.sn] = from_f<T>(sum);
+                    }
                 }
             }
-            continue;
-        }
-
-        float most[3] = {0, 0, 0};
-        if constexpr (std::is_same<T, f16>::value) {
+        } else {
+            float most[3] = {0, 0, 0};
+            if constexpr (F16) {
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const uint32_t m = max(max(sh.most[i][0], sh.most[i][1]), max(sh.most[i][2], sh.most[i][3]));
-                most[i] = to_f(__builtin_bit_cast(f16, (uint16_t)m));
+                for (int i = 0; i < 3; ++i) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int w = 0; w < kWalkWaves; ++w) m = max(m, sh.most[i][w]);
+                    most[i] = to_f(__builtin_bit_cast(f16, (uint16_t)m));
+                }
             }
-        }
-        const float most_in = sh.d.most_in * sh.d.grow, most_out = sh.d.most_out;  // float16 only
-        f32x4 across[OUT ? TT : 1];
-        float sm = 1.0f, sx = 1.0f;
-        if (OUT) {
-            sm = to_range<T>(most_in * most_out * most[0] * most[2] * (float)N + fabsf(skip));
-            // what the state before the chunk gives
+            const float most_in = d.most_in * d.grow;  // float16 only
+            f32x4 across[OUT ? HT : 1];
+            float sm = 1.0f;
+            if (OUT) {
+                sm = to_range<T>(most_in * d.most_out * most[0] * most[2] * (float)N + fabsf(skip));
+                // the pairs: tiles on the diagonal by the first waves, those below it by the others
+                auto pairs = [&](int ti, int si) {
+                    f32x4 m = {0, 0, 0, 0};
+                    const T* kp = sh.k + (16 * si + tl) * KS + 8 * gl;
+                    const T* qp = sh.q + (16 * ti + tl) * KS + 8 * gl;
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) m = mma<T>(row_frag<T>(kp + 32 * kk), row_frag<T>(qp + 32 * kk), m);
+                    return m;
+                };
+                auto keep = [&](int ti, int si, const f32x4& m) {
+                    struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(m[i] * sm);
+                    *reinterpret_cast<Four*>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl) = w;
+                };
+                if (wave < TT) {
+                    f32x4 m = pairs(wave, wave) * weights_within<T>(d, wave, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m[i] += 4 * gl + i == tl ? skip : 0.0f;
+                    keep(wave, wave, m);
+                } else if (wave >= 4) {
+                    for (int j = wave - 4; j < TT * (TT - 1) / 2; j += 4) {
+                        const int ti = j < 1 ? 1 : j < 3 ? 2 : 3, si = j - ti * (ti - 1) / 2;
+                        keep(ti, si, pairs(ti, si) * weights_across<T>(d, ti, si, lane));
+                    }
+                }
+                // what the state before the chunk gives
+                if (live) {
+#pragma unroll
+                    for (int t = 0; t < HT; ++t) across[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const Frag<T> f = row_frag<T>(sh.x + (16 * pq + tl) * KS + 32 * kk + 8 * gl);
+#pragma unroll
+                        for (int t = 0; t < HT; ++t)
+                            across[t] = mma<T>(f, row_frag<T>(sh.q + (16 * (HT * half + t) + tl) * KS + 32 * kk + 8 * gl), across[t]);
+                    }
+                }
+                __syncthreads();
+            }
             if (live) {
-                if constexpr (std::is_same<T, f16>::value) {
-                    float m = 0.0f;
+                Frag<T> vf[SS];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int s = 0; s < SS; ++s) vf[s] = column_frag<T>(sh.v + 32 * s * VS + 16 * pq, VS, lane);
+                if (OUT) {
+                    const float um = reciprocal_of_power(sm), ux = reciprocal_of_power(sx);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float v = fabsf(x[n][i]);
-                            m = fmaxf(m, v < INFINITY ? v : 0.0f);
+                    for (int t = 0; t < HT; ++t) {
+                        const int r = 16 * (HT * half + t) + tl, o = REVERSE ? Q - 1 - r : r;
+                        const T* mp = sh.m + r * MS + 8 * gl;
+                        f32x4 within = {0, 0, 0, 0};
+                        within = mma<T>(vf[0], row_frag<T>(mp), within);
+                        if (SS > 1 && half) within = mma<T>(vf[SS - 1], row_frag<T>(mp + 32), within);
+                        const float f = d.from[r] * ux;
+                        struct __attribute__((packed, aligned(sizeof(T)))) Four { T v[4]; } y;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y.v[i] = from_f<T>(fmaf(across[t][i], f, within[i] * um));
+                        const int there = P - (p0 + 16 * pq + 4 * gl);
+                        if (vectors) {
+                            if (o < nt && there > 0)
+                                *reinterpret_cast<Four*>((char*)result + (uint32_t)o * ((uint32_t)a.result.sl * (uint32_t)sizeof(T)) +
+                                                         4u * gl * (uint32_t)sizeof(T)) = y;
+                        } else {
+                            T* to = result + o * a.result.sl + 4 * gl * a.result.sn;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (o < nt && i < there) to[i * a.result.sn] = y.v[i];
                         }
-#pragma unroll
-                    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-                    sx = to_range<T>(m);
-                }
-#pragma unroll
-                for (int t = 0; t < TT; ++t) across[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    float e[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) e[i] = x[2 * kk][i] * sx, e[4 + i] = x[2 * kk + 1][i] * sx;
-                    const Frag<T> f = frag_of<T>(e);
-#pragma unroll
-                    for (int t = 0; t < TT; ++t)
-                        across[t] = mma<T>(f, pair_frag<T>(sh.q + (16 * t + tl) * KS + 32 * kk + 4 * gl), across[t]);
-                }
-            }
-            // the pairs' weights: a wave has rows 16 ti .. + 15, or half of them
-            const int ti = wave % TT;
-            Frag<T> qf[KK];
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) qf[kk] = row_frag<T>(sh.q + (16 * ti + tl) * KS + 32 * kk + 8 * gl);
-#pragma unroll
-            for (int j = 0; j < TT * TT / 4; ++j) {
-                const int si = wave / TT + j * (4 / TT);
-                f32x4 m = {0, 0, 0, 0};
-                if (si <= ti) {
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk)
-                        m = mma<T>(row_frag<T>(sh.k + (16 * si + tl) * KS + 32 * kk + 8 * gl), qf[kk], m);
-                    m *= pair_weights<T>(sh.d, ti, si, lane);
-                    if (si == ti) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m[i] += 4 * gl + i == tl ? skip : 0.0f;
                     }
                 }
-                struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
+                // the state after the chunk
+                const float sv = to_range<T>(most_in * most[1]), uv = reciprocal_of_power(sv);
+                Frag<T> part[SS][kParts<T>];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(m[i] * sm);
-                *reinterpret_cast<Four*>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl) = w;
-            }
-            __syncthreads();
-        }
-        if (!live) continue;
-        Frag<T> vf[SS];
+                for (int s = 0; s < SS; ++s) {
+                    const f32x4* to = reinterpret_cast<const f32x4*>(&d.to[32 * s + 8 * gl]);
+                    float w[8];
 #pragma unroll
-        for (int s = 0; s < SS; ++s) vf[s] = column_frag<T>(sh.v + 32 * s * VS + 16 * wave, VS, lane);
-        if (OUT) {
-            const float um = reciprocal_of_power(sm), ux = reciprocal_of_power(sx);
+                    for (int j = 0; j < 8; ++j) w[j] = frag_get<T>(vf[s], j) * (to[j / 4][j % 4] * sv);
+                    split<T>(w, part[s]);
+                }
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                f32x4 within = {0, 0, 0, 0};
+                for (int n = 0; n < NT; ++n) {
+                    f32x4 add = {0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s <= t / 2; ++s)
-                    within = mma<T>(vf[s], row_frag<T>(sh.m + (16 * t + tl) * MS + 32 * s + 8 * gl), within);
-                const int r = 16 * t + tl, o = REVERSE ? Q - 1 - r : r;
-                const float f = sh.d.from[r] * ux;
-                if (o < nt) {
-                    T* to = result + (t0 + o) * a.result.sl + (p0 + 16 * wave + 4 * gl) * a.result.sn;
-                    const int there = P - (p0 + 16 * wave + 4 * gl);
-                    Vec4<T> y;
+                    for (int s = 0; s < SS; ++s) {
+                        const Frag<T> kf = column_frag<T>(sh.k + 32 * s * KS + 16 * (NT * half + n), KS, lane);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y.v[i] = from_f<T>(fmaf(across[t][i], f, within[i] * um));
-                    if (there >= 4 && a.result.sn == 1) {
-                        *reinterpret_cast<Vec4<T>*>(to) = y;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i < there) to[i * a.result.sn] = y.v[i];
+                        for (int i = 0; i < kParts<T>; ++i) add = mma<T>(kf, part[s][i], add);
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[n][i] = fmaf(x[n][i], whole, add[i] * uv);
                 }
             }
         }
-        // the state after the chunk
-        const float sv = to_range<T>(most_in * most[1]), uv = reciprocal_of_power(sv);
-        Frag<T> hi[SS], lo[SS];
-#pragma unroll
-        for (int s = 0; s < SS; ++s) {
-            float w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = frag_get<T>(vf[s], j) * (sh.d.to[32 * s + 8 * gl + j] * sv);
-            split<T>(w, hi[s], lo[s]);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            f32x4 add = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < SS; ++s) {
-                const Frag<T> kf = column_frag<T>(sh.k + 32 * s * KS + 16 * n, KS, lane);
-                add = mma<T>(kf, hi[s], add);
-                if (kSplit<T>) add = mma<T>(kf, lo[s], add);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[n][i] = fmaf(x[n][i], whole, add[i] * uv);
-        }
+        if (F16 && OUT) most_state();
+        if (OUT) result += (REVERSE ? -Q : Q) * a.result.sl;
     }
     if (ENDS) {
-        put(a.seg_x + place(item), 1.0f);
-        if (pb == 0 && tid == 0) a.seg_decay[item * a.H + h] = decay;
+        put(a.seg_x, item, 1.0f);
+        if (pb == 0 && threadIdx.x == 0) a.seg_decay[item * a.H + h] = decay;
     } else if (a.x_out && pos == segments - 1) {
         // backwards: the gradient of the state before the first step
-        const float e = REVERSE && len > 0 ? exp_f<kFine<T>>(gs[it.beg * a.g.sl]) : 1.0f;
-        put(a.x_out + place(it.state), e);
+        put(a.x_out, it.state, REVERSE && len > 0 ? exp_f<kFine<T>>(gs[it.beg * a.g.sl]) : 1.0f);
     }
 }
 
-template <class T, int NP, bool REVERSE>
-hipError_t launch_walk_keys(const WalkArgs& a, hipStream_t s) {
+template <class T, int NP, bool REVERSE, bool FAST>
+static void launch_walk_lay(const WalkArgs& a, hipStream_t s) {
     const int64_t blocks = (a.P + kWalkValues - 1) / kWalkValues;
     const dim3 grid((unsigned)(a.items * a.H * blocks)), wg(kWalkThreads);
-    if (a.segment < a.q.L) hipLaunchKernelGGL((linear_walk_kernel<T, NP, false, REVERSE, true>), grid, wg, 0, s, a);
-    if (a.result.data) hipLaunchKernelGGL((linear_walk_kernel<T, NP, true, REVERSE, false>), grid, wg, 0, s, a);
-    else hipLaunchKernelGGL((linear_walk_kernel<T, NP, false, REVERSE, false>), grid, wg, 0, s, a);
+    if (a.segment < a.q.L) hipLaunchKernelGGL((linear_walk_kernel<T, NP, false, REVERSE, true, FAST>), grid, wg, 0, s, a);
+    if (a.result.data) hipLaunchKernelGGL((linear_walk_kernel<T, NP, true, REVERSE, false, FAST>), grid, wg, 0, s, a);
+    else if (!REVERSE) hipLaunchKernelGGL((linear_walk_kernel<T, NP, false, false, false, FAST>), grid, wg, 0, s, a);
+}
+template <class T, int NP, bool REVERSE>
+static hipError_t launch_walk_keys(const WalkArgs& a, hipStream_t s) {
+    if (a.fast) launch_walk_lay<T, NP, REVERSE, true>(a, s);
+    else launch_walk_lay<T, NP, REVERSE, false>(a, s);
     return hipGetLastError();
 }
 template <class T, bool REVERSE>
