@@ -340,6 +340,13 @@ __device__ __forceinline__ float across_rows(float v) {
     return v + __shfl_xor(v, 32);
 }
 
+// Neighbouring workgroups go to the eight dies in turn, each with a cache of its own.  The
+// place of workgroup `bid` of n in an order in which a die's workgroups are neighbours.
+__device__ __forceinline__ int64_t by_die(int64_t bid, int64_t n) {
+    const int64_t die = bid & 7, each = n >> 3, rest = n & 7;
+    return die * each + min(die, rest) + (bid >> 3);
+}
+
 // ---- decays of a chunk ----
 // With g_r the log decay of row r, the weight of the pair (t, s), s <= t, is
 // exp(g_{s+1} + .. + g_t).  It is never the quotient of two running products: those
