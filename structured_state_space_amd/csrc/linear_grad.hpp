@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
     const int count = (h1 - h0) * values;
     int h = h0, pb = 0;
     for (int k = 0; k < count; ++k) {
-        const int tid = FAST ? threadIdx.x : anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;
+        const int tid = anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;  // (addresses are not kept)
         const int p0 = pb * kPairValues, turn = (h - h0) & 1;
         const Decays<T>& d = sh.d[turn];
         Sums& sums = sh.sums[k & 1];
@@ -212,20 +212,6 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                 mv = max(mv, (uint32_t)__shfl_xor((int)mv, i)), my = max(my, (uint32_t)__shfl_xor((int)my, i));
             if (lane == 0) sh.most[0][wave] = mv, sh.most[1][wave] = my;
         }
-        // the states' fragments: keys n0 + 16 n + tl, values 32 kk + 8 gl .. + 7
-        f32x4 x[NT][PK][2], X[NT][PK][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int kk = 0; kk < PK; ++kk) {
-                x[n][kk][0] = x[n][kk][1] = X[n][kk][0] = X[n][kk][1] = f32x4{0, 0, 0, 0};
-                if (live && n0 + 16 * n < Np && p0 + 32 * kk < Pp) {
-                    const int64_t at = (row + h) * Np * Pp + ((n0 + 16 * n + tl) * Pp + p0 + 32 * kk + 8 * gl);
-                    const f32x4* s = reinterpret_cast<const f32x4*>(a.states + at);
-                    const f32x4* e = reinterpret_cast<const f32x4*>(a.ahead + at);
-                    x[n][kk][0] = s[0], x[n][kk][1] = s[1], X[n][kk][0] = e[0], X[n][kk][1] = e[1];
-                }
-            }
         __syncthreads();
         const int h_next = pb + 1 == values ? h + 1 : h, pb_next = pb + 1 == values ? 0 : pb + 1;
         if (k + 1 < count) load(h_next, pb_next);
@@ -280,10 +266,25 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                 if (first + 4 * j < BELOW) pairs(ti, si, weights_across<T>(d, ti, si, lane), qk[j], false);
             }
         }
+        const int h_now = h;
         if (wave == W - 2 && k) {
             collect(sh.sums[(k - 1) & 1]);
             if (pb == 0) finish(h - 1, turn ^ 1);
         }
+        // the states' fragments: keys n0 + 16 n + tl, values 32 kk + 8 gl .. + 7
+        f32x4 x[NT][PK][2], X[NT][PK][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int kk = 0; kk < PK; ++kk) {
+                x[n][kk][0] = x[n][kk][1] = X[n][kk][0] = X[n][kk][1] = f32x4{0, 0, 0, 0};
+                if (live && n0 + 16 * n < Np && p0 + 32 * kk < Pp) {
+                    const int64_t at = (row + h_now) * Np * Pp + ((n0 + 16 * n + tl) * Pp + p0 + 32 * kk + 8 * gl);
+                    const f32x4* s = reinterpret_cast<const f32x4*>(a.states + at);
+                    const f32x4* e = reinterpret_cast<const f32x4*>(a.ahead + at);
+                    x[n][kk][0] = s[0], x[n][kk][1] = s[1], X[n][kk][0] = e[0], X[n][kk][1] = e[1];
+                }
+            }
         __syncthreads();
         if (wave == W - 1 && h_next > h && h_next < h1) {
             keep_decays(turn ^ 1);
@@ -298,78 +299,99 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
         for (int n = 0; n < NT; ++n) {
             const int key = n0 + 16 * n;
             float whole = 0.0f;
-            f32x4 in[TW], out[TW];
 #pragma unroll
-            for (int t = 0; t < TW; ++t) in[t] = out[t] = f32x4{0, 0, 0, 0};
-            float sx = 1.0f, sX = 1.0f;
-            if constexpr (F16) {
-                float mx = 0.0f, mX = 0.0f;
+            for (int kk = 0; kk < PK; ++kk)
 #pragma unroll
-                for (int kk = 0; kk < PK; ++kk)
+                for (int i = 0; i < 8; ++i) whole = fmaf(x[n][kk][i / 4][i % 4], X[n][kk][i / 4][i % 4], whole);
+            // products of the states with a tile of steps (dy or v), and where they are scaled to
+            auto across = [&](const f32x4 (&state)[PK][2], const T* tile, f32x4 (&to)[TW]) {
+                const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
+                float s = 1.0f;
+                if constexpr (F16) {
+                    float m = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float u = fabsf(x[n][kk][i / 4][i % 4]), v = fabsf(X[n][kk][i / 4][i % 4]);
-                        mx = fmaxf(mx, u < INFINITY ? u : 0.0f), mX = fmaxf(mX, v < INFINITY ? v : 0.0f);
+                    for (int kk = 0; kk < PK; ++kk)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float u = fabsf(state[kk][i / 4][i % 4]);
+                            m = fmaxf(m, u < INFINITY ? u : 0.0f);
+                        }
+#pragma unroll
+                    for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
+                    s = to_range<T>(m);
+                }
+#pragma unroll
+                for (int t = 0; t < TW; ++t) to[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < PK; ++kk) {
+                    float u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = state[kk][i / 4][i % 4] * s;
+                    Frag<T> part[kParts<T>];
+                    split<T>(u, part);
+#pragma unroll
+                    for (int t = 0; t < TW; ++t) {
+                        const Frag<T> f = row_frag<T>(tile + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+#pragma unroll
+                        for (int i = 0; i < kParts<T>; ++i) to[t] = mma<T>(part[i], f, to[t]);
                     }
-#pragma unroll
-                for (int i = 1; i < 64; i <<= 1) mx = fmaxf(mx, __shfl_xor(mx, i)), mX = fmaxf(mX, __shfl_xor(mX, i));
-                sx = to_range<T>(mx), sX = to_range<T>(mX);
-            }
-#pragma unroll
-            for (int kk = 0; kk < PK; ++kk) {
-                float u[8], v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    whole = fmaf(x[n][kk][i / 4][i % 4], X[n][kk][i / 4][i % 4], whole);
-                    u[i] = x[n][kk][i / 4][i % 4] * sx, v[i] = X[n][kk][i / 4][i % 4] * sX;
                 }
-                Frag<T> part[kParts<T>];
-                split<T>(u, part);
+                return reciprocal_of_power(s);
+            };
+            struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; };
+            {
+                const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
+                f32x4 in[TW];
+                const float ux = across(x[n], sh.dy, in);
+                Frag<T> kf[SS];
+#pragma unroll
+                for (int s = 0; s < SS; ++s) kf[s] = column_frag<T>(sh.k + 32 * s * KS + key, KS, lane);
 #pragma unroll
                 for (int t = 0; t < TW; ++t) {
-                    const Frag<T> f = row_frag<T>(sh.dy + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+                    const int tt = TW * group + t, r = 16 * tt + tl;
+                    f32x4 w = {0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < kParts<T>; ++i) in[t] = mma<T>(part[i], f, in[t]);
+                    for (int s = 0; s < SS; ++s)
+                        if (s <= tt / 2) w = mma<T>(kf[s], row_frag<T>(sh.m + r * MS + 32 * s + 8 * gl), w);
+                    const float from = d.from[r] * ux;
+                    const Four q4 = *reinterpret_cast<const Four*>(sh.q + r * KS + key + 4 * gl);
+                    float before = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float u = in[t][i] * from;
+                        before = fmaf(u, to_f(q4.v[i]), before);
+                        dq[n][t][i] += fmaf(w[i], um, u);
+                    }
+                    before = across_rows(before);
+                    if (gl == 0) sums.before[tile + n][r] = before;
                 }
-                split<T>(v, part);
+            }
+            {
+                const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
+                f32x4 out[TW];
+                const float uX = across(X[n], sh.v, out);
+                Frag<T> qf[SS];
+#pragma unroll
+                for (int s = 0; s < SS; ++s) qf[s] = column_frag<T>(sh.q + 32 * s * KS + key, KS, lane);
 #pragma unroll
                 for (int t = 0; t < TW; ++t) {
-                    const Frag<T> f = row_frag<T>(sh.v + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+                    const int tt = TW * group + t, r = 16 * tt + tl;
+                    f32x4 w = {0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < kParts<T>; ++i) out[t] = mma<T>(part[i], f, out[t]);
+                    for (int s = 0; s < SS; ++s)
+                        if (s >= tt / 2) w = mma<T>(qf[s], column_frag<T>(sh.m + 32 * s * MS + 16 * tt, MS, lane), w);
+                    const float to = d.to[r] * next * uX, b = sh.beta[turn][r];
+                    const Four k4 = *reinterpret_cast<const Four*>(sh.k + r * KS + key + 4 * gl);
+                    float behind = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = out[t][i] * to;
+                        behind = fmaf(v, to_f(k4.v[i]), behind);
+                        dk[n][t][i] += fmaf(w[i], um, v * b);
+                    }
+                    behind = across_rows(behind);
+                    if (gl == 0) sums.behind[tile + n][r] = behind;
                 }
-            }
-            const float ux = reciprocal_of_power(sx), uX = reciprocal_of_power(sX);
-            Frag<T> kf[SS], qf[SS];
-#pragma unroll
-            for (int s = 0; s < SS; ++s) {
-                kf[s] = column_frag<T>(sh.k + 32 * s * KS + key, KS, lane);
-                qf[s] = column_frag<T>(sh.q + 32 * s * KS + key, KS, lane);
-            }
-#pragma unroll
-            for (int t = 0; t < TW; ++t) {
-                const int tt = TW * group + t, r = 16 * tt + tl;
-                f32x4 wq = {0, 0, 0, 0}, wk = {0, 0, 0, 0};
-#pragma unroll
-                for (int s = 0; s < SS; ++s) {
-                    if (s <= tt / 2) wq = mma<T>(kf[s], row_frag<T>(sh.m + r * MS + 32 * s + 8 * gl), wq);
-                    if (s >= tt / 2) wk = mma<T>(qf[s], column_frag<T>(sh.m + 32 * s * MS + 16 * tt, MS, lane), wk);
-                }
-                const float from = d.from[r] * ux, to = d.to[r] * next * uX, b = sh.beta[turn][r];
-                struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; };
-                const Four q4 = *reinterpret_cast<const Four*>(sh.q + r * KS + key + 4 * gl);
-                const Four k4 = *reinterpret_cast<const Four*>(sh.k + r * KS + key + 4 * gl);
-                float before = 0.0f, behind = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = in[t][i] * from, v = out[t][i] * to;
-                    before = fmaf(u, to_f(q4.v[i]), before);
-                    behind = fmaf(v, to_f(k4.v[i]), behind);
-                    dq[n][t][i] += fmaf(wq[i], um, u);
-                    dk[n][t][i] += fmaf(wk[i], um, v * b);
-                }
-                before = across_rows(before), behind = across_rows(behind);
-                if (gl == 0) sums.before[tile + n][r] = before, sums.behind[tile + n][r] = behind;
             }
             whole = across_rows(row_sum(whole));
             if (lane == 0) sums.whole[tile + n] = whole;

@@ -54,6 +54,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     if (!find_item(a.q, item, (int)a.segment, it) || it.state < 0) return;
     const int len = it.end - it.beg, segments = chunks_of(len, (int)a.segment);
     if (it.c >= segments) return;
+    if (ENDS && segments == 1) return;
     const int pos = REVERSE ? segments - 1 - it.c : it.c;  // in the order of the walk
     const int chunks = (len + Q - 1) / Q, per = (int)(a.segment / Q);
     const int c0 = it.c * per, c1 = min(c0 + per, chunks);
@@ -61,9 +62,11 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     const int N = (int)a.N, P = (int)a.P;
     const int p0 = pb * kWalkValues;
     const bool live = p0 + 16 * pq < P;
+    // the wave's tiles of rows: of four the first and last or the two between, as many pairs in either
+    auto tile = [&](int t) { return HT == 2 && t ? 3 - half : half; };
     f32x4 x[NT];
     // the lane's states of a row of a [rows, H, N, P] array: n = 16 (NT half + tile) + 4 gl + i, value p
-    auto exchange = [&](auto* base, int64_t r, auto&& each) {
+    auto exchange = [&](f32x4 (&x)[NT], auto* base, int64_t r, auto&& each) {
         const int lane = anew(threadIdx.x) & 63, p = p0 + 16 * pq + (lane & 15), n0 = 16 * NT * half + 4 * (lane >> 4);
         auto* at = base + ((r * a.H + h) * N + n0) * P + p;
 #pragma unroll
@@ -72,41 +75,14 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
             for (int i = 0; i < 4; ++i) x[n][i] = each(x[n][i], at + (16 * n + i) * P, n0 + 16 * n + i < N && p < P);
     };
     auto get = [&](const float* base, int64_t r) {
-        exchange(base, r, [](float, const float* at, bool there) { return there ? *at : 0.0f; });
+        exchange(x, base, r, [](float, const float* at, bool there) { return there ? *at : 0.0f; });
     };
     auto put = [&](float* base, int64_t r, float factor) {
-        exchange(base, r, [=](float v, float* at, bool there) {
+        exchange(x, base, r, [=](float v, float* at, bool there) {
             if (there) *at = v * factor;
             return v;
         });
     };
-#pragma unroll
-    for (int n = 0; n < NT; ++n) x[n] = f32x4{0, 0, 0, 0};
-    // the item of the segment at a place of the walk
-    auto item_at = [&](int j) { return item - it.c + (REVERSE ? segments - 1 - j : j); };
-    float decay = 1.0f;  // of the segment
-    if (ENDS) {
-        if (segments == 1) return;
-        if (pos == 0 || pos == segments - 1) {
-            // the last one's end is not needed: its place keeps the initial state, which the
-            // final state may overwrite while the second pass still needs it
-            if (a.x_in) get(a.x_in, it.state);
-            if (pos != 0) {
-                put(a.seg_x, item, 1.0f);
-                return;
-            }
-        }
-    } else if (segments == 1) {
-        if (a.x_in) get(a.x_in, it.state);
-    } else {
-        get(a.seg_x, item_at(pos == 0 ? segments - 1 : 0));
-        for (int j = 1; j < pos; ++j) {
-            const int64_t before = item_at(j);
-            const float e = a.seg_decay[before * a.H + h];
-            exchange(a.seg_x, before, [=](float v, const float* at, bool there) { return fmaf(v, e, there ? *at : 0.0f); });
-        }
-    }
-
     const int grp = h / (int)(a.H / a.G);
     // the next chunk's first step
     const int first = it.beg + (REVERSE ? c1 - 1 : c0) * Q;
@@ -161,8 +137,52 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     };
     if (count > 0) {
         load(0);
+        if (wave == kWalkWaves - 1) load_decays(0);
+    }
+    // the state, while the first chunk's loads are under way
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n] = f32x4{0, 0, 0, 0};
+    // the item of the segment at a place of the walk
+    auto item_at = [&](int j) { return item - it.c + (REVERSE ? segments - 1 - j : j); };
+    float decay = 1.0f;  // of the segment
+    if (ENDS) {
+        if (pos == 0 || pos == segments - 1) {
+            // the last one's end is not needed: its place keeps the initial state, which the
+            // final state may overwrite while the second pass still needs it
+            if (a.x_in) get(a.x_in, it.state);
+            if (pos != 0) {
+                put(a.seg_x, item, 1.0f);
+                return;
+            }
+        }
+    } else if (segments == 1) {
+        if (a.x_in) get(a.x_in, it.state);
+    } else {
+        get(a.seg_x, item_at(pos == 0 ? segments - 1 : 0));
+        // the segments between, several under way
+        constexpr int A = NT > 4 ? 2 : 4;
+        for (int j = 1; j < pos; j += A) {
+            f32x4 y[A][NT];
+            float e[A];
+#pragma unroll
+            for (int i = 0; i < A; ++i) {
+                const int64_t before = item_at(min(j + i, pos - 1));
+                e[i] = a.seg_decay[before * a.H + h];
+                exchange(y[i], a.seg_x, before, [](float, const float* at, bool there) { return there ? *at : 0.0f; });
+            }
+#pragma unroll
+            for (int i = 0; i < A; ++i)
+                if (j + i < pos) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[n][r] = fmaf(x[n][r], e[i], y[i][n][r]);
+                }
+        }
+    }
+
+    if (count > 0) {
         if (wave == kWalkWaves - 1) {
-            load_decays(0);
             put_decays<T>(sh.d[0], g, in, out, threadIdx.x & 63);
             if (count > 1) load_decays(1);
         }
@@ -174,7 +194,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     }
     for (int k = 0; k < count; ++k) {
         const int c = chunk(k), t0 = it.beg + c * Q, nt = min(Q, it.end - t0);
-        const int tid = FAST ? threadIdx.x : anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;
+        const int tid = anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;  // (addresses are not kept)
         const Decays<T>& d = sh.d[k & 1];
         if (saved && p0 + 16 * pq < Pp) {
             float* at = saved + (int64_t)c * a.H * Np * Pp + (16 * NT * half + 4 * gl) * Pp + p0 + 16 * pq + tl;
@@ -296,8 +316,8 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
 #pragma unroll
                     for (int i = 0; i < 4; ++i) m[i] += 4 * gl + i == tl ? skip : 0.0f;
                     keep(wave, wave, m);
-                } else if (wave >= 4) {
-                    for (int j = wave - 4; j < TT * (TT - 1) / 2; j += 4) {
+                } else if (wave >= 4 && wave < kWalkWaves - 1) {  // (the last wave has the decays)
+                    for (int j = wave - 4; j < TT * (TT - 1) / 2; j += 3) {
                         const int ti = j < 1 ? 1 : j < 3 ? 2 : 3, si = j - ti * (ti - 1) / 2;
                         keep(ti, si, pairs(ti, si) * weights_across<T>(d, ti, si, lane));
                     }
@@ -311,7 +331,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                         const Frag<T> f = row_frag<T>(sh.x + (16 * pq + tl) * KS + 32 * kk + 8 * gl);
 #pragma unroll
                         for (int t = 0; t < HT; ++t)
-                            across[t] = mma<T>(f, row_frag<T>(sh.q + (16 * (HT * half + t) + tl) * KS + 32 * kk + 8 * gl), across[t]);
+                            across[t] = mma<T>(f, row_frag<T>(sh.q + (16 * tile(t) + tl) * KS + 32 * kk + 8 * gl), across[t]);
                     }
                 }
                 __syncthreads();
@@ -324,11 +344,11 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                     const float um = reciprocal_of_power(sm), ux = reciprocal_of_power(sx);
 #pragma unroll
                     for (int t = 0; t < HT; ++t) {
-                        const int r = 16 * (HT * half + t) + tl, o = REVERSE ? Q - 1 - r : r;
+                        const int r = 16 * tile(t) + tl, o = REVERSE ? Q - 1 - r : r;
                         const T* mp = sh.m + r * MS + 8 * gl;
                         f32x4 within = {0, 0, 0, 0};
                         within = mma<T>(vf[0], row_frag<T>(mp), within);
-                        if (SS > 1 && half) within = mma<T>(vf[SS - 1], row_frag<T>(mp + 32), within);
+                        if (SS > 1 && t) within = mma<T>(vf[SS - 1], row_frag<T>(mp + 32), within);
                         const float f = d.from[r] * ux;
                         struct __attribute__((packed, aligned(sizeof(T)))) Four { T v[4]; } y;
 #pragma unroll
