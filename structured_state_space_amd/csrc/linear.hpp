@@ -58,12 +58,45 @@ __device__ __forceinline__ f32x4 mma<float>(const Frag<float>& a, const Frag<flo
     return c;
 }
 
+// two numbers rounded to the type, in a word
+template <class T>
+__device__ __forceinline__ uint32_t pack_two(float a, float b) {
+    if constexpr (std::is_same<T, bf16>::value) {  // (one instruction; number by number it took one each and a third)
+        using f32x2 = float __attribute__((ext_vector_type(2)));
+        using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    } else {
+        return __builtin_bit_cast(uint16_t, from_f<T>(a)) | (uint32_t)__builtin_bit_cast(uint16_t, from_f<T>(b)) << 16;
+    }
+}
 template <class T>
 __device__ __forceinline__ Frag<T> frag_of(const float (&x)[8]) {
-    Frag<T> f;
+    u32x4 w;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f.v[j] = __builtin_bit_cast(short, from_f<T>(x[j]));
-    return f;
+    for (int j = 0; j < 4; ++j) w[j] = pack_two<T>(x[2 * j], x[2 * j + 1]);
+    return {__builtin_bit_cast(i16x8, w)};
+}
+// four numbers, rounded to the type
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Quad {
+    uint32_t w[sizeof(T)];
+};
+template <class T>
+__device__ __forceinline__ Quad<T> four_of(const f32x4& x) {
+    if constexpr (sizeof(T) == 4)
+        return {{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}};
+    else return {{pack_two<T>(x[0], x[1]), pack_two<T>(x[2], x[3])}};
+}
+template <class T>
+__device__ __forceinline__ T get_of(const Quad<T>& f, int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(f.w[i]);
+    else return __builtin_bit_cast(T, (uint16_t)(f.w[i / 2] >> (16 * (i & 1))));
+}
+// in LDS, where they are aligned
+template <class T>
+__device__ __forceinline__ void put_four(T* at, const f32x4& x) {
+    struct __attribute__((aligned(4 * sizeof(T)))) Aligned { Quad<T> v; };
+    *reinterpret_cast<Aligned*>(at) = {four_of<T>(x)};
 }
 template <>
 __device__ __forceinline__ Frag<float> frag_of<float>(const float (&x)[8]) {
@@ -89,10 +122,10 @@ __device__ __forceinline__ void split(const float (&x)[8], Frag<T> (&part)[kPart
     float r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        // one number for all parts: a product would be rounded to f16 in one step for the
+        // one number for both parts: a product would be rounded to f16 in one step for the
         // first and by way of float32 for the second
         r[j] = x[j];
-        if (kParts<T> > 1) asm("" : "+v"(r[j]));
+        if (std::is_same<T, f16>::value) asm("" : "+v"(r[j]));
     }
     part[0] = frag_of<T>(r);
 #pragma unroll
@@ -334,10 +367,29 @@ __device__ __forceinline__ float row_sum(float v) {
     v += dpp<0x141>(v);   // the other quad of eight
     return v + dpp<0x140>(v);
 }
-// sums over lanes 16 and 32 apart, in every lane
+// the sum over a row's lanes from this one on, and up to this one
+__device__ __forceinline__ float row_suffix(float v) {
+    v += dpp_zero<0x101>(v);
+    v += dpp_zero<0x102>(v);
+    v += dpp_zero<0x104>(v);
+    return v + dpp_zero<0x108>(v);
+}
+__device__ __forceinline__ float row_prefix(float v) {
+    v += dpp_zero<0x111>(v);
+    v += dpp_zero<0x112>(v);
+    v += dpp_zero<0x114>(v);
+    return v + dpp_zero<0x118>(v);
+}
+// lane i's value, in every lane
+__device__ __forceinline__ float of_lane(float v, int i) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+}
+// sums over lanes 16 and 32 apart, in every lane (exchanges of registers, not by way of LDS)
 __device__ __forceinline__ float across_rows(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // Neighbouring workgroups go to the eight dies in turn, each with a cache of its own.  The
@@ -371,16 +423,12 @@ __device__ __forceinline__ void put_decays(Decays<T>& d, float g, float in, floa
     constexpr int Q = kChunk<T>, B = Q / 16;
     const bool row = lane < Q;
     g = row ? g : 0.0f, in = row ? in : 0.0f, out = row ? out : 0.0f;
-    float pre = g, suf = dpp_zero<0x101>(g);
-    pre += dpp_zero<0x111>(pre), suf += dpp_zero<0x101>(suf);
-    pre += dpp_zero<0x112>(pre), suf += dpp_zero<0x102>(suf);
-    pre += dpp_zero<0x114>(pre), suf += dpp_zero<0x104>(suf);
-    pre += dpp_zero<0x118>(pre), suf += dpp_zero<0x108>(suf);
+    const float pre = row_prefix(g), suf = row_suffix(dpp_zero<0x101>(g));
     float sum[B], before = 0.0f, after = 0.0f, all = 0.0f;
     const int block = lane >> 4;
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-        sum[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pre), 16 * b + 15));
+        sum[b] = of_lane(pre, 16 * b + 15);
         before += b < block ? sum[b] : 0.0f;
         after += b > block ? sum[b] : 0.0f;
         all += sum[b];
@@ -523,7 +571,10 @@ struct LinearStepArgs {
 };
 
 // The states kept for the backward pass, one before every chunk: row (first of the
-// sequence + chunk) of [rows, H, padded N, padded P], zero where there is none
+// sequence + chunk) of [rows, H, padded N / 16, padded P, 16], zero where there is none.
+// (Sixteen keys of a value lie together: the walk's lane has four of them, and stores a vector.
+// The walk is bound by its vector instructions, and a vector instead of four numbers saves a
+// sixteenth of them.)
 __host__ __device__ inline int64_t padded_keys(int64_t N) { return (N + 15) / 16 * 16; }
 __host__ __device__ inline int64_t padded_values(int64_t P) { return (P + 31) / 32 * 32; }
 __host__ __device__ inline int64_t linear_rows(int64_t S, int64_t L, bool packed, int Q) {

@@ -25,9 +25,12 @@ constexpr int kPairThreads = 512;
 // Values beyond 64 go block by block; every sum is linear in them.  q_t . k_s is formed
 // once for all heads.  A wave has 16 keys (or more), and all steps or some of them; results
 // lie transposed (lane: step, registers: four keys), so that rows of four keys are
-// multiplied with q and k at once.  The sums over pairs and keys go through LDS, of two
-// blocks in turn, and become dg and dbeta a block later, beside the other waves' work; so do
-// the next head's decays.
+// multiplied with q and k at once.  The sums over pairs and keys go through LDS and become dg
+// and dbeta a block later, in the last wave, beside the other waves' pairs; so do the decays
+// of the head after the next.
+// 128 chunks of 64 steps, 64 heads of 128 keys and 64 values, one group, bf16: 241 us.  The saved
+// states alone, 537 MB, take 113 us at a copy's rate; of the rest, vector instructions (a third
+// of them split the states) and the tiles' reads from LDS have most, at two waves to a SIMD.
 template <class T, int NP, bool FAST>
 __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const PairArgs a) {
     constexpr int TH = kPairThreads, W = TH / 64;
@@ -36,17 +39,25 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
     constexpr int GROUPS = TILES >= W ? 1 : W / TILES < TT ? W / TILES : TT, TW = TT / GROUPS;  // of the steps; tiles of one
     constexpr int KS = NP + kRoom<T>, VS = kPairValues + kRoom<T>, MS = Q + kRoom<T>;
     constexpr bool F16 = std::is_same<T, f16>::value;
-    struct Sums {  // of W over the pairs of a tile's rows and columns, and on the diagonal
-        float rows[TT][Q], columns[TT][Q], diagonal[Q];
-        float before[TILES][Q], behind[TILES][Q], whole[TILES], skip[TT];
+    // The states of the next block are loaded a block ahead, and v and dy two, where the registers
+    // and LDS take it.  In float32 two workgroups share a compute unit instead: 27 us at 256 chunks of
+    // 32 steps, 4 heads of 64 keys and values in two groups; loaded ahead, with one workgroup, 36.
+    constexpr bool EARLY = sizeof(T) == 2 && NT == 1;
+    constexpr int RING = EARLY ? 3 : 2;  // tiles of v and dy
+    struct PairSums {  // of W over the pairs of a tile's rows and columns, and on the diagonal
+        float rows[TT][Q], columns[TT][Q], diagonal[Q], skip[TT];
+    };
+    struct KeySums {
+        float before[TILES][Q], behind[TILES][Q], whole[TILES];
     };
     struct __attribute__((aligned(16))) Shared {
-        T q[Q * KS], k[Q * KS], v[Q * VS], dy[Q * VS], m[Q * MS];
-        Decays<T> d[2];
-        float beta[2][Q];
-        float next[2], across[2], most_beta[2];  // the decay to the next chunk's first step; over the chunk and it
-        Sums sums[2];
-        uint32_t most[2][W];
+        T q[Q * KS], k[Q * KS], v[RING][Q * VS], dy[RING][Q * VS], m[2][Q * MS];
+        Decays<T> d[4];
+        float beta[4][Q];
+        float next[4], across[4], most_beta[4];  // the decay to the next chunk's first step; over the chunk and it
+        PairSums pairs[3];
+        KeySums keys[2];
+        uint32_t most[2][2][W];
     };
     __shared__ Shared sh;
 
@@ -76,11 +87,14 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
         ck.clear(a.k.lay, N, nt, tid);
         cq.template store<false>(sh.q, a.qv.lay, tid);
         ck.template store<false>(sh.k, a.k.lay, tid);
-        for (int i = tid; i < Q * MS; i += TH) sh.m[i] = from_f<T>(0.0f);  // pairs s > t stay zero
+        for (int i = tid; i < 2 * Q * MS; i += TH) sh.m[0][i] = from_f<T>(0.0f);  // pairs s > t stay zero
     }
+    struct Block {  // of values of a head
+        int h, pb;
+    };
     Carrier<T, kPairValues, TH, FAST> cv, cy;
-    auto load = [&](int h, int pb) {
-        const int p0 = pb * kPairValues, tid = threadIdx.x;
+    auto load = [&](const Block& b) {
+        const int h = b.h, p0 = b.pb * kPairValues, tid = threadIdx.x;
         cv.load(a.v.data + it.row * a.v.sb + h * a.v.sg + t0 * a.v.sl + p0 * a.v.sn, a.v, P - p0, nt, tid);
         cy.load(a.dy.data + it.row * a.dy.sb + h * a.dy.sg + t0 * a.dy.sl + p0 * a.dy.sn, a.dy, P - p0, nt, tid);
     };
@@ -109,10 +123,10 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
             if (lane == 0) sh.most_beta[i] = m;
         }
     };
-    // the wave before it, lane r: a head's sums over its blocks of values
+    // and, lane r, a head's sums over its blocks of values
     float sum_row = 0.0f, sum_column = 0.0f, sum_diagonal = 0.0f, sum_before = 0.0f, sum_behind = 0.0f, sum_whole = 0.0f,
           sum_skip = 0.0f;
-    auto collect = [&](const Sums& s) {
+    auto collect = [&](const PairSums& s, const KeySums& o) {
         const int lane = anew(threadIdx.x) & 63;
         if (lane < Q) {
             const int own = lane >> 4;
@@ -123,10 +137,10 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
             }
             sum_diagonal += s.diagonal[lane];
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) sum_before += s.before[i][lane], sum_behind += s.behind[i][lane];
+            for (int i = 0; i < TILES; ++i) sum_before += o.before[i][lane], sum_behind += o.behind[i][lane];
         }
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) sum_whole += s.whole[i];
+        for (int i = 0; i < TILES; ++i) sum_whole += o.whole[i];
 #pragma unroll
         for (int i = 0; i < TT; ++i) sum_skip += s.skip[i];
     };
@@ -134,13 +148,14 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
         const int lane = anew(threadIdx.x) & 63, r = min(lane, Q - 1);
         const float b = sh.beta[i][r], own = b * sum_behind;
         // sums over the steps from r on, and before r
-        float from = sum_row + sum_before - b * sum_column, till = own;
+        float from = row_suffix(sum_row + sum_before - b * sum_column), till = row_prefix(own);
+        float later = 0.0f, earlier = 0.0f;
 #pragma unroll
-        for (int d = 1; d < Q; d <<= 1) {
-            const float f = __shfl_down(from, d), e = __shfl_up(till, d);
-            if (lane + d < Q) from += f;
-            if (lane >= d) till += e;
+        for (int i = 0; i < TT; ++i) {
+            const float f = of_lane(from, 16 * i), e = of_lane(till, 16 * i + 15);
+            later += i > (lane >> 4) ? f : 0.0f, earlier += i < (lane >> 4) ? e : 0.0f;
         }
+        from += later, till += earlier;
         const float dg = from + (till - own) + sh.across[i] * sum_whole;
         if (lane < nt) {
             // a reset takes part in no product, and the sums' rounding is not left in its place
@@ -154,29 +169,53 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
         sum_row = sum_column = sum_diagonal = sum_before = sum_behind = sum_whole = sum_skip = 0.0f;
     };
 
-    load(h0, 0);
+    const int count = (h1 - h0) * values;
+    auto behind = [&](const Block& b) { return b.pb + 1 == values ? Block{b.h + 1, 0} : Block{b.h, b.pb + 1}; };
+    auto place = [&](int h) { return (h - h0) & 3; };  // of a head's decays
+    // block k's tiles, loaded before
+    auto store = [&](const Block& b, int k) {
+        const int tid = threadIdx.x, i = k % RING;
+        cv.clear(a.v.lay, P - b.pb * kPairValues, nt, tid);
+        cy.clear(a.dy.lay, P - b.pb * kPairValues, nt, tid);
+        cv.template store<false>(sh.v[i], a.v.lay, tid);
+        cy.template store<false>(sh.dy[i], a.dy.lay, tid);
+        if constexpr (F16) {
+            uint32_t mv = cv.most(), my = cy.most();
+#pragma unroll
+            for (int i = 1; i < 64; i <<= 1)
+                mv = max(mv, (uint32_t)__shfl_xor((int)mv, i)), my = max(my, (uint32_t)__shfl_xor((int)my, i));
+            if ((tid & 63) == 0) sh.most[k & 1][0][wave] = mv, sh.most[k & 1][1][wave] = my;
+        }
+    };
+    Block now = {h0, 0}, next = now;  // blocks k and k + 1
+    load(next);
     if (wave == W - 1) {
         load_decays(h0);
         keep_decays(0);
         if (h0 + 1 < h1) load_decays(h0 + 1);
     }
+    store(next, 0);
+    if (count > 1) {
+        const Block second = behind(next);
+        load(second);
+    }
     __syncthreads();
 
     // the wave's pairs: a tile on the diagonal, or one or two below it
-    constexpr int BELOW = TT * (TT - 1) / 2, OWN = BELOW > 4 ? 2 : 1;
+    constexpr int BELOW = TT * (TT - 1) / 2, OWN = BELOW > 3 ? 2 : 1;
     auto below = [](int j, int& ti, int& si) {
         ti = j < 1 ? 1 : j < 3 ? 2 : 3;
         si = j - ti * (ti - 1) / 2;
     };
     const bool diagonal = wave < TT;
-    const int first = diagonal ? 0 : wave < 4 ? BELOW : wave - 4;
+    const int first = diagonal ? 0 : wave < 4 || wave == W - 1 ? BELOW : wave - 4;  // (the last wave has the sums)
     f32x4 qk[OWN];
 #pragma unroll
     for (int j = 0; j < OWN; ++j) {
         qk[j] = f32x4{0, 0, 0, 0};
         int ti = wave, si = wave;
-        if (!diagonal) below(first + 4 * j, ti, si);
-        if (diagonal ? j == 0 : first + 4 * j < BELOW) {
+        if (!diagonal) below(first + 3 * j, ti, si);
+        if (diagonal ? j == 0 : first + 3 * j < BELOW) {
             const int lane = threadIdx.x & 63;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
@@ -193,214 +232,223 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
 #pragma unroll
         for (int t = 0; t < TW; ++t) dq[n][t] = dk[n][t] = f32x4{0, 0, 0, 0};
 
-    const int count = (h1 - h0) * values;
-    int h = h0, pb = 0;
-    for (int k = 0; k < count; ++k) {
+    // the states' fragments: keys n0 + 16 n + tl, values 32 kk + 8 gl .. + 7.  A block's are loaded
+    // when the last one's have been used (EARLY).
+    f32x4 x[PK][2], X[PK][2];
+    auto load_states = [&](f32x4 (&to)[PK][2], const float* from, const Block& b, int n) {
+        const int lane = anew(threadIdx.x) & 63;
+        const float* at = from + (row + b.h) * Np * Pp + ((tile + n) * Pp + b.pb * kPairValues + 8 * (lane >> 4)) * 16 + (lane & 15);
+#pragma unroll
+        for (int kk = 0; kk < PK; ++kk) {
+            to[kk][0] = to[kk][1] = f32x4{0, 0, 0, 0};
+            if (live && n0 + 16 * n < Np && b.pb * kPairValues + 32 * kk < Pp) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) to[kk][i / 4][i % 4] = at[(32 * kk + i) * 16];
+            }
+        }
+    };
+    if (EARLY) load_states(x, a.states, next, 0), load_states(X, a.ahead, next, 0);
+    float sm = 1.0f;
+    // Block k's keys beside block k + 1's pairs and block k + 2's way to LDS, with one barrier (or
+    // two): with one block at a time, three barriers and the states loaded when they are needed,
+    // 272 us instead of 259.
+    for (int k = -1; k < count; ++k) {
         const int tid = anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;  // (addresses are not kept)
-        const int p0 = pb * kPairValues, turn = (h - h0) & 1;
-        const Decays<T>& d = sh.d[turn];
-        Sums& sums = sh.sums[k & 1];
-        if (k) __syncthreads();  // the last block's tiles have been read
-        cv.clear(a.v.lay, P - p0, nt, tid);
-        cy.clear(a.dy.lay, P - p0, nt, tid);
-        cv.template store<false>(sh.v, a.v.lay, tid);
-        cy.template store<false>(sh.dy, a.dy.lay, tid);
-        if constexpr (F16) {
-            uint32_t mv = cv.most(), my = cy.most();
-#pragma unroll
-            for (int i = 1; i < 64; i <<= 1)
-                mv = max(mv, (uint32_t)__shfl_xor((int)mv, i)), my = max(my, (uint32_t)__shfl_xor((int)my, i));
-            if (lane == 0) sh.most[0][wave] = mv, sh.most[1][wave] = my;
-        }
-        __syncthreads();
-        const int h_next = pb + 1 == values ? h + 1 : h, pb_next = pb + 1 == values ? 0 : pb + 1;
-        if (k + 1 < count) load(h_next, pb_next);
-
-        float sm = 1.0f;
-        if constexpr (F16) {
-            uint32_t mv = 0, my = 0;
-#pragma unroll
-            for (int i = 0; i < W; ++i) mv = max(mv, sh.most[0][i]), my = max(my, sh.most[1][i]);
-            sm = to_range<T>(fabsf(a.scale) * d.grow * sh.most_beta[turn] * (float)kPairValues *
-                             to_f(__builtin_bit_cast(f16, (uint16_t)mv)) * to_f(__builtin_bit_cast(f16, (uint16_t)my)));
-        }
-        // the pairs
-        auto pairs = [&](int ti, int si, const f32x4& u, const f32x4& kq, bool on) {
-            f32x4 dm = {0, 0, 0, 0};
-#pragma unroll
-            for (int kk = 0; kk < PK; ++kk)
-                dm = mma<T>(row_frag<T>(sh.v + (16 * si + tl) * VS + 32 * kk + 8 * gl),
-                            row_frag<T>(sh.dy + (16 * ti + tl) * VS + 32 * kk + 8 * gl), dm);
-            const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.beta[turn][16 * si + 4 * gl]);
-            struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
-            float column[4], part = 0.0f, skip = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float um = u[i] * dm[i], wt = um * kq[i];
-                const bool own = on && 4 * gl + i == tl;
-                if (own) sums.diagonal[16 * ti + tl] = wt;
-                column[i] = own ? 0.0f : wt;
-                skip = own ? dm[i] : skip;
-                part = fmaf(column[i], b[i], part);
-                w.v[i] = from_f<T>(um * b[i] * sm);
-            }
-            *reinterpret_cast<Four*>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl) = w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) column[i] = row_sum(column[i]);
-            if (tl == 0)
-                *reinterpret_cast<f32x4*>(&sums.columns[ti][16 * si + 4 * gl]) = f32x4{column[0], column[1], column[2], column[3]};
-            part = across_rows(part);
-            if (gl == 0) sums.rows[si][16 * ti + tl] = part;
-            if (on) {
-                skip = across_rows(row_sum(skip));
-                if (lane == 0) sums.skip[ti] = skip;
-            }
+        const Block far = behind(next);
+        auto take = [&]() {
+            if (k + 2 >= count) return;
+            store(far, k + 2);
+            const Block last = behind(far);
+            if (k + 3 < count) load(last);
         };
-        if (diagonal) {
-            pairs(wave, wave, weights_within<T>(d, wave, lane), qk[0], true);
-        } else {
+        if (RING > 2) take();
+        if (k >= 0 && live) {  // keys by steps: dq and dk
+            const Decays<T>& d = sh.d[place(now.h)];
+            const T *v = sh.v[k % RING], *dy = sh.dy[k % RING], *m = sh.m[k & 1];
+            KeySums& sums = sh.keys[k & 1];
+            const float um = reciprocal_of_power(sm), further = sh.next[place(now.h)];
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                int ti, si;
-                below(first + 4 * j, ti, si);
-                if (first + 4 * j < BELOW) pairs(ti, si, weights_across<T>(d, ti, si, lane), qk[j], false);
-            }
-        }
-        const int h_now = h;
-        if (wave == W - 2 && k) {
-            collect(sh.sums[(k - 1) & 1]);
-            if (pb == 0) finish(h - 1, turn ^ 1);
-        }
-        // the states' fragments: keys n0 + 16 n + tl, values 32 kk + 8 gl .. + 7
-        f32x4 x[NT][PK][2], X[NT][PK][2];
+            for (int n = 0; n < NT; ++n) {
+                const int key = n0 + 16 * n;
+                if (!EARLY) load_states(x, a.states, now, n), load_states(X, a.ahead, now, n);
+                float whole = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                for (int kk = 0; kk < PK; ++kk)
 #pragma unroll
-            for (int kk = 0; kk < PK; ++kk) {
-                x[n][kk][0] = x[n][kk][1] = X[n][kk][0] = X[n][kk][1] = f32x4{0, 0, 0, 0};
-                if (live && n0 + 16 * n < Np && p0 + 32 * kk < Pp) {
-                    const int64_t at = (row + h_now) * Np * Pp + ((n0 + 16 * n + tl) * Pp + p0 + 32 * kk + 8 * gl);
-                    const f32x4* s = reinterpret_cast<const f32x4*>(a.states + at);
-                    const f32x4* e = reinterpret_cast<const f32x4*>(a.ahead + at);
-                    x[n][kk][0] = s[0], x[n][kk][1] = s[1], X[n][kk][0] = e[0], X[n][kk][1] = e[1];
-                }
-            }
-        __syncthreads();
-        if (wave == W - 1 && h_next > h && h_next < h1) {
-            keep_decays(turn ^ 1);
-            if (h_next + 1 < h1) load_decays(h_next + 1);
-        }
-        h = h_next, pb = pb_next;
-        if (!live) continue;
-
-        // keys by steps: dq and dk
-        const float um = reciprocal_of_power(sm), next = sh.next[turn];
+                    for (int i = 0; i < 8; ++i) whole = fmaf(x[kk][i / 4][i % 4], X[kk][i / 4][i % 4], whole);
+                // products of the states with a tile of steps (dy or v), and where they are scaled to
+                auto across = [&](const f32x4 (&state)[PK][2], const T* tile, f32x4 (&to)[TW]) {
+                    const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
+                    float s = 1.0f;
+                    if constexpr (F16) {
+                        float m = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int key = n0 + 16 * n;
-            float whole = 0.0f;
+                        for (int kk = 0; kk < PK; ++kk)
 #pragma unroll
-            for (int kk = 0; kk < PK; ++kk)
+                            for (int i = 0; i < 8; ++i) {
+                                const float u = fabsf(state[kk][i / 4][i % 4]);
+                                m = fmaxf(m, u < INFINITY ? u : 0.0f);
+                            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) whole = fmaf(x[n][kk][i / 4][i % 4], X[n][kk][i / 4][i % 4], whole);
-            // products of the states with a tile of steps (dy or v), and where they are scaled to
-            auto across = [&](const f32x4 (&state)[PK][2], const T* tile, f32x4 (&to)[TW]) {
-                const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
-                float s = 1.0f;
-                if constexpr (F16) {
-                    float m = 0.0f;
+                        for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
+                        s = to_range<T>(m);
+                    }
 #pragma unroll
-                    for (int kk = 0; kk < PK; ++kk)
+                    for (int t = 0; t < TW; ++t) to[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float u = fabsf(state[kk][i / 4][i % 4]);
-                            m = fmaxf(m, u < INFINITY ? u : 0.0f);
-                        }
+                    for (int kk = 0; kk < PK; ++kk) {
+                        float u[8];
 #pragma unroll
-                    for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
-                    s = to_range<T>(m);
-                }
+                        for (int i = 0; i < 8; ++i) u[i] = state[kk][i / 4][i % 4] * s;
+                        Frag<T> part[kParts<T>];
+                        split<T>(u, part);
+                        Frag<T> f[TW];
 #pragma unroll
-                for (int t = 0; t < TW; ++t) to[t] = f32x4{0, 0, 0, 0};
+                        for (int t = 0; t < TW; ++t) f[t] = row_frag<T>(tile + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+                        // (products that wait for each other's sums do not follow each other)
 #pragma unroll
-                for (int kk = 0; kk < PK; ++kk) {
-                    float u[8];
+                        for (int i = 0; i < kParts<T>; ++i)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = state[kk][i / 4][i % 4] * s;
-                    Frag<T> part[kParts<T>];
-                    split<T>(u, part);
+                            for (int t = 0; t < TW; ++t) to[t] = mma<T>(part[i], f[t], to[t]);
+                    }
+                    return reciprocal_of_power(s);
+                };
+                struct __attribute__((aligned(4 * sizeof(T)))) Own { Quad<T> v; };
+                {
+                    const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
+                    f32x4 in[TW];
+                    const float ux = across(x, dy, in);
+                    if (EARLY && k + 1 < count) load_states(x, a.states, next, 0);
+                    Frag<T> kf[SS];
+#pragma unroll
+                    for (int s = 0; s < SS; ++s) kf[s] = column_frag<T>(sh.k + 32 * s * KS + key, KS, lane);
 #pragma unroll
                     for (int t = 0; t < TW; ++t) {
-                        const Frag<T> f = row_frag<T>(tile + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+                        const int tt = TW * group + t, r = 16 * tt + tl;
+                        f32x4 w = {0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < kParts<T>; ++i) to[t] = mma<T>(part[i], f, to[t]);
+                        for (int s = 0; s < SS; ++s)
+                            if (s <= tt / 2) w = mma<T>(kf[s], row_frag<T>(m + r * MS + 32 * s + 8 * gl), w);
+                        const float from = d.from[r] * ux;
+                        const Own q4 = *reinterpret_cast<const Own*>(sh.q + r * KS + key + 4 * gl);
+                        float before = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = in[t][i] * from;
+                            before = fmaf(u, to_f(get_of<T>(q4.v, i)), before);
+                            dq[n][t][i] += fmaf(w[i], um, u);
+                        }
+                        before = across_rows(before);
+                        if (gl == 0) sums.before[tile + n][r] = before;
                     }
                 }
-                return reciprocal_of_power(s);
-            };
-            struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; };
-            {
-                const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
-                f32x4 in[TW];
-                const float ux = across(x[n], sh.dy, in);
-                Frag<T> kf[SS];
+                {
+                    const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
+                    f32x4 out[TW];
+                    const float uX = across(X, v, out);
+                    if (EARLY && k + 1 < count) load_states(X, a.ahead, next, 0);
+                    Frag<T> qf[SS];
 #pragma unroll
-                for (int s = 0; s < SS; ++s) kf[s] = column_frag<T>(sh.k + 32 * s * KS + key, KS, lane);
+                    for (int s = 0; s < SS; ++s) qf[s] = column_frag<T>(sh.q + 32 * s * KS + key, KS, lane);
 #pragma unroll
-                for (int t = 0; t < TW; ++t) {
-                    const int tt = TW * group + t, r = 16 * tt + tl;
-                    f32x4 w = {0, 0, 0, 0};
+                    for (int t = 0; t < TW; ++t) {
+                        const int tt = TW * group + t, r = 16 * tt + tl;
+                        f32x4 w = {0, 0, 0, 0};
 #pragma unroll
-                    for (int s = 0; s < SS; ++s)
-                        if (s <= tt / 2) w = mma<T>(kf[s], row_frag<T>(sh.m + r * MS + 32 * s + 8 * gl), w);
-                    const float from = d.from[r] * ux;
-                    const Four q4 = *reinterpret_cast<const Four*>(sh.q + r * KS + key + 4 * gl);
-                    float before = 0.0f;
+                        for (int s = 0; s < SS; ++s)
+                            if (s >= tt / 2) w = mma<T>(qf[s], column_frag<T>(m + 32 * s * MS + 16 * tt, MS, lane), w);
+                        const float to = d.to[r] * further * uX, b = sh.beta[place(now.h)][r];
+                        const Own k4 = *reinterpret_cast<const Own*>(sh.k + r * KS + key + 4 * gl);
+                        float after = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = in[t][i] * from;
-                        before = fmaf(u, to_f(q4.v[i]), before);
-                        dq[n][t][i] += fmaf(w[i], um, u);
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = out[t][i] * to;
+                            after = fmaf(u, to_f(get_of<T>(k4.v, i)), after);
+                            dk[n][t][i] += fmaf(w[i], um, u * b);
+                        }
+                        after = across_rows(after);
+                        if (gl == 0) sums.behind[tile + n][r] = after;
                     }
-                    before = across_rows(before);
-                    if (gl == 0) sums.before[tile + n][r] = before;
                 }
+                whole = across_rows(row_sum(whole));
+                if (lane == 0) sums.whole[tile + n] = whole;
             }
-            {
-                const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
-                f32x4 out[TW];
-                const float uX = across(X[n], sh.v, out);
-                Frag<T> qf[SS];
-#pragma unroll
-                for (int s = 0; s < SS; ++s) qf[s] = column_frag<T>(sh.q + 32 * s * KS + key, KS, lane);
-#pragma unroll
-                for (int t = 0; t < TW; ++t) {
-                    const int tt = TW * group + t, r = 16 * tt + tl;
-                    f32x4 w = {0, 0, 0, 0};
-#pragma unroll
-                    for (int s = 0; s < SS; ++s)
-                        if (s >= tt / 2) w = mma<T>(qf[s], column_frag<T>(sh.m + 32 * s * MS + 16 * tt, MS, lane), w);
-                    const float to = d.to[r] * next * uX, b = sh.beta[turn][r];
-                    const Four k4 = *reinterpret_cast<const Four*>(sh.k + r * KS + key + 4 * gl);
-                    float behind = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = out[t][i] * to;
-                        behind = fmaf(v, to_f(k4.v[i]), behind);
-                        dk[n][t][i] += fmaf(w[i], um, v * b);
-                    }
-                    behind = across_rows(behind);
-                    if (gl == 0) sums.behind[tile + n][r] = behind;
-                }
-            }
-            whole = across_rows(row_sum(whole));
-            if (lane == 0) sums.whole[tile + n] = whole;
         }
+        if (k + 1 < count) {  // the pairs
+            const Decays<T>& d = sh.d[place(next.h)];
+            const T *v = sh.v[(k + 1) % RING], *dy = sh.dy[(k + 1) % RING];
+            T* m = sh.m[(k + 1) & 1];
+            PairSums& sums = sh.pairs[(k + 1) % 3];
+            if constexpr (F16) {
+                uint32_t mv = 0, my = 0;
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    mv = max(mv, sh.most[(k + 1) & 1][0][i]), my = max(my, sh.most[(k + 1) & 1][1][i]);
+                sm = to_range<T>(fabsf(a.scale) * d.grow * sh.most_beta[place(next.h)] * (float)kPairValues *
+                                 to_f(__builtin_bit_cast(f16, (uint16_t)mv)) * to_f(__builtin_bit_cast(f16, (uint16_t)my)));
+            }
+            auto pairs = [&](int ti, int si, const f32x4& u, const f32x4& kq, bool on) {
+                f32x4 dm = {0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < PK; ++kk)
+                    dm = mma<T>(row_frag<T>(v + (16 * si + tl) * VS + 32 * kk + 8 * gl),
+                                row_frag<T>(dy + (16 * ti + tl) * VS + 32 * kk + 8 * gl), dm);
+                const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.beta[place(next.h)][16 * si + 4 * gl]);
+                f32x4 w;
+                float column[4], part = 0.0f, skip = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float um = u[i] * dm[i], wt = um * kq[i];
+                    const bool own = on && 4 * gl + i == tl;
+                    if (own) sums.diagonal[16 * ti + tl] = wt;
+                    column[i] = own ? 0.0f : wt;
+                    skip = own ? dm[i] : skip;
+                    part = fmaf(column[i], b[i], part);
+                    w[i] = um * b[i] * sm;
+                }
+                put_four<T>(m + (16 * ti + tl) * MS + 16 * si + 4 * gl, w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) column[i] = row_sum(column[i]);
+                if (tl == 0)
+                    *reinterpret_cast<f32x4*>(&sums.columns[ti][16 * si + 4 * gl]) = f32x4{column[0], column[1], column[2], column[3]};
+                part = across_rows(part);
+                if (gl == 0) sums.rows[si][16 * ti + tl] = part;
+                if (on) {
+                    skip = across_rows(row_sum(skip));
+                    if (lane == 0) sums.skip[ti] = skip;
+                }
+            };
+            if (diagonal) {
+                pairs(wave, wave, weights_within<T>(d, wave, lane), qk[0], true);
+            } else {
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) {
+                    int ti, si;
+                    below(first + 3 * j, ti, si);
+                    if (first + 3 * j < BELOW) pairs(ti, si, weights_across<T>(d, ti, si, lane), qk[j], false);
+                }
+            }
+        }
+        if (wave == W - 1) {
+            if (k > 0) {
+                collect(sh.pairs[(k - 1) % 3], sh.keys[(k - 1) & 1]);
+                if (now.pb == 0) finish(now.h - 1, place(now.h - 1));
+            }
+            if (far.h > next.h && far.h < h1) {
+                keep_decays(place(far.h));
+                if (far.h + 1 < h1) load_decays(far.h + 1);
+            }
+        }
+        __syncthreads();
+        if (RING == 2) {
+            take();
+            __syncthreads();
+        }
+        now = next, next = far;
     }
-    __syncthreads();
-    if (wave == W - 2) {
-        collect(sh.sums[(count - 1) & 1]);
-        finish(h1 - 1, (h1 - 1 - h0) & 1);
+    if (wave == W - 1) {
+        collect(sh.pairs[(count - 1) % 3], sh.keys[(count - 1) & 1]);
+        finish(h1 - 1, place(h1 - 1));
     }
     if (!live) return;
     const int lane = anew(threadIdx.x) & 63, tl = lane & 15, gl = lane >> 4;

@@ -197,13 +197,10 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         const int tid = anew(threadIdx.x), lane = tid & 63, tl = lane & 15, gl = lane >> 4;  // (addresses are not kept)
         const Decays<T>& d = sh.d[k & 1];
         if (saved && p0 + 16 * pq < Pp) {
-            float* at = saved + (int64_t)c * a.H * Np * Pp + (16 * NT * half + 4 * gl) * Pp + p0 + 16 * pq + tl;
+            float* at = saved + (int64_t)c * a.H * Np * Pp + (NT * half * Pp + p0 + 16 * pq + tl) * 16 + 4 * gl;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                if (16 * (NT * half + n) < Np) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) at[(16 * n + i) * Pp] = x[n][i];
-                }
+                if (16 * (NT * half + n) < Np) *reinterpret_cast<f32x4*>(at + 16 * n * Pp) = x[n];
         }
         __syncthreads();  // the last chunk's tiles have been read
         ck.clear(a.key.lay, N, nt, tid);
@@ -218,12 +215,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
             if (live) {
                 T* to = sh.x + (16 * pq + tl) * KS + 16 * NT * half + 4 * gl;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(x[n][i] * sx);
-                    *reinterpret_cast<Four*>(to + 16 * n) = w;
-                }
+                for (int n = 0; n < NT; ++n) put_four<T>(to + 16 * n, x[n] * sx);
             }
         }
         {
@@ -306,10 +298,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                     return m;
                 };
                 auto keep = [&](int ti, int si, const f32x4& m) {
-                    struct __attribute__((aligned(4 * sizeof(T)))) Four { T v[4]; } w;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(m[i] * sm);
-                    *reinterpret_cast<Four*>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl) = w;
+                    put_four<T>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl, m * sm);
                 };
                 if (wave < TT) {
                     f32x4 m = pairs(wave, wave) * weights_within<T>(d, wave, lane);
@@ -350,19 +339,20 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                         within = mma<T>(vf[0], row_frag<T>(mp), within);
                         if (SS > 1 && t) within = mma<T>(vf[SS - 1], row_frag<T>(mp + 32), within);
                         const float f = d.from[r] * ux;
-                        struct __attribute__((packed, aligned(sizeof(T)))) Four { T v[4]; } y;
+                        f32x4 sum;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) y.v[i] = from_f<T>(fmaf(across[t][i], f, within[i] * um));
+                        for (int i = 0; i < 4; ++i) sum[i] = fmaf(across[t][i], f, within[i] * um);
+                        const Quad<T> y = four_of<T>(sum);
                         const int there = P - (p0 + 16 * pq + 4 * gl);
                         if (vectors) {
                             if (o < nt && there > 0)
-                                *reinterpret_cast<Four*>((char*)result + (uint32_t)o * ((uint32_t)a.result.sl * (uint32_t)sizeof(T)) +
+                                *reinterpret_cast<Quad<T>*>((char*)result + (uint32_t)o * ((uint32_t)a.result.sl * (uint32_t)sizeof(T)) +
                                                          4u * gl * (uint32_t)sizeof(T)) = y;
                         } else {
                             T* to = result + o * a.result.sl + 4 * gl * a.result.sn;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                if (o < nt && i < there) to[i * a.result.sn] = y.v[i];
+                                if (o < nt && i < there) to[i * a.result.sn] = get_of<T>(y, i);
                         }
                     }
                 }
@@ -377,18 +367,24 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                     for (int j = 0; j < 8; ++j) w[j] = frag_get<T>(vf[s], j) * (to[j / 4][j % 4] * sv);
                     split<T>(w, part[s]);
                 }
+                // (the tiles in turn: products that wait for each other's sums do not follow each other)
+                f32x4 add[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 add = {0, 0, 0, 0};
+                for (int n = 0; n < NT; ++n) add[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int s = 0; s < SS; ++s) {
-                        const Frag<T> kf = column_frag<T>(sh.k + 32 * s * KS + 16 * (NT * half + n), KS, lane);
+                for (int s = 0; s < SS; ++s) {
+                    Frag<T> kf[NT];
 #pragma unroll
-                        for (int i = 0; i < kParts<T>; ++i) add = mma<T>(kf, part[s][i], add);
-                    }
+                    for (int n = 0; n < NT; ++n) kf[n] = column_frag<T>(sh.k + 32 * s * KS + 16 * (NT * half + n), KS, lane);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[n][i] = fmaf(x[n][i], whole, add[i] * uv);
+                    for (int i = 0; i < kParts<T>; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) add[n] = mma<T>(kf[n], part[s][i], add[n]);
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[n][i] = fmaf(x[n][i], whole, add[n][i] * uv);
             }
         }
         if (F16 && OUT) most_state();
