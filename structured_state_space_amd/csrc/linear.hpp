@@ -226,7 +226,7 @@ struct Carrier {
     static __device__ __forceinline__ bool idle(int tid) { return kVectors < TH && tid >= kVectors; }
 
     static __device__ __forceinline__ void place(Lay lay, int tid, int k, int& step, int& col) {
-        const int e = tid + TH * k;
+        const uint32_t e = (uint32_t)tid + TH * k;
         if (lay == kByStep) {
             step = e % (Q / V) * V;
             col = e / (Q / V);
@@ -316,7 +316,7 @@ struct Carrier {
                     else *reinterpret_cast<uint16_t*>(at) = (uint16_t)(r[k][i / 2] >> (16 * (i & 1)));
                 }
             } else {
-                *reinterpret_cast<u32x4*>(to + (REVERSE ? Q - 1 - step : step) * kStride + col) = r[k];
+                *reinterpret_cast<u32x4*>(to + __umul24(REVERSE ? Q - 1 - step : step, kStride) + col) = r[k];
             }
         }
     }

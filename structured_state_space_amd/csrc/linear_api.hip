@@ -34,12 +34,16 @@ int64_t value_blocks(int64_t P) { return (P + 63) / 64; }
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Steps of a segment, whole chunks.  A walk has a workgroup per sequence, head and 64
-// values; where those leave more than half of the compute units idle, sequences are cut, for one more
-// launch over nearly all of the steps, which finds every segment's end state.
+// values; where those leave many of the compute units idle, sequences are cut, for one more
+// launch over nearly all of the steps, which finds every segment's end state.  Forwards,
+// 128 keys, 64 values, bf16, cut and not cut: 32 workgroups of 4096 steps 68 and 223 us, 96 147
+// and 225, 128 of 8192 290 and 439, 200 of 4096 257 and 226; 160 in float32 626 and 650.
+// Cut into about 512 workgroups: 32 heads of 16384 steps 191 us, into 256 218, 1024 222; of four
+// chunks or more, since every segment starts with its state and the first loads' latency.
 int64_t segment_steps(const Seqs& q, const Sizes& z) {
     const int64_t Q = chunk_of(z.dtype), wgs = (q.offsets ? 1 : q.S) * z.H * value_blocks(z.P);
     int64_t steps = q.L;
-    if (wgs < 128) {
+    if (wgs <= 160) {
         const int64_t cuts = (512 + wgs - 1) / wgs;
         steps = (q.L + cuts - 1) / cuts;
         if (steps < 4 * Q) steps = 4 * Q;
@@ -57,10 +61,15 @@ size_t saved_bytes(const Seqs& q, const Sizes& z) {
     return (size_t)(linear_rows(q.S, q.L, q.offsets != nullptr, chunk_of(z.dtype)) * z.H) * padded_keys(z.N) *
            padded_values(z.P) * sizeof(float);
 }
-// workgroups that share a group's heads in the pairs' kernel, and their heads
+// Workgroups that share a group's heads in the pairs' kernel, and their heads: as many as the
+// compute units take at once.  More add partial sums and fewer heads to each pipeline: forwards
+// and backwards at 4 x 2048 steps, 64 heads, one group, bf16, 522 us with twice and 550 with four times as
+// many, 509 so; 80 heads in eight groups over 1024 steps 177, 189 and 156.  Small tiles of float32
+// have two workgroups to a unit: 2 x 2048 steps, 32 heads, 258 us, with half 271, with twice 262.
 int64_t head_blocks(const Seqs& q, const Sizes& z, int* heads) {
     const int64_t items = item_count(q, chunk_of(z.dtype)), Hg = z.H / z.G;
-    int64_t blocks = (512 + items * z.G - 1) / (items * z.G);
+    const int64_t all = z.dtype == SSM_F32 && z.N <= 64 ? 512 : 256;
+    int64_t blocks = (all + items * z.G - 1) / (items * z.G);
     if (blocks > Hg) blocks = Hg;
     if (blocks > 8) blocks = 8;
     const int64_t each = (Hg + blocks - 1) / blocks;
