@@ -615,10 +615,11 @@ int ssm_linear_attention_step(const ssm_linear_token* p, void* stream);
  *   a = u  or (SSM_GATE_BEFORE)  u silu(z)
  *   n = (a - mean a) / sqrt(var a + eps)  or (rms)  a / sqrt(mean a^2 + eps)
  *   y = n weight + bias,  or (SSM_GATE_AFTER)  (n weight + bias) silu(z)
- * u, z, y and their gradients are activations, views [Bsz,H,L] as above; a group
- * has H/G channels.  Means, variances and sums are float32 (the parameters' gradients
- * float64 over the workgroups), the mean is taken before the squares.  A call with L = 1
- * is the form for single tokens.  An infinite or NaN input reaches its own step and group.
+ * u, z, y and their gradients are activations, views [Bsz,H,L] as above, with the same
+ * conventions (outputs must not overlap inputs or each other); a group has H/G channels.
+ * Means, variances and sums are float32 (the parameters' gradients float64 over the
+ * workgroups), the mean is taken before the squares.  A call with L = 1 is the form for
+ * single tokens.  An infinite or NaN input reaches its own step and group.
  * ---------------------------------------------------------------------- */
 #define SSM_GATE_NONE 0
 #define SSM_GATE_BEFORE 1

@@ -53,7 +53,8 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     Item it;
     if (!find_item(a.q, item, (int)a.segment, it) || it.state < 0) return;
     const int len = it.end - it.beg, segments = chunks_of(len, (int)a.segment);
-    if (it.c >= segments) return;
+    // (descending offsets make more segments than there are items: a sequence without all of its own is left out)
+    if (it.c >= segments || item - it.c + segments > a.items) return;
     if (ENDS && segments == 1) return;
     const int pos = REVERSE ? segments - 1 - it.c : it.c;  // in the order of the walk
     const int chunks = (len + Q - 1) / Q, per = (int)(a.segment / Q);

@@ -1111,7 +1111,7 @@ def layer_norm(u, weight=None, bias=None, z=None, gate="after", rms=False, group
     (or [Bsz,H], one token each), y = n weight + bias with n = (u - mean) /
     sqrt(var + eps), or with rms u / sqrt(mean u^2 + eps); weight, bias float32 [H].
     z (like u) gates with silu(z): the result (gate "after") or u itself
-    ("before").  Not seen by autograd.  Returns dict(y)."""
+    ("before").  y must not overlap u or z.  Not seen by autograd.  Returns dict(y)."""
     dev, steps, args = _norm(u, weight, bias, z, gate, rms, groups, eps)
     with _on(dev):
         if y is None:

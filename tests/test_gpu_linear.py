@@ -121,6 +121,30 @@ def test_segments(name, lengths):
     check(K.inputs(8, name, 1, 1, 1, 32, 32, 700, S=3, pace=0.03), name, "tokens", offsets=[5, 400, 400, 690])
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+def test_descending_offsets_stay_within_the_workspace(name):
+    """They make more pieces than the workspace has places: what they name is unspecified, the rest is not.
+    Two sequences of 700 steps and an empty one are cut into seven pieces (float32: thirteen), places
+    are for those of 700 steps and one more for each sequence."""
+    ssm = _ssm()
+    a = K.inputs(21, name, 1, 1, 1, 32, 32, 700, S=3, pace=0.03)
+    args, kw = K.call_args(a, name, "tokens")
+    tidy = torch.tensor([0, 700, 700, 700], dtype=torch.int32, device=DEV)
+    wrong = torch.tensor([0, 700, 0, 700], dtype=torch.int32, device=DEV)
+    want = ssm.linear_attention(*args, **kw, offsets=tidy, want_state=True)["x"]
+    need = ssm.linear_bytes(ssm.OP_LINEAR_ATTENTION, K.torch_type(name), 1, 1, 32, 32, 1, 700, S=3, packed=True)
+    assert need > 0
+    ws = torch.full((need + (1 << 16),), 77, dtype=torch.uint8, device=DEV)
+    out = ssm.linear_attention(*args, **kw, offsets=wrong, want_state=True, save=True, workspace=ws)
+    assert bool((ws[need:] == 77).all())
+    assert torch.equal(out["x"][0], want[0])
+    dy = K.on_device(a["dy"], name, "tokens")
+    need = ssm.linear_bytes(ssm.OP_LINEAR_ATTENTION_BACKWARD, K.torch_type(name), 1, 1, 32, 32, 1, 700, S=3, packed=True)
+    ws = torch.full((need + (1 << 16),), 77, dtype=torch.uint8, device=DEV)
+    ssm.linear_attention_backward(*args, dy, dx=_f32(a["dx"]), saved=out["saved"], offsets=wrong, workspace=ws, **kw)
+    assert bool((ws[need:] == 77).all())
+
+
 def test_backward_computes_the_states_again():
     ssm = _ssm()
     a = K.inputs(9, "bf16", 2, 4, 2, 64, 64, 200)
