@@ -159,9 +159,10 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_rows_kernel(const No
 //   da = (dn - mean dn - n mean(dn n)) / sqrt(variance + eps)
 // (without mean dn where the mean was not taken), dweight = sum dy' n, dbias = sum dy'.
 // The norm is computed again: its numbers are in registers, and the call takes nothing from
-// the forward pass.  Workgroups go over steps `rows` apart with the same channels in the same
-// lanes, so that the parameters' sums stay in registers until the end; each then has a row
-// of partial sums.
+// the forward pass.  Workgroups go over their steps with the same channels in the same lanes, so
+// that the parameters' sums stay in registers until the end; each then joins those of its lanes
+// and has a row of partial sums.  (A row for each step that a workgroup has at once, 32 of 64
+// channels: 16 x 2048 steps took 507 us, most of it the rows' sums.)
 template <class T, int LANES, int V>
 __global__ __launch_bounds__(norm_threads(LANES)) void norm_rows_grad_kernel(const NormGradArgs g) {
     const NormArgs& a = g.f;
@@ -170,18 +171,33 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_rows_grad_kernel(con
     int turn = 0;
     const int tid = threadIdx.x, D = (int)(a.H / a.G);
     const int grp = (int)(blockIdx.x % a.G);
-    const int64_t mine = (int64_t)(blockIdx.x / a.G) * R + tid / LANES;
+    const int64_t mine = (int64_t)(blockIdx.x / a.G) * R + tid / LANES, apart = g.rows * R;
     const int first = tid % LANES * 8;
     const int64_t steps = a.Bsz * a.L;
-    float dw[V][8], db[V][8], w[V][8], s[V][8];
+    // Four vectors of everything do not fit the registers: nothing is loaded ahead, and the sums are
+    // in LDS, a place for each thread.  (1024 threads with two vectors each had 360 bytes of a
+    // thread in memory: 2 x 2048 steps of 16384 channels, bf16, 580 us instead of 237.)
+    constexpr bool TIGHT = V == 4;
+    __shared__ float kept[TIGHT ? 2 * V * 8 : 1][TIGHT ? LANES : 1];
+    float dw[TIGHT ? 1 : V][8], db[TIGHT ? 1 : V][8], w[V][8], s[V][8];
+    auto parameters = [&]() {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = first + v * LANES * 8, there = D - c;
+        for (int v = 0; v < V; ++v) {
+            const int c = first + v * LANES * 8, there = D - c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[v][i] = db[v][i] = 0.0f, w[v][i] = 1.0f, s[v][i] = 0.0f;
-        if (a.weight) load8<float>(w[v], a.weight, grp * D + c, there);
-        if (a.bias && a.gate == SSM_GATE_AFTER) load8<float>(s[v], a.bias, grp * D + c, there);
-    }
+            for (int i = 0; i < 8; ++i) w[v][i] = 1.0f, s[v][i] = 0.0f;
+            if (a.weight) load8<float>(w[v], a.weight, grp * D + c, there);
+            if (a.bias && a.gate == SSM_GATE_AFTER) load8<float>(s[v], a.bias, grp * D + c, there);
+        }
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (TIGHT) kept[v * 8 + i][tid] = kept[(V + v) * 8 + i][tid] = 0.0f;
+            else dw[v][i] = db[v][i] = 0.0f;
+        }
+    if (!TIGHT) parameters();
     Raw8<T> un[V], zn[V], dn[V];
     auto load = [&](int64_t r) {
         const int64_t l = r % a.L, b = r / a.L;
@@ -195,17 +211,18 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_rows_grad_kernel(con
             dn[v].load(g.dy.data, y0 + c, there);
         }
     };
-    if (mine < steps) load(mine);
-    for (int64_t r = mine; r < steps; r += g.rows) {
+    if (!TIGHT && mine < steps) load(mine);
+    for (int64_t r = mine; r < steps; r += apart) {
         const int64_t l = r % a.L, b = r / a.L;
         float u[V][8], z[V][8], d[V][8], n[V][8];
+        if (TIGHT) load(r);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             un[v].get(u[v]);
             if (a.gate) zn[v].get(z[v]);
             dn[v].get(d[v]);
         }
-        if (r + g.rows < steps) load(r + g.rows);
+        if (!TIGHT && r + apart < steps) load(r + apart);
         float sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -225,6 +242,7 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_rows_grad_kernel(con
                 squares = fmaf(n[v][i], n[v][i], squares);
             }
         const float scale = inverse_root(group_sum<LANES>(squares, parts, turn) / (float)D + a.eps);
+        if (TIGHT) parameters();
         float m0 = 0.0f, m1 = 0.0f;
         const int64_t dz0 = b * g.dz.sb + l * g.dz.sl + grp * D;
 #pragma unroll
@@ -238,8 +256,13 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_rows_grad_kernel(con
                     dz[i] = d[v][i] * fmaf(n[v][i], w[v][i], s[v][i]) * silu_slope<T>(z[v][i]);
                     d[v][i] = i < there ? d[v][i] * silu_f<kFine<T>>(z[v][i]) : 0.0f;
                 }
-                dw[v][i] = fmaf(d[v][i], n[v][i], dw[v][i]);
-                db[v][i] += d[v][i];
+                if constexpr (TIGHT) {
+                    kept[v * 8 + i][tid] += d[v][i] * n[v][i];
+                    kept[(V + v) * 8 + i][tid] += d[v][i];
+                } else {
+                    dw[v][i] = fmaf(d[v][i], n[v][i], dw[v][i]);
+                    db[v][i] += d[v][i];
+                }
                 d[v][i] *= w[v][i];
                 m0 += d[v][i];
                 m1 = fmaf(d[v][i], n[v][i], m1);
@@ -266,14 +289,46 @@ __global__ __launch_bounds__(norm_threads(LANES)) void norm_rows_grad_kernel(con
             if (a.gate == SSM_GATE_BEFORE) store8<T>(dz, g.dz.data, dz0 + c, there);
         }
     }
-    if (g.parts) {
+    if (!g.parts) return;
+    if constexpr (R > 1) {  // the lanes of the same channels, in a wave and in the others
+        constexpr int W = norm_threads(LANES) / 64;
+        __shared__ float all[W][LANES * V * 8];
+        auto join = [&](auto& x) {
+            float* at = all[tid >> 6];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = first + v * LANES * 8, there = D - c;
-            if (there <= 0) continue;
-            store8<float>(dw[v], g.parts, mine * a.H + grp * D + c, there);
-            store8<float>(db[v], g.parts, (g.rows + mine) * a.H + grp * D + c, there);
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (LANES < 16) x[v][i] += dpp<0x140>(dpp<0x141>(x[v][i]));  // eight lanes on
+                    if constexpr (LANES < 32) x[v][i] += __shfl_xor(x[v][i], 16);
+                    if constexpr (LANES < 64) x[v][i] += __shfl_xor(x[v][i], 32);
+                    if ((tid & 63) < LANES) at[(v * 8 + i) * LANES + (tid & 63)] = x[v][i];
+                }
+            __syncthreads();
+            if (tid < LANES) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int k = 1; k < W; ++k) x[v][i] += all[k][(v * 8 + i) * LANES + tid];
+            }
+            __syncthreads();
+        };
+        join(dw), join(db);
+        if (tid >= LANES) return;
+    }
+    const int64_t row = blockIdx.x / a.G;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = first + v * LANES * 8, there = D - c;
+        if (there <= 0) continue;
+        if constexpr (TIGHT) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dw[0][i] = kept[v * 8 + i][tid], db[0][i] = kept[(V + v) * 8 + i][tid];
         }
+        store8<float>(dw[TIGHT ? 0 : v], g.parts, row * a.H + grp * D + c, there);
+        store8<float>(db[TIGHT ? 0 : v], g.parts, (g.rows + row) * a.H + grp * D + c, there);
     }
 }
 
@@ -646,14 +701,15 @@ static bool by_channel(const View3* const* v, int n) {
 }
 // threads of a step's group
 static int norm_lanes(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
-static int norm_grad_lanes(int64_t D) { return D > 4096 && D <= 8192 ? 512 : norm_lanes(D); }
+static int norm_grad_lanes(int64_t D) { return D > 4096 ? 512 : norm_lanes(D); }
 static int64_t step_blocks(int64_t L) { return (L + kSteps - 1) / kSteps; }
-// rows of partial sums: the workgroups that go over the steps, times the steps of each
+// Rows of partial sums: the workgroups that go over a group's steps, two to a compute unit (one of
+// 512 or 1024 threads).  Gated, bf16: 8192 steps of 4096 channels 93 us, with half as many 130;
+// 32768 of 512 55 us and of 64 24 us, with twice as many 63 and 31.
 static int64_t norm_rows(int64_t steps, int64_t D, int64_t G) {
     const int64_t R = norm_threads(norm_grad_lanes(D)) / norm_grad_lanes(D);
-    int64_t wgs = ((D > 4096 ? 256 : D > 2048 ? 512 : 1024) + G - 1) / G;
-    if (wgs * R > steps) wgs = (steps + R - 1) / R;
-    return wgs * R;
+    const int64_t wgs = ((D > 4096 ? 256 : 512) + G - 1) / G, all = (steps + R - 1) / R;
+    return wgs < all ? wgs : all;
 }
 // of the other order's
 static int64_t norm_step_rows(int64_t Bsz, int64_t L, int64_t G) {
@@ -727,9 +783,7 @@ hipError_t launch_norm(int dtype, const NormArgs& a, hipStream_t s) {
 
 template <class T, int LANES, int V>
 static void launch_rows_grad(const NormGradArgs& g, hipStream_t s) {
-    constexpr int R = norm_threads(LANES) / LANES;
-    hipLaunchKernelGGL((norm_rows_grad_kernel<T, LANES, V>), dim3((unsigned)(g.rows / R * g.f.G)), dim3(norm_threads(LANES)),
-                       0, s, g);
+    hipLaunchKernelGGL((norm_rows_grad_kernel<T, LANES, V>), dim3((unsigned)(g.rows * g.f.G)), dim3(norm_threads(LANES)), 0, s, g);
 }
 template <class T>
 static void launch_norm_grad_t(NormGradArgs& g, hipStream_t s) {
@@ -752,7 +806,7 @@ static void launch_norm_grad_t(NormGradArgs& g, hipStream_t s) {
     else if (D <= 2048) launch_rows_grad<T, 256, 1>(g, s);
     else if (D <= 4096) launch_rows_grad<T, 256, 2>(g, s);
     else if (D <= 8192) launch_rows_grad<T, 512, 2>(g, s);
-    else launch_rows_grad<T, 1024, 2>(g, s);
+    else launch_rows_grad<T, 512, 4>(g, s);
 }
 hipError_t launch_norm_backward(int dtype, NormGradArgs& g, hipStream_t s) {
     if (dtype == SSM_F32) launch_norm_grad_t<float>(g, s);
