@@ -24,7 +24,8 @@ __device__ __forceinline__ float silu_slope(float z) {
 // ---- channels contiguous ----
 // LANES threads have the channels of a group at one step, eight neighbours to a vector, V
 // vectors each: the step's numbers are read once, stay in registers between the sums (the
-// mean first, then the squares about it) and are written once.  Bound by memory.
+// mean first, then the squares about it) and are written once.  Bound by memory: gated, bf16,
+// 16384 steps of 2048 channels 38 us, 5.3 TB/s with part of the traffic in the last-level cache.
 // `turn` counts the sums of a workgroup: two places in turn need one barrier each.
 template <int LANES>
 using Parts = float[2][LANES > 64 ? LANES / 64 : 1];
@@ -519,7 +520,7 @@ template <class T, int R, bool KEEP, bool GATED, bool VEC>
 __global__ __launch_bounds__(kStepThreads) void norm_steps_kernel(const NormArgs a, int64_t blocks) {
     __shared__ __attribute__((aligned(16))) StepParts parts;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = threadIdx.x >> 4;
-    // neighbouring blocks of steps share cache lines: on one die
+    // neighbouring blocks of steps share cache lines: on one die (46 us instead of 50 at 16 x 512 x 3000)
     const int64_t bid = by_die(blockIdx.x, gridDim.x);
     const int D = (int)(a.H / a.G), grp = (int)(bid / blocks % a.G);
     const int64_t block = bid % blocks * kSteps, b = bid / blocks / a.G, first = (int64_t)grp * D;
@@ -699,7 +700,8 @@ static bool by_channel(const View3* const* v, int n) {
         if (v[i]->data && v[i]->sh != 1) return false;
     return true;
 }
-// threads of a step's group
+// Threads of a step's group, with one or two vectors each: 2048 channels, gated, bf16, 8192 steps, 25 us;
+// four vectors each, in a quarter of the threads, 34.
 static int norm_lanes(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
 static int norm_grad_lanes(int64_t D) { return D > 4096 ? 512 : norm_lanes(D); }
 static int64_t step_blocks(int64_t L) { return (L + kSteps - 1) / kSteps; }
@@ -711,7 +713,7 @@ static int64_t norm_rows(int64_t steps, int64_t D, int64_t G) {
     const int64_t wgs = ((D > 4096 ? 256 : 512) + G - 1) / G, all = (steps + R - 1) / R;
     return wgs < all ? wgs : all;
 }
-// of the other order's
+// Of the other order's, one to a compute unit: 16 x 512 x 3000, float32, 113 us, half as many 156, twice 132.
 static int64_t norm_step_rows(int64_t Bsz, int64_t L, int64_t G) {
     const int64_t all = Bsz * step_blocks(L), most = (256 + G - 1) / G;
     return all < most ? all : most;
@@ -732,7 +734,10 @@ static void launch_rows(const NormArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((norm_rows_kernel<T, LANES, V>), dim3((unsigned)((rows + R - 1) / R)), dim3(norm_threads(LANES)), 0, s,
                        a);
 }
-// channels of a lane: few where the group has few, more in registers while they fit
+// Channels of a lane: few where the group has few, more in registers while they fit.  float32, 16 x 3000
+// steps: 128 channels 28 us and 512 46 us, read twice instead 30 and 53.  Gradients keep 128 channels
+// alone: with 512, or the norm's input of them, registers went to memory (16 x 512 x 3000, dy read twice
+// 111 us instead of 113, but 256 channels 72 instead of 64).
 template <class T, bool GATED, bool VEC>
 static void launch_steps(const NormArgs& a, int64_t blocks, hipStream_t s) {
     const int64_t D = a.H / a.G;

@@ -573,8 +573,7 @@ struct LinearStepArgs {
 // The states kept for the backward pass, one before every chunk: row (first of the
 // sequence + chunk) of [rows, H, padded N / 16, padded P, 16], zero where there is none.
 // (Sixteen keys of a value lie together: the walk's lane has four of them, and stores a vector.
-// The walk is bound by its vector instructions, and a vector instead of four numbers saves a
-// sixteenth of them.)
+// A vector instead of four numbers saves it a sixteenth of its vector instructions.)
 __host__ __device__ inline int64_t padded_keys(int64_t N) { return (N + 15) / 16 * 16; }
 __host__ __device__ inline int64_t padded_values(int64_t P) { return (P + 31) / 32 * 32; }
 __host__ __device__ inline int64_t linear_rows(int64_t S, int64_t L, bool packed, int Q) {

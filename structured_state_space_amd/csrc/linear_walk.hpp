@@ -18,14 +18,16 @@ constexpr int kWalkValues = 64;  // values of a workgroup
 // stays in float32 in registers, as the matrix instruction leaves it: a wave has 16 values and
 // half of the keys, and of the results those values and half of the steps.  Rounded, the state
 // goes through LDS once a chunk, and so does M, a tile of 16 x 16 pairs from a wave.
-// (Four waves with all keys and steps of their values needed no exchange of the state, but
-// one wave to a SIMD waited half of the time: 265 us at 256 heads of 2048 steps, 128 keys
-// and 64 values, bf16.)
+// 256 heads of 2048 steps, 128 keys and 64 values, bf16, with the states saved: 153 us, two waves to
+// a SIMD that issue vector instructions in a third of the cycles (450 a wave and chunk, a fifth of
+// them for the split) and wait for each other, three barriers to a chunk.  (Four waves with all
+// keys and steps of their values needed no exchange of the state, but waited more: 265 us.  Two
+// sets of tiles and two barriers were no faster: forwards 240 heads of 8192 steps 523 us, not 447.)
 // Rounding to the activations' type: M and the state as operands for the results, which
 // are rounded to it anyway.  What is added to the state is split (kParts).
 // ENDS: the first of two passes, which finds each segment's end state for the second.
-// OUT: results wanted.  FAST: the tensors' usual layout (WalkArgs), without the code for others
-// between what runs: 8 kB of instructions instead of 50.
+// OUT: results wanted.  FAST: the tensors' usual layout (WalkArgs), in a kernel without the code for
+// others: 5200 instructions instead of 7900, and addresses that do not fill the registers.
 template <class T, int NP, bool OUT, bool REVERSE, bool ENDS, bool FAST>
 __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void linear_walk_kernel(const WalkArgs a) {
     constexpr int Q = kChunk<T>, TT = Q / 16, HT = TT / 2, KK = NP / 32, SS = Q / 32, NT = NP / 32;  // NT: of a wave
