@@ -88,6 +88,15 @@ def test_orders(name, order, size):
 
 
 @pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("order", ["tokens", "rows"])
+@pytest.mark.parametrize("size", [(1, 44, 1, 24, 16, 70), (1, 80, 2, 64, 64, 40), (1, 41, 1, 128, 70, 66), (1, 36, 1, 250, 130, 65)])
+def test_many_heads_of_a_group(name, order, size):
+    """A workgroup has several heads one after the other for the gradients of q and k, with one to three blocks of
+    values each, and not as many in the last."""
+    check(K.inputs(22, name, *size), name, order)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("beta,skip,carry", [(False, False, False), (True, False, True), (False, True, False)])
 def test_without_what_is_optional(name, beta, skip, carry):
     check(K.inputs(3, name, 2, 4, 2, 48, 40, 100, beta=beta, skip=skip, carry=carry), name, "tokens")

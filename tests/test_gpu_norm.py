@@ -137,6 +137,14 @@ def test_many_steps(order, H, groups):
     check(inputs(3, "f32", 3, H, 700 if H < 200 else 500, "", shift=0.0), "f32", order, groups, False)
 
 
+@pytest.mark.parametrize("name,H,groups,L", [("f32", 24, 1, 17000), ("bf16", 100, 1, 9000), ("f16", 200, 1, 4500),
+                                              ("f32", 384, 1, 2200), ("bf16", 700, 1, 2200), ("f32", 96, 4, 5000),
+                                              ("bf16", 9000, 1, 520), ("f32", 9000, 1, 260)])
+def test_more_steps_than_workgroups_have_at_once(name, H, groups, L):
+    """... also where a workgroup has several steps at a time and joins their sums at the end."""
+    check(inputs(5, name, 1, H, L, "before", shift=0.0), name, "tokens", groups, True, "before")
+
+
 def test_far_from_zero():
     """The mean is taken before the squares: 2^12 standard deviations away the variance is still there (each input is
     rounded to 2^-24 of the shift, and the bounds say what that leaves)."""
