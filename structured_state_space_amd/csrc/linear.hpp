@@ -320,7 +320,7 @@ struct Carrier {
             }
         }
     }
-    // the largest magnitude as bits: at or above kInf<T> where one is infinite or NaN
+    // the largest magnitude as bits (an infinity's or NaN's are above every number's)
     __device__ __forceinline__ uint32_t most() const {
         if constexpr (sizeof(T) == 2) {
             u16x2 w = {0, 0};
@@ -339,8 +339,11 @@ struct Carrier {
         }
     }
 };
+// Bits of the magnitude from which on a chunk goes row by row: 2^22, infinity in float16.  Below,
+// with put_decays' bounds, no product of a chunk's inputs passes float32: a weight of a pair stays
+// below N 2^44 2^60 2^14 <= 2^126 and what a chunk adds to the state below 64 2^44 2^60.
 template <class T>
-constexpr uint32_t kInf = sizeof(T) == 4 ? 0x7f800000u : std::is_same<T, f16>::value ? 0x7c00u : 0x7f80u;
+constexpr uint32_t kHuge = sizeof(T) == 4 ? 0x4a800000u : std::is_same<T, f16>::value ? 0x7c00u : 0x4a80u;
 
 // A power of two 2^e that brings magnitudes up to `most` (float32) below 2^15, where
 // float16 has them and 2^-39 of them; 1 for other types.  Bounded, so that it and its
@@ -355,6 +358,61 @@ __device__ __forceinline__ float to_range(float most) {
 __device__ __forceinline__ float reciprocal_of_power(float p) {
     return __uint_as_float((254u << 23) - __float_as_uint(p));
 }
+
+// Some of the products are infinite, NaN or beyond 2^64 (whose squares pass float32).
+template <int K>
+__device__ __forceinline__ bool far_out(const f32x4 (&x)[K]) {
+    float all = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) all = fmaf(x[k][i], x[k][i], all);
+    return !(all < INFINITY);
+}
+
+// The products of two tiles' rows where those pass float32 (lane: row l & 15 of either at its part of
+// the summed axis).  Rows with a number of 2^30 or more are taken 2^-98 times: bits 0 to 15 of `rows`
+// name those of `a`, bits 16 to 31 those of `b`.
+constexpr float kFar = 0x1p98f;
+template <class T, int KK>
+__device__ __forceinline__ f32x4 products_in_range(const T* a, const T* b, uint32_t& rows) {
+    auto most = [](const T* p) {
+        float m = 0.0f;
+        for (int kk = 0; kk < KK; ++kk) {
+            const Frag<T> f = row_frag<T>(p + 32 * kk);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(frag_get<T>(f, j)));
+        }
+        m = fmaxf(m, __shfl_xor(m, 16));
+        return fmaxf(m, __shfl_xor(m, 32));
+    };
+    auto taken = [](const T* p, float factor) {
+        const Frag<T> f = row_frag<T>(p);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = frag_get<T>(f, j) * factor;
+        return frag_of<T>(x);
+    };
+    const bool far_a = most(a) >= 0x1p30f, far_b = most(b) >= 0x1p30f;
+    const float fa = far_a ? 1.0f / kFar : 1.0f, fb = far_b ? 1.0f / kFar : 1.0f;
+    rows = (uint32_t)(__ballot(far_a) & 0xffff) | (uint32_t)(__ballot(far_b) & 0xffff) << 16;
+    f32x4 c = {0, 0, 0, 0};
+    for (int kk = 0; kk < KK; ++kk) c = mma<T>(taken(a + 32 * kk, fa), taken(b + 32 * kk, fb), c);
+    return c;
+}
+// Such a product's x y of row i of `a` and row j of `b`, brought back in the smaller of the factors:
+// nothing passes float32, at either end, that the whole product does not.
+__device__ __forceinline__ void bring_back(float& x, float& y, uint32_t rows, int i, int j) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float f = rows >> (k ? 16 + j : i) & 1 ? kFar : 1.0f;
+        const bool first = fabsf(x) < fabsf(y);
+        x *= first ? f : 1.0f, y *= first ? 1.0f : f;
+    }
+}
+// the type's largest number
+template <class T>
+constexpr float kLargest = std::is_same<T, f16>::value ? 65504.0f : sizeof(T) == 2 ? 0x1.fep127f : 0x1.fffffep127f;
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_zero(float v) {  // lanes without a source get 0
@@ -448,14 +506,15 @@ __device__ __forceinline__ void put_decays(Decays<T>& d, float g, float in, floa
         for (int b = 0; b < B; ++b) m += b > j && b < i ? sum[b] : 0.0f;
         d.between[i][j] = exp_f<F>(m);
     }
-    // growth that could pass the type's range in a part of a product, NaN or infinite weights
+    // growth and weights that could pass the type's range in a part of a product (kHuge), NaN
     constexpr bool H = std::is_same<T, f16>::value;
-    const float up = across_rows(row_sum(fmaxf(g, 0.0f)));
-    const bool odd = !(up < (H ? 4.0f : 40.0f)) || __ballot(g != g || !(fabsf(in) < INFINITY) || !(fabsf(out) < INFINITY));
+    const float up = across_rows(row_sum(fmaxf(g, 0.0f))), grow = exp_f<F>(up);
+    const bool odd = !(up < (H ? 4.0f : 40.0f)) ||
+                     __ballot(g != g || !(fabsf(in) * grow < 0x1p60f) || !(fabsf(out) < 0x1p14f));
     if (lane == 0) {
         d.whole = exp_f<F>(all);
         d.odd = odd;
-        if (H) d.grow = exp_f<F>(up);
+        if (H) d.grow = grow;
     }
     if constexpr (H) {
         float a = fabsf(in), b = fabsf(out);

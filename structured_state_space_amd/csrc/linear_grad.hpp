@@ -146,9 +146,10 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
     };
     auto finish = [&](int h, int i) {  // of head h, whose decays are in place i
         const int lane = anew(threadIdx.x) & 63, r = min(lane, Q - 1);
-        const float b = sh.beta[i][r], own = b * sum_behind;
+        // (a weight of zero takes part in nothing, whatever its step's keys and values make of its sums)
+        const float b = sh.beta[i][r], own = b == 0.0f ? 0.0f : b * sum_behind;
         // sums over the steps from r on, and before r
-        float from = row_suffix(sum_row + sum_before - b * sum_column), till = row_prefix(own);
+        float from = row_suffix(sum_row + sum_before - (b == 0.0f ? 0.0f : b * sum_column)), till = row_prefix(own);
         float later = 0.0f, earlier = 0.0f;
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
             later += i > (lane >> 4) ? f : 0.0f, earlier += i < (lane >> 4) ? e : 0.0f;
         }
         from += later, till += earlier;
-        const float dg = from + (till - own) + sh.across[i] * sum_whole;
+        const float dg = from + (till - own) + (sh.across[i] == 0.0f ? 0.0f : sh.across[i] * sum_whole);
         if (lane < nt) {
             // a reset takes part in no product, and the sums' rounding is not left in its place
             ((float*)a.dg.data)[it.row * a.dg.sb + h * a.dg.sh + (t0 + lane) * a.dg.sl] =
@@ -210,6 +211,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
     const bool diagonal = wave < TT;
     const int first = diagonal ? 0 : wave < 4 || wave == W - 1 ? BELOW : wave - 4;  // (the last wave has the sums)
     f32x4 qk[OWN];
+    uint32_t far_qk[OWN] = {};  // rows of keys and queries whose products are kept 2^-98 times
 #pragma unroll
     for (int j = 0; j < OWN; ++j) {
         qk[j] = f32x4{0, 0, 0, 0};
@@ -221,6 +223,10 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
             for (int kk = 0; kk < KK; ++kk)
                 qk[j] = mma<T>(row_frag<T>(sh.k + (16 * si + (lane & 15)) * KS + 32 * kk + 8 * (lane >> 4)),
                                row_frag<T>(sh.q + (16 * ti + (lane & 15)) * KS + 32 * kk + 8 * (lane >> 4)), qk[j]);
+            const f32x4 one[1] = {qk[j]};
+            if (!F16 && __builtin_expect(__ballot(far_out(one)) != 0, 0))
+                qk[j] = products_in_range<T, KK>(sh.k + (16 * si + (lane & 15)) * KS + 8 * (lane >> 4),
+                                                 sh.q + (16 * ti + (lane & 15)) * KS + 8 * (lane >> 4), far_qk[j]);
         }
     }
     // the wave's keys and steps
@@ -276,8 +282,8 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                 for (int kk = 0; kk < PK; ++kk)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) whole = fmaf(x[kk][i / 4][i % 4], X[kk][i / 4][i % 4], whole);
-                // products of the states with a tile of steps (dy or v), and where they are scaled to
-                auto across = [&](const f32x4 (&state)[PK][2], const T* tile, f32x4 (&to)[TW]) {
+                // products of the states with a tile of steps (dy or v), and what brings them back to scale
+                auto across = [&](f32x4 (&state)[PK][2], const float* all, const T* tile, f32x4 (&to)[TW]) {
                     const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
                     float s = 1.0f;
                     if constexpr (F16) {
@@ -293,23 +299,32 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                         for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
                         s = to_range<T>(m);
                     }
+                    while (true) {
 #pragma unroll
-                    for (int t = 0; t < TW; ++t) to[t] = f32x4{0, 0, 0, 0};
+                        for (int t = 0; t < TW; ++t) to[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int kk = 0; kk < PK; ++kk) {
-                        float u[8];
+                        for (int kk = 0; kk < PK; ++kk) {
+                            float u[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) u[i] = state[kk][i / 4][i % 4] * s;
-                        Frag<T> part[kParts<T>];
-                        split<T>(u, part);
-                        Frag<T> f[TW];
+                            for (int i = 0; i < 8; ++i) u[i] = F16 ? state[kk][i / 4][i % 4] * s : state[kk][i / 4][i % 4];
+                            Frag<T> part[kParts<T>];
+                            split<T>(u, part);
+                            Frag<T> f[TW];
 #pragma unroll
-                        for (int t = 0; t < TW; ++t) f[t] = row_frag<T>(tile + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
-                        // (products that wait for each other's sums do not follow each other)
+                            for (int t = 0; t < TW; ++t) f[t] = row_frag<T>(tile + (16 * (TW * group + t) + tl) * VS + 32 * kk + 8 * gl);
+                            // (products that wait for each other's sums do not follow each other)
 #pragma unroll
-                        for (int i = 0; i < kParts<T>; ++i)
+                            for (int i = 0; i < kParts<T>; ++i)
 #pragma unroll
-                            for (int t = 0; t < TW; ++t) to[t] = mma<T>(part[i], f[t], to[t]);
+                                for (int t = 0; t < TW; ++t) to[t] = mma<T>(part[i], f[t], to[t]);
+                        }
+                        // (a state or a value so large that the products pass float32: once more, 2^-64 times,
+                        // read again so that nothing is kept for it)
+                        if (F16 || s != 1.0f || __builtin_expect(__ballot(far_out(to)) == 0, 1)) break;
+                        s = 0x1p-64f;
+                        load_states(state, all, now, n);
+#pragma unroll
+                        for (int kk = 0; kk < PK; ++kk) state[kk][0] *= s, state[kk][1] *= s;
                     }
                     return reciprocal_of_power(s);
                 };
@@ -317,7 +332,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                 {
                     const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
                     f32x4 in[TW];
-                    const float ux = across(x, dy, in);
+                    const float ux = across(x, a.states, dy, in);
                     if (EARLY && k + 1 < count) load_states(x, a.states, next, 0);
                     Frag<T> kf[SS];
 #pragma unroll
@@ -329,23 +344,23 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
 #pragma unroll
                         for (int s = 0; s < SS; ++s)
                             if (s <= tt / 2) w = mma<T>(kf[s], row_frag<T>(m + r * MS + 32 * s + 8 * gl), w);
-                        const float from = d.from[r] * ux;
+                        const float from = d.from[r];
                         const Own q4 = *reinterpret_cast<const Own*>(sh.q + r * KS + key + 4 * gl);
                         float before = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float u = in[t][i] * from;
                             before = fmaf(u, to_f(get_of<T>(q4.v, i)), before);
-                            dq[n][t][i] += fmaf(w[i], um, u);
+                            dq[n][t][i] = fmaf(u, ux, fmaf(w[i], um, dq[n][t][i]));
                         }
-                        before = across_rows(before);
+                        before = across_rows(before) * ux;
                         if (gl == 0) sums.before[tile + n][r] = before;
                     }
                 }
                 {
                     const int lane = anew(tid) & 63, tl = lane & 15, gl = lane >> 4;
                     f32x4 out[TW];
-                    const float uX = across(X, v, out);
+                    const float uX = across(X, a.ahead, v, out);
                     if (EARLY && k + 1 < count) load_states(X, a.ahead, next, 0);
                     Frag<T> qf[SS];
 #pragma unroll
@@ -357,16 +372,16 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
 #pragma unroll
                         for (int s = 0; s < SS; ++s)
                             if (s >= tt / 2) w = mma<T>(qf[s], column_frag<T>(m + 32 * s * MS + 16 * tt, MS, lane), w);
-                        const float to = d.to[r] * further * uX, b = sh.beta[place(now.h)][r];
+                        const float to = d.to[r] * further, b = sh.beta[place(now.h)][r] * uX;
                         const Own k4 = *reinterpret_cast<const Own*>(sh.k + r * KS + key + 4 * gl);
                         float after = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float u = out[t][i] * to;
                             after = fmaf(u, to_f(get_of<T>(k4.v, i)), after);
-                            dk[n][t][i] += fmaf(w[i], um, u * b);
+                            dk[n][t][i] = fmaf(u, b, fmaf(w[i], um, dk[n][t][i]));
                         }
-                        after = across_rows(after);
+                        after = across_rows(after) * uX;
                         if (gl == 0) sums.behind[tile + n][r] = after;
                     }
                 }
@@ -387,24 +402,43 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                 sm = to_range<T>(fabsf(a.scale) * d.grow * sh.most_beta[place(next.h)] * (float)kPairValues *
                                  to_f(__builtin_bit_cast(f16, (uint16_t)mv)) * to_f(__builtin_bit_cast(f16, (uint16_t)my)));
             }
-            auto pairs = [&](int ti, int si, const f32x4& u, const f32x4& kq, bool on) {
+            auto pairs = [&](int ti, int si, const f32x4& u, const f32x4& kq, uint32_t far_kq, bool on) {
                 f32x4 dm = {0, 0, 0, 0};
+                uint32_t far_dm = 0;
 #pragma unroll
                 for (int kk = 0; kk < PK; ++kk)
                     dm = mma<T>(row_frag<T>(v + (16 * si + tl) * VS + 32 * kk + 8 * gl),
                                 row_frag<T>(dy + (16 * ti + tl) * VS + 32 * kk + 8 * gl), dm);
+                const f32x4 one[1] = {dm};
+                if (!F16 && __builtin_expect(__ballot(far_out(one)) != 0, 0))
+                    dm = products_in_range<T, PK>(v + (16 * si + tl) * VS + 8 * gl, dy + (16 * ti + tl) * VS + 8 * gl, far_dm);
                 const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.beta[place(next.h)][16 * si + 4 * gl]);
                 f32x4 w;
                 float column[4], part = 0.0f, skip = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float um = u[i] * dm[i], wt = um * kq[i];
                     const bool own = on && 4 * gl + i == tl;
+                    const float um = u[i] * dm[i];
+                    float wt = um * kq[i], ub = um * b[i], wb = ub * kq[i], yv = dm[i];
+                    if (__builtin_expect((far_kq | far_dm) != 0, 0)) {
+                        auto product = [&](float x) {
+                            float y = kq[i];
+                            bring_back(x, y, far_dm, 4 * gl + i, tl);
+                            bring_back(x, y, far_kq, 4 * gl + i, tl);
+                            return x * y;
+                        };
+                        float one = 1.0f;
+                        wt = product(um), wb = product(ub);
+                        bring_back(ub, one, far_dm, 4 * gl + i, tl), ub *= one, one = 1.0f;
+                        bring_back(yv, one, far_dm, 4 * gl + i, tl), yv *= one;
+                        // a value that nothing is to be weighted with must not make an infinity of that
+                        if (kq[i] == 0.0f && fabsf(um) < INFINITY) ub = fminf(fmaxf(ub, -kLargest<T>), kLargest<T>);
+                    }
                     if (own) sums.diagonal[16 * ti + tl] = wt;
                     column[i] = own ? 0.0f : wt;
-                    skip = own ? dm[i] : skip;
-                    part = fmaf(column[i], b[i], part);
-                    w[i] = um * b[i] * sm;
+                    skip = own ? yv : skip;
+                    part += own ? 0.0f : wb;
+                    w[i] = ub * sm;
                 }
                 put_four<T>(m + (16 * ti + tl) * MS + 16 * si + 4 * gl, w);
 #pragma unroll
@@ -419,13 +453,13 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                 }
             };
             if (diagonal) {
-                pairs(wave, wave, weights_within<T>(d, wave, lane), qk[0], true);
+                pairs(wave, wave, weights_within<T>(d, wave, lane), qk[0], far_qk[0], true);
             } else {
 #pragma unroll
                 for (int j = 0; j < OWN; ++j) {
                     int ti, si;
                     below(first + 3 * j, ti, si);
-                    if (first + 3 * j < BELOW) pairs(ti, si, weights_across<T>(d, ti, si, lane), qk[j], false);
+                    if (first + 3 * j < BELOW) pairs(ti, si, weights_across<T>(d, ti, si, lane), qk[j], far_qk[j], false);
                 }
             }
         }

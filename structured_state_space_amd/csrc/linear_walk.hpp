@@ -43,6 +43,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         uint32_t most[3][kWalkWaves];
         float most_x[kWalkWaves];
         int odd[kWalkWaves];
+        int passed;  // a chunk whose products passed float32, counted from 1
         float sums[2][2][kWalkValues];
     };
     __shared__ Shared sh;
@@ -193,6 +194,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
             if (F16) most_state();
             // pairs s > t within two blocks of a product stay zero
             for (int i = threadIdx.x; i < Q * MS; i += kWalkThreads) sh.m[i] = from_f<T>(0.0f);
+            if (threadIdx.x == 0) sh.passed = 0;
         }
     }
     for (int k = 0; k < count; ++k) {
@@ -231,7 +233,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                 }
                 if (lane == 0) sh.most[0][wave] = mk, sh.most[1][wave] = mv, sh.most[2][wave] = mq;
             }
-            const bool any = __ballot(max(max(mk, mv), mq) >= kInf<T>) != 0;
+            const bool any = __ballot(max(max(mk, mv), mq) >= kHuge<T>) != 0;
             if (lane == 0) sh.odd[wave] = any;
         }
         __syncthreads();
@@ -246,11 +248,76 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         int odd = d.odd;
 #pragma unroll
         for (int i = 0; i < kWalkWaves; ++i) odd |= sh.odd[i];
+        float most[3] = {0, 0, 0}, most_in = 0.0f, most_m = 0.0f;  // float16 only
+        if constexpr (F16) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int w = 0; w < kWalkWaves; ++w) m = max(m, sh.most[i][w]);
+                most[i] = to_f(__builtin_bit_cast(f16, (uint16_t)m));
+            }
+            most_in = d.most_in * d.grow;
+            most_m = most_in * d.most_out * most[0] * most[2] * (float)N;
+        }
+        f32x4 across[OUT ? HT : 1];
+        float sm = 1.0f;
+        if (OUT && !odd) {
+            sm = to_range<T>(most_m + fabsf(skip));
+            // the pairs: tiles on the diagonal by the first waves, those below it by the others
+            auto pairs = [&](int ti, int si) {
+                f32x4 m = {0, 0, 0, 0};
+                const T* kp = sh.k + (16 * si + tl) * KS + 8 * gl;
+                const T* qp = sh.q + (16 * ti + tl) * KS + 8 * gl;
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) m = mma<T>(row_frag<T>(kp + 32 * kk), row_frag<T>(qp + 32 * kk), m);
+                return m;
+            };
+            auto keep = [&](int ti, int si, const f32x4& m) {
+                put_four<T>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl, m * sm);
+            };
+            if (wave < TT) {
+                f32x4 m = pairs(wave, wave) * weights_within<T>(d, wave, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] += 4 * gl + i == tl ? skip : 0.0f;
+                keep(wave, wave, m);
+            } else if (wave >= 4 && wave < kWalkWaves - 1) {  // (the last wave has the decays)
+                for (int j = wave - 4; j < TT * (TT - 1) / 2; j += 3) {
+                    const int ti = j < 1 ? 1 : j < 3 ? 2 : 3, si = j - ti * (ti - 1) / 2;
+                    keep(ti, si, pairs(ti, si) * weights_across<T>(d, ti, si, lane));
+                }
+            }
+            // what the state before the chunk gives
+            if (live) {
+#pragma unroll
+                for (int t = 0; t < HT; ++t) across[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    const Frag<T> f = row_frag<T>(sh.x + (16 * pq + tl) * KS + 32 * kk + 8 * gl);
+#pragma unroll
+                    for (int t = 0; t < HT; ++t)
+                        across[t] = mma<T>(f, row_frag<T>(sh.q + (16 * tile(t) + tl) * KS + 32 * kk + 8 * gl), across[t]);
+                }
+                if (__ballot(far_out(across)) && lane == 0) sh.passed = k + 1;
+            }
+            __syncthreads();
+        }
+        Frag<T> vf[SS];  // (under way while the test waits)
+        if (live) {
+#pragma unroll
+            for (int s = 0; s < SS; ++s) vf[s] = column_frag<T>(sh.v + 32 * s * VS + 16 * pq, VS, lane);
+        }
+        if (OUT && !odd) odd = sh.passed == k + 1;
         if (__builtin_expect(odd, 0)) {
-            // An infinity or NaN among the inputs would reach earlier rows through the products'
-            // zeros: the chunk goes row by row, as the formula says.
+            // An infinity or NaN among the inputs, or one that comes of their products, would reach
+            // other rows through the products' zeros: the chunk goes row by row, as the formula says.
+            // (A weight above one comes last, one below it first: then nothing passes float32 that the
+            // formula keeps within it.)
             for (int r = REVERSE ? Q - nt : 0; r < (REVERSE ? Q : nt); ++r) {
-                const float e = exp_f<kFine<T>>(d.g[r]), in_r = d.in[r];
+                const float e = exp_f<kFine<T>>(d.g[r]), in_r = d.in[r], out_r = d.out[r];
+                const bool in_first = fabsf(in_r) <= 1.0f, out_first = fabsf(out_r) <= 1.0f;
+                const float in_a = in_first ? in_r : 1.0f, in_b = in_first ? 1.0f : in_r;
+                const float out_a = out_first ? out_r : 1.0f, out_b = out_first ? 1.0f : out_r;
                 const float v = to_f(sh.v[r * VS + 16 * pq + tl]);
                 float sum = 0.0f;
 #pragma unroll
@@ -259,8 +326,8 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                     for (int i = 0; i < 4; ++i) {
                         const int at = 16 * (NT * half + n) + 4 * gl + i;
                         if (at < N && p0 + 16 * pq + tl < P) {  // (what does not exist stays zero)
-                            x[n][i] = fmaf(x[n][i], e, in_r * to_f(sh.k[r * KS + at]) * v);
-                            if (OUT) sum = fmaf(x[n][i], to_f(sh.q[r * KS + at]), sum);
+                            x[n][i] = fmaf(x[n][i], e, in_a * to_f(sh.k[r * KS + at]) * v * in_b);
+                            if (OUT) sum = fmaf(x[n][i], out_a * to_f(sh.q[r * KS + at]), sum);
                         }
                     }
                 if (OUT) {
@@ -268,127 +335,71 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                     if (gl == 0) sh.sums[r & 1][half][16 * pq + tl] = sum;
                     __syncthreads();
                     if (half == 0 && gl == 0 && p0 + 16 * pq + tl < P) {
-                        sum = (sum + sh.sums[r & 1][1][16 * pq + tl]) * d.out[r];
+                        sum = (sum + sh.sums[r & 1][1][16 * pq + tl]) * out_b;
                         if (a.D) sum = fmaf(skip, v, sum);
                         const int o = REVERSE ? Q - 1 - r : r;
                         result[o * a.result.sl + tl * a.result.sn] = from_f<T>(sum);
                     }
                 }
             }
-        } else {
-            float most[3] = {0, 0, 0};
-            if constexpr (F16) {
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int w = 0; w < kWalkWaves; ++w) m = max(m, sh.most[i][w]);
-                    most[i] = to_f(__builtin_bit_cast(f16, (uint16_t)m));
-                }
-            }
-            const float most_in = d.most_in * d.grow;  // float16 only
-            f32x4 across[OUT ? HT : 1];
-            float sm = 1.0f;
+        }
+        if (live && !odd) {
             if (OUT) {
-                sm = to_range<T>(most_in * d.most_out * most[0] * most[2] * (float)N + fabsf(skip));
-                // the pairs: tiles on the diagonal by the first waves, those below it by the others
-                auto pairs = [&](int ti, int si) {
-                    f32x4 m = {0, 0, 0, 0};
-                    const T* kp = sh.k + (16 * si + tl) * KS + 8 * gl;
-                    const T* qp = sh.q + (16 * ti + tl) * KS + 8 * gl;
+                const float um = reciprocal_of_power(sm), ux = reciprocal_of_power(sx);
 #pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) m = mma<T>(row_frag<T>(kp + 32 * kk), row_frag<T>(qp + 32 * kk), m);
-                    return m;
-                };
-                auto keep = [&](int ti, int si, const f32x4& m) {
-                    put_four<T>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl, m * sm);
-                };
-                if (wave < TT) {
-                    f32x4 m = pairs(wave, wave) * weights_within<T>(d, wave, lane);
+                for (int t = 0; t < HT; ++t) {
+                    const int r = 16 * tile(t) + tl, o = REVERSE ? Q - 1 - r : r;
+                    const T* mp = sh.m + r * MS + 8 * gl;
+                    f32x4 within = {0, 0, 0, 0};
+                    within = mma<T>(vf[0], row_frag<T>(mp), within);
+                    if (SS > 1 && t) within = mma<T>(vf[SS - 1], row_frag<T>(mp + 32), within);
+                    const float f = d.from[r] * ux;
+                    f32x4 sum;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m[i] += 4 * gl + i == tl ? skip : 0.0f;
-                    keep(wave, wave, m);
-                } else if (wave >= 4 && wave < kWalkWaves - 1) {  // (the last wave has the decays)
-                    for (int j = wave - 4; j < TT * (TT - 1) / 2; j += 3) {
-                        const int ti = j < 1 ? 1 : j < 3 ? 2 : 3, si = j - ti * (ti - 1) / 2;
-                        keep(ti, si, pairs(ti, si) * weights_across<T>(d, ti, si, lane));
+                    for (int i = 0; i < 4; ++i) sum[i] = fmaf(across[t][i], f, within[i] * um);
+                    const Quad<T> y = four_of<T>(sum);
+                    const int there = P - (p0 + 16 * pq + 4 * gl);
+                    if (vectors) {
+                        if (o < nt && there > 0)
+                            *reinterpret_cast<Quad<T>*>((char*)result + (uint32_t)o * ((uint32_t)a.result.sl * (uint32_t)sizeof(T)) +
+                                                     4u * gl * (uint32_t)sizeof(T)) = y;
+                    } else {
+                        T* to = result + o * a.result.sl + 4 * gl * a.result.sn;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (o < nt && i < there) to[i * a.result.sn] = get_of<T>(y, i);
                     }
                 }
-                // what the state before the chunk gives
-                if (live) {
-#pragma unroll
-                    for (int t = 0; t < HT; ++t) across[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) {
-                        const Frag<T> f = row_frag<T>(sh.x + (16 * pq + tl) * KS + 32 * kk + 8 * gl);
-#pragma unroll
-                        for (int t = 0; t < HT; ++t)
-                            across[t] = mma<T>(f, row_frag<T>(sh.q + (16 * tile(t) + tl) * KS + 32 * kk + 8 * gl), across[t]);
-                    }
-                }
-                __syncthreads();
             }
-            if (live) {
-                Frag<T> vf[SS];
+            // the state after the chunk
+            const float sv = to_range<T>(most_in * most[1]), uv = reciprocal_of_power(sv);
+            Frag<T> part[SS][kParts<T>];
 #pragma unroll
-                for (int s = 0; s < SS; ++s) vf[s] = column_frag<T>(sh.v + 32 * s * VS + 16 * pq, VS, lane);
-                if (OUT) {
-                    const float um = reciprocal_of_power(sm), ux = reciprocal_of_power(sx);
+            for (int s = 0; s < SS; ++s) {
+                const f32x4* to = reinterpret_cast<const f32x4*>(&d.to[32 * s + 8 * gl]);
+                float w[8];
 #pragma unroll
-                    for (int t = 0; t < HT; ++t) {
-                        const int r = 16 * tile(t) + tl, o = REVERSE ? Q - 1 - r : r;
-                        const T* mp = sh.m + r * MS + 8 * gl;
-                        f32x4 within = {0, 0, 0, 0};
-                        within = mma<T>(vf[0], row_frag<T>(mp), within);
-                        if (SS > 1 && t) within = mma<T>(vf[SS - 1], row_frag<T>(mp + 32), within);
-                        const float f = d.from[r] * ux;
-                        f32x4 sum;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sum[i] = fmaf(across[t][i], f, within[i] * um);
-                        const Quad<T> y = four_of<T>(sum);
-                        const int there = P - (p0 + 16 * pq + 4 * gl);
-                        if (vectors) {
-                            if (o < nt && there > 0)
-                                *reinterpret_cast<Quad<T>*>((char*)result + (uint32_t)o * ((uint32_t)a.result.sl * (uint32_t)sizeof(T)) +
-                                                         4u * gl * (uint32_t)sizeof(T)) = y;
-                        } else {
-                            T* to = result + o * a.result.sl + 4 * gl * a.result.sn;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (o < nt && i < there) to[i * a.result.sn] = get_of<T>(y, i);
-                        }
-                    }
-                }
-                // the state after the chunk
-                const float sv = to_range<T>(most_in * most[1]), uv = reciprocal_of_power(sv);
-                Frag<T> part[SS][kParts<T>];
-#pragma unroll
-                for (int s = 0; s < SS; ++s) {
-                    const f32x4* to = reinterpret_cast<const f32x4*>(&d.to[32 * s + 8 * gl]);
-                    float w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = frag_get<T>(vf[s], j) * (to[j / 4][j % 4] * sv);
-                    split<T>(w, part[s]);
-                }
-                // (the tiles in turn: products that wait for each other's sums do not follow each other)
-                f32x4 add[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) add[n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int s = 0; s < SS; ++s) {
-                    Frag<T> kf[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) kf[n] = column_frag<T>(sh.k + 32 * s * KS + 16 * (NT * half + n), KS, lane);
-#pragma unroll
-                    for (int i = 0; i < kParts<T>; ++i)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) add[n] = mma<T>(kf[n], part[s][i], add[n]);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[n][i] = fmaf(x[n][i], whole, add[n][i] * uv);
+                for (int j = 0; j < 8; ++j) w[j] = frag_get<T>(vf[s], j) * (to[j / 4][j % 4] * sv);
+                split<T>(w, part[s]);
             }
+            // (the tiles in turn: products that wait for each other's sums do not follow each other)
+            f32x4 add[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) add[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < SS; ++s) {
+                Frag<T> kf[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) kf[n] = column_frag<T>(sh.k + 32 * s * KS + 16 * (NT * half + n), KS, lane);
+#pragma unroll
+                for (int i = 0; i < kParts<T>; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) add[n] = mma<T>(kf[n], part[s][i], add[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[n][i] = fmaf(x[n][i], whole, add[n][i] * uv);
         }
         if (F16 && OUT) most_state();
         if (OUT) result += (REVERSE ? -Q : Q) * a.result.sl;
