@@ -259,6 +259,9 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
             }
             most_in = d.most_in * d.grow;
             most_m = most_in * d.most_out * most[0] * most[2] * (float)N;
+            // M keeps 2^-39 of this, 2^-19 of a number: beside a step of the lowest numbers ordinary ones would
+            // have lost all of theirs, and go row by row
+            if (OUT) odd |= !(most_m < 0x1p20f);
         }
         f32x4 across[OUT ? HT : 1];
         float sm = 1.0f;

@@ -18,7 +18,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-LARGEST = {"f32": float(np.finfo(np.float32).max), "bf16": 2.0 ** 128 - 2.0 ** 120}
+LARGEST = {"f32": float(np.finfo(np.float32).max), "bf16": 2.0 ** 128 - 2.0 ** 120, "f16": 65504.0}
 
 
 def compare(a, name, order="tokens", offsets=None, skip_y=(), skip=("dbeta",), at=()):
@@ -55,7 +55,7 @@ SIZES = [(1, 4, 2, 32, 40, 150), (2, 2, 1, 128, 64, 130), (1, 2, 1, 250, 100, 70
 AT = (5, 20, 21, 31, 32, 64, 69)
 
 
-@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("size", SIZES)
 @pytest.mark.parametrize("what,zero", [("k", "v"), ("k", "beta"), ("v", "beta"), ("v", "k"), ("kv", "beta"), ("qkv", "beta")])
 def test_masked_keys_and_values(name, size, what, zero):
@@ -77,7 +77,7 @@ def test_masked_places_that_are_read(name, what, zero):
     compare(a, name, at=AT)
 
 
-@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("order", ["rows", "mixed"])
 def test_masked_places_in_other_orders(name, order):
     a = K.inputs(43, name, 1, 2, 1, 40, 40, 150, skip=False)
@@ -87,7 +87,7 @@ def test_masked_places_in_other_orders(name, order):
     compare(a, name, order, at=AT)
 
 
-@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 def test_masked_places_of_packed_and_cut_sequences(name):
     a = K.inputs(44, name, 1, 1, 1, 32, 48, 900, S=3, skip=False, pace=0.03)
     at = (*AT, 300, 420, 555, 600, 899)
