@@ -346,13 +346,13 @@ template <class T>
 constexpr uint32_t kHuge = sizeof(T) == 4 ? 0x4a800000u : std::is_same<T, f16>::value ? 0x7c00u : 0x4a80u;
 
 // A power of two 2^e that brings magnitudes up to `most` (float32) below 2^15, where
-// float16 has them and 2^-39 of them; 1 for other types.  Bounded, so that it and its
-// reciprocal are float32.
+// float16 has them and 2^-39 of them; 1 for other types.  Bounded by what float32's largest
+// number needs and so that its reciprocal is float32.
 template <class T>
 __device__ __forceinline__ float to_range(float most) {
     if constexpr (!std::is_same<T, f16>::value) return 1.0f;
     const int e = 127 + 14 - (int)((__float_as_uint(most) >> 23) & 0xff);  // 14 - floor(log2 most)
-    return most > 0.0f ? __uint_as_float((uint32_t)(min(max(e, -110), 110) + 127) << 23) : 1.0f;
+    return most > 0.0f ? __uint_as_float((uint32_t)(min(max(e, -113), 110) + 127) << 23) : 1.0f;
 }
 // 1 / a power of two
 __device__ __forceinline__ float reciprocal_of_power(float p) {

@@ -123,3 +123,13 @@ def test_products_that_come_back(name, sizes):
     if "k" in sizes:
         a["g"][..., [t + 1 for t in at]] = -np.inf      # large keys meet the products of their own step alone
     compare(a, name)
+
+
+def test_float16_with_states_near_float32s_end():
+    """States of up to 3e38 as operands of float16: results that a small scale brings back."""
+    for L in (1, 70):
+        a = K.inputs(48, "f16", 1, 2, 1, 32, 32, L, skip=False, scale=2.0 ** -110, pace=0.01)
+        a["q"] = K.rounded(a["q"] * 1e-3, "f16")
+        a["x0"] = K.rounded(a["x0"] / np.abs(a["x0"]).max() * 2.9e38, "f32")
+        a["dx"] = K.rounded(a["dx"] * 1e-36, "f32")
+        compare(a, "f16", skip=("dq",), at=range(L))
