@@ -29,6 +29,10 @@ __global__ __launch_bounds__(kTokenThreads) void linear_step_kernel(const Linear
     }
     const int grp = (int)(h / (a.H / a.G));
     const float beta = a.beta ? a.beta[b * a.beta_row + h * a.beta_head] : 1.0f;
+    // (weights above one come last: beta k must not pass float32 where the value is zero, nor scale q where
+    // the state is)
+    const float first = fabsf(beta) <= 1.0f ? beta : 1.0f, last = fabsf(beta) <= 1.0f ? 1.0f : beta;
+    const float q_first = fabsf(a.scale) <= 1.0f ? a.scale : 1.0f, q_last = fabsf(a.scale) <= 1.0f ? 1.0f : a.scale;
     const float e = exp_f<kFine<T>>(a.g[b * a.g_row + h * a.g_head]);
     const int p0 = pb * kTokenValues, wide = min(kTokenValues, P - p0) / V;  // vectors of a row
     const int rows = kTokenThreads / wide, r = tid / wide, p = p0 + tid % wide * V;
@@ -37,8 +41,8 @@ __global__ __launch_bounds__(kTokenThreads) void linear_step_kernel(const Linear
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = to_f(((const T*)a.v)[b * a.v_row + h * a.v_head + (p + i) * a.v_value]);
     for (int n = tid; n < N; n += kTokenThreads) {
-        ks[n] = beta * to_f(((const T*)a.k)[b * a.k_row + grp * a.k_group + n * a.k_key]);
-        qs[n] = a.scale * to_f(((const T*)a.q)[b * a.q_row + grp * a.q_group + n * a.q_key]);
+        ks[n] = first * to_f(((const T*)a.k)[b * a.k_row + grp * a.k_group + n * a.k_key]);
+        qs[n] = q_first * to_f(((const T*)a.q)[b * a.q_row + grp * a.q_group + n * a.q_key]);
     }
     __syncthreads();
     float* x = a.x + ((row * a.H + h) * N) * P + p;
@@ -60,7 +64,7 @@ __global__ __launch_bounds__(kTokenThreads) void linear_step_kernel(const Linear
                     const float k = ks[n], q = qs[n];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        s[j].v[i] = fmaf(s[j].v[i], e, k * v[i]);
+                        s[j].v[i] = fmaf(s[j].v[i], e, k * v[i] * last);
                         y[i] = fmaf(s[j].v[i], q, y[i]);
                     }
                     *reinterpret_cast<Vec*>(x + (int64_t)n * P) = s[j];
@@ -75,6 +79,7 @@ __global__ __launch_bounds__(kTokenThreads) void linear_step_kernel(const Linear
     for (int c = tid; c < wide * V; c += kTokenThreads) {
         float sum = 0.0f;
         for (int k = 0; k < rows; ++k) sum += part[k * wide * V + c];
+        sum *= q_last;
         if (a.D) sum = fmaf(a.D[h], to_f(((const T*)a.v)[b * a.v_row + h * a.v_head + (p0 + c) * a.v_value]), sum);
         ((T*)a.y)[b * a.y_row + h * a.y_head + (p0 + c) * a.y_value] = from_f<T>(sum);
     }

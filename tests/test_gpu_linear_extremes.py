@@ -125,6 +125,27 @@ def test_products_that_come_back(name, sizes):
     compare(a, name)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("beta", [0.0, 1.0, 2.5])
+def test_step_with_a_masked_key(name, beta):
+    """One token whose key or value (or query) is the lowest number and whose other one (state) is zero."""
+    ssm = _ssm()
+    a = K.inputs(47, name, 2, 4, 2, 32, 40, 1, skip=False)
+    a["beta"][:] = beta
+    for what, zero in (("k", ("v",)), ("v", ("k",)), ("q", ("x0", "v"))):
+        b = {n: v.copy() if isinstance(v, np.ndarray) else v for n, v in a.items()}
+        hide(b, name, what, (0,))
+        for n in zero:
+            b[n][:] = 0.0
+        b["scale"] = 3.0 if what == "q" else b["scale"]
+        spans = S.dense_spans(2, 1)
+        args, kw = K.call_args(b, name, "rows")
+        x = kw.pop("x0")
+        kw["beta"] = kw["beta"][..., 0]
+        y = ssm.linear_attention_step(*(t[..., 0] for t in args), x, **kw)["y"]
+        K.assert_all(dict(y=_np(y)[..., None], x=_np(x)), K.forward(b, spans), K.forward(b, spans, True), b, name, spans)
+
+
 def test_float16_with_states_near_float32s_end():
     """States of up to 3e38 as operands of float16: results that a small scale brings back."""
     for L in (1, 70):
