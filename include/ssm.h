@@ -531,8 +531,9 @@ int ssm_selective_step(const ssm_selective_token* p, void* stream);
  *     over 64 steps, float16 up to 4; beyond, the forward pass goes step by step and
  *     the backward pass may overflow).
  *   - Results of 16-bit types are rounded from sums of products whose one factor (the
- *     weight of a pair of steps, the state) was rounded to the type; states, dg, dbeta
- *     and dD come from float32 numbers or from two (bfloat16: three) parts of 16 bits.
+ *     weight of a pair of steps, the state) was rounded to the type; D v is added in
+ *     float32; states, dg, dbeta and dD come from float32 numbers or from two (bfloat16:
+ *     three) parts of 16 bits.
  *   - An infinite or NaN input makes its own head (or, of q and k, its group) infinite
  *     or NaN from its step on, and nothing before; the head's (group's) gradients are
  *     infinite or NaN.

@@ -12,8 +12,8 @@ constexpr int kWalkValues = 64;  // values of a workgroup
 
 // A workgroup has one head, 64 of its values and one segment of a sequence, and takes a
 // chunk of rows at a time.  With the pairs' weights M_ts = out_t (q_t . k_s) E_ts in_s
-// (s <= t, D on the diagonal) the chunk's results are
-//   result_t = sum_s M_ts value_s + out_t E_t x^T q_t,
+// (s <= t) the chunk's results are
+//   result_t = sum_s M_ts value_s + out_t E_t x^T q_t + D value_t,
 // and the state becomes E x + sum_s E'_s in_s k_s value_s^T: four matrix products.  The state
 // stays in float32 in registers, as the matrix instruction leaves it: a wave has 16 values and
 // half of the keys, and of the results those values and half of the steps.  Rounded, the state
@@ -24,7 +24,7 @@ constexpr int kWalkValues = 64;  // values of a workgroup
 // keys and steps of their values needed no exchange of the state, but waited more: 265 us.  Two
 // sets of tiles and two barriers were no faster: forwards 240 heads of 8192 steps 523 us, not 447.)
 // Rounding to the activations' type: M and the state as operands for the results, which
-// are rounded to it anyway.  What is added to the state is split (kParts).
+// are rounded to it anyway (D value stays in float32).  What is added to the state is split (kParts).
 // ENDS: the first of two passes, which finds each segment's end state for the second.
 // OUT: results wanted.  FAST: the tensors' usual layout (WalkArgs), in a kernel without the code for
 // others: 5200 instructions instead of 7900, and addresses that do not fill the registers.
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         f32x4 across[OUT ? HT : 1];
         float sm = 1.0f;
         if (OUT && !odd) {
-            sm = to_range<T>(most_m + fabsf(skip));
+            sm = to_range<T>(most_m);
             // the pairs: tiles on the diagonal by the first waves, those below it by the others
             auto pairs = [&](int ti, int si) {
                 f32x4 m = {0, 0, 0, 0};
@@ -280,10 +280,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                 put_four<T>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl, m * sm);
             };
             if (wave < TT) {
-                f32x4 m = pairs(wave, wave) * weights_within<T>(d, wave, lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) m[i] += 4 * gl + i == tl ? skip : 0.0f;
-                keep(wave, wave, m);
+                keep(wave, wave, pairs(wave, wave) * weights_within<T>(d, wave, lane));
             } else if (wave >= 4 && wave < kWalkWaves - 1) {  // (the last wave has the decays)
                 for (int j = wave - 4; j < TT * (TT - 1) / 2; j += 3) {
                     const int ti = j < 1 ? 1 : j < 3 ? 2 : 3, si = j - ti * (ti - 1) / 2;
@@ -348,6 +345,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         }
         if (live && !odd) {
             if (OUT) {
+                struct __attribute__((aligned(4 * sizeof(T)))) Own { Quad<T> v; };
                 const float um = reciprocal_of_power(sm), ux = reciprocal_of_power(sx);
 #pragma unroll
                 for (int t = 0; t < HT; ++t) {
@@ -360,6 +358,11 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                     f32x4 sum;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sum[i] = fmaf(across[t][i], f, within[i] * um);
+                    if (a.D) {  // (in float32: on M's diagonal it would be rounded with M, alike in all steps)
+                        const Own v4 = *reinterpret_cast<const Own*>(sh.v + r * VS + 16 * pq + 4 * gl);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[i] = fmaf(skip, to_f(get_of<T>(v4.v, i)), sum[i]);
+                    }
                     const Quad<T> y = four_of<T>(sum);
                     const int there = P - (p0 + 16 * pq + 4 * gl);
                     if (vectors) {
