@@ -471,7 +471,7 @@ struct Decays {
     float head[Q], tail[Q];        // exp(sum from t's block's start to t) out_t; exp(sum behind s to its block's end) in_s
     float from[Q], to[Q];          // the same from the chunk's start, to its end
     float between[B][B];           // [i][j]: exp(sum over the blocks between j < i)
-    float whole;                   // exp(sum of all)
+    float all, whole;              // the sum of all, and its exponential
     float most_in, most_out, grow; // largest weights; at least as much as any product of decays (float16 only)
     int odd;                       // the chunk has to be walked step by step
 };
@@ -512,7 +512,7 @@ __device__ __forceinline__ void put_decays(Decays<T>& d, float g, float in, floa
     const bool odd = !(up < (H ? 4.0f : 40.0f)) ||
                      __ballot(g != g || !(fabsf(in) * grow < 0x1p60f) || !(fabsf(out) < 0x1p14f));
     if (lane == 0) {
-        d.whole = exp_f<F>(all);
+        d.all = all, d.whole = exp_f<F>(all);
         d.odd = odd;
         if (H) d.grow = grow;
     }
@@ -576,7 +576,7 @@ struct WalkArgs {
     int64_t segment;                  // steps of a segment, whole chunks
     int64_t items;                    // segments of all sequences
     float* seg_x;                     // [items, H, N, P]: what a segment leaves of a state of zero (the first: of x_in)
-    float* seg_decay;                 // [items, H]
+    float* seg_decay;                 // [items, H]: the sum of a segment's log decays
 };
 
 struct LinearArgs {

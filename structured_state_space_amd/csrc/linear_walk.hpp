@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     for (int n = 0; n < NT; ++n) x[n] = f32x4{0, 0, 0, 0};
     // the item of the segment at a place of the walk
     auto item_at = [&](int j) { return item - it.c + (REVERSE ? segments - 1 - j : j); };
-    float decay = 1.0f;  // of the segment
+    double decay = 0.0;  // its logarithm, of the segment
     if (ENDS) {
         if (pos == 0 || pos == segments - 1) {
             // the last one's end is not needed: its place keeps the initial state, which the
@@ -163,7 +163,9 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         if (a.x_in) get(a.x_in, it.state);
     } else {
         get(a.seg_x, item_at(pos == 0 ? segments - 1 : 0));
-        // the segments between, several under way
+        // the segments between, several under way.  A segment's decay is the exponential of the sum of
+        // its logarithms, taken twice by halves: a product of its chunks' decays could pass float32 on
+        // the way to a number, and what is zero stays zero beside one that does.
         constexpr int A = NT > 4 ? 2 : 4;
         for (int j = 1; j < pos; j += A) {
             f32x4 y[A][NT];
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
 #pragma unroll
             for (int i = 0; i < A; ++i) {
                 const int64_t before = item_at(min(j + i, pos - 1));
-                e[i] = a.seg_decay[before * a.H + h];
+                e[i] = exp_f<kFine<T>>(0.5f * a.seg_decay[before * a.H + h]);
                 exchange(y[i], a.seg_x, before, [](float, const float* at, bool there) { return there ? *at : 0.0f; });
             }
 #pragma unroll
@@ -180,7 +182,8 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[n][r] = fmaf(x[n][r], e[i], y[i][n][r]);
+                        for (int r = 0; r < 4; ++r)
+                            x[n][r] = x[n][r] == 0.0f ? y[i][n][r] : fmaf(x[n][r] * e[i], e[i], y[i][n][r]);
                 }
         }
     }
@@ -244,7 +247,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         }
 
         const float whole = d.whole;
-        decay *= whole;
+        decay += d.all;
         int odd = d.odd;
 #pragma unroll
         for (int i = 0; i < kWalkWaves; ++i) odd |= sh.odd[i];
@@ -412,7 +415,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     }
     if (ENDS) {
         put(a.seg_x, item, 1.0f);
-        if (pb == 0 && threadIdx.x == 0) a.seg_decay[item * a.H + h] = decay;
+        if (pb == 0 && threadIdx.x == 0) a.seg_decay[item * a.H + h] = (float)decay;
     } else if (a.x_out && pos == segments - 1) {
         // backwards: the gradient of the state before the first step
         put(a.x_out, it.state, REVERSE && len > 0 ? exp_f<kFine<T>>(gs[it.beg * a.g.sl]) : 1.0f);

@@ -154,3 +154,35 @@ def test_float16_with_states_near_float32s_end():
         a["x0"] = K.rounded(a["x0"] / np.abs(a["x0"]).max() * 2.9e38, "f32")
         a["dx"] = K.rounded(a["dx"] * 1e-36, "f32")
         compare(a, "f16", skip=("dq",), at=range(L))
+
+
+def forward_alone(a, name):
+    ssm = _ssm()
+    Bsz, H, P, L = a["v"].shape
+    G, N = a["q"].shape[1:3]
+    assert ssm.linear_bytes(ssm.OP_LINEAR_ATTENTION, K.torch_type(name), Bsz, H, N, P, G, L) > 0      # cut
+    spans = S.dense_spans(Bsz, L)
+    args, kw = K.call_args(a, name, "tokens")
+    f = ssm.linear_attention(*args, **kw, want_state=True)
+    K.assert_all({n: _np(f[n]) for n in FORWARD}, K.forward(a, spans), K.forward(a, spans, True), a, name, spans)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [40, 64, 200])
+def test_growth_over_pieces(name, N):
+    """A cut sequence that grows by more than float32 over a piece, before anything is in its state: what is zero stays
+    zero, keys that the kernel pads with among it."""
+    a = K.inputs(61, name, 1, 1, 1, N, 24, 1700, carry=False)
+    a["g"][..., :1300] = K.rounded((3.5 if name == "f16" else 38.0) / 64, "f32")     # the most that products take
+    a["k"][..., :1300] = 0.0
+    forward_alone(a, name)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_growth_and_decay_within_a_piece(name):
+    """Every piece of 512 steps grows by e^100 and falls by as much, as its states do, from 1e-35 and back."""
+    a = K.inputs(62, name, 1, 64, 4, 16, 8, 4096, beta=False)
+    a["g"][:] = K.rounded(np.where(np.arange(4096) % 512 < 256, 1.0, -1.0) * 100.0 / 256, "f32")
+    a["x0"] = K.rounded(a["x0"] * 1e-35, "f32")
+    a["k"][:] = 0.0
+    forward_alone(a, name)
