@@ -625,6 +625,11 @@ int ssm_linear_attention_step(const ssm_linear_token* p, void* stream);
  * Means, variances and sums are float32 (the parameters' gradients float64 over the
  * workgroups), the mean is taken before the squares.  A call with L = 1 is the form for
  * single tokens.  An infinite or NaN input reaches its own step and group.
+ * Sizes beside those of the views, from less than 2^32 threads in a launch: with channels
+ * contiguous in every tensor (sh = 1, groups of up to 32768) Bsz L G below 2^32 / t, where
+ * t = 8, 16, 32, 64, 256 or 1024 threads have a group of up to 64, 128, 256, 1024, 4096 or
+ * 32768 channels; in any other order Bsz ceil(L/64) G below 2^22.  Backwards G alone counts,
+ * below 2^24 and 2^22.
  * ---------------------------------------------------------------------- */
 #define SSM_GATE_NONE 0
 #define SSM_GATE_BEFORE 1

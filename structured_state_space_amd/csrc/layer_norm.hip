@@ -722,9 +722,33 @@ int64_t norm_part_rows(int64_t Bsz, int64_t L, int64_t D, int64_t G) {
     const int64_t a = norm_rows(Bsz * L, D, G), b = norm_step_rows(Bsz, L, G);
     return a > b ? a : b;  // either order of the tensors
 }
-bool norm_fits(int64_t Bsz, int64_t L, int64_t D, int64_t G) {
-    const int64_t steps = Bsz * step_blocks(L), most = (int64_t)1 << 32;
-    return Bsz * L < most && G < most && Bsz * L < most / G && grid_fits(Bsz * L * G, norm_lanes(D)) && grid_fits(steps * G, kStepThreads);
+// The two orders' grids, forwards and backwards; a call is refused by its own order's alone.
+static bool rows_fit(int64_t Bsz, int64_t L, int64_t D, int64_t G, bool grad) {
+    const int lanes = (int)(grad ? norm_grad_lanes(D) : norm_lanes(D)), threads = norm_threads(lanes), R = threads / lanes;
+    if (Bsz * L >= ((int64_t)1 << 40) / G) return false;
+    return grid_fits(grad ? norm_rows(Bsz * L, D, G) * G : (Bsz * L * G + R - 1) / R, threads);
+}
+static bool steps_fit(int64_t Bsz, int64_t L, int64_t G, bool grad) {
+    if (Bsz * step_blocks(L) >= ((int64_t)1 << 40) / G) return false;
+    return grid_fits((grad ? norm_step_rows(Bsz, L, G) : Bsz * step_blocks(L)) * G, kStepThreads);
+}
+static bool rows_order(const NormArgs& a) {
+    const View3* v[] = {&a.u, &a.z, &a.y};
+    return a.H / a.G <= kMostChannels && by_channel(v, 3);
+}
+static bool rows_order(const NormGradArgs& g) {
+    const View3* v[] = {&g.f.u, &g.f.z, &g.dy, &g.du, &g.dz};
+    return g.f.H / g.f.G <= kMostChannelsGrad && by_channel(v, 5);
+}
+bool norm_fits(const NormArgs& a) {
+    return rows_order(a) ? rows_fit(a.Bsz, a.L, a.H / a.G, a.G, false) : steps_fit(a.Bsz, a.L, a.G, false);
+}
+bool norm_fits(const NormGradArgs& g) {
+    const NormArgs& a = g.f;
+    return rows_order(g) ? rows_fit(a.Bsz, a.L, a.H / a.G, a.G, true) : steps_fit(a.Bsz, a.L, a.G, true);
+}
+bool norm_grad_may_fit(int64_t Bsz, int64_t L, int64_t D, int64_t G) {
+    return (D <= kMostChannelsGrad && rows_fit(Bsz, L, D, G, true)) || steps_fit(Bsz, L, G, true);
 }
 
 template <class T, int LANES, int V>
@@ -766,7 +790,7 @@ template <class T>
 static void launch_norm_t(const NormArgs& a, hipStream_t s) {
     const int64_t D = a.H / a.G, blocks = step_blocks(a.L);
     const View3* v[] = {&a.u, &a.z, &a.y};
-    if (D > kMostChannels || !by_channel(v, 3)) {
+    if (!rows_order(a)) {
         if (by_step(v, 3, D, a.L)) a.gate ? launch_steps<T, true, true>(a, blocks, s) : launch_steps<T, false, true>(a, blocks, s);
         else a.gate ? launch_steps<T, true, false>(a, blocks, s) : launch_steps<T, false, false>(a, blocks, s);
     } else if (D <= 64) launch_rows<T, 8, 1>(a, s);
@@ -795,7 +819,7 @@ static void launch_norm_grad_t(NormGradArgs& g, hipStream_t s) {
     const NormArgs& a = g.f;
     const int64_t D = a.H / a.G, blocks = step_blocks(a.L);
     const View3* v[] = {&a.u, &a.z, &g.dy, &g.du, &g.dz};
-    if (D > kMostChannelsGrad || !by_channel(v, 5)) {
+    if (!rows_order(g)) {
         g.rows = norm_step_rows(a.Bsz, a.L, a.G);
         if (by_step(v, 5, D, a.L))
             a.gate ? launch_steps_grad<T, true, true>(g, blocks, s) : launch_steps_grad<T, false, true>(g, blocks, s);

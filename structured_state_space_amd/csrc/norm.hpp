@@ -27,7 +27,10 @@ __device__ __forceinline__ float inverse_root(float v) {
     return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
 }
 
-bool norm_fits(int64_t Bsz, int64_t L, int64_t D, int64_t G);
+// the grid of the kernel that the views select; whether either order's gradients have one for these sizes
+bool norm_fits(const NormArgs& a);
+bool norm_fits(const NormGradArgs& g);
+bool norm_grad_may_fit(int64_t Bsz, int64_t L, int64_t D, int64_t G);
 int64_t norm_part_rows(int64_t Bsz, int64_t L, int64_t D, int64_t G);
 hipError_t launch_norm(int dtype, const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_backward(int dtype, NormGradArgs& g, hipStream_t s);

@@ -8,8 +8,7 @@ namespace {
 
 int check_norm_sizes(int64_t Bsz, int64_t H, int64_t L, int64_t G) {
     SSM_TRY(check_sizes(Bsz, H, L, Bsz, false));
-    if (G < 1 || H % G != 0) return SSM_ERR_INVALID_ARGUMENT;
-    return norm_fits(Bsz, L, H / G, G) ? SSM_OK : SSM_ERR_UNSUPPORTED;
+    return G < 1 || H % G != 0 ? SSM_ERR_INVALID_ARGUMENT : SSM_OK;
 }
 
 int check_norm(const ssm_norm* p, ssm_sequences* q, NormArgs* a) {
@@ -39,6 +38,7 @@ extern "C" {
 int ssm_layer_norm_bytes(int64_t Bsz, int64_t H, int64_t L, int64_t G, size_t* bytes) {
     if (!bytes) return SSM_ERR_INVALID_ARGUMENT;
     SSM_TRY(check_norm_sizes(Bsz, H, L, G));
+    if (!norm_grad_may_fit(Bsz, L, H / G, G)) return SSM_ERR_UNSUPPORTED;
     *bytes = backward_bytes(Bsz, H, L, G);
     return SSM_OK;
 }
@@ -49,6 +49,7 @@ int ssm_layer_norm(const ssm_norm* p, const ssm_view* y, void* stream) {
     SSM_TRY(check_norm(p, &q, &a));
     SSM_TRY(check_view(y, p->dtype, true, true, &q, p->H));
     a.y = view_of(y);
+    if (!norm_fits(a)) return SSM_ERR_UNSUPPORTED;
     return device_status(launch_norm(p->dtype, a, (hipStream_t)stream));
 }
 
@@ -62,9 +63,10 @@ int ssm_layer_norm_backward(const ssm_norm* p, const ssm_view* dy, const ssm_vie
     SSM_TRY(check_view(dz, p->dtype, p->gate != SSM_GATE_NONE, true, &q, p->H));
     if ((p->gate == SSM_GATE_NONE && dz && dz->data) || !aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(ws, 256))
         return SSM_ERR_INVALID_ARGUMENT;
+    g.dy = view_of(dy), g.du = view_of(du), g.dz = view_of(dz);
+    if (!norm_fits(g)) return SSM_ERR_UNSUPPORTED;
     const bool sums = dweight || dbias;
     if (sums && (!ws || ws_bytes < backward_bytes(p->Bsz, p->H, p->L, p->G))) return SSM_ERR_WORKSPACE;
-    g.dy = view_of(dy), g.du = view_of(du), g.dz = view_of(dz);
     g.dweight = dweight, g.dbias = dbias;
     g.parts = sums ? (float*)ws : nullptr;
     g.rows = 0;

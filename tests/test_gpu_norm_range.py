@@ -1,0 +1,31 @@
+"""Layer norm at sizes where a launch or an index could end."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DEV = "cuda:0"
+
+
+def _ssm():
+    from structured_state_space_amd import ssm
+    return ssm
+
+
+def test_more_than_2_to_22_rows_of_tokens():
+    """Flattened tokens with a norm for each head: 2^22 (token, group) rows, as one token each and as steps of a batch
+    (the same kernel on the same rows: the same bits)."""
+    ssm = _ssm()
+    Bsz, H, G = 1 << 16, 2048, 64
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    u, z, dy = (torch.randn((Bsz, H), generator=gen, device=DEV).bfloat16() for _ in range(3))
+    w = torch.randn(H, generator=gen, device=DEV)
+    more = dict(weight=w, gate="before", rms=True, groups=G)
+    y = ssm.layer_norm(u, z=z, **more)["y"]
+    g = ssm.layer_norm_backward(u, dy, z=z, **more)
+    steps = lambda t: t.view(16, Bsz // 16, H).transpose(1, 2)  # noqa: E731
+    want = ssm.layer_norm(steps(u), z=steps(z), **more)["y"]
+    back = ssm.layer_norm_backward(steps(u), steps(dy), z=steps(z), **more)
+    assert torch.equal(steps(y), want)
+    assert all(torch.equal(steps(g[k]), back[k]) for k in ("du", "dz")) and torch.equal(g["dweight"], back["dweight"])

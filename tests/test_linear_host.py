@@ -196,6 +196,22 @@ def test_norm_bytes():
     assert ssm.lib.ssm_layer_norm_bytes(2, 8, 16, 2, ctypes.byref(out)) == ssm.OK and out.value >= 2 * 8 * 4
 
 
+@pytest.mark.parametrize("sizes", [(65536, 8192, 1, 64), (32768, 8192, 1, 128), (1 << 19, 512, 1, 8), (16, 8192, 4096, 64)])
+def test_norms_of_many_tokens_have_a_workspace(sizes):
+    """More than 2^22 (token, group) rows: what the order of contiguous channels takes is not refused by the other's grid."""
+    out = ctypes.c_size_t()
+    assert ssm.lib.ssm_layer_norm_bytes(*sizes, ctypes.byref(out)) == ssm.OK and out.value > 0
+
+
+def test_norms_are_refused_by_the_grid_of_their_own_order():
+    """Forwards, every second channel of 2^22 rows, and contiguous ones of 2^32 threads (refused before anything runs)."""
+    for kw in (dict(Bsz=32768, H=8192, L=1, G=128, u=_view(sb=16384, sh=2)), dict(Bsz=1 << 20, H=512, L=1, G=512, u=_view(sh=1))):
+        p = _norm(**{**dict(gate=0, z=_view(data=None)), **kw})
+        assert ssm.lib.ssm_layer_norm(p, _view(sb=8192, sh=1), None) == UNSUPPORTED
+    out = ctypes.c_size_t()
+    assert ssm.lib.ssm_layer_norm_bytes(1, 1 << 24, 1, 1 << 24, ctypes.byref(out)) == UNSUPPORTED
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     q, v, g = torch.zeros(1, 1, 4, 8), torch.zeros(1, 2, 4, 8), torch.zeros(1, 2, 8)
     for call in (lambda: ssm.linear_attention(q, q, v, g), lambda: ssm.linear_attention_backward(q, q, v, g, v),
