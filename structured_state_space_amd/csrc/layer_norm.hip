@@ -666,28 +666,32 @@ __global__ __launch_bounds__(kStepThreads) void norm_steps_grad_kernel(const Nor
 }
 
 // The parameters' gradients: the rows of partial sums added up in float64, sixteen channels
-// to a workgroup and sixteen threads to a channel, eight rows under way.
+// to a workgroup at a time and sixteen threads to a channel, eight rows under way.
 __global__ __launch_bounds__(256) void norm_sums_kernel(const NormGradArgs g) {
     __shared__ double part[16][16];
     const int tid = threadIdx.x, c = tid & 15, k = tid >> 4;
-    const int64_t H = g.f.H, blocks = (H + 15) / 16, h = blockIdx.x % blocks * 16 + c;
-    const int which = (int)(blockIdx.x / blocks);
-    float* to = which ? g.dbias : g.dweight;
-    if (!to) return;
-    double sum = 0.0;
-    if (h < H)
-        for (int64_t r = k; r < g.rows; r += 16 * 8) {
-            float v[8];
+    const int64_t H = g.f.H, blocks = (H + 15) / 16;
+    for (int64_t unit = blockIdx.x; unit < 2 * blocks; unit += gridDim.x) {
+        const int64_t h = unit % blocks * 16 + c;
+        const int which = (int)(unit / blocks);
+        float* to = which ? g.dbias : g.dweight;
+        if (!to) continue;
+        double sum = 0.0;
+        if (h < H)
+            for (int64_t r = k; r < g.rows; r += 16 * 8) {
+                float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = r + 16 * i < g.rows ? g.parts[(which * g.rows + r + 16 * i) * H + h] : 0.0f;
+                for (int i = 0; i < 8; ++i) v[i] = r + 16 * i < g.rows ? g.parts[(which * g.rows + r + 16 * i) * H + h] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += v[i];
+                for (int i = 0; i < 8; ++i) sum += v[i];
+            }
+        __syncthreads();  // the last channels' sums have been read
+        part[k][c] = sum;
+        __syncthreads();
+        if (k == 0 && h < H) {
+            for (int i = 1; i < 16; ++i) sum += part[i][c];
+            to[h] = (float)sum;
         }
-    part[k][c] = sum;
-    __syncthreads();
-    if (k == 0 && h < H) {
-        for (int i = 1; i < 16; ++i) sum += part[i][c];
-        to[h] = (float)sum;
     }
 }
 
@@ -841,7 +845,10 @@ hipError_t launch_norm_backward(int dtype, NormGradArgs& g, hipStream_t s) {
     if (dtype == SSM_F32) launch_norm_grad_t<float>(g, s);
     else if (dtype == SSM_BF16) launch_norm_grad_t<bf16>(g, s);
     else launch_norm_grad_t<f16>(g, s);
-    if (g.parts) hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((g.f.H + 15) / 16 * 2)), dim3(256), 0, s, g);
+    if (g.parts) {  // (a workgroup has several units of channels only where one each would pass a launch's 2^32 threads)
+        const int64_t units = (g.f.H + 15) / 16 * 2, most = (int64_t)1 << 23;
+        hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)(units < most ? units : most)), dim3(256), 0, s, g);
+    }
     return hipGetLastError();
 }
 

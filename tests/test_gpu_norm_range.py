@@ -29,3 +29,18 @@ def test_more_than_2_to_22_rows_of_tokens():
     back = ssm.layer_norm_backward(steps(u), steps(dy), z=steps(z), **more)
     assert torch.equal(steps(y), want)
     assert all(torch.equal(steps(g[k]), back[k]) for k in ("du", "dz")) and torch.equal(g["dweight"], back["dweight"])
+
+
+def test_gradients_of_2_to_27_parameters():
+    """The parameters' sums in more units of sixteen channels than a launch of one each has threads for."""
+    ssm = _ssm()
+    H, G = (1 << 27) + 1024, (1 << 21) + 16
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    u, dy = (torch.randn((1, H), generator=gen, device=DEV).bfloat16() for _ in range(2))
+    w = torch.ones(H, device=DEV)
+    g = ssm.layer_norm_backward(u, dy, weight=w, bias=w, groups=G)
+    for i in (0, G // 2, G - 1):
+        at = slice(64 * i, 64 * i + 64)
+        part = ssm.layer_norm_backward(u[:, at].contiguous(), dy[:, at].contiguous(), weight=w[at], bias=w[at])
+        assert torch.equal(g["du"][:, at], part["du"])
+        assert torch.equal(g["dweight"][at], part["dweight"]) and torch.equal(g["dbias"][at], part["dbias"])
