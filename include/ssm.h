@@ -623,8 +623,9 @@ int ssm_linear_attention_step(const ssm_linear_token* p, void* stream);
  * u, z, y and their gradients are activations, views [Bsz,H,L] as above, with the same
  * conventions (outputs must not overlap inputs or each other); a group has H/G channels.
  * Means, variances and sums are float32 (the parameters' gradients float64 over the
- * workgroups), the mean is taken before the squares.  A call with L = 1 is the form for
- * single tokens.  An infinite or NaN input reaches its own step and group.
+ * workgroups), the mean is taken before the squares; a group whose squares add up beyond
+ * float32 (inputs from 1e19 on) has an n of 0.  A call with L = 1 is the form for single
+ * tokens.  An infinite or NaN input reaches its own step and group.
  * Sizes beside those of the views, from less than 2^32 threads in a launch: with channels
  * contiguous in every tensor (sh = 1, groups of up to 32768) Bsz L G below 2^32 / t, where
  * t = 8, 16, 32, 64, 256 or 1024 threads have a group of up to 64, 128, 256, 1024, 4096 or

@@ -20,11 +20,14 @@ struct NormGradArgs {
     int64_t rows;
 };
 
-// 1 / sqrt(v): the hardware's (one unit) and one step of Newton's method
+// 1 / sqrt(v): the hardware's (one unit; it takes subnormal numbers for zero) and one step of Newton's method
 __device__ __forceinline__ float inverse_root(float v) {
-    const float r = __builtin_amdgcn_rsqf(v);
+    const bool low = v < 0x1p-126f;
+    v *= low ? 0x1p24f : 1.0f;
+    float r = __builtin_amdgcn_rsqf(v);
     const float e = fmaf(-v * r, r, 1.0f);
-    return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
+    r = fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
+    return r * (low ? 0x1p12f : 1.0f);
 }
 
 // the grid of the kernel that the views select; whether either order's gradients have one for these sizes

@@ -44,3 +44,21 @@ def test_gradients_of_2_to_27_parameters():
         part = ssm.layer_norm_backward(u[:, at].contiguous(), dy[:, at].contiguous(), weight=w[at], bias=w[at])
         assert torch.equal(g["du"][:, at], part["du"])
         assert torch.equal(g["dweight"][at], part["dweight"]) and torch.equal(g["dbias"][at], part["dbias"])
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("order", ["tokens", "rows"])
+def test_variances_below_the_normal_numbers(order, rms):
+    """eps of zero and inputs of 1e-20: the mean square is a subnormal number of float32, whose root is not zero.
+    Squares are rounded to multiples of 2^-149, half of one each, and so is their mean: (1 + 1/2) 2^-150 of it, half
+    of that relative to the root; 200 half steps for all else, as in the norm's other tests."""
+    import oracle.linear_oracle as O
+    from tests.selective_cases import on_device, rounded
+    ssm = _ssm()
+    D = 48
+    u = rounded(np.random.default_rng(3).standard_normal((2, D, 9)) * 1e-20, "f32")
+    got = ssm.layer_norm(on_device(u, "f32", order), rms=rms, eps=0.0)["y"].double().cpu().numpy()
+    want, _, r = O.norm(u, None, None, None, "after", rms, 1, 0.0)
+    square = 1.0 / r[:, 0] ** 2
+    tol = np.abs(want) * (1.5 * 2.0 ** -150 / square / 2.0) + 200.0 * 2.0 ** -24 * (np.abs(want) + 1.0)
+    assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all()
