@@ -465,7 +465,7 @@ __device__ __forceinline__ int64_t by_die(int64_t bid, int64_t n) {
 // exp(sum to the end of s's block) exp(sum of the blocks between) exp(sum within t's),
 // each a sum of terms that are there; within a block the sums are formed pair by pair.
 template <class T>
-struct Decays {
+struct __attribute__((aligned(16))) Decays {  // (several lie one behind the other, and are read four numbers at a time)
     static constexpr int Q = kChunk<T>, B = Q / 16;
     float g[Q], in[Q], out[Q];     // of each row: log decay, weight towards the state, weight of what is read
     float head[Q], tail[Q];        // exp(sum from t's block's start to t) out_t; exp(sum behind s to its block's end) in_s
