@@ -530,10 +530,10 @@ int ssm_selective_step(const ssm_selective_token* p, void* stream);
  *     activations' type with room (float32 and bfloat16: sums of positive g up to 40
  *     over 64 steps, float16 up to 4; beyond, the forward pass goes step by step and
  *     the backward pass may overflow).
- *   - Results of 16-bit types are rounded from sums of products whose one factor (the
- *     weight of a pair of steps, the state) was rounded to the type; D v is added in
- *     float32; states, dg, dbeta and dD come from float32 numbers or from two (bfloat16:
- *     three) parts of 16 bits.
+ *   - Sums are float32.  Beside the activations the factors of their products are float32
+ *     numbers, in 16-bit types as two parts of the type or, for states, dg, dbeta and dD in
+ *     bfloat16, three: results of 16-bit types have the error of their own rounding.
+ *     Roundings of dg are relative to its chunk's sums.
  *   - An infinite or NaN input makes its own head (or, of q and k, its group) infinite
  *     or NaN from its step on, and nothing before; the head's (group's) gradients are
  *     infinite or NaN.

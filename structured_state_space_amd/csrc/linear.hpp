@@ -98,6 +98,19 @@ __device__ __forceinline__ void put_four(T* at, const f32x4& x) {
     struct __attribute__((aligned(4 * sizeof(T)))) Aligned { Quad<T> v; };
     *reinterpret_cast<Aligned*>(at) = {four_of<T>(x)};
 }
+// the same in parts, `apart` elements from one to the next
+template <class T, int K>
+__device__ __forceinline__ void put_parts(T* at, int apart, f32x4 x) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        put_four<T>(at + k * apart, x);
+        if (k + 1 < K) {
+            const Quad<T> f = four_of<T>(x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] -= to_f(get_of<T>(f, i));
+        }
+    }
+}
 template <>
 __device__ __forceinline__ Frag<float> frag_of<float>(const float (&x)[8]) {
     Frag<float> f;
@@ -117,8 +130,13 @@ __device__ __forceinline__ float frag_get<float>(const Frag<float>& f, int j) {
 // in bf16 (24 bits; two, 16 bits, left errors of 2.4e-6 in the states).
 template <class T>
 constexpr int kParts = sizeof(T) == 4 ? 1 : std::is_same<T, f16>::value ? 2 : 3;
+// Those of the operands that only give results of the type (the weights of pairs, the state in y and
+// dv): two in bf16 as well, 2^-17 of each.  In one part the results had the error of two roundings
+// instead of one.
 template <class T>
-__device__ __forceinline__ void split(const float (&x)[8], Frag<T> (&part)[kParts<T>]) {
+constexpr int kShort = sizeof(T) == 4 ? 1 : 2;
+template <class T, int K>
+__device__ __forceinline__ void split(const float (&x)[8], Frag<T> (&part)[K]) {
     float r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -129,7 +147,7 @@ __device__ __forceinline__ void split(const float (&x)[8], Frag<T> (&part)[kPart
     }
     part[0] = frag_of<T>(r);
 #pragma unroll
-    for (int i = 1; i < kParts<T>; ++i) {
+    for (int i = 1; i < K; ++i) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] -= frag_get<T>(part[i - 1], j);
         part[i] = frag_of<T>(r);
@@ -170,6 +188,30 @@ __device__ __forceinline__ Frag<float> pair_frag<float>(const float* p) {
     for (int j = 0; j < 4; ++j) f.v[j] = a[j], f.v[4 + j] = b[j];
     return f;
 }
+// the first four of these, and four zeros
+template <class T>
+__device__ __forceinline__ Frag<T> half_frag(const T* p) {
+    return {__builtin_shufflevector(*reinterpret_cast<const i16x4*>(p), i16x4{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7)};
+}
+template <>
+__device__ __forceinline__ Frag<float> half_frag<float>(const float* p) {
+    Frag<float> f;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.v[j] = a[j], f.v[4 + j] = 0.0f;
+    return f;
+}
+// The weights of a chunk's pairs in LDS, a row per later step: 32 rows have 32 columns, the next 32
+// 64 (products take 32 at a time), with 16 bytes of room behind each.
+template <class T>
+struct PairPlaces {
+    static constexpr int kSize = kChunk<T> / 32 == 1 ? 32 * (32 + kRoom<T>) : 32 * (96 + 2 * kRoom<T>);
+    static __device__ __forceinline__ constexpr int stride(int block) { return 32 * (block + 1) + kRoom<T>; }
+    // row r, which is in block r / 32
+    static __device__ __forceinline__ constexpr int row(int block, int r) {
+        return (block ? 32 * (32 + kRoom<T>) : 0) + (r - 32 * block) * stride(block);
+    }
+};
 // eight steps of a column: the summed axis down the rows.  Sixteen lanes read four
 // rows of sixteen numbers and get a column each (ds_read_b64_tr_b16); every lane of
 // the wave takes part.  `p`: the tile's column 0 of the 16, row 0 of the 32.

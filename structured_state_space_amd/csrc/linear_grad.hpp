@@ -20,8 +20,8 @@ constexpr int kPairThreads = 512;
 //   dg_r = sum over pairs t >= r > s of beta_s W_ts, over t >= r of q_t . before_t, over s < r of
 //          beta_s k_s . behind_s, and E <x, X>:
 // a step's decay takes part in every product over it.  All of dg and dbeta are sums in
-// float32 of float32 numbers: x and X are split (kParts), and only u beta dM is rounded to the
-// activations' type, for dq and dk, which are of that type.
+// float32 of float32 numbers: x and X are split (kParts); u beta dM, for dq and dk alone, is an
+// operand in two parts (kShort).
 // Values beyond 64 go block by block; every sum is linear in them.  q_t . k_s is formed
 // once for all heads.  A wave has 16 keys (or more), and all steps or some of them; results
 // lie transposed (lane: step, registers: four keys), so that rows of four keys are
@@ -37,7 +37,8 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
     constexpr int Q = kChunk<T>, TT = Q / 16, KK = NP / 32, SS = Q / 32, PK = kPairValues / 32;
     constexpr int TILES = NP / 16, NT = TILES > W ? TILES / W : 1;  // tiles of keys, and those of a wave
     constexpr int GROUPS = TILES >= W ? 1 : W / TILES < TT ? W / TILES : TT, TW = TT / GROUPS;  // of the steps; tiles of one
-    constexpr int KS = NP + kRoom<T>, VS = kPairValues + kRoom<T>, MS = Q + kRoom<T>;
+    constexpr int KS = NP + kRoom<T>, VS = kPairValues + kRoom<T>, K2 = kShort<T>;
+    using Pairs = PairPlaces<T>;
     constexpr bool F16 = std::is_same<T, f16>::value;
     // The states of the next block are loaded a block ahead, and v and dy two, where the registers
     // and LDS take it.  In float32 two workgroups share a compute unit instead: 27 us at 256 chunks of
@@ -47,11 +48,12 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
     struct PairSums {  // of W over the pairs of a tile's rows and columns, and on the diagonal
         float rows[TT][Q], columns[TT][Q], diagonal[Q], skip[TT];
     };
+    constexpr int KEYS = TILES / NT;  // a wave's tiles are added up
     struct KeySums {
-        float before[TILES][Q], behind[TILES][Q], whole[TILES];
+        float before[KEYS][Q], behind[KEYS][Q], whole[KEYS];
     };
     struct __attribute__((aligned(16))) Shared {
-        T q[Q * KS], k[Q * KS], v[RING][Q * VS], dy[RING][Q * VS], m[2][Q * MS];
+        T q[Q * KS], k[Q * KS], v[RING][Q * VS], dy[RING][Q * VS], m[2][K2 * Pairs::kSize];
         Decays<T> d[4];
         float beta[4][Q];
         float next[4], across[4], most_beta[4];  // the decay to the next chunk's first step; over the chunk and it
@@ -87,7 +89,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
         ck.clear(a.k.lay, N, nt, tid);
         cq.template store<false>(sh.q, a.qv.lay, tid);
         ck.template store<false>(sh.k, a.k.lay, tid);
-        for (int i = tid; i < 2 * Q * MS; i += TH) sh.m[0][i] = from_f<T>(0.0f);  // pairs s > t stay zero
+        for (int i = tid; i < 2 * K2 * Pairs::kSize; i += TH) sh.m[0][i] = from_f<T>(0.0f);  // pairs s > t stay zero
     }
     struct Block {  // of values of a head
         int h, pb;
@@ -137,10 +139,10 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
             }
             sum_diagonal += s.diagonal[lane];
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) sum_before += o.before[i][lane], sum_behind += o.behind[i][lane];
+            for (int i = 0; i < KEYS; ++i) sum_before += o.before[i][lane], sum_behind += o.behind[i][lane];
         }
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) sum_whole += o.whole[i];
+        for (int i = 0; i < KEYS; ++i) sum_whole += o.whole[i];
 #pragma unroll
         for (int i = 0; i < TT; ++i) sum_skip += s.skip[i];
     };
@@ -273,6 +275,8 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
             const T *v = sh.v[k % RING], *dy = sh.dy[k % RING], *m = sh.m[k & 1];
             KeySums& sums = sh.keys[k & 1];
             const float um = reciprocal_of_power(sm), further = sh.next[place(now.h)];
+            // (added up over a wave's tiles in LDS, not in registers)
+            auto keep = [&](float& to, float x, int n) { to = n ? to + x : x; };
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int key = n0 + 16 * n;
@@ -343,18 +347,22 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                         f32x4 w = {0, 0, 0, 0};
 #pragma unroll
                         for (int s = 0; s < SS; ++s)
-                            if (s <= tt / 2) w = mma<T>(kf[s], row_frag<T>(m + r * MS + 32 * s + 8 * gl), w);
+                            if (s <= tt / 2) {
+                                const T* mp = m + Pairs::row(tt / 2, r) + 32 * s + 8 * gl;
+#pragma unroll
+                                for (int i = K2 - 1; i >= 0; --i) w = mma<T>(kf[s], row_frag<T>(mp + i * Pairs::kSize), w);
+                            }
                         const float from = d.from[r];
                         const Own q4 = *reinterpret_cast<const Own*>(sh.q + r * KS + key + 4 * gl);
-                        float before = 0.0f;
+                        float sum = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float u = in[t][i] * from;
-                            before = fmaf(u, to_f(get_of<T>(q4.v, i)), before);
+                            sum = fmaf(u, to_f(get_of<T>(q4.v, i)), sum);
                             dq[n][t][i] = fmaf(u, ux, fmaf(w[i], um, dq[n][t][i]));
                         }
-                        before = across_rows(before) * ux;
-                        if (gl == 0) sums.before[tile + n][r] = before;
+                        sum = across_rows(sum) * ux;
+                        if (gl == 0) keep(sums.before[tile / NT][r], sum, n);
                     }
                 }
                 {
@@ -371,22 +379,27 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                         f32x4 w = {0, 0, 0, 0};
 #pragma unroll
                         for (int s = 0; s < SS; ++s)
-                            if (s >= tt / 2) w = mma<T>(qf[s], column_frag<T>(m + 32 * s * MS + 16 * tt, MS, lane), w);
+                            if (s >= tt / 2) {
+                                const T* mp = m + Pairs::row(s, 32 * s) + 16 * tt;
+#pragma unroll
+                                for (int i = K2 - 1; i >= 0; --i)
+                                    w = mma<T>(qf[s], column_frag<T>(mp + i * Pairs::kSize, Pairs::stride(s), lane), w);
+                            }
                         const float to = d.to[r] * further, b = sh.beta[place(now.h)][r] * uX;
                         const Own k4 = *reinterpret_cast<const Own*>(sh.k + r * KS + key + 4 * gl);
-                        float after = 0.0f;
+                        float sum = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float u = out[t][i] * to;
-                            after = fmaf(u, to_f(get_of<T>(k4.v, i)), after);
+                            sum = fmaf(u, to_f(get_of<T>(k4.v, i)), sum);
                             dk[n][t][i] = fmaf(u, b, fmaf(w[i], um, dk[n][t][i]));
                         }
-                        after = across_rows(after) * uX;
-                        if (gl == 0) sums.behind[tile + n][r] = after;
+                        sum = across_rows(sum) * uX;
+                        if (gl == 0) keep(sums.behind[tile / NT][r], sum, n);
                     }
                 }
                 whole = across_rows(row_sum(whole));
-                if (lane == 0) sums.whole[tile + n] = whole;
+                if (lane == 0) keep(sums.whole[tile / NT], whole, n);
             }
         }
         if (k + 1 < count) {  // the pairs
@@ -440,7 +453,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                     part += own ? 0.0f : wb;
                     w[i] = ub * sm;
                 }
-                put_four<T>(m + (16 * ti + tl) * MS + 16 * si + 4 * gl, w);
+                put_parts<T, K2>(m + Pairs::row(ti >> 1, 16 * ti + tl) + 16 * si + 4 * gl, Pairs::kSize, w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) column[i] = row_sum(column[i]);
                 if (tl == 0)

@@ -16,35 +16,42 @@ constexpr int kWalkValues = 64;  // values of a workgroup
 //   result_t = sum_s M_ts value_s + out_t E_t x^T q_t + D value_t,
 // and the state becomes E x + sum_s E'_s in_s k_s value_s^T: four matrix products.  The state
 // stays in float32 in registers, as the matrix instruction leaves it: a wave has 16 values and
-// half of the keys, and of the results those values and half of the steps.  Rounded, the state
-// goes through LDS once a chunk, and so does M, a tile of 16 x 16 pairs from a wave.
+// half of the keys, and of the results those values and half of the steps.  The registers are
+// operands as they are: a wave multiplies its keys with all steps, and either half gives the other
+// its steps' results through LDS once a chunk.  (The rounded state itself there, of all keys for
+// half of the steps, takes twice the room in two parts, and a unit then one workgroup instead of
+// two.)  M goes through LDS, a tile of 16 x 16 pairs from a wave.
 // 256 heads of 2048 steps, 128 keys and 64 values, bf16, with the states saved: 153 us, two waves to
 // a SIMD that issue vector instructions in a third of the cycles (450 a wave and chunk, a fifth of
 // them for the split) and wait for each other, three barriers to a chunk.  (Four waves with all
 // keys and steps of their values needed no exchange of the state, but waited more: 265 us.  Two
 // sets of tiles and two barriers were no faster: forwards 240 heads of 8192 steps 523 us, not 447.)
-// Rounding to the activations' type: M and the state as operands for the results, which
-// are rounded to it anyway (D value stays in float32).  What is added to the state is split (kParts).
+// M and the state are operands in two parts of 16 bits (kShort), what is added to the state in
+// kParts, and D value stays in float32: the results have the error of their own rounding.  (In one
+// part: 1.4 times that, for 16384 steps of 32 heads in 185 us instead of 197 and 4 x 2048 steps of 64
+// heads with their gradients in 538 instead of 565.)
 // ENDS: the first of two passes, which finds each segment's end state for the second.
 // OUT: results wanted.  FAST: the tensors' usual layout (WalkArgs), in a kernel without the code for
 // others: 5200 instructions instead of 7900, and addresses that do not fill the registers.
 template <class T, int NP, bool OUT, bool REVERSE, bool ENDS, bool FAST>
 __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void linear_walk_kernel(const WalkArgs a) {
     constexpr int Q = kChunk<T>, TT = Q / 16, HT = TT / 2, KK = NP / 32, SS = Q / 32, NT = NP / 32;  // NT: of a wave
-    constexpr int KS = NP + kRoom<T>, VS = kWalkValues + kRoom<T>, MS = Q + kRoom<T>;
+    constexpr int KS = NP + kRoom<T>, VS = kWalkValues + kRoom<T>, K2 = kShort<T>;
+    using Pairs = PairPlaces<T>;
     constexpr bool F16 = std::is_same<T, f16>::value;
     struct __attribute__((aligned(16))) Shared {
         T k[Q * KS];
         T v[Q * VS];
         T q[OUT ? Q * KS : 8];
-        T x[OUT ? kWalkValues * KS : 8];  // a row per value
-        T m[OUT ? Q * MS : 8];
+        T m[OUT ? K2 * Pairs::kSize : 8];
+        union {
+            f32x4 across[OUT ? kWalkWaves : 1][HT][64];  // for each wave, what its other keys' wave has for it
+            float sums[2][2][kWalkValues];
+        };
         Decays<T> d[2];
         uint32_t most[3][kWalkWaves];
         float most_x[kWalkWaves];
         int odd[kWalkWaves];
-        int passed;  // a chunk whose products passed float32, counted from 1
-        float sums[2][2][kWalkValues];
     };
     __shared__ Shared sh;
 
@@ -67,7 +74,8 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
     const int p0 = pb * kWalkValues;
     const bool live = p0 + 16 * pq < P;
     // the wave's tiles of rows: of four the first and last or the two between, as many pairs in either
-    auto tile = [&](int t) { return HT == 2 && t ? 3 - half : half; };
+    auto tile_of = [](int half, int t) { return HT == 2 && t ? 3 - half : half; };
+    auto tile = [&](int t) { return tile_of(half, t); };
     f32x4 x[NT];
     // the lane's states of a row of a [rows, H, N, P] array: n = 16 (NT half + tile) + 4 gl + i, value p
     auto exchange = [&](f32x4 (&x)[NT], auto* base, int64_t r, auto&& each) {
@@ -196,8 +204,7 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         if (OUT) {
             if (F16) most_state();
             // pairs s > t within two blocks of a product stay zero
-            for (int i = threadIdx.x; i < Q * MS; i += kWalkThreads) sh.m[i] = from_f<T>(0.0f);
-            if (threadIdx.x == 0) sh.passed = 0;
+            for (int i = threadIdx.x; i < K2 * Pairs::kSize; i += kWalkThreads) sh.m[i] = from_f<T>(0.0f);
         }
     }
     for (int k = 0; k < count; ++k) {
@@ -216,14 +223,18 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
         ck.template store<REVERSE>(sh.k, a.key.lay, tid);
         cv.template store<REVERSE>(sh.v, a.value.lay, tid);
         float sx = 1.0f;
+        Frag<T> state[OUT ? (NT + 1) / 2 : 1][K2];
         if (OUT) {
             cq.clear(a.query.lay, N, nt, tid);
             cq.template store<REVERSE>(sh.q, a.query.lay, tid);
             if (F16) sx = to_range<T>(fmaxf(sh.most_x[pq], sh.most_x[pq + 4]));
-            if (live) {
-                T* to = sh.x + (16 * pq + tl) * KS + 16 * NT * half + 4 * gl;
+            // the state's registers are operands as they are, of the wave's half of the keys
 #pragma unroll
-                for (int n = 0; n < NT; ++n) put_four<T>(to + 16 * n, x[n] * sx);
+            for (int n = 0; n < NT; n += 2) {
+                float u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = i < 4 ? x[n][i] * sx : NT > 1 ? x[n + (NT > 1)][i - 4] * sx : 0.0f;
+                split<T>(u, state[n / 2]);
             }
         }
         {
@@ -236,7 +247,14 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                 }
                 if (lane == 0) sh.most[0][wave] = mk, sh.most[1][wave] = mv, sh.most[2][wave] = mq;
             }
-            const bool any = __ballot(max(max(mk, mv), mq) >= kHuge<T>) != 0;
+            float mx = 0.0f;  // (a state whose products with the queries could pass float32)
+            if (OUT && !F16) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(x[n][i]));
+            }
+            const bool any = __ballot(max(max(mk, mv), mq) >= kHuge<T> || mx >= 0x1p64f) != 0;
             if (lane == 0) sh.odd[wave] = any;
         }
         __syncthreads();
@@ -266,21 +284,54 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
             // have lost all of theirs, and go row by row
             if (OUT) odd |= !(most_m < 0x1p20f);
         }
-        f32x4 across[OUT ? HT : 1];
+        auto from_state = [&](int h, f32x4 (&to)[HT]) {
+#pragma unroll
+            for (int t = 0; t < HT; ++t) to[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                Frag<T> f[HT];
+#pragma unroll
+                for (int t = 0; t < HT; ++t) {
+                    const T* qp = sh.q + (16 * tile_of(h, t) + tl) * KS + 16 * (NT * half + n) + 4 * gl;
+                    f[t] = NT > 1 ? pair_frag<T>(qp) : half_frag<T>(qp);
+                }
+                // (products that wait for each other's sums do not follow each other)
+#pragma unroll
+                for (int i = 0; i < K2; ++i)
+#pragma unroll
+                    for (int t = 0; t < HT; ++t) to[t] = mma<T>(state[n / 2][i], f[t], to[t]);
+            }
+        };
         float sm = 1.0f;
         if (OUT && !odd) {
             sm = to_range<T>(most_m);
+            // what the state before the chunk gives: either half has the other one's results of half of the steps
+            if (live) {
+                f32x4 other[HT];
+                from_state(1 - half, other);
+#pragma unroll
+                for (int t = 0; t < HT; ++t) sh.across[wave ^ 4][t][lane] = other[t];
+            }
             // the pairs: tiles on the diagonal by the first waves, those below it by the others
             auto pairs = [&](int ti, int si) {
                 f32x4 m = {0, 0, 0, 0};
                 const T* kp = sh.k + (16 * si + tl) * KS + 8 * gl;
                 const T* qp = sh.q + (16 * ti + tl) * KS + 8 * gl;
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) m = mma<T>(row_frag<T>(kp + 32 * kk), row_frag<T>(qp + 32 * kk), m);
+                for (int k0 = 0; k0 < KK; k0 += 2) {
+                    Frag<T> kf[2], qf[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (k0 + i < KK) kf[i] = row_frag<T>(kp + 32 * (k0 + i)), qf[i] = row_frag<T>(qp + 32 * (k0 + i));
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (k0 + i < KK) m = mma<T>(kf[i], qf[i], m);
+                }
                 return m;
             };
             auto keep = [&](int ti, int si, const f32x4& m) {
-                put_four<T>(sh.m + (16 * ti + tl) * MS + 16 * si + 4 * gl, m * sm);
+                put_parts<T, K2>(sh.m + Pairs::row(ti >> 1, 16 * ti + tl) + 16 * si + 4 * gl, Pairs::kSize, m * sm);
             };
             if (wave < TT) {
                 keep(wave, wave, pairs(wave, wave) * weights_within<T>(d, wave, lane));
@@ -290,27 +341,8 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
                     keep(ti, si, pairs(ti, si) * weights_across<T>(d, ti, si, lane));
                 }
             }
-            // what the state before the chunk gives
-            if (live) {
-#pragma unroll
-                for (int t = 0; t < HT; ++t) across[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    const Frag<T> f = row_frag<T>(sh.x + (16 * pq + tl) * KS + 32 * kk + 8 * gl);
-#pragma unroll
-                    for (int t = 0; t < HT; ++t)
-                        across[t] = mma<T>(f, row_frag<T>(sh.q + (16 * tile(t) + tl) * KS + 32 * kk + 8 * gl), across[t]);
-                }
-                if (__ballot(far_out(across)) && lane == 0) sh.passed = k + 1;
-            }
             __syncthreads();
         }
-        Frag<T> vf[SS];  // (under way while the test waits)
-        if (live) {
-#pragma unroll
-            for (int s = 0; s < SS; ++s) vf[s] = column_frag<T>(sh.v + 32 * s * VS + 16 * pq, VS, lane);
-        }
-        if (OUT && !odd) odd = sh.passed == k + 1;
         if (__builtin_expect(odd, 0)) {
             // An infinity or NaN among the inputs, or one that comes of their products, would reach
             // other rows through the products' zeros: the chunk goes row by row, as the formula says.
@@ -347,20 +379,31 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
             }
         }
         if (live && !odd) {
+            Frag<T> vf[SS];
+#pragma unroll
+            for (int s = 0; s < SS; ++s) vf[s] = column_frag<T>(sh.v + 32 * s * VS + 16 * pq, VS, lane);
             if (OUT) {
                 struct __attribute__((aligned(4 * sizeof(T)))) Own { Quad<T> v; };
                 const float um = reciprocal_of_power(sm), ux = reciprocal_of_power(sx);
+                f32x4 within[HT], across[HT];
+                from_state(half, across);
+#pragma unroll
+                for (int t = 0; t < HT; ++t) within[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int i = K2 - 1; i >= 0; --i)
+#pragma unroll
+                    for (int s = SS - 1; s >= 0; --s)
+#pragma unroll
+                        for (int t = s; t < HT; ++t)
+                            within[t] = mma<T>(vf[s], row_frag<T>(sh.m + Pairs::row(t, 16 * tile(t) + tl) + i * Pairs::kSize + 32 * s + 8 * gl), within[t]);
 #pragma unroll
                 for (int t = 0; t < HT; ++t) {
                     const int r = 16 * tile(t) + tl, o = REVERSE ? Q - 1 - r : r;
-                    const T* mp = sh.m + r * MS + 8 * gl;
-                    f32x4 within = {0, 0, 0, 0};
-                    within = mma<T>(vf[0], row_frag<T>(mp), within);
-                    if (SS > 1 && t) within = mma<T>(vf[SS - 1], row_frag<T>(mp + 32), within);
+                    across[t] += sh.across[wave][t][lane];
                     const float f = d.from[r] * ux;
                     f32x4 sum;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[i] = fmaf(across[t][i], f, within[i] * um);
+                    for (int i = 0; i < 4; ++i) sum[i] = fmaf(across[t][i], f, within[t][i] * um);
                     if (a.D) {  // (in float32: on M's diagonal it would be rounded with M, alike in all steps)
                         const Own v4 = *reinterpret_cast<const Own*>(sh.v + r * VS + 16 * pq + 4 * gl);
 #pragma unroll

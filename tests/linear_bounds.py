@@ -13,9 +13,9 @@ dg_r   is a running sum over its chunk of R_t - C_s (R_t = q_t . dq_t, C_s = bet
        the head) and of <x, X>.  R and C are sums of signed terms: what rounding does to them is
        relative to the root of their terms' squares, which the sums themselves have on average.
 dD     sums of dy v, COUNT relative to the root of their squares.
-y, dv  one rounding of the result, one of each weight of a pair within the chunk, one of each
-       state's number: half steps of the type relative to the terms M_ts v_s and x_np q_n.
-dq, dk one rounding of the result and one of each weight u beta dM (the states are split)."""
+y, dv, dq, dk   one rounding of the result.  The weights of pairs and the states are operands in two
+       parts of the type: the square of its half step, relative to the terms M_ts v_s, x_np q_n and
+       u_ts beta_s dM_ts k_s, beside COUNT half steps of float32."""
 import numpy as np
 
 import oracle.linear_oracle as O
@@ -92,8 +92,8 @@ def results(a, name, spans):
                 X = np.exp(b["g"][row, :, t])[:, None, None] * (
                     X + a["scale"] * b["q"][row, :, :, t][:, :, None] * b["dy"][row, :, :, t][:, None, :])
     whole = dict(y=y, dv=grads["dv"], dq=grads["dq"], dk=grads["dk"])
-    half = HALF_STEP[name] / np.sqrt(3.0)
-    return {n: half * np.sqrt(np.nansum(whole[n] ** 2) + sq[n]) * (1.0 + 2.0 ** -5) for n in sq}
+    half, fine = HALF_STEP[name] / np.sqrt(3.0), HALF_STEP[name] ** 2 + count(a) * U
+    return {n: half * np.sqrt(np.nansum(whole[n] ** 2)) * (1.0 + 2.0 ** -5) + fine * np.sqrt(sq[n]) for n in sq}
 
 
 def off(got, want):

@@ -24,12 +24,12 @@ def test_the_bound_of_dg_sees_a_lost_part_and_a_scale(name, size):
 @pytest.mark.parametrize("name", ["bf16", "f16"])
 @pytest.mark.parametrize("size", SIZES)
 def test_the_bounds_of_results_see_a_rounding_too_many(name, size):
-    """Results that are rounded to a type of two bits less: four times the error of one rounding."""
+    """A part as large as the result, rounded before it is added: an operand in one part alone."""
     a = K.inputs(72, name, *size)
     spans = S.dense_spans(size[0], size[5])
     want = {"y": K.forward(a, spans)["y"], **K.backward(a, spans)}
     for n, bound in B.results(a, name, spans).items():
         fine = K.rounded(want[n], name)
         assert B.off(fine, want[n]) < bound, n
-        step = 2.0 ** np.floor(np.log2(np.abs(want[n]) + 1e-300)) * K.HALF_STEP[name] * 8.0
-        assert B.off(np.round(want[n] / step) * step, want[n]) > bound, n
+        other = np.random.default_rng(73).standard_normal(want[n].shape) * np.abs(want[n])
+        assert B.off(K.rounded(want[n] - other, name) + K.rounded(other, name), want[n]) > bound, n
