@@ -381,11 +381,14 @@ struct Carrier {
         }
     }
 };
-// Bits of the magnitude from which on a chunk goes row by row: 2^22, infinity in float16.  Below,
-// with put_decays' bounds, no product of a chunk's inputs passes float32: a weight of a pair stays
-// below N 2^44 2^60 2^14 <= 2^126 and what a chunk adds to the state below 64 2^44 2^60.
+// Bits of the magnitudes from which on a chunk goes row by row: 2^22 for queries and keys, 2^39 for
+// values, infinity in float16.  Below, with put_decays' bounds, no product of a chunk's inputs passes
+// float32: a weight of a pair stays below N 2^44 2^60 2^14 <= 2^126 and what a chunk adds to the
+// state below 64 2^22 2^39 2^60 = 2^127.
 template <class T>
 constexpr uint32_t kHuge = sizeof(T) == 4 ? 0x4a800000u : std::is_same<T, f16>::value ? 0x7c00u : 0x4a80u;
+template <class T>
+constexpr uint32_t kHugeValue = sizeof(T) == 4 ? 0x53000000u : std::is_same<T, f16>::value ? 0x7c00u : 0x5300u;
 
 // A power of two 2^e that brings magnitudes up to `most` (float32) below 2^15, where
 // float16 has them and 2^-39 of them; 1 for other types.  Bounded by what float32's largest

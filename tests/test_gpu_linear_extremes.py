@@ -126,6 +126,16 @@ def test_products_that_come_back(name, sizes):
 
 
 @pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_large_numbers_whose_products_fit(name):
+    """Queries and keys of 1e5, values and gradients of 1e10 throughout, as of a scaled loss."""
+    a = K.inputs(49, name, 1, 4, 2, 64, 48, 150, skip=False)
+    for n, s in dict(q=1e5, k=1e5, v=1e10, dy=1e10).items():
+        a[n] = K.rounded(a[n] * s, name)
+    a["x0"], a["dx"] = K.rounded(a["x0"] * 1e15, "f32"), K.rounded(a["dx"] * 1e15, "f32")
+    compare(a, name, skip=())
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("beta", [0.0, 1.0, 2.5])
 def test_step_with_a_masked_key(name, beta):
     """One token whose key or value (or query) is the lowest number and whose other one (state) is zero."""
