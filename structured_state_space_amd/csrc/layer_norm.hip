@@ -765,7 +765,8 @@ static void launch_rows(const NormArgs& a, hipStream_t s) {
 // Channels of a lane: few where the group has few, more in registers while they fit.  float32, 16 x 3000
 // steps: 128 channels 28 us and 512 46 us, read twice instead 30 and 53.  Gradients keep 128 channels
 // alone: with 512, or the norm's input of them, registers went to memory (16 x 512 x 3000, dy read twice
-// 111 us instead of 113, but 256 channels 72 instead of 64).
+// 111 us instead of 113, but 256 channels 72 instead of 64).  Beyond, u is read three times and dy twice:
+// 510 MB where 197 would do.  LDS, of which a workgroup has 14 KB of 160, is not used for them.
 template <class T, bool GATED, bool VEC>
 static void launch_steps(const NormArgs& a, int64_t blocks, hipStream_t s) {
     const int64_t D = a.H / a.G;

@@ -36,9 +36,9 @@ size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 // Steps of a segment, whole chunks.  A walk has a workgroup per sequence, head and 64
 // values; where those leave many of the compute units idle, sequences are cut, for one more
 // launch over nearly all of the steps, which finds every segment's end state.  Forwards,
-// 128 keys, 64 values, bf16, cut and not cut: 32 workgroups of 4096 steps 68 and 223 us, 96 147
-// and 225, 128 of 8192 290 and 439, 200 of 4096 257 and 226; 160 in float32 626 and 650.
-// Cut into about 512 workgroups: 32 heads of 16384 steps 191 us, into 256 218, 1024 222; of four
+// 128 keys, 64 values, bf16, cut and not cut: 32 workgroups of 4096 steps 73 and 237 us, 96 146
+// and 238, 128 of 8192 281 and 467, 200 of 4096 252 and 236; 160 in float32 514 and 591.
+// Cut into about 512 workgroups: 32 heads of 16384 steps 190 us, into 256 211, 1024 236; of four
 // chunks or more, since every segment starts with its state and the first loads' latency.
 int64_t segment_steps(const Seqs& q, const Sizes& z) {
     const int64_t Q = chunk_of(z.dtype), wgs = (q.offsets ? 1 : q.S) * z.H * value_blocks(z.P);
@@ -63,9 +63,9 @@ size_t saved_bytes(const Seqs& q, const Sizes& z) {
 }
 // Workgroups that share a group's heads in the pairs' kernel, and their heads: as many as the
 // compute units take at once.  More add partial sums and fewer heads to each pipeline: forwards
-// and backwards at 4 x 2048 steps, 64 heads, one group, bf16, 522 us with twice and 550 with four times as
-// many, 509 so; 80 heads in eight groups over 1024 steps 177, 189 and 156.  Small tiles of float32
-// have two workgroups to a unit: 2 x 2048 steps, 32 heads, 258 us, with half 271, with twice 262.
+// and backwards at 4 x 2048 steps, 64 heads, one group, bf16, 551 us with twice and 563 with four times as
+// many, 533 so; 80 heads in eight groups over 1024 steps 179, 193 and 158.  Small tiles of float32
+// have two workgroups to a unit: 2 x 2048 steps, 32 heads, 255 us, with half 268, with twice 262.
 int64_t head_blocks(const Seqs& q, const Sizes& z, int* heads) {
     const int64_t items = item_count(q, chunk_of(z.dtype)), Hg = z.H / z.G;
     const int64_t all = z.dtype == SSM_F32 && z.N <= 64 ? 512 : 256;

@@ -28,7 +28,7 @@ constexpr int kPairThreads = 512;
 // multiplied with q and k at once.  The sums over pairs and keys go through LDS and become dg
 // and dbeta a block later, in the last wave, beside the other waves' pairs; so do the decays
 // of the head after the next.
-// 128 chunks of 64 steps, 64 heads of 128 keys and 64 values, one group, bf16: 231 us.  The saved
+// 128 chunks of 64 steps, 64 heads of 128 keys and 64 values, one group, bf16: 240 us.  The saved
 // states alone, 537 MB, take 113 us at a copy's rate; of the rest, vector instructions (a third
 // of them split the states) and the tiles' reads from LDS have most, at two waves to a SIMD.
 template <class T, int NP, bool FAST>

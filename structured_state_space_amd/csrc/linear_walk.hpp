@@ -21,18 +21,19 @@ constexpr int kWalkValues = 64;  // values of a workgroup
 // its steps' results through LDS once a chunk.  (The rounded state itself there, of all keys for
 // half of the steps, takes twice the room in two parts, and a unit then one workgroup instead of
 // two.)  M goes through LDS, a tile of 16 x 16 pairs from a wave.
-// 256 heads of 2048 steps, 128 keys and 64 values, bf16, with the states saved: 153 us, two waves to
-// a SIMD that issue vector instructions in a third of the cycles (450 a wave and chunk, a fifth of
-// them for the split) and wait for each other, three barriers to a chunk.  (Four waves with all
-// keys and steps of their values needed no exchange of the state, but waited more: 265 us.  Two
-// sets of tiles and two barriers were no faster: forwards 240 heads of 8192 steps 523 us, not 447.)
+// 256 heads of 2048 steps, 128 keys and 64 values, bf16, with the states saved: 163 us, two waves to
+// a SIMD that issue vector instructions in half of the cycles (570 a wave and chunk, a quarter of
+// them for the splits) and wait for each other, three barriers to a chunk.  (Four waves with all
+// keys and steps of their values needed no exchange of the state, but waited more; two sets of tiles
+// and two barriers were no faster: with M and the state in one part 265 us instead of 153, and forwards
+// 240 heads of 8192 steps 523 us instead of 447.)
 // M and the state are operands in two parts of 16 bits (kShort), what is added to the state in
 // kParts, and D value stays in float32: the results have the error of their own rounding.  (In one
-// part: 1.4 times that, for 16384 steps of 32 heads in 185 us instead of 197 and 4 x 2048 steps of 64
-// heads with their gradients in 538 instead of 565.)
+// part: 1.4 times that, for 6% less time over 16384 steps of 32 heads and 5% over 4 x 2048 steps of 64
+// with their gradients.)
 // ENDS: the first of two passes, which finds each segment's end state for the second.
 // OUT: results wanted.  FAST: the tensors' usual layout (WalkArgs), in a kernel without the code for
-// others: 5200 instructions instead of 7900, and addresses that do not fill the registers.
+// others: 5800 instructions instead of 8100, and addresses that do not fill the registers.
 template <class T, int NP, bool OUT, bool REVERSE, bool ENDS, bool FAST>
 __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void linear_walk_kernel(const WalkArgs a) {
     constexpr int Q = kChunk<T>, TT = Q / 16, HT = TT / 2, KK = NP / 32, SS = Q / 32, NT = NP / 32;  // NT: of a wave
