@@ -539,8 +539,8 @@ int ssm_selective_step(const ssm_selective_token* p, void* stream);
  *     infinite or NaN.
  *   - Finite inputs give what the formula does also where q . k or dy . v pass float32, such as
  *     a masked step that holds the type's lowest numbers with a beta, k or v of zero: sums are
- *     infinite or NaN only where the magnitudes of their own terms add up beyond float32 (of dg:
- *     where those of beta dbeta do).
+ *     infinite or NaN only where the magnitudes of their own terms add up beyond float32, dq and
+ *     dk also where scale beta (dy . v) is beyond it, dg where beta dbeta is.
  * Sizes: those of the selective operators, N <= 256, P <= 256.
  * ---------------------------------------------------------------------- */
 
