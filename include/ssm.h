@@ -533,14 +533,16 @@ int ssm_selective_step(const ssm_selective_token* p, void* stream);
  *   - Sums are float32.  Beside the activations the factors of their products are float32
  *     numbers, in 16-bit types as two parts of the type or, for states, dg, dbeta and dD in
  *     bfloat16, three: results of 16-bit types have the error of their own rounding.
- *     Roundings of dg are relative to its chunk's sums.
+ *     Roundings of dg are relative to its chunk's sums.  float16's parts are relative to the
+ *     largest of their chunk: 2^-39 of it is kept, of weights of pairs 2^-50.
  *   - An infinite or NaN input makes its own head (or, of q and k, its group) infinite
  *     or NaN from its step on, and nothing before; the head's (group's) gradients are
  *     infinite or NaN.
  *   - Finite inputs give what the formula does also where q . k or dy . v pass float32, such as
  *     a masked step that holds the type's lowest numbers with a beta, k or v of zero: sums are
  *     infinite or NaN only where the magnitudes of their own terms add up beyond float32, dq and
- *     dk also where scale beta (dy . v) is beyond it, dg where beta dbeta is.
+ *     dk also where scale beta (dy . v) is beyond it (it counts as the type's largest number
+ *     where q . k is zero), dg where beta dbeta is.
  * Sizes: those of the selective operators, N <= 256, P <= 256.
  * ---------------------------------------------------------------------- */
 

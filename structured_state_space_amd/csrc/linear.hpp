@@ -98,7 +98,11 @@ __device__ __forceinline__ void put_four(T* at, const f32x4& x) {
     struct __attribute__((aligned(4 * sizeof(T)))) Aligned { Quad<T> v; };
     *reinterpret_cast<Aligned*>(at) = {four_of<T>(x)};
 }
-// the same in parts, `apart` elements from one to the next
+// The same in parts, `apart` elements from one to the next.  float16's second part is taken kLift
+// times: below 2^-14 it would have ever fewer bits, and so would what is small beside the chunk's
+// largest weight (2^-50 of it is kept, instead of 2^-39).
+template <class T>
+constexpr float kLift = std::is_same<T, f16>::value ? 0x1p11f : 1.0f;
 template <class T, int K>
 __device__ __forceinline__ void put_parts(T* at, int apart, f32x4 x) {
 #pragma unroll
@@ -107,7 +111,7 @@ __device__ __forceinline__ void put_parts(T* at, int apart, f32x4 x) {
         if (k + 1 < K) {
             const Quad<T> f = four_of<T>(x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] -= to_f(get_of<T>(f, i));
+            for (int i = 0; i < 4; ++i) x[i] = (x[i] - to_f(get_of<T>(f, i))) * kLift<T>;
         }
     }
 }

@@ -346,12 +346,13 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                         const int tt = TW * group + t, r = 16 * tt + tl;
                         f32x4 w = {0, 0, 0, 0};
 #pragma unroll
-                        for (int s = 0; s < SS; ++s)
-                            if (s <= tt / 2) {
-                                const T* mp = m + Pairs::row(tt / 2, r) + 32 * s + 8 * gl;
+                        for (int i = K2 - 1; i >= 0; --i) {
 #pragma unroll
-                                for (int i = K2 - 1; i >= 0; --i) w = mma<T>(kf[s], row_frag<T>(mp + i * Pairs::kSize), w);
-                            }
+                            for (int s = 0; s < SS; ++s)
+                                if (s <= tt / 2)
+                                    w = mma<T>(kf[s], row_frag<T>(m + Pairs::row(tt / 2, r) + i * Pairs::kSize + 32 * s + 8 * gl), w);
+                            w *= i ? 1.0f / kLift<T> : 1.0f;
+                        }
                         const float from = d.from[r];
                         const Own q4 = *reinterpret_cast<const Own*>(sh.q + r * KS + key + 4 * gl);
                         float sum = 0.0f;
@@ -378,13 +379,13 @@ __global__ __launch_bounds__(kPairThreads, 2) void linear_pairs_kernel(const Pai
                         const int tt = TW * group + t, r = 16 * tt + tl;
                         f32x4 w = {0, 0, 0, 0};
 #pragma unroll
-                        for (int s = 0; s < SS; ++s)
-                            if (s >= tt / 2) {
-                                const T* mp = m + Pairs::row(s, 32 * s) + 16 * tt;
+                        for (int i = K2 - 1; i >= 0; --i) {
 #pragma unroll
-                                for (int i = K2 - 1; i >= 0; --i)
-                                    w = mma<T>(qf[s], column_frag<T>(mp + i * Pairs::kSize, Pairs::stride(s), lane), w);
-                            }
+                            for (int s = 0; s < SS; ++s)
+                                if (s >= tt / 2)
+                                    w = mma<T>(qf[s], column_frag<T>(m + Pairs::row(s, 32 * s) + i * Pairs::kSize + 16 * tt, Pairs::stride(s), lane), w);
+                            w *= i ? 1.0f / kLift<T> : 1.0f;
+                        }
                         const float to = d.to[r] * further, b = sh.beta[place(now.h)][r] * uX;
                         const Own k4 = *reinterpret_cast<const Own*>(sh.k + r * KS + key + 4 * gl);
                         float sum = 0.0f;

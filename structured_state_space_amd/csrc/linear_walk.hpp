@@ -281,9 +281,9 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
             }
             most_in = d.most_in * d.grow;
             most_m = most_in * d.most_out * most[0] * most[2] * (float)N;
-            // M keeps 2^-39 of this, 2^-17 at least: beside a step of the lowest numbers ordinary ones would
-            // have lost all of theirs, and go row by row
-            if (OUT) odd |= !(most_m < 0x1p22f);
+            // M keeps 2^-50 of this, 2^-22 at least: beside a step of the lowest queries and keys ordinary ones
+            // would lose theirs, and go row by row
+            if (OUT) odd |= !(most_m < 0x1p28f);
         }
         auto from_state = [&](int h, f32x4 (&to)[HT]) {
 #pragma unroll
@@ -392,12 +392,15 @@ __global__ __launch_bounds__(kWalkThreads, NP * sizeof(T) > 256 ? 2 : 4) void li
 #pragma unroll
                 for (int t = 0; t < HT; ++t) within[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int i = K2 - 1; i >= 0; --i)
+                for (int i = K2 - 1; i >= 0; --i) {
 #pragma unroll
                     for (int s = SS - 1; s >= 0; --s)
 #pragma unroll
                         for (int t = s; t < HT; ++t)
                             within[t] = mma<T>(vf[s], row_frag<T>(sh.m + Pairs::row(t, 16 * tile(t) + tl) + i * Pairs::kSize + 32 * s + 8 * gl), within[t]);
+#pragma unroll
+                    for (int t = 0; t < HT; ++t) within[t] *= i ? 1.0f / kLift<T> : 1.0f;
+                }
 #pragma unroll
                 for (int t = 0; t < HT; ++t) {
                     const int r = 16 * tile(t) + tl, o = REVERSE ? Q - 1 - r : r;

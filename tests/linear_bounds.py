@@ -73,7 +73,7 @@ def results(a, name, spans):
     grads = O.attention_grad(a["q"], a["k"], a["v"], a["g"], a["beta"], a["D"], a["scale"], a["x0"], a["dy"], a["dx"], spans)
     sq = dict(y=0.0, dv=0.0, dq=0.0, dk=0.0)
     for s, (row, beg, end) in enumerate(spans):
-        X = np.zeros(states[s, beg].shape) if a["dx"] is None else a["dx"][s].copy()
+        X = np.zeros((H, a["q"].shape[2], a["v"].shape[2])) if a["dx"] is None else a["dx"][s].copy()
         for t0 in reversed(range(beg, end, Q)):
             t1 = min(t0 + Q, end)
             q, k, v, dy = (b[n][row, :, :, t0:t1] for n in ("q", "k", "v", "dy"))

@@ -77,6 +77,23 @@ def test_masked_places_that_are_read(name, what, zero):
     compare(a, name, at=AT)
 
 
+@pytest.mark.parametrize("size", SIZES)
+def test_small_numbers_beside_masked_ones_in_float16(size):
+    """Keys and values of 3e-3 beside the lowest ones, which weigh nothing: the weights of pairs keep their bits."""
+    a = K.inputs(50, "f16", *size, skip=False)
+    for n in "kv":
+        a[n] = K.rounded(a[n] * 3e-3, "f16")
+    a["x0"] = K.rounded(a["x0"] * 1e-5, "f32")
+    hide(a, "f16", "kv", AT)
+    a["beta"][..., list(AT)] = 0.0
+    a["dy"][..., list(AT)] = 0.0
+    ssm, spans = _ssm(), S.dense_spans(size[0], size[5])
+    args, kw = K.call_args(a, "f16", "tokens")
+    g = ssm.linear_attention_backward(*args, K.on_device(a["dy"], "f16", "tokens"), dx=_f32(a["dx"]), **kw)
+    want, mag = K.backward(a, spans), K.backward(a, spans, True)
+    K.assert_all({n: _np(g[n]) for n in ("dq", "dk", "dv")}, want, mag, a, "f16", spans)
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("order", ["rows", "mixed"])
 def test_masked_places_in_other_orders(name, order):
